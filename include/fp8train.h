@@ -16,8 +16,10 @@
  *   fprop, dgrad, wgrad (+ sum of dW^2)                 fp8_gemm_multi_sumsq
  *   AdamW on that sum + cast of the next step's W       fused_adamw_multi_tensor_presummed
  *
- * plus current scaling (fp8_cast_transpose_amax_current_multi) and MXFP8 block scaling
- * (fp8_mx_cast_multi, fp8_mx_gemm_multi).
+ * plus current scaling (fp8_cast_transpose_amax_current_multi), MXFP8 block scaling
+ * (fp8_mx_cast_multi, fp8_mx_gemm_multi), its 4-bit forms (fp4_cast_multi, fp4_gemm_multi) and the
+ * root-mean-square norm in front of a Linear, quantising its output (fp8_rmsnorm_cast), with its
+ * backward pass (fp8_rmsnorm_backward).
  *
  * Sources, cited by page title and section:
  *   [P1] "算子与编译器：FP8 训练与优化器 Kernel" (charles2530.github.io)
@@ -343,6 +345,154 @@ fp8t_status fp8_mx_gemm_multi_sumsq(const fp8t_mx_gemm_desc* gemms, int32_t n_ge
 /* Scratch bytes fp8_mx_gemm_multi_sumsq needs (0 on invalid input or no problem selected). */
 size_t fp8_mx_gemm_sumsq_workspace_bytes(const fp8t_mx_gemm_desc* gemms, int32_t n_gemms,
                                          const int32_t* sumsq_of);
+
+/* How a tensor is quantised (fp8_rmsnorm_cast; the 4-bit calls take the last two). */
+typedef enum fp8t_quant {
+    FP8T_Q_NONE = 0,   /* not quantised                                                           */
+    FP8T_Q_FP8 = 1,    /* E4M3 / E5M2 with one per-tensor scale (the cast of delayed scaling)      */
+    FP8T_Q_MXFP8 = 2,  /* E4M3 / E5M2 with one E8M0 scale per 32 values (fp8_mx_cast_multi's)      */
+    FP8T_Q_MXFP4 = 3,  /* E2M1 with one E8M0 scale per 32 values                                  */
+    FP8T_Q_NVFP4 = 4   /* E2M1 with one E4M3 scale per 16 values and one per-tensor f32 scale      */
+} fp8t_quant;
+
+/*
+ * 4-bit block scaling: the 4-bit forms of the microscaled formats of [P2 §九]. E2M1 holds 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives (codes 0..7, sign in bit 3); rounding is to nearest even,
+ * saturating at +-6. Two codes to a byte, the first in the low four bits.
+ *   MXFP4: X = floor(log2(amax)) - 2 of the block's 32 values, clamped to [-127, 127] (amax 0: -127;
+ *          infinite: 127), scale byte X + 127, code = e2m1(x * 2^-X). A NaN in the block gives the byte
+ *          0xFF (E2M1 has no NaN; the codes of such a block are those at unit scale, a NaN becomes 6).
+ *   NVFP4: g is the tensor's f32 scale, s = e4m3((amax * g) / 6) of the block's 16 values, saturating at
+ *          448, code = e2m1(x * (g / s)), every f32 operation rounded separately; s = 0 gives zero codes;
+ *          a NaN gives the byte 0x7F. The tensor stands for code * s / g. A g of 2688 / amax (= 448 * 6 /
+ *          amax) uses the whole range: fp8_scale_update with d_fp8_max = 2688 gives it under delayed
+ *          scaling.
+ * Scale layout: the 512-byte atoms of MXFP8 (128 rows x 4 consecutive scales: byte (i % 32) * 16 +
+ * (i / 32) * 4 + j), [ceil(MN / 128)][atoms along K], with K padded to a multiple of 256, so 2 (MXFP4) or
+ * 4 (NVFP4) atoms per 256 values of K. The scales of K's padding are zero bytes.
+ */
+typedef struct fp8t_fp4_cast_tensor {
+    const void* x_bf16;      /* rows x cols BF16, row-major; cols a multiple of 32                  */
+    int64_t rows, cols;
+    fp8t_quant quant;        /* FP8T_Q_MXFP4 or FP8T_Q_NVFP4                                       */
+    const float* d_scale;    /* NVFP4: 1 float, g. MXFP4: NULL                                    */
+    void* q_row;             /* rows x cols/2 bytes, blocks along each row (K = cols), or NULL     */
+    void* scales_row;        /* fp4_scale_bytes(rows, cols, quant)                                */
+    void* q_col;             /* cols x rows/2 bytes, TRANSPOSED: row c holds the codes of column c,
+                                blocks down the column (K = rows, then a multiple of 32), or NULL   */
+    void* scales_col;        /* fp4_scale_bytes(cols, rows, quant)                                */
+    float* d_amax_inout;     /* NVFP4: 1 float, max-accumulated with max|x| (as
+                                fp8_cast_transpose_amax), or NULL                                 */
+    float* d_scale_inv_out;  /* NVFP4: 1 float, 1 / g, or NULL                                    */
+} fp8t_fp4_cast_tensor;
+
+/* Bytes of the scales of a 4-bit operand with mn rows and contraction k (0 on invalid input). */
+size_t fp4_scale_bytes(int64_t mn, int64_t k, fp8t_quant quant);
+
+/*
+ * fp4_cast_multi — 4-bit quantisation of several BF16 matrices, each into its row-wise copy and / or its
+ * column-wise copy. The 4-bit tensor-core instruction reads K-major operands only, so the column-wise
+ * copy is transposed; with W stored in x out and both copies of X, W and dY, the GEMMs of a step are
+ *   fprop  Y  = X.W     : A = X row-wise,     B = W column-wise
+ *   dgrad  dX = dY.W^T  : A = dY row-wise,    B = W row-wise
+ *   wgrad  dW = X^T.dY  : A = X column-wise,  B = dY column-wise
+ * Rows of the scale atoms past the matrix are written as zero bytes. At least one copy per tensor; up to
+ * 8 tensors share a launch. Matrix and scale pointers 16-byte aligned. Errors: INVALID_ARG,
+ * UNSUPPORTED_SHAPE (cols, or rows with a column-wise copy, not a multiple of 32), MISALIGNED, CUDA.
+ *   tensors   HOST array of n_tensors (1 .. 4096) descriptors (read during the call only).
+ */
+fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensors, void* stream);
+
+/* One 4-bit GEMM: D = bf16(sum_k a_ik b_jk * (a_scale_inv * b_scale_inv)), scales of the blocks included. */
+typedef struct fp8t_fp4_gemm_desc {
+    const void* A;                 /* M x K/2 bytes (K-major)                                       */
+    const void* A_scales;          /* fp4_scale_bytes(M, K, quant)                                  */
+    const void* B;                 /* N x K/2 bytes (K-major)                                       */
+    const void* B_scales;          /* fp4_scale_bytes(N, K, quant)                                  */
+    fp8t_quant quant;              /* FP8T_Q_MXFP4 or FP8T_Q_NVFP4, of both operands                */
+    int64_t M, N, K;               /* M > 0 any, N a multiple of 8, K a multiple of 32              */
+    const float* d_a_scale_inv;    /* 1 float each (device), or NULL for 1: 1 / g of the operands   */
+    const float* d_b_scale_inv;
+    void* D_bf16;                  /* M x N BF16, row-major                                         */
+} fp8t_fp4_gemm_desc;
+
+/*
+ * fp4_gemm_multi — 4-bit block-scaled GEMMs on the block-scaled tensor cores (FP32 accumulation, BF16
+ * output), grouped: consecutive descriptors with the same quant share a launch (up to 24). The
+ * accumulation order over k is unspecified but fixed for given sizes: the result is the same on every
+ * run, and within 2 BF16 ulp + 1e-5 * sum_k |a b| * scales of the exact value. The scales of rows past M
+ * or N are read but do not matter; those of K's padding must be zero bytes (the casts write them).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED (pointers 16-byte aligned, scale inverses 4), CUDA.
+ */
+fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, void* stream);
+
+/*
+ * fp8_rmsnorm_cast — the root-mean-square norm in front of a Linear, with the residual's addition and
+ * with its output quantised in the same pass, so X is never written and read again in BF16
+ * [P1 优化器 kernel 的带宽账: every split kernel re-reads its tensors; P2 §四 quantize]:
+ *   h    = bf16(f32(x) + f32(residual))         (h = x without a residual)
+ *   rstd = 1 / sqrt(sum_c h^2 / cols + eps)
+ *   y    = (f32(h) * rstd) * f32(gamma)          f32, statistics in f32
+ * y is written as BF16 (y_bf16) and / or quantised from its f32 value (q): FP8T_Q_FP8 as
+ * fp8_cast_transpose_amax (d_scale, d_amax_inout, d_scale_inv_out; the amax is max|y| in f32), the
+ * block formats along each row as fp8_mx_cast_multi's and fp4_cast_multi's row-wise copies, with amax and
+ * exponents of the f32 values. (A column-wise copy, for wgrad, is a cast of y_bf16.)
+ * A row with an infinite or NaN element, or whose sum of squares overflows f32, follows the formula.
+ */
+typedef struct fp8t_rmsnorm {
+    const void* x_bf16;             /* rows x cols                                                  */
+    const void* residual_bf16;      /* rows x cols, or NULL                                         */
+    const void* gamma_bf16;         /* cols                                                         */
+    int64_t rows, cols;             /* rows > 0; cols a multiple of 16 (32 with a block format), at
+                                       most 16384                                                   */
+    float eps;                      /* finite, >= 0                                                 */
+    void* h_bf16;                   /* rows x cols or NULL; may be x or residual itself. NULL without
+                                       a residual                                                   */
+    float* d_rstd_out;              /* rows floats (for the backward pass), or NULL                 */
+    void* y_bf16;                   /* rows x cols, or NULL                                         */
+    fp8t_quant quant;
+    fp8t_format fmt;                /* FP8 and MXFP8: element format                                */
+    void* q;                        /* rows x cols codes (cols / 2 bytes a row for the 4-bit ones)   */
+    void* scales;                   /* MXFP8: atoms [ceil(rows/128)][ceil(cols/128)]; 4-bit:
+                                       fp4_scale_bytes(rows, cols, quant). The scales of rows that
+                                       fill up the last atom are not written                        */
+    const float* d_scale;           /* FP8, NVFP4: 1 float                                          */
+    float* d_amax_inout;            /* FP8: 1 float, max-accumulated; NVFP4: the same, or NULL       */
+    float* d_scale_inv_out;         /* FP8, NVFP4: 1 float, or NULL                                 */
+} fp8t_rmsnorm;
+
+/* Errors: INVALID_ARG (NULL input, neither y_bf16 nor a quantised output, an output without what it
+ * needs, or one that quant does not have), UNSUPPORTED_SHAPE, MISALIGNED (matrices, gamma, codes and
+ * scales 16 bytes, scalars and rstd 4), CUDA. */
+fp8t_status fp8_rmsnorm_cast(const fp8t_rmsnorm* desc, void* stream);
+
+/*
+ * fp8_rmsnorm_backward — gradients of fp8_rmsnorm_cast's y with respect to h (the same for x and
+ * residual) and gamma, from the gradient of y, all in f32 with one rounding at the end:
+ *   g = dy * gamma, xh = h * rstd
+ *   dh     = rstd * (g - xh * (sum_c g * xh) / cols)  (+ dres: the gradient that reaches h directly)
+ *   dgamma = sum over the rows of dy * xh             (fixed order: the same on every run)
+ */
+typedef struct fp8t_rmsnorm_grad {
+    const void* dy_bf16;            /* rows x cols                                                  */
+    const void* h_bf16;             /* rows x cols: the forward pass's h (x without a residual)      */
+    const void* gamma_bf16;         /* cols                                                         */
+    const float* d_rstd;            /* rows floats, from the forward pass                           */
+    const void* dres_bf16;          /* rows x cols, or NULL                                         */
+    int64_t rows, cols;             /* as in fp8_rmsnorm_cast                                       */
+    void* dh_bf16;                  /* rows x cols; may be dy or dres itself                         */
+    float* dgamma_f32;              /* cols, overwritten, or NULL                                   */
+    void* dgamma_bf16;              /* cols, overwritten, or NULL (a gradient for fused_adamw_*)      */
+} fp8t_rmsnorm_grad;
+
+/*   d_workspace   device scratch of fp8_rmsnorm_backward_workspace_bytes, 16-byte aligned, contents on
+ *                 entry ignored; needed when a dgamma is asked for. Calls that may run at the same time
+ *                 need their own. */
+fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Scratch bytes fp8_rmsnorm_backward needs (0 on invalid input). */
+size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
  * fp8_scale_update — roll each tensor's amax history and compute the next scale

@@ -20,7 +20,9 @@ __all__ = ["fp8_cast_transpose_amax", "fp8_cast_transpose_amax_multi",
            "fp8_gemm_multi_sumsq", "fp8_gemm_sumsq_workspace_bytes",
            "fused_adamw_multi_tensor_presummed", "fp8_mx_cast_multi", "fp8_mx_gemm_multi",
            "fp8_mx_gemm_multi_sumsq", "fp8_mx_gemm_sumsq_workspace_bytes",
-           "mx_scale_bytes",
+           "mx_scale_bytes", "fp4_scale_bytes", "fp4_cast_multi", "fp4_gemm_multi", "fp8_rmsnorm_cast",
+           "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes",
+           "Q_NONE", "Q_FP8", "Q_MXFP8", "Q_MXFP4", "Q_NVFP4", "FP4_MAX",
            "fp8t_check_device_error", "fp8t_debug_expire_waits", "fp8t_set_wait_timeout_ns",
            "Fp8TrainError", "E4M3", "E5M2", "K_MAJOR", "MN_MAJOR", "AMAX_MAX", "AMAX_MOST_RECENT", "FP8_MAX", "load",
            "LIB_PATH"]
@@ -28,7 +30,9 @@ __all__ = ["fp8_cast_transpose_amax", "fp8_cast_transpose_amax_multi",
 E4M3, E5M2 = 0, 1
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 K_MAJOR, MN_MAJOR = 0, 1
+Q_NONE, Q_FP8, Q_MXFP8, Q_MXFP4, Q_NVFP4 = 0, 1, 2, 3, 4
 FP8_MAX = {E4M3: 448.0, E5M2: 57344.0}
+FP4_MAX = 448.0 * 6.0        # NVFP4's largest scale times its largest value (fp8_max of its scale update)
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8train.so")
 
 
@@ -253,6 +257,130 @@ def fp8_mx_gemm_multi_sumsq(gemms, sumsq_out, workspace, stream=None):
     _check(load().fp8_mx_gemm_multi_sumsq(_mx_gemm_array(gemms), len(gemms), flags, _ptr(sumsq_out),
                                           _ptr(workspace), workspace.numel(), _stream(stream)),
            "fp8_mx_gemm_multi_sumsq")
+
+
+def fp4_scale_bytes(mn, k, quant):
+    """Bytes of the scales of a 4-bit operand with mn rows (M or N) and contraction k; quant Q_MXFP4 or
+    Q_NVFP4. Any mn > 0; K is padded to a multiple of 256."""
+    return int(load().fp4_scale_bytes(int(mn), int(k), int(quant)))
+
+
+def _sized(t, n, what):
+    """``t`` as a pointer, after a check that it holds at least n bytes (None passes)."""
+    if t is not None and t.numel() * t.element_size() < n:
+        raise ValueError(f"{what} holds fewer than {n} bytes")
+    return _ptr(t)
+
+
+def _scalar(t, what):
+    """A float32 device scalar (or None) as a pointer."""
+    if t is not None and (t.dtype != torch.float32 or t.numel() < 1):
+        raise ValueError(f"{what} must be a float32 tensor of one element")
+    return _ptr(t)
+
+
+def _bf16(t, shape, what):
+    """A BF16 tensor of the given shape (or None) as a pointer."""
+    if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape):
+        raise ValueError(f"{what} must be bfloat16 {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def fp4_cast_multi(casts, stream=None):
+    """4-bit quantisation. ``casts``: dicts with x (BF16 [rows, cols]), quant (Q_MXFP4 or Q_NVFP4), q_row
+    (uint8 [rows, cols / 2]) / sf_row and / or q_col (uint8 [cols, rows / 2]: transposed) / sf_col, scales
+    uint8 tensors of fp4_scale_bytes; for NVFP4 also scale (float32 [1]) and optionally amax
+    (max-accumulated) and scale_inv."""
+    arr = (_abi.Fp4CastTensor * len(casts))()
+    for i, c in enumerate(casts):
+        x, quant = c["x"], int(c["quant"])
+        if x.dim() != 2:
+            raise ValueError("x must be a matrix")
+        rows, cols = x.shape
+        q_row, q_col = c.get("q_row"), c.get("q_col")
+        arr[i] = _abi.Fp4CastTensor(
+            _bf16(x, (rows, cols), "x"), rows, cols, quant, _scalar(c.get("scale"), "scale"),
+            _sized(q_row, rows * cols // 2, "q_row"),
+            _sized(c.get("sf_row"), fp4_scale_bytes(rows, cols, quant) if q_row is not None else 0, "sf_row"),
+            _sized(q_col, rows * cols // 2, "q_col"),
+            _sized(c.get("sf_col"), fp4_scale_bytes(cols, rows, quant) if q_col is not None else 0, "sf_col"),
+            _scalar(c.get("amax"), "amax"), _scalar(c.get("scale_inv"), "scale_inv"))
+    _check(load().fp4_cast_multi(arr, len(casts), _stream(stream)), "fp4_cast_multi")
+
+
+def fp4_gemm_multi(gemms, stream=None):
+    """4-bit block-scaled GEMMs: dicts with A (uint8 [M, K / 2]), a_sf, B (uint8 [N, K / 2]), b_sf, quant,
+    D (BF16 [M, N]) and optionally a_scale_inv, b_scale_inv (float32 [1]); D = bf16(A . B^T) with the
+    operands' block scales, times the scale inverses."""
+    arr = (_abi.Fp4GemmDesc * len(gemms))()
+    for i, g in enumerate(gemms):
+        A, B, quant = g["A"], g["B"], int(g["quant"])
+        M, K2 = A.shape
+        N = B.shape[0]
+        if A.dtype != torch.uint8 or B.dtype != torch.uint8 or B.shape[1] != K2:
+            raise ValueError("A and B must be uint8 codes [M, K / 2] and [N, K / 2]")
+        arr[i] = _abi.Fp4GemmDesc(
+            _ptr(A), _sized(g["a_sf"], fp4_scale_bytes(M, 2 * K2, quant), "a_sf"),
+            _ptr(B), _sized(g["b_sf"], fp4_scale_bytes(N, 2 * K2, quant), "b_sf"), quant, M, N, 2 * K2,
+            _scalar(g.get("a_scale_inv"), "a_scale_inv"), _scalar(g.get("b_scale_inv"), "b_scale_inv"),
+            _bf16(g["D"], (M, N), "D"))
+    _check(load().fp4_gemm_multi(arr, len(gemms), _stream(stream)), "fp4_gemm_multi")
+
+
+def fp8_rmsnorm_cast(x, gamma, eps, *, residual=None, h=None, rstd=None, y=None, quant=Q_NONE, fmt=E4M3,
+                     q=None, sf=None, scale=None, amax=None, scale_inv=None, stream=None):
+    """h = bf16(x + residual); y = h / sqrt(mean(h^2) + eps) * gamma for each row of x (BF16 [rows, cols]).
+
+    Writes h (BF16, with a residual; may be x or residual), rstd (float32 [rows], for the backward pass), y
+    (BF16) and, as ``quant`` says, y's codes ``q`` (uint8): Q_FP8 with scale, amax (max-accumulated) and
+    scale_inv (float32 [1] each), Q_MXFP8 / Q_MXFP4 / Q_NVFP4 with ``sf`` (uint8 scale atoms along the
+    rows), Q_NVFP4 also with scale and optionally amax and scale_inv."""
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, cols = x.shape
+    quant = int(quant)
+    four = quant in (Q_MXFP4, Q_NVFP4)
+    sf_bytes = 0
+    if sf is not None:
+        sf_bytes = fp4_scale_bytes(rows, cols, quant) if four else -(-rows // 128) * -(-cols // 128) * 512
+    if rstd is not None and (rstd.dtype != torch.float32 or rstd.numel() < rows):
+        raise ValueError("rstd must be float32 with one element per row")
+    d = _abi.RmsNorm(_bf16(x, (rows, cols), "x"), _bf16(residual, (rows, cols), "residual"),
+                     _bf16(gamma, (cols,), "gamma"), rows, cols, float(eps), _bf16(h, (rows, cols), "h"),
+                     _ptr(rstd), _bf16(y, (rows, cols), "y"), quant, int(fmt),
+                     _sized(q, rows * cols // 2 if four else rows * cols, "q"), _sized(sf, sf_bytes, "sf"),
+                     _scalar(scale, "scale"), _scalar(amax, "amax"), _scalar(scale_inv, "scale_inv"))
+    _check(load().fp8_rmsnorm_cast(C.byref(d), _stream(stream)), "fp8_rmsnorm_cast")
+
+
+def fp8_rmsnorm_backward_workspace_bytes(rows, cols):
+    return int(load().fp8_rmsnorm_backward_workspace_bytes(int(rows), int(cols)))
+
+
+def fp8_rmsnorm_backward(dy, h, gamma, rstd, dh, *, dres=None, dgamma=None, dgamma_bf16=None,
+                         workspace=None, stream=None):
+    """Gradients of fp8_rmsnorm_cast: ``dh`` (BF16 [rows, cols]; may be dy or dres) from dy and the forward
+    pass's h and rstd, with dres added where given; ``dgamma`` (float32 [cols]) and / or ``dgamma_bf16``.
+
+    ``workspace`` is a uint8 CUDA tensor of at least ``fp8_rmsnorm_backward_workspace_bytes`` bytes."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    rows, cols = dy.shape
+    if rstd.dtype != torch.float32 or rstd.numel() < rows:
+        raise ValueError("rstd must be float32 with one element per row")
+    if dgamma is not None and (dgamma.dtype != torch.float32 or dgamma.numel() < cols):
+        raise ValueError("dgamma must be float32 with one element per column")
+    if workspace is None and (dgamma is not None or dgamma_bf16 is not None):
+        workspace = torch.empty(fp8_rmsnorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
+                                device=dy.device)
+        if stream is not None:
+            workspace.record_stream(stream)      # freed on return, read by kernels of that stream
+    d = _abi.RmsNormGrad(_bf16(dy, (rows, cols), "dy"), _bf16(h, (rows, cols), "h"), _bf16(gamma, (cols,), "gamma"),
+                         _ptr(rstd), _bf16(dres, (rows, cols), "dres"), rows, cols, _bf16(dh, (rows, cols), "dh"),
+                         _ptr(dgamma), _bf16(dgamma_bf16, (cols,), "dgamma_bf16"))
+    _check(load().fp8_rmsnorm_backward(C.byref(d), _ptr(workspace),
+                                       0 if workspace is None else workspace.numel(), _stream(stream)),
+           "fp8_rmsnorm_backward")
 
 
 def fp8_scale_update(amax, history, fp8_max, algo, margin, scale, scale_inv, stream=None):

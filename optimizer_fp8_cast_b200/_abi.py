@@ -58,6 +58,37 @@ class MxGemmDesc(C.Structure):
                 ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("D_bf16", C.c_void_p)]
 
 
+class Fp4CastTensor(C.Structure):
+    """fp8t_fp4_cast_tensor."""
+    _fields_ = [("x_bf16", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64), ("quant", C.c_int),
+                ("d_scale", C.c_void_p), ("q_row", C.c_void_p), ("scales_row", C.c_void_p),
+                ("q_col", C.c_void_p), ("scales_col", C.c_void_p), ("d_amax_inout", C.c_void_p),
+                ("d_scale_inv_out", C.c_void_p)]
+
+
+class Fp4GemmDesc(C.Structure):
+    """fp8t_fp4_gemm_desc."""
+    _fields_ = [("A", C.c_void_p), ("A_scales", C.c_void_p), ("B", C.c_void_p), ("B_scales", C.c_void_p),
+                ("quant", C.c_int), ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64),
+                ("d_a_scale_inv", C.c_void_p), ("d_b_scale_inv", C.c_void_p), ("D_bf16", C.c_void_p)]
+
+
+class RmsNorm(C.Structure):
+    """fp8t_rmsnorm."""
+    _fields_ = [("x_bf16", C.c_void_p), ("residual_bf16", C.c_void_p), ("gamma_bf16", C.c_void_p),
+                ("rows", C.c_int64), ("cols", C.c_int64), ("eps", C.c_float), ("h_bf16", C.c_void_p),
+                ("d_rstd_out", C.c_void_p), ("y_bf16", C.c_void_p), ("quant", C.c_int), ("fmt", C.c_int),
+                ("q", C.c_void_p), ("scales", C.c_void_p), ("d_scale", C.c_void_p),
+                ("d_amax_inout", C.c_void_p), ("d_scale_inv_out", C.c_void_p)]
+
+
+class RmsNormGrad(C.Structure):
+    """fp8t_rmsnorm_grad."""
+    _fields_ = [("dy_bf16", C.c_void_p), ("h_bf16", C.c_void_p), ("gamma_bf16", C.c_void_p),
+                ("d_rstd", C.c_void_p), ("dres_bf16", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("dh_bf16", C.c_void_p), ("dgamma_f32", C.c_void_p), ("dgamma_bf16", C.c_void_p)]
+
+
 def declare(L):
     vp, i32, i64, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_float
     L.fp8_cast_transpose_amax.restype = C.c_int
@@ -90,6 +121,18 @@ def declare(L):
                                           C.c_size_t, vp]
     L.fp8_mx_gemm_sumsq_workspace_bytes.restype = C.c_size_t
     L.fp8_mx_gemm_sumsq_workspace_bytes.argtypes = [C.POINTER(MxGemmDesc), i32, C.POINTER(C.c_int32)]
+    L.fp4_scale_bytes.restype = C.c_size_t
+    L.fp4_scale_bytes.argtypes = [i64, i64, C.c_int]
+    L.fp4_cast_multi.restype = C.c_int
+    L.fp4_cast_multi.argtypes = [C.POINTER(Fp4CastTensor), i32, vp]
+    L.fp4_gemm_multi.restype = C.c_int
+    L.fp4_gemm_multi.argtypes = [C.POINTER(Fp4GemmDesc), i32, vp]
+    L.fp8_rmsnorm_cast.restype = C.c_int
+    L.fp8_rmsnorm_cast.argtypes = [C.POINTER(RmsNorm), vp]
+    L.fp8_rmsnorm_backward.restype = C.c_int
+    L.fp8_rmsnorm_backward.argtypes = [C.POINTER(RmsNormGrad), vp, C.c_size_t, vp]
+    L.fp8_rmsnorm_backward_workspace_bytes.restype = C.c_size_t
+    L.fp8_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
     L.fp8_gemm.restype = C.c_int
     L.fp8_gemm.argtypes = [vp, C.c_int, vp, C.c_int, i64, i64, i64, vp, vp, vp, vp]
     L.fp8_scale_update.restype = C.c_int

@@ -18,10 +18,13 @@
 #include "fp8train.h"
 #include "cast_transpose_amax.cuh"
 #include "current_scaling.cuh"
+#include "fp4_cast.cuh"
 #include "fused_adamw.cuh"
 #include "gemm_tcgen05.cuh"
 #include "gemm_mx_wide.cuh"
+#include "gemm_fp4.cuh"
 #include "mx_cast.cuh"
+#include "rmsnorm.cuh"
 #include "scale_update.cuh"
 
 namespace {
@@ -52,7 +55,9 @@ struct DeviceInfo {
   int gemm_wide_clusters = 0;  // ... of its wide-tile form
   int gemm_mx_clusters = 0;    // ... of its MXFP8 variant
   int gemm_mxw_clusters = 0;   // ... of the MXFP8 256 x 384 kernel
+  int gemm_fp4_clusters = 0;   // ... of the 4-bit 256 x 384 kernel (fewer of its two forms)
   int mx_cast_blocks_per_sm = 0;
+  int fp4_cast_blocks_per_sm = 0;
   int cast_blocks_per_sm = 0;
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
@@ -149,6 +154,33 @@ fp8t_status current_device(DeviceInfo** out) {
       if (e != cudaSuccess || d.mx_cast_blocks_per_sm < 1) {
         (void)cudaGetLastError();
         d.mx_cast_blocks_per_sm = 1;
+      }
+      e = cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               fp8t::gemm::kSmemBytes4<false>);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 fp8t::gemm::kSmemBytes4<true>);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 fp8t::fp4::kCastSmemBytes);
+      if (e != cudaSuccess) {
+        d.state = 0;
+        return fail(FP8T_ERR_CUDA, "cudaFuncSetAttribute(4-bit): %s", cudaGetErrorString(e));
+      }
+      cfg.blockDim = dim3(fp8t::gemm::kThreadsX, 1, 1);
+      cfg.dynamicSmemBytes = fp8t::gemm::kSmemBytes4<true>;
+      clusters = 0;
+      e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true>, &cfg);
+      if (e != cudaSuccess || clusters < 1) {
+        (void)cudaGetLastError();
+        clusters = sms / 2;
+      }
+      d.gemm_fp4_clusters = clusters;
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.fp4_cast_blocks_per_sm, fp8t::fp4::k_fp4_cast,
+                                                        fp8t::fp4::kCastThreads, fp8t::fp4::kCastSmemBytes);
+      if (e != cudaSuccess || d.fp4_cast_blocks_per_sm < 1) {
+        (void)cudaGetLastError();
+        d.fp4_cast_blocks_per_sm = 1;
       }
       e = cudaFuncSetAttribute(fp8t::cast::k_cast_transpose_amax<false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::cast::kSmemBytes);
@@ -988,6 +1020,350 @@ fp8t_status fp8_gemm(const void* A, fp8t_format a_fmt, const void* B, fp8t_forma
                      void* D_bf16, void* stream) {
   const fp8t_gemm_desc d = {A, a_fmt, B, b_fmt, M, N, K, d_a_scale_inv, d_b_scale_inv, D_bf16};
   return fp8_gemm_multi(&d, 1, stream);
+}
+
+// ------------------------------------------------------------------ 4-bit cast
+size_t fp4_scale_bytes(int64_t mn, int64_t k, fp8t_quant quant) {
+  if (mn <= 0 || k <= 0 || mn >= (int64_t(1) << 31) || k >= (int64_t(1) << 31) ||
+      (quant != FP8T_Q_MXFP4 && quant != FP8T_Q_NVFP4))
+    return 0;
+  return static_cast<size_t>((mn + 127) / 128 * fp8t::blk::atoms_per_row(k, quant) * 512);
+}
+
+fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensors, void* stream) {
+  t_last_error.clear();
+  if (!tensors || n_tensors < 1 || n_tensors > 4096)
+    return fail(FP8T_ERR_INVALID_ARG, "fp4_cast: tensors NULL or n_tensors out of range");
+  const int64_t lim = int64_t(1) << 31;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const fp8t_fp4_cast_tensor& t = tensors[i];
+    if (!t.x_bf16 || (!t.q_row && !t.q_col) || (t.q_row && !t.scales_row) || (t.q_col && !t.scales_col))
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_cast: tensor %d: NULL input, or an output without its scales", i);
+    if (t.quant != FP8T_Q_MXFP4 && t.quant != FP8T_Q_NVFP4)
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_cast: tensor %d: quant must be MXFP4 or NVFP4", i);
+    if (t.quant == FP8T_Q_NVFP4 ? !t.d_scale : (t.d_scale || t.d_amax_inout || t.d_scale_inv_out))
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_cast: tensor %d: NVFP4 needs a scale; MXFP4 has no scale, amax or scale inverse", i);
+    if (t.rows <= 0 || t.cols <= 0)
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_cast: tensor %d: rows and cols must be > 0", i);
+    if (t.cols % 32 || (t.q_col && t.rows % 32) || t.rows >= lim || t.cols >= lim ||
+        t.rows * t.cols >= (int64_t(1) << 40))
+      return fail(FP8T_ERR_UNSUPPORTED_SHAPE,
+                  "fp4_cast: tensor %d: cols (and rows with a column-wise copy) must be multiples of 32, rows*cols < 2^40", i);
+    if (!aligned(t.x_bf16, 16) || !aligned(t.q_row, 16) || !aligned(t.q_col, 16) ||
+        !aligned(t.scales_row, 16) || !aligned(t.scales_col, 16) || !aligned(t.d_scale, 4) ||
+        !aligned(t.d_amax_inout, 4) || !aligned(t.d_scale_inv_out, 4))
+      return fail(FP8T_ERR_MISALIGNED, "fp4_cast: tensor %d: misaligned pointer", i);
+  }
+  DeviceInfo* dev = nullptr;
+  fp8t_status st = current_device(&dev);
+  if (st != FP8T_OK) return st;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  using namespace fp8t::fp4;
+  static thread_local CastGroup group;
+  for (int32_t b0 = 0; b0 < n_tensors; b0 += kCastTensors) {
+    const int32_t b1 = std::min<int32_t>(n_tensors, b0 + kCastTensors);
+    std::memset(&group, 0, sizeof(group));
+    group.n = b1 - b0;
+    int64_t tiles = 0;
+    for (int32_t i = b0; i < b1; ++i) {
+      const fp8t_fp4_cast_tensor& t = tensors[i];
+      CastTensor& T = group.t[i - b0];
+      cuuint64_t dims[2] = {static_cast<cuuint64_t>(t.cols), static_cast<cuuint64_t>(t.rows)};
+      cuuint64_t strides[1] = {static_cast<cuuint64_t>(t.cols) * 2};
+      cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kTile)};
+      cuuint32_t es[2] = {1, 1};
+      CUresult r = fn(&T.x_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(t.x_bf16),
+                      dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit cast input) failed (%d)", (int)r);
+      T.q_row = static_cast<uint8_t*>(t.q_row);
+      T.sf_row = static_cast<uint8_t*>(t.scales_row);
+      T.q_col = static_cast<uint8_t*>(t.q_col);
+      T.sf_col = static_cast<uint8_t*>(t.scales_col);
+      T.scale = t.d_scale;
+      T.amax_bits = reinterpret_cast<unsigned int*>(t.d_amax_inout);
+      T.scale_inv = t.d_scale_inv_out;
+      T.rows = t.rows;
+      T.cols = t.cols;
+      T.tiles_c = (t.cols + kTile - 1) / kTile;
+      T.tile_start = tiles;
+      T.kind = t.quant;
+      tiles += ((t.rows + kTile - 1) / kTile) * T.tiles_c;
+    }
+    group.total_tiles = tiles;
+    const int64_t grid = std::min<int64_t>(tiles, static_cast<int64_t>(dev->sms) * dev->fp4_cast_blocks_per_sm);
+    k_fp4_cast<<<static_cast<unsigned>(grid), kCastThreads, kCastSmemBytes, as_stream(stream)>>>(group);
+    if ((st = after_launch("fp4_cast launch")) != FP8T_OK) return st;
+  }
+  return FP8T_OK;
+}
+
+// ------------------------------------------------------------------ 4-bit GEMM
+fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, void* stream) {
+  t_last_error.clear();
+  if (!gemms || n_gemms < 1 || n_gemms > 4096)
+    return fail(FP8T_ERR_INVALID_ARG, "fp4_gemm: gemms NULL or n_gemms out of range");
+  const int64_t lim = int64_t(1) << 31;
+  for (int32_t i = 0; i < n_gemms; ++i) {
+    const fp8t_fp4_gemm_desc& d = gemms[i];
+    if (!d.A || !d.B || !d.A_scales || !d.B_scales || !d.D_bf16)
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_gemm: problem %d: NULL pointer", i);
+    if (d.quant != FP8T_Q_MXFP4 && d.quant != FP8T_Q_NVFP4)
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_gemm: problem %d: quant must be MXFP4 or NVFP4", i);
+    if (d.M <= 0 || d.N <= 0 || d.K <= 0)
+      return fail(FP8T_ERR_INVALID_ARG, "fp4_gemm: problem %d: M, N, K must be > 0", i);
+    if (d.N % 8 || d.K % 32 || d.M >= lim || d.N >= lim || d.K >= lim ||
+        (std::max(d.M, d.N) + 511) / 128 * ((d.K + 255) / 256) >= (int64_t(1) << 30))
+      return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: problem %d: N must be a multiple of 8 and K of 32", i);
+    if (!aligned(d.A, 16) || !aligned(d.B, 16) || !aligned(d.D_bf16, 16) || !aligned(d.A_scales, 16) ||
+        !aligned(d.B_scales, 16) || !aligned(d.d_a_scale_inv, 4) || !aligned(d.d_b_scale_inv, 4))
+      return fail(FP8T_ERR_MISALIGNED, "fp4_gemm: problem %d: misaligned pointer", i);
+  }
+  DeviceInfo* dev = nullptr;
+  fp8t_status st = current_device(&dev);
+  if (st != FP8T_OK) return st;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  using namespace fp8t::gemm;
+  // scales: rows of 256 words (1 KB); one (MXFP4) or two (NVFP4) rows per 128 rows and 256 values of K
+  auto encode_sf = [&](CUtensorMap* map, const void* ptr, int64_t mn, int64_t K, bool nv) -> fp8t_status {
+    const cuuint32_t per = nv ? 2 : 1;
+    cuuint64_t dims[2] = {256, static_cast<cuuint64_t>((mn + 127) / 128 * ((K + 255) / 256) * per)};
+    cuuint64_t strides[1] = {1024};
+    cuuint32_t box[2] = {256, per};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit scales) failed (%d)", (int)r);
+    return FP8T_OK;
+  };
+  static thread_local Group group;
+  for (int32_t b0 = 0, b1 = 0; b0 < n_gemms; b0 = b1) {
+    const bool nv = gemms[b0].quant == FP8T_Q_NVFP4;
+    b1 = b0 + 1;
+    while (b1 < n_gemms && b1 - b0 < kMaxProblems && gemms[b1].quant == gemms[b0].quant) ++b1;
+    std::memset(&group, 0, sizeof(group));
+    group.n = b1 - b0;
+    int64_t tiles = 0;
+    for (int32_t i = b0; i < b1; ++i) {
+      const fp8t_fp4_gemm_desc& d = gemms[i];
+      Problem& P = group.p[i - b0];
+      if ((st = encode_kmajor(&P.a, d.A, d.M, d.K / 2, kHalf)) != FP8T_OK) return st;
+      if ((st = encode_kmajor(&P.b, d.B, d.N, d.K / 2, kHalf)) != FP8T_OK) return st;
+      if ((st = encode_kmajor(&P.b64, d.B, d.N, d.K / 2, kHalf / 2)) != FP8T_OK) return st;
+      if ((st = encode_sf(&P.sfa, d.A_scales, d.M, d.K, nv)) != FP8T_OK) return st;
+      if ((st = encode_sf(&P.sfb, d.B_scales, d.N, d.K, nv)) != FP8T_OK) return st;
+      cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(d.M)};
+      cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.N) * 2};
+      cuuint32_t box[2] = {32, 32};
+      cuuint32_t es[2] = {1, 1};
+      CUresult r = fn(&P.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.D_bf16, dims, strides, box, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (D) failed (%d)", (int)r);
+      P.sa = d.d_a_scale_inv;
+      P.sb = d.d_b_scale_inv;
+      P.M = static_cast<int32_t>(d.M);
+      P.N = static_cast<int32_t>(d.N);
+      P.K = static_cast<int32_t>(d.K);
+      P.kb128 = static_cast<int32_t>((d.K + 255) / 256);       // this kernel's k-blocks: 256 values
+      P.sumsq_slot = -1;
+      P.tiles_n = static_cast<int32_t>((d.N + kBNx - 1) / kBNx);
+      P.tile_start = static_cast<int32_t>(tiles);
+      tiles += ((d.M + kBM - 1) / kBM) * P.tiles_n;
+      if (tiles >= (int64_t(1) << 30))
+        return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
+    }
+    group.total_tiles = static_cast<int32_t>(tiles);
+    const int64_t grid = 2 * std::min<int64_t>(tiles, dev->gemm_fp4_clusters);
+    build_schedule(group, static_cast<int>(grid / 2), false, true);
+    if (nv)
+      k_fp4_gemm<true><<<static_cast<unsigned>(grid), kThreadsX, kSmemBytes4<true>, as_stream(stream)>>>(group);
+    else
+      k_fp4_gemm<false><<<static_cast<unsigned>(grid), kThreadsX, kSmemBytes4<false>, as_stream(stream)>>>(group);
+    if ((st = after_launch("fp4_gemm launch")) != FP8T_OK) return st;
+  }
+  return FP8T_OK;
+}
+
+// ------------------------------------------------------------------ RMSNorm
+}  // extern "C"
+
+namespace {
+
+// Threads and vectors per thread of a norm launch. Rows of up to 1024 columns take a warp each, four to a
+// CTA. Wider rows take a CTA: four vectors per thread when there are rows enough to fill the GPU (few
+// threads per row: cheap sums, many rows in flight), else the fewest vectors that 512 threads hold.
+struct NormShape {
+  bool warp_row;
+  int vpt, threads;
+};
+NormShape norm_shape(int64_t rows, int64_t cols, bool spread) {
+  using namespace fp8t::norm;
+  const int nvec = static_cast<int>(cols / 8);
+  NormShape s;
+  s.warp_row = cols <= kMaxWarpCols;
+  if (s.warp_row) {
+    s.vpt = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
+    s.threads = 32 * kRowsPerCta;
+    return s;
+  }
+  s.vpt = 4;
+  if (spread && rows <= 148) s.vpt = nvec <= kMaxThreads ? 1 : nvec <= 2 * kMaxThreads ? 2 : 4;
+  s.threads = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+  return s;
+}
+
+// CTAs of the backward pass (partial dgamma rows): four 128-thread CTAs per SM, fewer of wider ones.
+int64_t norm_backward_ctas(int64_t rows, int64_t cols) {
+  using namespace fp8t::norm;
+  const NormShape s = norm_shape(rows, cols, false);
+  const int64_t per_cta = s.warp_row ? kRowsPerCta : 1;
+  return std::min<int64_t>((rows + per_cta - 1) / per_cta, 148 * std::max(1, 512 / s.threads));
+}
+
+bool norm_cols_ok(int64_t rows, int64_t cols, int64_t multiple) {
+  return cols % multiple == 0 && cols <= fp8t::norm::kMaxCols && rows < (int64_t(1) << 31);
+}
+
+template <int Q>
+void launch_norm(const fp8t::norm::Fwd& p, const NormShape& s, int sms, cudaStream_t stream) {
+  using namespace fp8t::norm;
+  const int64_t per_cta = s.warp_row ? kRowsPerCta : 1;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(
+      (p.rows + per_cta - 1) / per_cta, static_cast<int64_t>(sms) * std::max(1, 1024 / s.threads)));
+  if (s.warp_row) {
+    if (s.vpt == 1)      k_rmsnorm_cast<1, true, Q><<<grid, s.threads, 0, stream>>>(p);
+    else if (s.vpt == 2) k_rmsnorm_cast<2, true, Q><<<grid, s.threads, 0, stream>>>(p);
+    else                 k_rmsnorm_cast<4, true, Q><<<grid, s.threads, 0, stream>>>(p);
+  } else {
+    if (s.vpt == 1)      k_rmsnorm_cast<1, false, Q><<<grid, s.threads, 0, stream>>>(p);
+    else if (s.vpt == 2) k_rmsnorm_cast<2, false, Q><<<grid, s.threads, 0, stream>>>(p);
+    else                 k_rmsnorm_cast<4, false, Q><<<grid, s.threads, 0, stream>>>(p);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8t_status fp8_rmsnorm_cast(const fp8t_rmsnorm* desc, void* stream) {
+  t_last_error.clear();
+  if (!desc) return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: desc NULL");
+  const fp8t_rmsnorm& d = *desc;
+  if (!d.x_bf16 || !d.gamma_bf16) return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: NULL input or gamma");
+  if (d.rows <= 0 || d.cols <= 0) return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: rows and cols must be > 0");
+  if (!(d.eps >= 0.0f) || !std::isfinite(d.eps))
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: eps must be finite and >= 0");
+  if (d.quant < FP8T_Q_NONE || d.quant > FP8T_Q_NVFP4)
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: unknown quant %d", (int)d.quant);
+  if (d.h_bf16 && !d.residual_bf16)
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: h without a residual (it is x)");
+  const bool fp8 = d.quant == FP8T_Q_FP8, nv = d.quant == FP8T_Q_NVFP4, none = d.quant == FP8T_Q_NONE;
+  const bool block = !none && !fp8;
+  if (none ? !d.y_bf16 || d.q : !d.q)
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: neither y nor codes asked for, or codes without a quant");
+  if (block != (d.scales != nullptr))
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: scales go with the block formats and only with them");
+  if ((fp8 || nv) ? !d.d_scale || (fp8 && !d.d_amax_inout) : d.d_scale || d.d_amax_inout || d.d_scale_inv_out)
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: FP8 needs a scale and an amax slot, NVFP4 a scale; the others have none");
+  if ((fp8 || d.quant == FP8T_Q_MXFP8) && d.fmt != FP8T_E4M3 && d.fmt != FP8T_E5M2)
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_cast: unknown format %d", (int)d.fmt);
+  if (!norm_cols_ok(d.rows, d.cols, block ? 32 : 16))
+    return fail(FP8T_ERR_UNSUPPORTED_SHAPE,
+                "fp8_rmsnorm_cast: cols must be a multiple of 16 (32 with block scales) and at most %d", fp8t::norm::kMaxCols);
+  if (!aligned(d.x_bf16, 16) || !aligned(d.residual_bf16, 16) || !aligned(d.gamma_bf16, 16) ||
+      !aligned(d.h_bf16, 16) || !aligned(d.y_bf16, 16) || !aligned(d.q, 16) || !aligned(d.scales, 16) ||
+      !aligned(d.d_rstd_out, 4) || !aligned(d.d_scale, 4) || !aligned(d.d_amax_inout, 4) ||
+      !aligned(d.d_scale_inv_out, 4))
+    return fail(FP8T_ERR_MISALIGNED, "fp8_rmsnorm_cast: misaligned pointer");
+  DeviceInfo* dev = nullptr;
+  fp8t_status st = current_device(&dev);
+  if (st != FP8T_OK) return st;
+  fp8t::norm::Fwd p = {};
+  p.x = static_cast<const uint4*>(d.x_bf16);
+  p.res = static_cast<const uint4*>(d.residual_bf16);
+  p.gamma = static_cast<const uint4*>(d.gamma_bf16);
+  p.h = static_cast<uint4*>(d.h_bf16);
+  p.rstd = d.d_rstd_out;
+  p.y = static_cast<uint4*>(d.y_bf16);
+  p.q = static_cast<uint8_t*>(d.q);
+  p.sf = static_cast<uint8_t*>(d.scales);
+  p.scale = d.d_scale;
+  p.amax_bits = reinterpret_cast<unsigned int*>(d.d_amax_inout);
+  p.scale_inv = d.d_scale_inv_out;
+  p.rows = d.rows;
+  p.cols = static_cast<int32_t>(d.cols);
+  p.fmt = d.fmt;
+  p.eps = d.eps;
+  const NormShape s = norm_shape(d.rows, d.cols, true);
+  switch (d.quant) {
+    case FP8T_Q_NONE: launch_norm<fp8t::blk::kNone>(p, s, dev->sms, as_stream(stream)); break;
+    case FP8T_Q_FP8: launch_norm<fp8t::blk::kFP8>(p, s, dev->sms, as_stream(stream)); break;
+    case FP8T_Q_MXFP8: launch_norm<fp8t::blk::kMXFP8>(p, s, dev->sms, as_stream(stream)); break;
+    case FP8T_Q_MXFP4: launch_norm<fp8t::blk::kMXFP4>(p, s, dev->sms, as_stream(stream)); break;
+    case FP8T_Q_NVFP4: launch_norm<fp8t::blk::kNVFP4>(p, s, dev->sms, as_stream(stream)); break;
+  }
+  return after_launch("fp8_rmsnorm_cast launch");
+}
+
+size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || !norm_cols_ok(rows, cols, 16)) return 0;
+  return static_cast<size_t>(norm_backward_ctas(rows, cols) * cols * 4);
+}
+
+fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspace,
+                                 size_t workspace_bytes, void* stream) {
+  t_last_error.clear();
+  if (!desc) return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_backward: desc NULL");
+  const fp8t_rmsnorm_grad& d = *desc;
+  if (!d.dy_bf16 || !d.h_bf16 || !d.gamma_bf16 || !d.d_rstd || !d.dh_bf16)
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_backward: NULL pointer");
+  if (d.rows <= 0 || d.cols <= 0) return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_backward: rows and cols must be > 0");
+  if (!norm_cols_ok(d.rows, d.cols, 16))
+    return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp8_rmsnorm_backward: cols must be a multiple of 16 and at most %d",
+                fp8t::norm::kMaxCols);
+  if (!aligned(d.dy_bf16, 16) || !aligned(d.h_bf16, 16) || !aligned(d.gamma_bf16, 16) || !aligned(d.d_rstd, 4) ||
+      !aligned(d.dres_bf16, 16) || !aligned(d.dh_bf16, 16) || !aligned(d.dgamma_f32, 4) ||
+      !aligned(d.dgamma_bf16, 2) || !aligned(d_workspace, 16))
+    return fail(FP8T_ERR_MISALIGNED, "fp8_rmsnorm_backward: misaligned pointer");
+  const bool want = d.dgamma_f32 || d.dgamma_bf16;
+  const int64_t ctas = norm_backward_ctas(d.rows, d.cols);
+  if (want && (!d_workspace || workspace_bytes < static_cast<size_t>(ctas * d.cols * 4)))
+    return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_backward: workspace of %zu bytes needed",
+                static_cast<size_t>(ctas * d.cols * 4));
+  DeviceInfo* dev = nullptr;
+  fp8t_status st = current_device(&dev);
+  if (st != FP8T_OK) return st;
+  using namespace fp8t::norm;
+  Bwd p = {};
+  p.dy = static_cast<const uint4*>(d.dy_bf16);
+  p.h = static_cast<const uint4*>(d.h_bf16);
+  p.gamma = static_cast<const uint4*>(d.gamma_bf16);
+  p.rstd = d.d_rstd;
+  p.dres = static_cast<const uint4*>(d.dres_bf16);
+  p.dh = static_cast<uint4*>(d.dh_bf16);
+  p.partials = want ? static_cast<float*>(d_workspace) : nullptr;
+  p.rows = d.rows;
+  p.cols = static_cast<int32_t>(d.cols);
+  const NormShape s = norm_shape(d.rows, d.cols, false);
+  const unsigned grid = static_cast<unsigned>(ctas);
+  if (s.warp_row) {
+    if (s.vpt == 1)      k_rmsnorm_backward<1, true><<<grid, s.threads, 0, as_stream(stream)>>>(p);
+    else if (s.vpt == 2) k_rmsnorm_backward<2, true><<<grid, s.threads, 0, as_stream(stream)>>>(p);
+    else                 k_rmsnorm_backward<4, true><<<grid, s.threads, 0, as_stream(stream)>>>(p);
+  } else {
+    k_rmsnorm_backward<4, false><<<grid, s.threads, 0, as_stream(stream)>>>(p);
+  }
+  if ((st = after_launch("fp8_rmsnorm_backward launch")) != FP8T_OK) return st;
+  if (want) {
+    k_rmsnorm_dgamma<<<static_cast<unsigned>((d.cols + 31) / 32), 32 * kReduceWarps, 0, as_stream(stream)>>>(
+        p.partials, static_cast<int>(ctas), p.cols, d.dgamma_f32, static_cast<uint16_t*>(d.dgamma_bf16));
+    st = after_launch("fp8_rmsnorm_backward dgamma launch");
+  }
+  return st;
 }
 
 // ------------------------------------------------------------------ scale update
