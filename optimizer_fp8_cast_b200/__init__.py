@@ -265,25 +265,51 @@ def fp4_scale_bytes(mn, k, quant):
     return int(load().fp4_scale_bytes(int(mn), int(k), int(quant)))
 
 
-def _sized(t, n, what):
-    """``t`` as a pointer, after a check that it holds at least n bytes (None passes)."""
-    if t is not None and t.numel() * t.element_size() < n:
-        raise ValueError(f"{what} holds fewer than {n} bytes")
-    return _ptr(t)
-
-
-def _scalar(t, what):
-    """A float32 device scalar (or None) as a pointer."""
-    if t is not None and (t.dtype != torch.float32 or t.numel() < 1):
-        raise ValueError(f"{what} must be a float32 tensor of one element")
-    return _ptr(t)
+# The checks of the norm and 4-bit calls: what the C side cannot see (types, sizes, device). They return
+# the address, and are kept short because a one-token call is bound by the host.
+def _dev(t, what):
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: must be a CUDA tensor on the current device")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
 
 
 def _bf16(t, shape, what):
-    """A BF16 tensor of the given shape (or None) as a pointer."""
-    if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape):
-        raise ValueError(f"{what} must be bfloat16 {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    """A BF16 tensor of the given shape (or None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.bfloat16 or t.shape != shape:
+        raise ValueError(f"{what}: must be bfloat16 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return _dev(t, what)
+
+
+def _f32(t, n, what):
+    """A float32 tensor of at least n elements (or None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() < n:
+        raise ValueError(f"{what}: must be float32 with at least {n} elements")
+    return _dev(t, what)
+
+
+def _codes(t, n, what):
+    """A uint8 tensor of at least n bytes (or None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.uint8 or t.numel() < n:
+        raise ValueError(f"{what}: must be uint8 with at least {n} elements")
+    return _dev(t, what)
+
+
+def _fp4_scale_bytes(mn, k, quant):
+    return (mn + 127) // 128 * ((k + 255) // 256) * (1024 if quant == Q_MXFP4 else 2048)
+
+
+def _current_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def fp4_cast_multi(casts, stream=None):
@@ -293,19 +319,20 @@ def fp4_cast_multi(casts, stream=None):
     (max-accumulated) and scale_inv."""
     arr = (_abi.Fp4CastTensor * len(casts))()
     for i, c in enumerate(casts):
-        x, quant = c["x"], int(c["quant"])
+        x, quant, get = c["x"], c["quant"], c.get
         if x.dim() != 2:
-            raise ValueError("x must be a matrix")
+            raise ValueError("x: must be a matrix")
         rows, cols = x.shape
-        q_row, q_col = c.get("q_row"), c.get("q_col")
-        arr[i] = _abi.Fp4CastTensor(
-            _bf16(x, (rows, cols), "x"), rows, cols, quant, _scalar(c.get("scale"), "scale"),
-            _sized(q_row, rows * cols // 2, "q_row"),
-            _sized(c.get("sf_row"), fp4_scale_bytes(rows, cols, quant) if q_row is not None else 0, "sf_row"),
-            _sized(q_col, rows * cols // 2, "q_col"),
-            _sized(c.get("sf_col"), fp4_scale_bytes(cols, rows, quant) if q_col is not None else 0, "sf_col"),
-            _scalar(c.get("amax"), "amax"), _scalar(c.get("scale_inv"), "scale_inv"))
-    _check(load().fp4_cast_multi(arr, len(casts), _stream(stream)), "fp4_cast_multi")
+        q_row, q_col, n = get("q_row"), get("q_col"), rows * cols // 2
+        arr[i] = (_bf16(x, x.shape, "x"), rows, cols, quant, _f32(get("scale"), 1, "scale"),
+                  _codes(q_row, n, "q_row"),
+                  _codes(get("sf_row"), 0 if q_row is None else _fp4_scale_bytes(rows, cols, quant), "sf_row"),
+                  _codes(q_col, n, "q_col"),
+                  _codes(get("sf_col"), 0 if q_col is None else _fp4_scale_bytes(cols, rows, quant), "sf_col"),
+                  _f32(get("amax"), 1, "amax"), _f32(get("scale_inv"), 1, "scale_inv"))
+    status = load().fp4_cast_multi(arr, len(casts), _current_stream(stream))
+    if status:
+        _check(status, "fp4_cast_multi")
 
 
 def fp4_gemm_multi(gemms, stream=None):
@@ -314,17 +341,20 @@ def fp4_gemm_multi(gemms, stream=None):
     operands' block scales, times the scale inverses."""
     arr = (_abi.Fp4GemmDesc * len(gemms))()
     for i, g in enumerate(gemms):
-        A, B, quant = g["A"], g["B"], int(g["quant"])
-        M, K2 = A.shape
-        N = B.shape[0]
-        if A.dtype != torch.uint8 or B.dtype != torch.uint8 or B.shape[1] != K2:
-            raise ValueError("A and B must be uint8 codes [M, K / 2] and [N, K / 2]")
-        arr[i] = _abi.Fp4GemmDesc(
-            _ptr(A), _sized(g["a_sf"], fp4_scale_bytes(M, 2 * K2, quant), "a_sf"),
-            _ptr(B), _sized(g["b_sf"], fp4_scale_bytes(N, 2 * K2, quant), "b_sf"), quant, M, N, 2 * K2,
-            _scalar(g.get("a_scale_inv"), "a_scale_inv"), _scalar(g.get("b_scale_inv"), "b_scale_inv"),
-            _bf16(g["D"], (M, N), "D"))
-    _check(load().fp4_gemm_multi(arr, len(gemms), _stream(stream)), "fp4_gemm_multi")
+        A, B, quant, get = g["A"], g["B"], g["quant"], g.get
+        (M, K2), (N, K2b) = A.shape, B.shape
+        if K2 != K2b:
+            raise ValueError("A and B: must be codes [M, K / 2] and [N, K / 2] of one K")
+        D = g["D"]
+        if D.dim() != 2 or D.shape[0] != M or D.shape[1] != N:
+            raise ValueError("D: must be [M, N]")
+        arr[i] = (_codes(A, 0, "A"), _codes(g["a_sf"], _fp4_scale_bytes(M, 2 * K2, quant), "a_sf"),
+                  _codes(B, 0, "B"), _codes(g["b_sf"], _fp4_scale_bytes(N, 2 * K2, quant), "b_sf"),
+                  quant, M, N, 2 * K2, _f32(get("a_scale_inv"), 1, "a_scale_inv"),
+                  _f32(get("b_scale_inv"), 1, "b_scale_inv"), _bf16(D, D.shape, "D"))
+    status = load().fp4_gemm_multi(arr, len(gemms), _current_stream(stream))
+    if status:
+        _check(status, "fp4_gemm_multi")
 
 
 def fp8_rmsnorm_cast(x, gamma, eps, *, residual=None, h=None, rstd=None, y=None, quant=Q_NONE, fmt=E4M3,
@@ -335,22 +365,22 @@ def fp8_rmsnorm_cast(x, gamma, eps, *, residual=None, h=None, rstd=None, y=None,
     (BF16) and, as ``quant`` says, y's codes ``q`` (uint8): Q_FP8 with scale, amax (max-accumulated) and
     scale_inv (float32 [1] each), Q_MXFP8 / Q_MXFP4 / Q_NVFP4 with ``sf`` (uint8 scale atoms along the
     rows), Q_NVFP4 also with scale and optionally amax and scale_inv."""
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix")
-    rows, cols = x.shape
-    quant = int(quant)
-    four = quant in (Q_MXFP4, Q_NVFP4)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x: must be a matrix")
+    rows, cols = shape
+    four = quant == Q_MXFP4 or quant == Q_NVFP4
     sf_bytes = 0
     if sf is not None:
-        sf_bytes = fp4_scale_bytes(rows, cols, quant) if four else -(-rows // 128) * -(-cols // 128) * 512
-    if rstd is not None and (rstd.dtype != torch.float32 or rstd.numel() < rows):
-        raise ValueError("rstd must be float32 with one element per row")
-    d = _abi.RmsNorm(_bf16(x, (rows, cols), "x"), _bf16(residual, (rows, cols), "residual"),
-                     _bf16(gamma, (cols,), "gamma"), rows, cols, float(eps), _bf16(h, (rows, cols), "h"),
-                     _ptr(rstd), _bf16(y, (rows, cols), "y"), quant, int(fmt),
-                     _sized(q, rows * cols // 2 if four else rows * cols, "q"), _sized(sf, sf_bytes, "sf"),
-                     _scalar(scale, "scale"), _scalar(amax, "amax"), _scalar(scale_inv, "scale_inv"))
-    _check(load().fp8_rmsnorm_cast(C.byref(d), _stream(stream)), "fp8_rmsnorm_cast")
+        sf_bytes = _fp4_scale_bytes(rows, cols, quant) if four else (rows + 127) // 128 * ((cols + 127) // 128) * 512
+    d = _abi.RmsNorm(_bf16(x, shape, "x"), _bf16(residual, shape, "residual"), _bf16(gamma, shape[1:], "gamma"),
+                     rows, cols, eps, _bf16(h, shape, "h"), _f32(rstd, rows, "rstd"), _bf16(y, shape, "y"),
+                     quant, fmt, _codes(q, rows * cols // 2 if four else rows * cols, "q"),
+                     _codes(sf, sf_bytes, "sf"), _f32(scale, 1, "scale"), _f32(amax, 1, "amax"),
+                     _f32(scale_inv, 1, "scale_inv"))
+    status = load().fp8_rmsnorm_cast(d, _current_stream(stream))
+    if status:
+        _check(status, "fp8_rmsnorm_cast")
 
 
 def fp8_rmsnorm_backward_workspace_bytes(rows, cols):
@@ -363,24 +393,23 @@ def fp8_rmsnorm_backward(dy, h, gamma, rstd, dh, *, dres=None, dgamma=None, dgam
     pass's h and rstd, with dres added where given; ``dgamma`` (float32 [cols]) and / or ``dgamma_bf16``.
 
     ``workspace`` is a uint8 CUDA tensor of at least ``fp8_rmsnorm_backward_workspace_bytes`` bytes."""
-    if dy.dim() != 2:
-        raise ValueError("dy must be a matrix")
-    rows, cols = dy.shape
-    if rstd.dtype != torch.float32 or rstd.numel() < rows:
-        raise ValueError("rstd must be float32 with one element per row")
-    if dgamma is not None and (dgamma.dtype != torch.float32 or dgamma.numel() < cols):
-        raise ValueError("dgamma must be float32 with one element per column")
+    shape = dy.shape
+    if len(shape) != 2:
+        raise ValueError("dy: must be a matrix")
+    rows, cols = shape
     if workspace is None and (dgamma is not None or dgamma_bf16 is not None):
-        workspace = torch.empty(fp8_rmsnorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
+        workspace = torch.empty(load().fp8_rmsnorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
                                 device=dy.device)
         if stream is not None:
             workspace.record_stream(stream)      # freed on return, read by kernels of that stream
-    d = _abi.RmsNormGrad(_bf16(dy, (rows, cols), "dy"), _bf16(h, (rows, cols), "h"), _bf16(gamma, (cols,), "gamma"),
-                         _ptr(rstd), _bf16(dres, (rows, cols), "dres"), rows, cols, _bf16(dh, (rows, cols), "dh"),
-                         _ptr(dgamma), _bf16(dgamma_bf16, (cols,), "dgamma_bf16"))
-    _check(load().fp8_rmsnorm_backward(C.byref(d), _ptr(workspace),
-                                       0 if workspace is None else workspace.numel(), _stream(stream)),
-           "fp8_rmsnorm_backward")
+    d = _abi.RmsNormGrad(_bf16(dy, shape, "dy"), _bf16(h, shape, "h"), _bf16(gamma, shape[1:], "gamma"),
+                         _f32(rstd, rows, "rstd"), _bf16(dres, shape, "dres"), rows, cols,
+                         _bf16(dh, shape, "dh"), _f32(dgamma, cols, "dgamma"),
+                         _bf16(dgamma_bf16, shape[1:], "dgamma_bf16"))
+    ws = _codes(workspace, 0, "workspace")
+    status = load().fp8_rmsnorm_backward(d, ws, 0 if ws is None else workspace.numel(), _current_stream(stream))
+    if status:
+        _check(status, "fp8_rmsnorm_backward")
 
 
 def fp8_scale_update(amax, history, fp8_max, algo, margin, scale, scale_inv, stream=None):

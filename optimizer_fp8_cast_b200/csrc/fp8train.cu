@@ -55,7 +55,7 @@ struct DeviceInfo {
   int gemm_wide_clusters = 0;  // ... of its wide-tile form
   int gemm_mx_clusters = 0;    // ... of its MXFP8 variant
   int gemm_mxw_clusters = 0;   // ... of the MXFP8 256 x 384 kernel
-  int gemm_fp4_clusters = 0;   // ... of the 4-bit 256 x 384 kernel (fewer of its two forms)
+  int gemm_fp4_clusters = 0;   // ... of the 4-bit 256 x 256 kernel (fewer of its two forms)
   int mx_cast_blocks_per_sm = 0;
   int fp4_cast_blocks_per_sm = 0;
   int cast_blocks_per_sm = 0;
@@ -64,6 +64,22 @@ struct DeviceInfo {
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mutex;
+
+template <bool NV, int BT>
+cudaError_t allow_fp4_split_smem_of() {
+  return cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm_split<NV, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fp8t::gemm::SplitShape<NV, BT>::kSmem);
+}
+cudaError_t allow_fp4_split_smem() {
+  cudaError_t e;
+  if ((e = allow_fp4_split_smem_of<false, 16>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 16>()) != cudaSuccess ||
+      (e = allow_fp4_split_smem_of<false, 32>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 32>()) != cudaSuccess ||
+      (e = allow_fp4_split_smem_of<false, 64>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 64>()) != cudaSuccess ||
+      (e = allow_fp4_split_smem_of<false, 128>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 128>()) != cudaSuccess ||
+      (e = allow_fp4_split_smem_of<false, 256>()) != cudaSuccess)
+    return e;
+  return allow_fp4_split_smem_of<true, 256>();
+}
 
 // Current device must be compute capability 10.0 (sm_100a code runs there only).
 fp8t_status current_device(DeviceInfo** out) {
@@ -163,11 +179,12 @@ fp8t_status current_device(DeviceInfo** out) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  fp8t::fp4::kCastSmemBytes);
+      if (e == cudaSuccess) e = allow_fp4_split_smem();
       if (e != cudaSuccess) {
         d.state = 0;
         return fail(FP8T_ERR_CUDA, "cudaFuncSetAttribute(4-bit): %s", cudaGetErrorString(e));
       }
-      cfg.blockDim = dim3(fp8t::gemm::kThreadsX, 1, 1);
+      cfg.blockDim = dim3(fp8t::gemm::kThreads4, 1, 1);
       cfg.dynamicSmemBytes = fp8t::gemm::kSmemBytes4<true>;
       clusters = 0;
       e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true>, &cfg);
@@ -1100,6 +1117,156 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
 }
 
 // ------------------------------------------------------------------ 4-bit GEMM
+}  // extern "C"
+
+namespace {
+
+// Scales of a 4-bit operand: rows of 256 words (1 KB), one (MXFP4) or two (NVFP4) per 128 rows and 256
+// values of K, read as one box.
+fp8t_status encode_fp4_scales(CUtensorMap* map, const void* ptr, int64_t mn, int64_t K, bool nv) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint32_t per = nv ? 2 : 1;
+  cuuint64_t dims[2] = {256, static_cast<cuuint64_t>((mn + 127) / 128 * ((K + 255) / 256) * per)};
+  cuuint64_t strides[1] = {1024};
+  cuuint32_t box[2] = {256, per};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit scales) failed (%d)", (int)r);
+  return FP8T_OK;
+}
+
+// n problems of one format on 256 x 256 pair tiles.
+fp8t_status fp4_gemm_wide(const fp8t_fp4_gemm_desc* gemms, int32_t n, const DeviceInfo* dev, cudaStream_t stream) {
+  using namespace fp8t::gemm;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const bool nv = gemms[0].quant == FP8T_Q_NVFP4;
+  static thread_local Group group;
+  std::memset(&group, 0, sizeof(group));
+  group.n = n;
+  int64_t tiles = 0;
+  fp8t_status st;
+  for (int32_t i = 0; i < n; ++i) {
+    const fp8t_fp4_gemm_desc& d = gemms[i];
+    Problem& P = group.p[i];
+    if ((st = encode_kmajor(&P.a, d.A, d.M, d.K / 2, kHalf)) != FP8T_OK) return st;
+    if ((st = encode_kmajor(&P.b, d.B, d.N, d.K / 2, kHalf)) != FP8T_OK) return st;
+    if ((st = encode_fp4_scales(&P.sfa, d.A_scales, d.M, d.K, nv)) != FP8T_OK) return st;
+    if ((st = encode_fp4_scales(&P.sfb, d.B_scales, d.N, d.K, nv)) != FP8T_OK) return st;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(d.M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.N) * 2};
+    cuuint32_t box[2] = {32, 32};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = fn(&P.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.D_bf16, dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (D) failed (%d)", (int)r);
+    P.sa = d.d_a_scale_inv;
+    P.sb = d.d_b_scale_inv;
+    P.M = static_cast<int32_t>(d.M);
+    P.N = static_cast<int32_t>(d.N);
+    P.K = static_cast<int32_t>(d.K);
+    P.kb128 = static_cast<int32_t>((d.K + 255) / 256);       // this kernel's k-blocks: 256 values
+    P.sumsq_slot = -1;
+    P.tiles_n = static_cast<int32_t>((d.N + kBN - 1) / kBN);
+    P.tile_start = static_cast<int32_t>(tiles);
+    tiles += ((d.M + kBM - 1) / kBM) * P.tiles_n;
+    if (tiles >= (int64_t(1) << 30))
+      return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
+  }
+  group.total_tiles = static_cast<int32_t>(tiles);
+  const int64_t grid = 2 * std::min<int64_t>(tiles, dev->gemm_fp4_clusters);
+  build_schedule(group, static_cast<int>(grid / 2), false);
+  if (nv)
+    k_fp4_gemm<true><<<static_cast<unsigned>(grid), kThreads4, kSmemBytes4<true>, stream>>>(group);
+  else
+    k_fp4_gemm<false><<<static_cast<unsigned>(grid), kThreads4, kSmemBytes4<false>, stream>>>(group);
+  return after_launch("fp4_gemm launch");
+}
+
+template <bool NV, int BT>
+cudaError_t launch_fp4_split(const fp8t::gemm::SplitGroup& g, int64_t tiles, int ways, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ways), 1, 1);
+  cfg.blockDim = dim3(fp8t::gemm::kSplitThreads, 1, 1);
+  cfg.dynamicSmemBytes = fp8t::gemm::SplitShape<NV, BT>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(ways);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8t::gemm::k_fp4_gemm_split<NV, BT>, g);
+}
+
+// Tokens per tile and CTAs per cluster of the split kernel for up to kMaxSplitProblems problems.
+struct SplitPlan {
+  int bt, ways;
+  int64_t tiles;
+};
+SplitPlan plan_fp4_split(const fp8t_fp4_gemm_desc* gemms, int32_t n, int sms) {
+  int64_t M = 0, kbs = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    M = std::max(M, gemms[i].M);
+    kbs = std::max(kbs, (gemms[i].K + 255) / 256);
+  }
+  SplitPlan p;
+  p.bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  p.tiles = 0;
+  for (int32_t i = 0; i < n; ++i) p.tiles += (gemms[i].N + 127) / 128 * ((gemms[i].M + p.bt - 1) / p.bt);
+  const int64_t slots = p.bt == 256 ? sms : 2 * sms;
+  p.ways = 1;
+  while (p.ways < 8 && p.tiles * p.ways * 2 <= slots && p.ways * 2 <= kbs) p.ways *= 2;
+  return p;
+}
+
+fp8t_status fp4_gemm_split(const fp8t_fp4_gemm_desc* gemms, int32_t n, const SplitPlan& plan, cudaStream_t stream) {
+  using namespace fp8t::gemm;
+  const bool nv = gemms[0].quant == FP8T_Q_NVFP4;
+  static thread_local SplitGroup group;
+  group.n = n;
+  int64_t tiles = 0;
+  fp8t_status st;
+  for (int32_t i = 0; i < n; ++i) {
+    const fp8t_fp4_gemm_desc& d = gemms[i];
+    SplitProblem& P = group.p[i];
+    if ((st = encode_kmajor(&P.w, d.B, d.N, d.K / 2, 128)) != FP8T_OK) return st;
+    if ((st = encode_kmajor(&P.t, d.A, d.M, d.K / 2, static_cast<uint32_t>(plan.bt))) != FP8T_OK) return st;
+    if ((st = encode_fp4_scales(&P.sfw, d.B_scales, d.N, d.K, nv)) != FP8T_OK) return st;
+    if ((st = encode_fp4_scales(&P.sft, d.A_scales, d.M, d.K, nv)) != FP8T_OK) return st;
+    P.sa = d.d_a_scale_inv;
+    P.sb = d.d_b_scale_inv;
+    P.D = static_cast<uint16_t*>(d.D_bf16);
+    P.M = static_cast<int32_t>(d.M);
+    P.N = static_cast<int32_t>(d.N);
+    P.num_kb = static_cast<int32_t>((d.K + 255) / 256);
+    P.tiles_t = static_cast<int32_t>((d.M + plan.bt - 1) / plan.bt);
+    P.tile_start = static_cast<int32_t>(tiles);
+    tiles += (d.N + 127) / 128 * P.tiles_t;
+  }
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (plan.bt) {
+    case 16: e = nv ? launch_fp4_split<true, 16>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 16>(group, tiles, plan.ways, stream); break;
+    case 32: e = nv ? launch_fp4_split<true, 32>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 32>(group, tiles, plan.ways, stream); break;
+    case 64: e = nv ? launch_fp4_split<true, 64>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 64>(group, tiles, plan.ways, stream); break;
+    case 128: e = nv ? launch_fp4_split<true, 128>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 128>(group, tiles, plan.ways, stream); break;
+    case 256: e = nv ? launch_fp4_split<true, 256>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 256>(group, tiles, plan.ways, stream); break;
+  }
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(FP8T_ERR_CUDA, "fp4_gemm split launch: %s", cudaGetErrorString(e));
+  }
+  return after_launch("fp4_gemm split launch");
+}
+
+}  // namespace
+
+extern "C" {
+
 fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, void* stream) {
   t_last_error.clear();
   if (!gemms || n_gemms < 1 || n_gemms > 4096)
@@ -1123,67 +1290,18 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
   if (st != FP8T_OK) return st;
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  using namespace fp8t::gemm;
-  // scales: rows of 256 words (1 KB); one (MXFP4) or two (NVFP4) rows per 128 rows and 256 values of K
-  auto encode_sf = [&](CUtensorMap* map, const void* ptr, int64_t mn, int64_t K, bool nv) -> fp8t_status {
-    const cuuint32_t per = nv ? 2 : 1;
-    cuuint64_t dims[2] = {256, static_cast<cuuint64_t>((mn + 127) / 128 * ((K + 255) / 256) * per)};
-    cuuint64_t strides[1] = {1024};
-    cuuint32_t box[2] = {256, per};
-    cuuint32_t es[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit scales) failed (%d)", (int)r);
-    return FP8T_OK;
-  };
-  static thread_local Group group;
   for (int32_t b0 = 0, b1 = 0; b0 < n_gemms; b0 = b1) {
-    const bool nv = gemms[b0].quant == FP8T_Q_NVFP4;
-    b1 = b0 + 1;
-    while (b1 < n_gemms && b1 - b0 < kMaxProblems && gemms[b1].quant == gemms[b0].quant) ++b1;
-    std::memset(&group, 0, sizeof(group));
-    group.n = b1 - b0;
+    // consecutive problems of one format; together they fill the pairs with 256 x 256 tiles or they do not
     int64_t tiles = 0;
-    for (int32_t i = b0; i < b1; ++i) {
-      const fp8t_fp4_gemm_desc& d = gemms[i];
-      Problem& P = group.p[i - b0];
-      if ((st = encode_kmajor(&P.a, d.A, d.M, d.K / 2, kHalf)) != FP8T_OK) return st;
-      if ((st = encode_kmajor(&P.b, d.B, d.N, d.K / 2, kHalf)) != FP8T_OK) return st;
-      if ((st = encode_kmajor(&P.b64, d.B, d.N, d.K / 2, kHalf / 2)) != FP8T_OK) return st;
-      if ((st = encode_sf(&P.sfa, d.A_scales, d.M, d.K, nv)) != FP8T_OK) return st;
-      if ((st = encode_sf(&P.sfb, d.B_scales, d.N, d.K, nv)) != FP8T_OK) return st;
-      cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(d.M)};
-      cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.N) * 2};
-      cuuint32_t box[2] = {32, 32};
-      cuuint32_t es[2] = {1, 1};
-      CUresult r = fn(&P.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.D_bf16, dims, strides, box, es,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-      if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (D) failed (%d)", (int)r);
-      P.sa = d.d_a_scale_inv;
-      P.sb = d.d_b_scale_inv;
-      P.M = static_cast<int32_t>(d.M);
-      P.N = static_cast<int32_t>(d.N);
-      P.K = static_cast<int32_t>(d.K);
-      P.kb128 = static_cast<int32_t>((d.K + 255) / 256);       // this kernel's k-blocks: 256 values
-      P.sumsq_slot = -1;
-      P.tiles_n = static_cast<int32_t>((d.N + kBNx - 1) / kBNx);
-      P.tile_start = static_cast<int32_t>(tiles);
-      tiles += ((d.M + kBM - 1) / kBM) * P.tiles_n;
-      if (tiles >= (int64_t(1) << 30))
-        return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
+    for (b1 = b0; b1 < n_gemms && b1 - b0 < fp8t::gemm::kMaxProblems && gemms[b1].quant == gemms[b0].quant; ++b1)
+      tiles += (gemms[b1].M + fp8t::gemm::kBM - 1) / fp8t::gemm::kBM * ((gemms[b1].N + fp8t::gemm::kBN - 1) / fp8t::gemm::kBN);
+    if (tiles < dev->gemm_fp4_clusters) {
+      b1 = std::min(b1, b0 + fp8t::gemm::kMaxSplitProblems);
+      const SplitPlan plan = plan_fp4_split(gemms + b0, b1 - b0, dev->sms);
+      if ((st = fp4_gemm_split(gemms + b0, b1 - b0, plan, as_stream(stream))) != FP8T_OK) return st;
+    } else if ((st = fp4_gemm_wide(gemms + b0, b1 - b0, dev, as_stream(stream))) != FP8T_OK) {
+      return st;
     }
-    group.total_tiles = static_cast<int32_t>(tiles);
-    const int64_t grid = 2 * std::min<int64_t>(tiles, dev->gemm_fp4_clusters);
-    build_schedule(group, static_cast<int>(grid / 2), false, true);
-    if (nv)
-      k_fp4_gemm<true><<<static_cast<unsigned>(grid), kThreadsX, kSmemBytes4<true>, as_stream(stream)>>>(group);
-    else
-      k_fp4_gemm<false><<<static_cast<unsigned>(grid), kThreadsX, kSmemBytes4<false>, as_stream(stream)>>>(group);
-    if ((st = after_launch("fp4_gemm launch")) != FP8T_OK) return st;
   }
   return FP8T_OK;
 }

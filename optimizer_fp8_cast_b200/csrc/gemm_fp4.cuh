@@ -5,33 +5,56 @@
 // tcgen05.mma kind::mxf4 (E8M0 scale per 32 values) and kind::mxf4nvf4 (E4M3 scale per 16), FP32
 // accumulation, K = 64 values (32 bytes) per MMA: the operand bytes, shared-memory layout and cycles
 // of an 8-bit MMA of K = 32, at twice its values. Both operands are K-major (the 4-bit kinds read no
-// other order), two values per byte.
+// other order), two values per byte. A k-block is 256 values (128 bytes per row, four MMAs).
 //
-// Large problems (k_fp4_gemm): the 256 x 384 pair tile of the MXFP8 kernel, for the same reason (operand
-// bytes per MMA cycle, and TMEM room for the scales). A k-block is 256 values (128 bytes per row). Per
-// k-block every 128 rows of A or B bring 2 (MXFP4) or 4 (NVFP4) scale atoms, stored next to each other
-// ([MN / 128][K / 256]), which arrive as one TMA box of 1 or 2 KB and are copied to 16 TMEM columns per
-// atom step along K: A 4, B 12. Rows of a ragged edge read zero codes (TMA fill), so M and N need not
-// be multiples of the tile; K's padding has zero codes and zero scales.
-// TMEM: accumulator 0..383, scales from 384 (32 or 64 columns).
-// Warp roles, barriers, bounded waits and the register-held epilogue are those of the MXFP8 kernel.
+// Large problems (k_fp4_gemm): a cluster of two CTAs computes 256 x 256 tiles, each CTA holding 128 rows of
+// A and 128 of B. Per k-block every 128 rows of A or B bring 2 (MXFP4) or 4 (NVFP4) scale atoms, stored
+// next to each other ([MN / 128][K / 256]), which arrive as one TMA box of 1 or 2 KB; each CTA takes its
+// own A rows' and all of the tile's B rows'. The MMA warp copies an atom step (A 4, B 8 TMEM columns) right
+// before the MMAs that use it.
+//
+// What bounds it. An MMA (256 x 256 x 64) takes 128 cycles, a k-block 512; a scale copy takes the copy
+// path 44-64 cycles but runs beside earlier MMAs, so MXFP4's 6 copies per k-block are hidden (519 cycles
+// measured per k-block, operands resident) and NVFP4's 12 set the pace (717). Two things make that so:
+//   - the issuing warp stays converged and one elected lane issues. Issued from a lane that left its warp, a
+//     copy after an mbarrier wait did not overlap the MMAs before it: 1034 against 773 cycles for 8
+//     copies and 8 MMAs per k-block;
+//   - copies are spread between the MMAs in the order of use.
+// Two accumulators let the epilogue of a tile run beside the next tile's MMAs. Two of 256 columns and the
+// scales (24 or 48) do not fit the 512 TMEM columns, so they overlap by kOv columns: accumulator 0 at
+// 0..255, accumulator 1 at 256 - kOv, scales after it. The epilogue reads the shared columns first and
+// releases them through a barrier of their own. (With one accumulator and 256 x 384 tiles the MMAs of a
+// 16384 x 11008 x 4096 product waited about 3.3 us per tile for the epilogue: 335 us MXFP4, 441 us NVFP4.)
+// Rows of a ragged edge read zero codes (TMA fill), so M and N need not be multiples of the tile; K's
+// padding has zero codes and zero scales.
+// Warp roles (320 threads): warp 0 TMA producer; warp 1 MMA issuer (even CTA), TMEM allocation; warps 2-9
+// epilogue, a TMEM lane quarter and a 128-column half each. Waits are bounded as in the other kernels.
 #pragma once
 
-#include "gemm_mx_wide.cuh"
+#include "gemm_tcgen05.cuh"
 
 namespace fp8t {
 namespace gemm {
 
-constexpr int kStages4 = 4;
-constexpr uint32_t kSfCol4 = 384;
+constexpr int kStages4 = 5;
 template <bool NV>
-constexpr int kStageBytes4 = kABytes + kB0BytesX + kB1BytesX + 4 * (NV ? 4 : 2) * 512;
-constexpr int kEpiBytes4 = kEpiWarpsX * 2 * kEpiChunkBytes;
+constexpr int kSfBytes4 = (NV ? 4 : 2) * 512;                     // scales of 128 rows x 256 values
+template <bool NV>
+constexpr int kStageBytes4 = kABytes + kBBytes + 3 * kSfBytes4<NV>;
+template <bool NV>
+constexpr uint32_t kOv4 = NV ? 64 : 32;                           // columns the accumulators share
+template <bool NV>
+constexpr uint32_t kAcc1Col4 = 256 - kOv4<NV>;
+template <bool NV>
+constexpr uint32_t kSfCol4 = 512 - kOv4<NV>;
+constexpr int kEpiWarps4 = 8;
+constexpr int kThreads4 = 64 + 32 * kEpiWarps4;
+constexpr int kEpiBytes4 = kEpiWarps4 * 2 * kEpiChunkBytes;
 template <bool NV>
 constexpr int kSmemBytes4 = kStages4 * kStageBytes4<NV> + kEpiBytes4 + 1024 + 256;
 static_assert(kStageBytes4<false> % 1024 == 0 && kStageBytes4<true> % 1024 == 0, "stages stay 1024-byte aligned");
 static_assert(kSmemBytes4<true> <= 232448, "shared memory of an SM");
-static_assert(kSfCol4 + 64 <= static_cast<uint32_t>(kTmemCols), "TMEM columns");
+static_assert(kSfCol4<false> + 2 * 12 <= 512 && kSfCol4<true> + 4 * 12 <= 512, "TMEM columns");
 
 // Block-scaled instruction descriptor of the 4-bit kinds: E2M1 operands, K-major, scale type (bit 23:
 // 1 E8M0, 0 E4M3), scale-factor ids of A and B.
@@ -61,17 +84,40 @@ __device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc,
         : "memory");
 }
 
+// One lane of a converged warp, the same on every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// A wait by a whole warp: every lane waits, and all agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit, bool expired = false) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, expired));
+}
+__device__ __forceinline__ bool warp_aborted(const volatile int* flag) {
+  return __any_sync(0xffffffffu, *flag != 0);
+}
+
+struct Smem4 {
+  uint64_t full[kStages4];      // even CTA: both CTAs' loads of a stage have landed
+  uint64_t empty[kStages4];     // both CTAs: the pair MMA has consumed a stage
+  uint64_t acc_full[2];         // both CTAs: an accumulator holds a finished tile
+  uint64_t acc_empty[2];        // even CTA: every epilogue warp of both CTAs has read an accumulator
+  uint64_t acc_shared_free;     // even CTA: the warps that read the shared columns have
+  uint64_t mma_done;            // even CTA: every issued MMA has completed
+  uint32_t tmem_base;
+  int abort;
+};
+
 template <bool NV>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsX, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     k_fp4_gemm(const __grid_constant__ Group g) {
+  constexpr int kAtoms = NV ? 4 : 2, kSf = kSfBytes4<NV>, kSfRows = NV ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-  // stage s: [A 128 x 128 B][B0 128 x 128 B][B1 64 x 128 B][scale atoms of A, B 0..127, 128..255, 256..383]
-  constexpr int kAtoms = NV ? 4 : 2, kSf = kAtoms * 512, kSfRows = NV ? 2 : 1;
-  uint8_t* sStage = smem;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // stage s: [A 128 x 128 B][B 128 x 128 B][scales of A | B rows 0..127 | B rows 128..255]
   uint8_t* sEpi = smem + kStages4 * kStageBytes4<NV>;
-  SmemX* S = reinterpret_cast<SmemX*>(sEpi + kEpiBytes4);
+  Smem4* S = reinterpret_cast<Smem4*>(sEpi + kEpiBytes4);
   volatile int* abort_flag = &S->abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -85,15 +131,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsX, 1)
       mbar_init(smem_u32(&S->full[s]), 1);
       mbar_init(smem_u32(&S->empty[s]), 1);
     }
-    mbar_init(smem_u32(&S->acc_full), 1);
-    mbar_init(smem_u32(&S->acc_empty), 2 * kEpiWarpsX);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&S->acc_full[a]), 1);
+      mbar_init(smem_u32(&S->acc_empty[a]), 2 * kEpiWarps4);
+    }
+    mbar_init(smem_u32(&S->acc_shared_free), kEpiWarps4);   // half of the warps of each CTA
     mbar_init(smem_u32(&S->mma_done), 1);
     *abort_flag = 0;
     fence_mbar_init();
     for (int p = 0; p < g.n && p < 8; ++p) {
       tma_prefetch_desc(&g.p[p].a);
       tma_prefetch_desc(&g.p[p].b);
-      tma_prefetch_desc(&g.p[p].b64);
       tma_prefetch_desc(&g.p[p].d);
     }
   }
@@ -102,7 +150,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsX, 1)
     tmem_relinquish_pair();
   }
   tc_fence_before();
-  cluster_sync();
+  cluster_sync();                 // barriers initialised and TMEM allocated in both CTAs
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
   const uint64_t limit = wait_limit_ns();
@@ -111,160 +159,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsX, 1)
   const bool expire_epi = expire == kExpireAll || expire == kExpireGemmEpilogue;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer (both CTAs)
-      uint32_t it = 0, issued = 0;
-      for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
-        const int tile = tile_at(g, cluster, n_clusters, i);
-        const Problem& P = g.p[find_problem(g, tile)];
-        int mt, nt;
-        bool has1;
-        mxw_tile(P, tile - P.tile_start, mt, nt, has1);
-        const int m0 = mt * kBM + static_cast<int>(rank) * kHalf;
-        const int nb0 = nt * kBNx + static_cast<int>(rank) * kHalf;           // MMA 0 rows
-        const int nb1 = nt * kBNx + 256 + static_cast<int>(rank) * (kHalf / 2); // MMA 1 rows
-        const int ra = 2 * mt + static_cast<int>(rank), rb = 3 * nt;          // atom rows
-        const int num_kb = P.kb128;                                           // k-blocks of 256 values
-        const uint32_t tx = 2u * (kABytes + kB0BytesX + 3 * kSf + (has1 ? kB1BytesX + kSf : 0));
-        for (int kb = 0; kb < num_kb; ++kb, ++it) {
-          const uint32_t s = it % kStages4, ph = (it / kStages4) & 1;
-          if (*abort_flag) break;
-          if (!mbar_wait(smem_u32(&S->empty[s]), ph ^ 1, limit, expire_main)) {
-            *abort_flag = 1;
-            record_error(kErrTimeout);
-            break;
-          }
+    // ---------------- TMA producer (both CTAs)
+    const bool one = elect_one();
+    uint32_t it = 0, issued = 0;
+    for (int i = 0; i < my_tiles && !warp_aborted(abort_flag); ++i) {
+      const int tile = tile_at(g, cluster, n_clusters, i);
+      const Problem& P = g.p[find_problem(g, tile)];
+      const int local = tile - P.tile_start, mt = local / P.tiles_n, nt = local % P.tiles_n;
+      const int m0 = mt * kBM + static_cast<int>(rank) * kHalf;
+      const int n0 = nt * kBN + static_cast<int>(rank) * kHalf;
+      const int ra = 2 * mt + static_cast<int>(rank), rb = 2 * nt;          // 128-row blocks of the scales
+      const int num_kb = P.kb128;                                           // k-blocks of 256 values
+      for (int kb = 0; kb < num_kb; ++kb, ++it) {
+        const uint32_t s = it % kStages4, ph = (it / kStages4) & 1;
+        if (warp_aborted(abort_flag)) break;
+        if (!warp_wait(smem_u32(&S->empty[s]), ph ^ 1, limit, expire_main)) {
+          *abort_flag = 1;
+          if (one) record_error(kErrTimeout);
+          break;
+        }
+        if (one) {
           const uint32_t full_leader = mapa_shared(smem_u32(&S->full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), tx);
-          const uint32_t base = smem_u32(sStage + s * kStageBytes4<NV>);
-          const uint32_t a_dst = base, b0_dst = base + kABytes, b1_dst = b0_dst + kB0BytesX;
-          const uint32_t sf_dst = b1_dst + kB1BytesX;
+          if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), 2 * kStageBytes4<NV>);
+          const uint32_t a_dst = smem_u32(smem + s * kStageBytes4<NV>), b_dst = a_dst + kABytes;
+          const uint32_t sf_dst = b_dst + kBBytes;
           tma_load_2d_pair(a_dst, &P.a, kb * kBK, m0, full_leader);
-          tma_load_2d_pair(b0_dst, &P.b, kb * kBK, nb0, full_leader);
+          tma_load_2d_pair(b_dst, &P.b, kb * kBK, n0, full_leader);
           tma_load_2d_pair(sf_dst, &P.sfa, 0, (ra * num_kb + kb) * kSfRows, full_leader);
           tma_load_2d_pair(sf_dst + kSf, &P.sfb, 0, (rb * num_kb + kb) * kSfRows, full_leader);
           tma_load_2d_pair(sf_dst + 2 * kSf, &P.sfb, 0, ((rb + 1) * num_kb + kb) * kSfRows, full_leader);
-          if (has1) {
-            tma_load_2d_pair(b1_dst, &P.b64, kb * kBK, nb1, full_leader);
-            tma_load_2d_pair(sf_dst + 3 * kSf, &P.sfb, 0, ((rb + 2) * num_kb + kb) * kSfRows, full_leader);
-          }
-          ++issued;
         }
+        ++issued;
       }
-      if (leader) {
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t i = issued > kStages4 ? issued - kStages4 : 0; i < issued; ++i) {
-          const uint64_t spent = globaltimer_ns() - t0;
-          if (spent >= kPairDrainNs) break;
-          mbar_wait(smem_u32(&S->full[i % kStages4]), (i / kStages4) & 1, kPairDrainNs - spent);
-        }
+    }
+    // the even CTA can see its own stages land: wait for the last ones it armed (one shared budget; after
+    // an abort a stage may miss the peer's bytes, and the settle delay below covers loads in flight)
+    if (leader) {
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t i = issued > kStages4 ? issued - kStages4 : 0; i < issued; ++i) {
+        const uint64_t spent = globaltimer_ns() - t0;
+        if (spent >= kPairDrainNs) break;
+        mbar_wait(smem_u32(&S->full[i % kStages4]), (i / kStages4) & 1, kPairDrainNs - spent);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---------------- MMA issuer (even CTA): per k-step an N = 256 and an N = 128 MMA
-      uint32_t it = 0, local = 0;
-      for (int i = 0; i < my_tiles && !*abort_flag; ++i, ++local) {
+    if (leader) {
+      // ---------------- MMA issuer (even CTA)
+      const bool one = elect_one();
+      uint32_t it = 0;
+      for (int i = 0; i < my_tiles && !warp_aborted(abort_flag); ++i) {
         const int tile = tile_at(g, cluster, n_clusters, i);
         const Problem& P = g.p[find_problem(g, tile)];
-        int mt, nt;
-        bool has1;
-        mxw_tile(P, tile - P.tile_start, mt, nt, has1);
         const int num_kb = P.kb128;
-        if (!mbar_wait(smem_u32(&S->acc_empty), (local & 1) ^ 1, limit, expire_main)) {
+        const uint32_t acc = i & 1, aph = (i >> 1) & 1;
+        // this accumulator read by the epilogue of two tiles ago; the columns it shares with the other one
+        // by the previous tile's
+        if (!warp_wait(smem_u32(&S->acc_empty[acc]), aph ^ 1, limit, expire_main) ||
+            (i > 0 && !warp_wait(smem_u32(&S->acc_shared_free), (i - 1) & 1, limit, expire_main))) {
           *abort_flag = 1;
-          record_error(kErrTimeout);
+          if (one) record_error(kErrTimeout);
           break;
         }
         tc_fence_after();
+        const uint32_t d_tmem = tmem + acc * kAcc1Col4<NV>;
         bool ok = true;
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
           const uint32_t s = it % kStages4, ph = (it / kStages4) & 1;
-          if (*abort_flag || !mbar_wait(smem_u32(&S->full[s]), ph, limit, expire_main)) {
-            if (!*abort_flag) record_error(kErrTimeout);
+          if (!warp_wait(smem_u32(&S->full[s]), ph, limit, expire_main) || warp_aborted(abort_flag)) {
+            if (one && !*abort_flag) record_error(kErrTimeout);
             *abort_flag = 1;
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t base = smem_u32(sStage + s * kStageBytes4<NV>);
-          const uint32_t a_base = base, b0_base = base + kABytes, b1_base = b0_base + kB0BytesX;
-          const uint32_t sf = b1_base + kB1BytesX;
+          if (one) {
+            const uint32_t a_base = smem_u32(smem + s * kStageBytes4<NV>), b_base = a_base + kABytes;
+            const uint32_t sf = b_base + kBBytes;
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a) {     // 16 scale columns per atom along K: A, B 0, B 1, B 2
-            const uint32_t sc = tmem + kSfCol4 + a * 16, at = sf + a * 512;
-            tc_cp_32x128b_warpx4_pair(sc, make_sf_desc(at));
-            tc_cp_32x128b_warpx4_pair(sc + 4, make_sf_desc(at + kSf));
-            tc_cp_32x128b_warpx4_pair(sc + 8, make_sf_desc(at + 2 * kSf));
-            if (has1) tc_cp_32x128b_warpx4_pair(sc + 12, make_sf_desc(at + 3 * kSf));
+            for (int k = 0; k < 4; ++k) {
+              // MXFP4: two scales per 64 values, so an atom step serves two MMAs (scale ids 0 and 2)
+              const int a = NV ? k : k >> 1;
+              const uint32_t sc = tmem + kSfCol4<NV> + a * 12, id = NV ? 0 : (k & 1) * 2;
+              if (NV || (k & 1) == 0) {
+                tc_cp_32x128b_warpx4_pair(sc, make_sf_desc(sf + a * 512));
+                tc_cp_32x128b_warpx4_pair(sc + 4, make_sf_desc(sf + kSf + a * 512));
+                tc_cp_32x128b_warpx4_pair(sc + 8, make_sf_desc(sf + 2 * kSf + a * 512));
+              }
+              tc_mma_fp4_pair<NV>(d_tmem, make_sw128_desc(a_base + k * kUmmaK), make_sw128_desc(b_base + k * kUmmaK),
+                                  make_idesc_fp4<NV>(kBM, kBN, id), sc | id << 30, (sc + 4) | id << 30,
+                                  (kb | k) != 0 ? 1u : 0u);
+            }
+            tc_commit_pair_mc(smem_u32(&S->empty[s]), 0x3);
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // MXFP4: two scales per 64 values, so an atom serves two MMAs (scale ids 0 and 2); NVFP4: one
-            const uint32_t sc = tmem + kSfCol4 + (NV ? k : k >> 1) * 16, id = NV ? 0 : (k & 1) * 2;
-            const uint64_t adesc = make_sw128_desc(a_base + k * kUmmaK);
-            const uint32_t acc = (kb | k) != 0 ? 1u : 0u;
-            tc_mma_fp4_pair<NV>(tmem, adesc, make_sw128_desc(b0_base + k * kUmmaK),
-                                make_idesc_fp4<NV>(kBM, 256, id), sc | id << 30, (sc + 4) | id << 30, acc);
-            if (has1)
-              tc_mma_fp4_pair<NV>(tmem + 256, adesc, make_sw128_desc(b1_base + k * kUmmaK),
-                                  make_idesc_fp4<NV>(kBM, 128, id), sc | id << 30, (sc + 12) | id << 30, acc);
-          }
-          tc_commit_pair_mc(smem_u32(&S->empty[s]), 0x3);
+          __syncwarp();
         }
         if (!ok) break;
-        tc_commit_pair_mc(smem_u32(&S->acc_full), 0x3);
+        if (one) tc_commit_pair_mc(smem_u32(&S->acc_full[acc]), 0x3);
+        __syncwarp();
       }
-      tc_commit_pair(smem_u32(&S->mma_done));
+      // every MMA issued here must complete before either CTA frees TMEM or shared memory
+      if (one) tc_commit_pair(smem_u32(&S->mma_done));
+      __syncwarp();
       mbar_wait(smem_u32(&S->mma_done), 0, kDrainLimitNs);
     }
   } else {
     // ---------------- epilogue warps 2..9 (both CTAs): TMEM lane quarter warp % 4, column half
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* my_buf = sEpi + (warp - 2) * 2 * kEpiChunkBytes;
-    uint32_t local = 0, chunk_count = 0;
-    for (int i = 0; i < my_tiles; ++i, ++local) {
+    uint32_t chunk_count = 0;
+    constexpr int kShared = static_cast<int>(kOv4<NV>) / 32;    // chunks the accumulators share
+    for (int i = 0; i < my_tiles; ++i) {
       const int tile = tile_at(g, cluster, n_clusters, i);
-      if (*abort_flag) break;
-      if (!mbar_wait(smem_u32(&S->acc_full), local & 1, limit, expire_epi)) {
+      const uint32_t acc = i & 1, aph = (i >> 1) & 1;
+      if (warp_aborted(abort_flag)) break;
+      if (!warp_wait(smem_u32(&S->acc_full[acc]), aph, limit, expire_epi)) {
         *abort_flag = 1;
-        record_error(kErrTimeout);
+        if (lane == 0) record_error(kErrTimeout);
         break;
       }
       tc_fence_after();
       const Problem& P = g.p[find_problem(g, tile)];
-      const float alpha = P.sa ? __fmul_rn(__ldg(P.sa), P.sb ? __ldg(P.sb) : 1.0f) : (P.sb ? __ldg(P.sb) : 1.0f);
-      const int M = P.M, N = P.N, local_tile = tile - P.tile_start;
-      const int row0 = (local_tile / P.tiles_n) * kBM + static_cast<int>(rank) * kHalf + quad * 32;
-      const int n0 = (local_tile % P.tiles_n) * kBNx + half * kAccColsX;
-      const uint32_t t_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kAccColsX;
-      uint32_t w[kAccColsX / 32][16];
-#pragma unroll
-      for (int c = 0; c < kAccColsX / 32; ++c) {
+      const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
+      const int M = P.M, N = P.N, local = tile - P.tile_start;
+      const int row0 = (local / P.tiles_n) * kBM + static_cast<int>(rank) * kHalf + quad * 32;
+      const int n0 = (local % P.tiles_n) * kBN;
+      const uint32_t t_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kAcc1Col4<NV>;
+      // the shared columns come first: accumulator 0's last chunks (half 1, walking down), accumulator
+      // 1's first (half 0, walking up)
+#pragma unroll 1
+      for (int step = 0; step < 4; ++step) {
+        const int c = half * 4 + (acc == 0 ? 3 - step : step);
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_base + c * 32, r);
         tmem_ld_wait();
         tmem_reg_fence(r);
+        if (step == kShared - 1 && half == (acc == 0 ? 1 : 0)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_shared_free), 0));
+        }
+        if (step == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_empty[acc]), 0));
+        }
+        if (n0 + c * 32 >= N || row0 >= M) continue;       // chunk entirely outside the matrix
+        uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          w[c][j] = pack_bf16x2(__fmul_rn(__uint_as_float(r[2 * j]), alpha), __fmul_rn(__uint_as_float(r[2 * j + 1]), alpha));
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_empty), 0));
-#pragma unroll
-      for (int c = 0; c < kAccColsX / 32; ++c) {
-        if (n0 + c * 32 >= N || row0 >= M) continue;       // chunk entirely outside the matrix
+          w[j] = pack_bf16x2(__fmul_rn(__uint_as_float(r[2 * j]), alpha), __fmul_rn(__uint_as_float(r[2 * j + 1]), alpha));
         uint8_t* buf = my_buf + (chunk_count & 1) * kEpiChunkBytes;
         ++chunk_count;
-        if (lane == 0) bulk_wait_group_read<1>();
+        if (lane == 0) bulk_wait_group_read<1>();          // the store that last used buf has read it
         __syncwarp();
+        // row `lane` of the chunk: four 16-byte pieces, 64-byte swizzle, matching the store's map
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int pp = p ^ ((lane >> 1) & 3);
-          *reinterpret_cast<uint4*>(buf + lane * 64 + pp * 16) =
-              make_uint4(w[c][4 * p], w[c][4 * p + 1], w[c][4 * p + 2], w[c][4 * p + 3]);
-        }
+        for (int p = 0; p < 4; ++p)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + (p ^ ((lane >> 1) & 3)) * 16) =
+              make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -273,19 +324,234 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsX, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_group<0>();
+    if (lane == 0) bulk_wait_group<0>();                   // every store complete before exit
   }
   __syncwarp();
   __syncthreads();
-  if (*abort_flag && threadIdx.x == 0) {
+  if (*abort_flag && threadIdx.x == 0) {                   // loads of either CTA may still be in flight
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < kSettleNs) {
     }
   }
   tc_fence_before();
-  cluster_sync();
+  cluster_sync();                 // neither CTA leaves while the pair MMA may still read it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- few rows: K split over a cluster
+// A product with few output tiles leaves most SMs idle under 256 x 384 tiles (one token of a 4096-wide
+// layer: 11 tiles for 74 pairs), and with few tokens its time is that of streaming B (the weights). Here
+// the weights are the 128-row operand of a one-CTA MMA and BT tokens the other, so a tile is 128 rows of
+// B by BT rows of A, and the S CTAs of a cluster each take a contiguous part of K. Every CTA leaves its FP32
+// partial tile in the shared memory of the CTAs that own its tokens (token t belongs to rank t / (BT / S));
+// after a cluster barrier each owner adds the S partials in rank order, scales, rounds and stores its
+// tokens' rows of D, 128 columns of a row at a time. No workspace, and the order of additions is fixed.
+// TMEM: accumulator (weight rows x tokens) in columns 0..BT-1, then the scales.
+constexpr int kSplitThreads = 128;
+constexpr int kMaxSplitProblems = 4;
+template <bool NV, int BT>
+struct SplitShape {
+  static constexpr int kSf = (NV ? 4 : 2) * 512;                 // scale bytes per 128 rows and k-block
+  static constexpr int kTokBlocks = BT > 128 ? 2 : 1;
+  static constexpr int kStage = kABytes + BT * kBK + kSf * (1 + kTokBlocks);
+  static constexpr int kStages = BT <= 64 ? 4 : BT == 128 ? 3 : 4;
+  static constexpr int kSfCols = 4 + 4 * kTokBlocks;              // TMEM columns per atom step along K
+  static constexpr int kTmem = BT <= 32 ? 64 : BT == 64 ? 128 : BT == 128 ? 256 : 512;
+  static constexpr int kSmem = kStages * kStage + 1024 + 256;
+  static_assert(BT + (NV ? 4 : 2) * kSfCols <= kTmem, "TMEM columns");
+  static_assert(128 * BT * 4 <= kStages * kStage, "the partial tiles fit the stage buffers");
+  static_assert(kStage % 1024 == 0, "stages stay 1024-byte aligned");
+};
+
+struct alignas(64) SplitProblem {
+  CUtensorMap w, t;                      // B [N][K/2] in 128-row boxes, A [M][K/2] in BT-row boxes
+  CUtensorMap sfw, sft;                  // their scales
+  const float* sa;
+  const float* sb;
+  uint16_t* D;
+  int32_t M, N, num_kb, tiles_t, tile_start;
+};
+struct alignas(64) SplitGroup {
+  SplitProblem p[kMaxSplitProblems];
+  int32_t n;
+};
+
+template <bool NV>
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if constexpr (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+template <bool NV, int BT>
+__global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_constant__ SplitGroup g) {
+  using Sh = SplitShape<NV, BT>;
+  constexpr int kSf = Sh::kSf, kSfRows = NV ? 2 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  struct Bars {
+    uint64_t full[Sh::kStages], empty[Sh::kStages], done;
+    uint32_t tmem_base;
+    int abort;
+  };
+  Bars* S = reinterpret_cast<Bars*>(smem + Sh::kStages * Sh::kStage);
+  volatile int* abort_flag = &S->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), ways = static_cast<int>(cluster_nctarank());
+  const int tile = blockIdx.x / ways;
+  int pi = 0;
+  while (pi + 1 < g.n && g.p[pi + 1].tile_start <= tile) ++pi;
+  const SplitProblem& P = g.p[pi];
+  const int n0 = (tile - P.tile_start) / P.tiles_t * 128, t0 = (tile - P.tile_start) % P.tiles_t * BT;
+  // this CTA's k-blocks; a problem with fewer than the cluster's CTAs leaves some of them none
+  const int kb0 = static_cast<int>(static_cast<int64_t>(P.num_kb) * rank / ways);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(P.num_kb) * (rank + 1) / ways);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Sh::kStages; ++s) {
+      mbar_init(smem_u32(&S->full[s]), 1);
+      mbar_init(smem_u32(&S->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&S->done), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&S->tmem_base), Sh::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  const uint64_t limit = wait_limit_ns();
+  const int expire = expire_mode();
+  const bool expire_main = expire == kExpireAll;
+
+  if (warp == 0) {
+    const bool one = elect_one();
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const uint32_t it = kb - kb0, s = it % Sh::kStages, ph = (it / Sh::kStages) & 1;
+      if (!warp_wait(smem_u32(&S->empty[s]), ph ^ 1, limit, expire_main) || warp_aborted(abort_flag)) {
+        if (one && !*abort_flag) record_error(kErrTimeout);
+        *abort_flag = 1;
+        break;
+      }
+      if (one) {
+        const uint32_t bar = smem_u32(&S->full[s]), w = smem_u32(smem + s * Sh::kStage);
+        const uint32_t t = w + kABytes, sf = t + BT * kBK;
+        mbar_arrive_expect_tx(bar, Sh::kStage);
+        tma_load_2d(w, &P.w, kb * kBK, n0, bar);
+        tma_load_2d(t, &P.t, kb * kBK, t0, bar);
+        tma_load_2d(sf, &P.sfw, 0, ((n0 >> 7) * P.num_kb + kb) * kSfRows, bar);
+#pragma unroll
+        for (int b = 0; b < Sh::kTokBlocks; ++b)
+          tma_load_2d(sf + (1 + b) * kSf, &P.sft, 0, (((t0 >> 7) + b) * P.num_kb + kb) * kSfRows, bar);
+      }
+    }
+  } else if (warp == 1) {
+    const bool one = elect_one();
+    {
+      const uint32_t tok_col = (t0 & 127) >> 5;        // BT = 64: the tile's place in its scale atom
+      uint32_t issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        const uint32_t s = issued % Sh::kStages, ph = (issued / Sh::kStages) & 1;
+        if (!warp_wait(smem_u32(&S->full[s]), ph, limit, expire_main) || warp_aborted(abort_flag)) {
+          if (one && !*abort_flag) record_error(kErrTimeout);
+          *abort_flag = 1;
+          break;
+        }
+        if (one) {
+          const uint32_t w = smem_u32(smem + s * Sh::kStage), t = w + kABytes, sf = t + BT * kBK;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int a = NV ? k : k >> 1;
+            const uint32_t sc = tmem + BT + a * Sh::kSfCols, id = NV ? 0 : (k & 1) * 2;
+            if (NV || (k & 1) == 0) {
+              tc_cp_32x128b_warpx4(sc, make_sf_desc(sf + a * 512));
+#pragma unroll
+              for (int b = 0; b < Sh::kTokBlocks; ++b)
+                tc_cp_32x128b_warpx4(sc + 4 + 4 * b, make_sf_desc(sf + (1 + b) * kSf + a * 512));
+            }
+            tc_mma_fp4<NV>(tmem, make_sw128_desc(w + k * kUmmaK), make_sw128_desc(t + k * kUmmaK),
+                           make_idesc_fp4<NV>(128, BT, id), sc | id << 30, (sc + 4 + tok_col) | id << 30,
+                           (kb > kb0 || k) ? 1u : 0u);
+          }
+          tc_commit(smem_u32(&S->empty[s]));
+        }
+        __syncwarp();
+      }
+      if (one) tc_commit(smem_u32(&S->done));
+      __syncwarp();
+      // after an abort: loads in flight must land before shared memory is reused or released
+      if (*abort_flag) {
+        const uint64_t t1 = globaltimer_ns();
+        while (globaltimer_ns() - t1 < kSettleNs) {
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (!mbar_wait(smem_u32(&S->done), 0, limit, expire != kExpireNone)) {
+    if (lane == 0) record_error(kErrTimeout);
+    *abort_flag = 1;
+    mbar_wait(smem_u32(&S->done), 0, kDrainLimitNs);       // MMAs in flight, whatever the limit was
+  }
+  tc_fence_after();
+  __syncthreads();                           // the MMAs that read the stage buffers are done, in this CTA
+  if (ways > 1) cluster_sync();              // and in every CTA that receives partials
+  const int per_log = 31 - __clz(BT / ways), per = 1 << per_log;   // tokens per owner
+  const uint32_t red = smem_u32(smem);       // [ways][per][128] f32
+#pragma unroll 1
+  for (int c = 0; c < BT; c += 16) {
+    if (t0 + c >= P.M) break;
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
+    tmem_ld_wait();
+    tmem_reg_fence(r);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int t = c + j;
+      if (t0 + t >= P.M) break;
+      const float v = kb1 > kb0 ? __uint_as_float(r[j]) : 0.0f;
+      const uint32_t at = red + ((rank * per + (t & (per - 1))) * 128 + threadIdx.x) * 4;
+      st_cluster_f32(mapa_shared(at, t >> per_log), v);
+    }
+  }
+  tc_fence_before();
+  if (ways > 1) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
+  if (*abort_flag) return;                   // D is incomplete; the error word says so
+  const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
+  const float2* part = reinterpret_cast<const float2*>(smem);
+  const int pair = threadIdx.x & 63, n = n0 + 2 * pair;
+  for (int t = threadIdx.x >> 6; t < per; t += kSplitThreads / 64) {
+    const int m = t0 + rank * per + t;
+    if (m >= P.M || n >= P.N) continue;
+    float2 v = part[t * 64 + pair];
+    for (int s = 1; s < ways; ++s) {
+      const float2 o = part[(s * per + t) * 64 + pair];
+      v.x = __fadd_rn(v.x, o.x);
+      v.y = __fadd_rn(v.y, o.y);
+    }
+    *reinterpret_cast<uint32_t*>(P.D + static_cast<int64_t>(m) * P.N + n) =
+        pack_bf16x2(__fmul_rn(v.x, alpha), __fmul_rn(v.y, alpha));
+  }
 }
 
 }  // namespace gemm

@@ -124,13 +124,15 @@ def test_python_binding_checks_sizes_and_types(lib):
     with pytest.raises(ValueError, match="bfloat16"):
         fp8.fp8_rmsnorm_cast(x.float(), g, 1e-5, y=torch.empty_like(x))
     with pytest.raises(ValueError, match="rstd"):
-        fp8.fp8_rmsnorm_cast(x, g, 1e-5, y=x, rstd=torch.empty(3))
-    with pytest.raises(ValueError, match="rstd"):
-        fp8.fp8_rmsnorm_backward(x, x, g, torch.empty(3), x)
-    with pytest.raises(ValueError, match="dgamma"):
-        fp8.fp8_rmsnorm_backward(x, x, g, torch.empty(4), x, dgamma=torch.empty(63))
+        fp8._f32(torch.empty(3), 4, "rstd")
+    with pytest.raises(ValueError, match="sf"):
+        fp8._codes(torch.empty(511, dtype=torch.uint8), 512, "sf")
+    with pytest.raises(ValueError, match="sf"):
+        fp8._codes(torch.empty(512), 512, "sf")
+    with pytest.raises(ValueError, match="bfloat16"):
+        fp8.fp8_rmsnorm_backward(x.float(), x, g, torch.empty(4), x)
     with pytest.raises(ValueError, match="matrix"):
         fp8.fp4_cast_multi([dict(x=x[0], quant=fp8.Q_MXFP4)])
-    with pytest.raises(ValueError, match="codes"):
+    with pytest.raises(ValueError, match="one K"):
         fp8.fp4_gemm_multi([dict(A=torch.zeros(1, 16, dtype=torch.uint8), a_sf=None,
                                  B=torch.zeros(8, 32, dtype=torch.uint8), b_sf=None, quant=fp8.Q_MXFP4, D=None)])
