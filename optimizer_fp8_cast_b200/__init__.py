@@ -7,6 +7,7 @@ status. Every step of the path runs in the library's kernels; there is no CPU or
 fallback, and a missing library is an error.
 """
 import ctypes as C
+import importlib.util
 import os
 
 import torch
@@ -34,6 +35,7 @@ Q_NONE, Q_FP8, Q_MXFP8, Q_MXFP4, Q_NVFP4 = 0, 1, 2, 3, 4
 FP8_MAX = {E4M3: 448.0, E5M2: 57344.0}
 FP4_MAX = 448.0 * 6.0        # NVFP4's largest scale times its largest value (fp8_max of its scale update)
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8train.so")
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 
 
 class Fp8TrainError(RuntimeError):
@@ -265,151 +267,44 @@ def fp4_scale_bytes(mn, k, quant):
     return int(load().fp4_scale_bytes(int(mn), int(k), int(quant)))
 
 
-# The checks of the norm and 4-bit calls: what the C side cannot see (types, sizes, device). They return
-# the address, and are kept short because a one-token call is bound by the host.
-def _dev(t, what):
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{what}: must be a CUDA tensor on the current device")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: must be contiguous")
-    return t.data_ptr()
-
-
-def _bf16(t, shape, what):
-    """A BF16 tensor of the given shape (or None)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.bfloat16 or t.shape != shape:
-        raise ValueError(f"{what}: must be bfloat16 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return _dev(t, what)
-
-
-def _f32(t, n, what):
-    """A float32 tensor of at least n elements (or None)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or t.numel() < n:
-        raise ValueError(f"{what}: must be float32 with at least {n} elements")
-    return _dev(t, what)
-
-
-def _codes(t, n, what):
-    """A uint8 tensor of at least n bytes (or None)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.uint8 or t.numel() < n:
-        raise ValueError(f"{what}: must be uint8 with at least {n} elements")
-    return _dev(t, what)
-
-
-def _fp4_scale_bytes(mn, k, quant):
-    return (mn + 127) // 128 * ((k + 255) // 256) * (1024 if quant == Q_MXFP4 else 2048)
-
-
-def _current_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-
-
-def fp4_cast_multi(casts, stream=None):
-    """4-bit quantisation. ``casts``: dicts with x (BF16 [rows, cols]), quant (Q_MXFP4 or Q_NVFP4), q_row
-    (uint8 [rows, cols / 2]) / sf_row and / or q_col (uint8 [cols, rows / 2]: transposed) / sf_col, scales
-    uint8 tensors of fp4_scale_bytes; for NVFP4 also scale (float32 [1]) and optionally amax
-    (max-accumulated) and scale_inv."""
-    arr = (_abi.Fp4CastTensor * len(casts))()
-    for i, c in enumerate(casts):
-        x, quant, get = c["x"], c["quant"], c.get
-        if x.dim() != 2:
-            raise ValueError("x: must be a matrix")
-        rows, cols = x.shape
-        q_row, q_col, n = get("q_row"), get("q_col"), rows * cols // 2
-        arr[i] = (_bf16(x, x.shape, "x"), rows, cols, quant, _f32(get("scale"), 1, "scale"),
-                  _codes(q_row, n, "q_row"),
-                  _codes(get("sf_row"), 0 if q_row is None else _fp4_scale_bytes(rows, cols, quant), "sf_row"),
-                  _codes(q_col, n, "q_col"),
-                  _codes(get("sf_col"), 0 if q_col is None else _fp4_scale_bytes(cols, rows, quant), "sf_col"),
-                  _f32(get("amax"), 1, "amax"), _f32(get("scale_inv"), 1, "scale_inv"))
-    status = load().fp4_cast_multi(arr, len(casts), _current_stream(stream))
-    if status:
-        _check(status, "fp4_cast_multi")
-
-
-def fp4_gemm_multi(gemms, stream=None):
-    """4-bit block-scaled GEMMs: dicts with A (uint8 [M, K / 2]), a_sf, B (uint8 [N, K / 2]), b_sf, quant,
-    D (BF16 [M, N]) and optionally a_scale_inv, b_scale_inv (float32 [1]); D = bf16(A . B^T) with the
-    operands' block scales, times the scale inverses."""
-    arr = (_abi.Fp4GemmDesc * len(gemms))()
-    for i, g in enumerate(gemms):
-        A, B, quant, get = g["A"], g["B"], g["quant"], g.get
-        (M, K2), (N, K2b) = A.shape, B.shape
-        if K2 != K2b:
-            raise ValueError("A and B: must be codes [M, K / 2] and [N, K / 2] of one K")
-        D = g["D"]
-        if D.dim() != 2 or D.shape[0] != M or D.shape[1] != N:
-            raise ValueError("D: must be [M, N]")
-        arr[i] = (_codes(A, 0, "A"), _codes(g["a_sf"], _fp4_scale_bytes(M, 2 * K2, quant), "a_sf"),
-                  _codes(B, 0, "B"), _codes(g["b_sf"], _fp4_scale_bytes(N, 2 * K2, quant), "b_sf"),
-                  quant, M, N, 2 * K2, _f32(get("a_scale_inv"), 1, "a_scale_inv"),
-                  _f32(get("b_scale_inv"), 1, "b_scale_inv"), _bf16(D, D.shape, "D"))
-    status = load().fp4_gemm_multi(arr, len(gemms), _current_stream(stream))
-    if status:
-        _check(status, "fp4_gemm_multi")
-
-
-def fp8_rmsnorm_cast(x, gamma, eps, *, residual=None, h=None, rstd=None, y=None, quant=Q_NONE, fmt=E4M3,
-                     q=None, sf=None, scale=None, amax=None, scale_inv=None, stream=None):
-    """h = bf16(x + residual); y = h / sqrt(mean(h^2) + eps) * gamma for each row of x (BF16 [rows, cols]).
-
-    Writes h (BF16, with a residual; may be x or residual), rstd (float32 [rows], for the backward pass), y
-    (BF16) and, as ``quant`` says, y's codes ``q`` (uint8): Q_FP8 with scale, amax (max-accumulated) and
-    scale_inv (float32 [1] each), Q_MXFP8 / Q_MXFP4 / Q_NVFP4 with ``sf`` (uint8 scale atoms along the
-    rows), Q_NVFP4 also with scale and optionally amax and scale_inv."""
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError("x: must be a matrix")
-    rows, cols = shape
-    four = quant == Q_MXFP4 or quant == Q_NVFP4
-    sf_bytes = 0
-    if sf is not None:
-        sf_bytes = _fp4_scale_bytes(rows, cols, quant) if four else (rows + 127) // 128 * ((cols + 127) // 128) * 512
-    d = _abi.RmsNorm(_bf16(x, shape, "x"), _bf16(residual, shape, "residual"), _bf16(gamma, shape[1:], "gamma"),
-                     rows, cols, eps, _bf16(h, shape, "h"), _f32(rstd, rows, "rstd"), _bf16(y, shape, "y"),
-                     quant, fmt, _codes(q, rows * cols // 2 if four else rows * cols, "q"),
-                     _codes(sf, sf_bytes, "sf"), _f32(scale, 1, "scale"), _f32(amax, 1, "amax"),
-                     _f32(scale_inv, 1, "scale_inv"))
-    status = load().fp8_rmsnorm_cast(d, _current_stream(stream))
-    if status:
-        _check(status, "fp8_rmsnorm_cast")
-
-
 def fp8_rmsnorm_backward_workspace_bytes(rows, cols):
+    """Scratch bytes of fp8_rmsnorm_backward (0 on invalid input)."""
     return int(load().fp8_rmsnorm_backward_workspace_bytes(int(rows), int(cols)))
 
 
-def fp8_rmsnorm_backward(dy, h, gamma, rstd, dh, *, dres=None, dgamma=None, dgamma_bf16=None,
-                         workspace=None, stream=None):
-    """Gradients of fp8_rmsnorm_cast: ``dh`` (BF16 [rows, cols]; may be dy or dres) from dy and the forward
-    pass's h and rstd, with dres added where given; ``dgamma`` (float32 [cols]) and / or ``dgamma_bf16``.
+def _workspace(n, like, stream):
+    t = torch.empty(n, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)      # freed when the call returns, read by kernels of that stream
+    return t
 
-    ``workspace`` is a uint8 CUDA tensor of at least ``fp8_rmsnorm_backward_workspace_bytes`` bytes."""
-    shape = dy.shape
-    if len(shape) != 2:
-        raise ValueError("dy: must be a matrix")
-    rows, cols = shape
-    if workspace is None and (dgamma is not None or dgamma_bf16 is not None):
-        workspace = torch.empty(load().fp8_rmsnorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
-                                device=dy.device)
-        if stream is not None:
-            workspace.record_stream(stream)      # freed on return, read by kernels of that stream
-    d = _abi.RmsNormGrad(_bf16(dy, shape, "dy"), _bf16(h, shape, "h"), _bf16(gamma, shape[1:], "gamma"),
-                         _f32(rstd, rows, "rstd"), _bf16(dres, shape, "dres"), rows, cols,
-                         _bf16(dh, shape, "dh"), _f32(dgamma, cols, "dgamma"),
-                         _bf16(dgamma_bf16, shape[1:], "dgamma_bf16"))
-    ws = _codes(workspace, 0, "workspace")
-    status = load().fp8_rmsnorm_backward(d, ws, 0 if ws is None else workspace.numel(), _current_stream(stream))
-    if status:
-        _check(status, "fp8_rmsnorm_backward")
+
+def _load_binding():
+    """The calls of csrc/binding.cpp (norm and 4-bit entry points), with the library's addresses."""
+    spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+    if spec is None or not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is not built: run `python -c \"import __graft_entry__ as g; g.build()\"` "
+                           "or `python -m optimizer_fp8_cast_b200.build`")
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    lib = load()
+    m.bind(*(C.cast(getattr(lib, f), C.c_void_p).value for f in
+             ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes", "fp4_cast_multi",
+              "fp4_gemm_multi", "fp4_scale_bytes")), _check, _workspace)
+    return m
+
+
+_BOUND = ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp4_cast_multi", "fp4_gemm_multi")
+
+
+def __getattr__(name):
+    # the calls of the compiled binding, loaded at their first use
+    if name in _BOUND:
+        m = _load_binding()
+        for f in _BOUND:
+            globals()[f] = getattr(m, f)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def fp8_scale_update(amax, history, fp8_max, algo, margin, scale, scale_inv, stream=None):

@@ -1,4 +1,5 @@
-"""Build libfp8train.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build libfp8train.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and _binding.so (the
+Python binding of the calls whose host time matters, csrc/binding.cpp) with the host compiler.
 
     python -m optimizer_fp8_cast_b200.build [--verbose-ptxas]
 
@@ -15,6 +16,9 @@ SRC_DIR = os.path.join(HERE, "csrc")
 MAIN = os.path.join(SRC_DIR, "fp8train.cu")
 HEADER = os.path.join(ROOT, "include", "fp8train.h")
 LIB = os.path.join(HERE, "libfp8train.so")
+BINDING_SRC = os.path.join(SRC_DIR, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
@@ -26,6 +30,29 @@ def _sources():
     return out
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the extension against the installed torch's headers (it is loaded after torch, whose
+    libraries give its symbols)."""
+    if not force and os.path.exists(BINDING) and \
+            os.path.getmtime(BINDING) >= max(os.path.getmtime(BINDING_SRC), os.path.getmtime(HEADER)):
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                    "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                    "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+                    "-isystem", os.path.join(base, "include"),
+                    "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                    "-isystem", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+                    BINDING_SRC, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch",
+                    "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -34,6 +61,7 @@ def needs_build() -> bool:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_binding(force)
     if not force and not needs_build():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()

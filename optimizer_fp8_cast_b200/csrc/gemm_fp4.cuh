@@ -112,7 +112,7 @@ struct Smem4 {
 template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     k_fp4_gemm(const __grid_constant__ Group g) {
-  constexpr int kAtoms = NV ? 4 : 2, kSf = kSfBytes4<NV>, kSfRows = NV ? 2 : 1;
+  constexpr int kSf = kSfBytes4<NV>, kSfRows = NV ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   // stage s: [A 128 x 128 B][B 128 x 128 B][scales of A | B rows 0..127 | B rows 128..255]

@@ -297,3 +297,27 @@ def test_training_step_products(cuda_lib, kind, T, fin, fout):
             R, ab = reference(a, b, 1.0)
             assert gemm_within_tolerance(bf16_bits(D), R, ab).all()
     cuda_lib.fp8t_check_device_error()
+
+
+def test_refusals_raise_and_launch_nothing(cuda_lib):
+    """A status of the library becomes an Fp8TrainError; wrong devices and layouts a ValueError."""
+    A, sa, _ = operand(16, 64, bq.MXFP4, 1)
+    D = torch.full((16, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    ok = dict(A=A, a_sf=sa, B=A, b_sf=sa, quant=bq.MXFP4, D=D)
+    for bad in ([], [dict(ok, quant=2)], [ok, dict(ok, quant=0)]):
+        with pytest.raises(cuda_lib.Fp8TrainError, match="INVALID_ARG"):
+            cuda_lib.fp4_gemm_multi(bad)
+    with pytest.raises(ValueError, match="a_sf"):
+        cuda_lib.fp4_gemm_multi([dict(ok, a_sf=sa[:-1])])
+    with pytest.raises(ValueError, match="a_sf"):
+        cuda_lib.fp4_gemm_multi([dict(ok, a_sf=sa.cpu())])
+    with pytest.raises(ValueError, match="D"):
+        cuda_lib.fp4_gemm_multi([dict(ok, D=D.t()[:, :8])])
+    with pytest.raises(ValueError, match="contiguous"):
+        cuda_lib.fp4_gemm_multi([dict(ok, D=D.t())])
+    with pytest.raises(cuda_lib.Fp8TrainError, match="INVALID_ARG"):          # a required operand missing
+        cuda_lib.fp4_gemm_multi([dict(ok, D=None)])
+    with pytest.raises(cuda_lib.Fp8TrainError, match="MISALIGNED"):
+        cuda_lib.fp4_gemm_multi([dict(ok, a_sf=torch.cat([sa, sa])[4:])])
+    torch.cuda.synchronize()
+    assert (D == 7).all()

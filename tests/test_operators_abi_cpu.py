@@ -116,23 +116,42 @@ def test_rmsnorm_backward_refusals(lib):
 
 
 def test_python_binding_checks_sizes_and_types(lib):
-    """The binding refuses what the C side cannot see: too small outputs, wrong types, CPU tensors."""
+    """The binding refuses what the C side cannot see: wrong types and shapes, CPU tensors, unknown names."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     g = torch.ones(64, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="CUDA"):
+    u = torch.zeros(1, 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x: must be a CUDA tensor"):
         fp8.fp8_rmsnorm_cast(x, g, 1e-5, y=torch.empty_like(x))
-    with pytest.raises(ValueError, match="bfloat16"):
+    with pytest.raises(ValueError, match="x: must be a bfloat16 matrix"):
         fp8.fp8_rmsnorm_cast(x.float(), g, 1e-5, y=torch.empty_like(x))
-    with pytest.raises(ValueError, match="rstd"):
-        fp8._f32(torch.empty(3), 4, "rstd")
-    with pytest.raises(ValueError, match="sf"):
-        fp8._codes(torch.empty(511, dtype=torch.uint8), 512, "sf")
-    with pytest.raises(ValueError, match="sf"):
-        fp8._codes(torch.empty(512), 512, "sf")
-    with pytest.raises(ValueError, match="bfloat16"):
+    with pytest.raises(ValueError, match="x: must be a matrix"):
+        fp8.fp8_rmsnorm_cast(g, g, 1e-5, y=g)
+    with pytest.raises(TypeError, match="unexpected argument 'bias'"):
+        fp8.fp8_rmsnorm_cast(x, g, 1e-5, bias=x)
+    with pytest.raises(TypeError, match="two values for argument 'eps'"):
+        fp8.fp8_rmsnorm_cast(x, g, 1e-5, eps=1e-5)
+    with pytest.raises(TypeError, match="missing argument 'gamma'"):
+        fp8.fp8_rmsnorm_cast(x)
+    with pytest.raises(TypeError, match="at most 3 positional"):
+        fp8.fp8_rmsnorm_cast(x, g, 1e-5, x)
+    with pytest.raises(TypeError, match="x: must be a tensor"):
+        fp8.fp8_rmsnorm_cast(3, g, 1e-5)
+    with pytest.raises(ValueError, match="dy: must be a bfloat16"):
         fp8.fp8_rmsnorm_backward(x.float(), x, g, torch.empty(4), x)
+    with pytest.raises(TypeError, match="missing argument"):
+        fp8.fp8_rmsnorm_backward(x, x, g, torch.empty(4))
     with pytest.raises(ValueError, match="matrix"):
         fp8.fp4_cast_multi([dict(x=x[0], quant=fp8.Q_MXFP4)])
+    with pytest.raises(TypeError, match="list of dicts"):
+        fp8.fp4_cast_multi([x])
+    with pytest.raises(TypeError, match="list of dicts"):
+        fp8.fp4_gemm_multi(dict(A=u))
     with pytest.raises(ValueError, match="one K"):
-        fp8.fp4_gemm_multi([dict(A=torch.zeros(1, 16, dtype=torch.uint8), a_sf=None,
-                                 B=torch.zeros(8, 32, dtype=torch.uint8), b_sf=None, quant=fp8.Q_MXFP4, D=None)])
+        fp8.fp4_gemm_multi([dict(A=u, a_sf=None, B=torch.zeros(8, 32, dtype=torch.uint8), b_sf=None,
+                                 quant=fp8.Q_MXFP4, D=None)])
+
+
+def test_binding_documents_its_calls(lib):
+    for f in (fp8.fp8_rmsnorm_cast, fp8.fp8_rmsnorm_backward, fp8.fp4_cast_multi, fp8.fp4_gemm_multi):
+        assert f.__doc__ and f.__text_signature__
+    assert all(hasattr(fp8, n) for n in fp8.__all__)
