@@ -75,10 +75,9 @@ cudaError_t allow_fp4_split_smem() {
   if ((e = allow_fp4_split_smem_of<false, 16>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 16>()) != cudaSuccess ||
       (e = allow_fp4_split_smem_of<false, 32>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 32>()) != cudaSuccess ||
       (e = allow_fp4_split_smem_of<false, 64>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 64>()) != cudaSuccess ||
-      (e = allow_fp4_split_smem_of<false, 128>()) != cudaSuccess || (e = allow_fp4_split_smem_of<true, 128>()) != cudaSuccess ||
-      (e = allow_fp4_split_smem_of<false, 256>()) != cudaSuccess)
+      (e = allow_fp4_split_smem_of<false, 128>()) != cudaSuccess)
     return e;
-  return allow_fp4_split_smem_of<true, 256>();
+  return allow_fp4_split_smem_of<true, 128>();
 }
 
 // Current device must be compute capability 10.0 (sm_100a code runs there only).
@@ -1215,12 +1214,11 @@ SplitPlan plan_fp4_split(const fp8t_fp4_gemm_desc* gemms, int32_t n, int sms) {
     kbs = std::max(kbs, (gemms[i].K + 255) / 256);
   }
   SplitPlan p;
-  p.bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  p.bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   p.tiles = 0;
-  for (int32_t i = 0; i < n; ++i) p.tiles += (gemms[i].N + 127) / 128 * ((gemms[i].M + p.bt - 1) / p.bt);
-  const int64_t slots = p.bt == 256 ? sms : 2 * sms;
+  for (int32_t i = 0; i < n; ++i) p.tiles += (gemms[i].N + 127) / 128;
   p.ways = 1;
-  while (p.ways < 8 && p.tiles * p.ways * 2 <= slots && p.ways * 2 <= kbs) p.ways *= 2;
+  while (p.ways < 8 && p.tiles * p.ways * 2 <= 2 * sms && p.ways * 2 <= kbs) p.ways *= 2;
   return p;
 }
 
@@ -1244,9 +1242,8 @@ fp8t_status fp4_gemm_split(const fp8t_fp4_gemm_desc* gemms, int32_t n, const Spl
     P.M = static_cast<int32_t>(d.M);
     P.N = static_cast<int32_t>(d.N);
     P.num_kb = static_cast<int32_t>((d.K + 255) / 256);
-    P.tiles_t = static_cast<int32_t>((d.M + plan.bt - 1) / plan.bt);
     P.tile_start = static_cast<int32_t>(tiles);
-    tiles += (d.N + 127) / 128 * P.tiles_t;
+    tiles += (d.N + 127) / 128;
   }
   cudaError_t e = cudaErrorInvalidValue;
   switch (plan.bt) {
@@ -1254,7 +1251,6 @@ fp8t_status fp4_gemm_split(const fp8t_fp4_gemm_desc* gemms, int32_t n, const Spl
     case 32: e = nv ? launch_fp4_split<true, 32>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 32>(group, tiles, plan.ways, stream); break;
     case 64: e = nv ? launch_fp4_split<true, 64>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 64>(group, tiles, plan.ways, stream); break;
     case 128: e = nv ? launch_fp4_split<true, 128>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 128>(group, tiles, plan.ways, stream); break;
-    case 256: e = nv ? launch_fp4_split<true, 256>(group, tiles, plan.ways, stream) : launch_fp4_split<false, 256>(group, tiles, plan.ways, stream); break;
   }
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
@@ -1290,18 +1286,17 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
   if (st != FP8T_OK) return st;
+  // consecutive problems of one format and size class share a launch: at most 128 rows (the split kernel) or
+  // more (256 x 256 tiles)
   for (int32_t b0 = 0, b1 = 0; b0 < n_gemms; b0 = b1) {
-    // consecutive problems of one format; together they fill the pairs with 256 x 256 tiles or they do not
-    int64_t tiles = 0;
-    for (b1 = b0; b1 < n_gemms && b1 - b0 < fp8t::gemm::kMaxProblems && gemms[b1].quant == gemms[b0].quant; ++b1)
-      tiles += (gemms[b1].M + fp8t::gemm::kBM - 1) / fp8t::gemm::kBM * ((gemms[b1].N + fp8t::gemm::kBN - 1) / fp8t::gemm::kBN);
-    if (tiles < dev->gemm_fp4_clusters) {
-      b1 = std::min(b1, b0 + fp8t::gemm::kMaxSplitProblems);
-      const SplitPlan plan = plan_fp4_split(gemms + b0, b1 - b0, dev->sms);
-      if ((st = fp4_gemm_split(gemms + b0, b1 - b0, plan, as_stream(stream))) != FP8T_OK) return st;
-    } else if ((st = fp4_gemm_wide(gemms + b0, b1 - b0, dev, as_stream(stream))) != FP8T_OK) {
-      return st;
+    const bool few = gemms[b0].M <= fp8t::gemm::kMaxSplitRows;
+    const int most = few ? fp8t::gemm::kMaxSplitProblems : fp8t::gemm::kMaxProblems;
+    for (b1 = b0; b1 < n_gemms && b1 - b0 < most && gemms[b1].quant == gemms[b0].quant &&
+                  (gemms[b1].M <= fp8t::gemm::kMaxSplitRows) == few; ++b1) {
     }
+    st = few ? fp4_gemm_split(gemms + b0, b1 - b0, plan_fp4_split(gemms + b0, b1 - b0, dev->sms), as_stream(stream))
+             : fp4_gemm_wide(gemms + b0, b1 - b0, dev, as_stream(stream));
+    if (st != FP8T_OK) return st;
   }
   return FP8T_OK;
 }

@@ -340,24 +340,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
 }
 
 // ---------------------------------------------------------------- few rows: K split over a cluster
-// A product with few output tiles leaves most SMs idle under 256 x 384 tiles (one token of a 4096-wide
-// layer: 11 tiles for 74 pairs), and with few tokens its time is that of streaming B (the weights). Here
-// the weights are the 128-row operand of a one-CTA MMA and BT tokens the other, so a tile is 128 rows of
-// B by BT rows of A, and the S CTAs of a cluster each take a contiguous part of K. Every CTA leaves its FP32
+// A product of at most 128 rows (tokens) leaves most SMs idle under 256 x 256 tiles (a 4096-wide layer: 16
+// tiles for 74 pairs), and its time is that of streaming B (the weights). Here the weights are the 128-row
+// operand of a one-CTA MMA and the BT tokens the other, so a tile is 128 rows of B by all rows of A, and
+// the S CTAs of a cluster each take a contiguous part of K. Every CTA leaves its FP32
 // partial tile in the shared memory of the CTAs that own its tokens (token t belongs to rank t / (BT / S));
 // after a cluster barrier each owner adds the S partials in rank order, scales, rounds and stores its
 // tokens' rows of D, 128 columns of a row at a time. No workspace, and the order of additions is fixed.
 // TMEM: accumulator (weight rows x tokens) in columns 0..BT-1, then the scales.
 constexpr int kSplitThreads = 128;
 constexpr int kMaxSplitProblems = 4;
+constexpr int64_t kMaxSplitRows = 128;
 template <bool NV, int BT>
 struct SplitShape {
   static constexpr int kSf = (NV ? 4 : 2) * 512;                 // scale bytes per 128 rows and k-block
-  static constexpr int kTokBlocks = BT > 128 ? 2 : 1;
-  static constexpr int kStage = kABytes + BT * kBK + kSf * (1 + kTokBlocks);
-  static constexpr int kStages = BT <= 64 ? 4 : BT == 128 ? 3 : 4;
-  static constexpr int kSfCols = 4 + 4 * kTokBlocks;              // TMEM columns per atom step along K
-  static constexpr int kTmem = BT <= 32 ? 64 : BT == 64 ? 128 : BT == 128 ? 256 : 512;
+  static constexpr int kStage = kABytes + BT * kBK + 2 * kSf;
+  static constexpr int kStages = BT <= 64 ? 4 : 3;                // two CTAs per SM
+  static constexpr int kSfCols = 8;                               // TMEM columns per atom step along K
+  static constexpr int kTmem = BT <= 32 ? 64 : 2 * BT;
   static constexpr int kSmem = kStages * kStage + 1024 + 256;
   static_assert(BT + (NV ? 4 : 2) * kSfCols <= kTmem, "TMEM columns");
   static_assert(128 * BT * 4 <= kStages * kStage, "the partial tiles fit the stage buffers");
@@ -370,7 +370,7 @@ struct alignas(64) SplitProblem {
   const float* sa;
   const float* sb;
   uint16_t* D;
-  int32_t M, N, num_kb, tiles_t, tile_start;
+  int32_t M, N, num_kb, tile_start;
 };
 struct alignas(64) SplitGroup {
   SplitProblem p[kMaxSplitProblems];
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   int pi = 0;
   while (pi + 1 < g.n && g.p[pi + 1].tile_start <= tile) ++pi;
   const SplitProblem& P = g.p[pi];
-  const int n0 = (tile - P.tile_start) / P.tiles_t * 128, t0 = (tile - P.tile_start) % P.tiles_t * BT;
+  const int n0 = (tile - P.tile_start) * 128;
   // this CTA's k-blocks; a problem with fewer than the cluster's CTAs leaves some of them none
   const int kb0 = static_cast<int>(static_cast<int64_t>(P.num_kb) * rank / ways);
   const int kb1 = static_cast<int>(static_cast<int64_t>(P.num_kb) * (rank + 1) / ways);
@@ -455,18 +455,15 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
         const uint32_t t = w + kABytes, sf = t + BT * kBK;
         mbar_arrive_expect_tx(bar, Sh::kStage);
         tma_load_2d(w, &P.w, kb * kBK, n0, bar);
-        tma_load_2d(t, &P.t, kb * kBK, t0, bar);
+        tma_load_2d(t, &P.t, kb * kBK, 0, bar);
         tma_load_2d(sf, &P.sfw, 0, ((n0 >> 7) * P.num_kb + kb) * kSfRows, bar);
-#pragma unroll
-        for (int b = 0; b < Sh::kTokBlocks; ++b)
-          tma_load_2d(sf + (1 + b) * kSf, &P.sft, 0, (((t0 >> 7) + b) * P.num_kb + kb) * kSfRows, bar);
+        tma_load_2d(sf + kSf, &P.sft, 0, kb * kSfRows, bar);
       }
     }
   } else if (warp == 1) {
     const bool one = elect_one();
+    uint32_t issued = 0;
     {
-      const uint32_t tok_col = (t0 & 127) >> 5;        // BT = 64: the tile's place in its scale atom
-      uint32_t issued = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++issued) {
         const uint32_t s = issued % Sh::kStages, ph = (issued / Sh::kStages) & 1;
         if (!warp_wait(smem_u32(&S->full[s]), ph, limit, expire_main) || warp_aborted(abort_flag)) {
@@ -482,12 +479,10 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
             const uint32_t sc = tmem + BT + a * Sh::kSfCols, id = NV ? 0 : (k & 1) * 2;
             if (NV || (k & 1) == 0) {
               tc_cp_32x128b_warpx4(sc, make_sf_desc(sf + a * 512));
-#pragma unroll
-              for (int b = 0; b < Sh::kTokBlocks; ++b)
-                tc_cp_32x128b_warpx4(sc + 4 + 4 * b, make_sf_desc(sf + (1 + b) * kSf + a * 512));
+              tc_cp_32x128b_warpx4(sc + 4, make_sf_desc(sf + kSf + a * 512));
             }
             tc_mma_fp4<NV>(tmem, make_sw128_desc(w + k * kUmmaK), make_sw128_desc(t + k * kUmmaK),
-                           make_idesc_fp4<NV>(128, BT, id), sc | id << 30, (sc + 4 + tok_col) | id << 30,
+                           make_idesc_fp4<NV>(128, BT, id), sc | id << 30, (sc + 4) | id << 30,
                            (kb > kb0 || k) ? 1u : 0u);
           }
           tc_commit(smem_u32(&S->empty[s]));
@@ -517,7 +512,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   const uint32_t red = smem_u32(smem);       // [ways][per][128] f32
 #pragma unroll 1
   for (int c = 0; c < BT; c += 16) {
-    if (t0 + c >= P.M) break;
+    if (c >= P.M) break;
     uint32_t r[16];
     tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
     tmem_ld_wait();
@@ -525,7 +520,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int t = c + j;
-      if (t0 + t >= P.M) break;
+      if (t >= P.M) break;
       const float v = kb1 > kb0 ? __uint_as_float(r[j]) : 0.0f;
       const uint32_t at = red + ((rank * per + (t & (per - 1))) * 128 + threadIdx.x) * 4;
       st_cluster_f32(mapa_shared(at, t >> per_log), v);
@@ -541,7 +536,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   const float2* part = reinterpret_cast<const float2*>(smem);
   const int pair = threadIdx.x & 63, n = n0 + 2 * pair;
   for (int t = threadIdx.x >> 6; t < per; t += kSplitThreads / 64) {
-    const int m = t0 + rank * per + t;
+    const int m = rank * per + t;
     if (m >= P.M || n >= P.N) continue;
     float2 v = part[t * 64 + pair];
     for (int s = 1; s < ways; ++s) {
