@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <string>
 #include <utility>
@@ -179,6 +180,9 @@ fp8t_status current_device(DeviceInfo** out) {
         e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  fp8t::fp4::kCastSmemBytes);
       if (e == cudaSuccess) e = allow_fp4_split_smem();
+      for (auto* k : {fp8t::norm::k_rmsnorm_backward<1>, fp8t::norm::k_rmsnorm_backward<2>, fp8t::norm::k_rmsnorm_backward<4>})
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::norm::kBwdMaxSmem);
       if (e != cudaSuccess) {
         d.state = 0;
         return fail(FP8T_ERR_CUDA, "cudaFuncSetAttribute(4-bit): %s", cudaGetErrorString(e));
@@ -1306,14 +1310,14 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
 
 namespace {
 
-// Threads and vectors per thread of a norm launch. Rows of up to 1024 columns take a warp each, four to a
-// CTA. Wider rows take a CTA: four vectors per thread when there are rows enough to fill the GPU (few
-// threads per row: cheap sums, many rows in flight), else the fewest vectors that 512 threads hold.
+// Threads and vectors per thread of a forward launch. Rows of up to 1024 columns take a warp each, four to a
+// CTA. Wider rows take a CTA: with rows enough to fill the GPU, the vectors per thread that leave few threads
+// to sum over; else the fewest that 512 threads hold.
 struct NormShape {
   bool warp_row;
   int vpt, threads;
 };
-NormShape norm_shape(int64_t rows, int64_t cols, bool spread) {
+NormShape norm_shape(int64_t rows, int64_t cols) {
   using namespace fp8t::norm;
   const int nvec = static_cast<int>(cols / 8);
   NormShape s;
@@ -1323,38 +1327,63 @@ NormShape norm_shape(int64_t rows, int64_t cols, bool spread) {
     s.threads = 32 * kRowsPerCta;
     return s;
   }
-  s.vpt = 4;
-  if (spread && rows <= 148) s.vpt = nvec <= kMaxThreads ? 1 : nvec <= 2 * kMaxThreads ? 2 : 4;
+  const int fewest = nvec <= kMaxThreads ? 1 : nvec <= 2 * kMaxThreads ? 2 : 4;
+  s.vpt = rows <= 148 ? fewest : std::max(2, fewest);
   s.threads = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
   return s;
 }
 
-// CTAs of the backward pass (partial dgamma rows): four 128-thread CTAs per SM, fewer of wider ones.
-int64_t norm_backward_ctas(int64_t rows, int64_t cols) {
+// Backward: vectors per thread, threads per row group, groups per CTA, CTAs (at most one per SM, fewer when
+// there are fewer rows; groups only as far as rows fill them).
+struct NormBwdShape {
+  int vpt, group, groups;
+  int64_t ctas;
+};
+NormBwdShape norm_backward_shape(int64_t rows, int64_t cols) {
   using namespace fp8t::norm;
-  const NormShape s = norm_shape(rows, cols, false);
-  const int64_t per_cta = s.warp_row ? kRowsPerCta : 1;
-  return std::min<int64_t>((rows + per_cta - 1) / per_cta, 148 * std::max(1, 512 / s.threads));
+  const int nvec = static_cast<int>(cols / 8);
+  NormBwdShape s;
+  s.vpt = nvec <= 32 ? 1 : nvec <= kBwdThreads ? 2 : 4;     // two row groups or more while two vectors do
+  s.group = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+  const int most = std::min(kBwdThreads / s.group, s.group == 32 ? 16 : 15);      // barrier ids 1..15
+  s.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (rows + kBwdCtas - 1) / kBwdCtas)));
+  s.ctas = std::min<int64_t>(kBwdCtas, (rows + s.groups - 1) / s.groups);
+  return s;
 }
 
 bool norm_cols_ok(int64_t rows, int64_t cols, int64_t multiple) {
   return cols % multiple == 0 && cols <= fp8t::norm::kMaxCols && rows < (int64_t(1) << 31);
 }
 
+// Persistent grid: as many CTAs as are resident at once (looked up once per kernel and size).
+template <int VPT, bool WARP_ROW, int Q>
+void launch_norm_as(const fp8t::norm::Fwd& p, int threads, int sms, cudaStream_t stream) {
+  using namespace fp8t::norm;
+  static std::atomic<int> resident[kMaxThreads / 32 + 1];
+  int n = resident[threads / 32].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_rmsnorm_cast<VPT, WARP_ROW, Q>, threads, 0) != cudaSuccess ||
+        n < 1) {
+      (void)cudaGetLastError();
+      n = 1;
+    }
+    resident[threads / 32].store(n, std::memory_order_relaxed);
+  }
+  const int64_t per_cta = WARP_ROW ? kRowsPerCta : 1;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.rows + per_cta - 1) / per_cta, static_cast<int64_t>(sms) * n));
+  k_rmsnorm_cast<VPT, WARP_ROW, Q><<<grid, threads, 0, stream>>>(p);
+}
+
 template <int Q>
 void launch_norm(const fp8t::norm::Fwd& p, const NormShape& s, int sms, cudaStream_t stream) {
-  using namespace fp8t::norm;
-  const int64_t per_cta = s.warp_row ? kRowsPerCta : 1;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(
-      (p.rows + per_cta - 1) / per_cta, static_cast<int64_t>(sms) * std::max(1, 1024 / s.threads)));
   if (s.warp_row) {
-    if (s.vpt == 1)      k_rmsnorm_cast<1, true, Q><<<grid, s.threads, 0, stream>>>(p);
-    else if (s.vpt == 2) k_rmsnorm_cast<2, true, Q><<<grid, s.threads, 0, stream>>>(p);
-    else                 k_rmsnorm_cast<4, true, Q><<<grid, s.threads, 0, stream>>>(p);
+    if (s.vpt == 1)      launch_norm_as<1, true, Q>(p, s.threads, sms, stream);
+    else if (s.vpt == 2) launch_norm_as<2, true, Q>(p, s.threads, sms, stream);
+    else                 launch_norm_as<4, true, Q>(p, s.threads, sms, stream);
   } else {
-    if (s.vpt == 1)      k_rmsnorm_cast<1, false, Q><<<grid, s.threads, 0, stream>>>(p);
-    else if (s.vpt == 2) k_rmsnorm_cast<2, false, Q><<<grid, s.threads, 0, stream>>>(p);
-    else                 k_rmsnorm_cast<4, false, Q><<<grid, s.threads, 0, stream>>>(p);
+    if (s.vpt == 1)      launch_norm_as<1, false, Q>(p, s.threads, sms, stream);
+    else if (s.vpt == 2) launch_norm_as<2, false, Q>(p, s.threads, sms, stream);
+    else                 launch_norm_as<4, false, Q>(p, s.threads, sms, stream);
   }
 }
 
@@ -1411,7 +1440,7 @@ fp8t_status fp8_rmsnorm_cast(const fp8t_rmsnorm* desc, void* stream) {
   p.cols = static_cast<int32_t>(d.cols);
   p.fmt = d.fmt;
   p.eps = d.eps;
-  const NormShape s = norm_shape(d.rows, d.cols, true);
+  const NormShape s = norm_shape(d.rows, d.cols);
   switch (d.quant) {
     case FP8T_Q_NONE: launch_norm<fp8t::blk::kNone>(p, s, dev->sms, as_stream(stream)); break;
     case FP8T_Q_FP8: launch_norm<fp8t::blk::kFP8>(p, s, dev->sms, as_stream(stream)); break;
@@ -1424,7 +1453,7 @@ fp8t_status fp8_rmsnorm_cast(const fp8t_rmsnorm* desc, void* stream) {
 
 size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || !norm_cols_ok(rows, cols, 16)) return 0;
-  return static_cast<size_t>(norm_backward_ctas(rows, cols) * cols * 4);
+  return static_cast<size_t>(norm_backward_shape(rows, cols).ctas * cols * 4);
 }
 
 fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspace,
@@ -1443,7 +1472,8 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
       !aligned(d.dgamma_bf16, 2) || !aligned(d_workspace, 16))
     return fail(FP8T_ERR_MISALIGNED, "fp8_rmsnorm_backward: misaligned pointer");
   const bool want = d.dgamma_f32 || d.dgamma_bf16;
-  const int64_t ctas = norm_backward_ctas(d.rows, d.cols);
+  const NormBwdShape s = norm_backward_shape(d.rows, d.cols);
+  const int64_t ctas = s.ctas;
   if (want && (!d_workspace || workspace_bytes < static_cast<size_t>(ctas * d.cols * 4)))
     return fail(FP8T_ERR_INVALID_ARG, "fp8_rmsnorm_backward: workspace of %zu bytes needed",
                 static_cast<size_t>(ctas * d.cols * 4));
@@ -1461,15 +1491,12 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
   p.partials = want ? static_cast<float*>(d_workspace) : nullptr;
   p.rows = d.rows;
   p.cols = static_cast<int32_t>(d.cols);
-  const NormShape s = norm_shape(d.rows, d.cols, false);
-  const unsigned grid = static_cast<unsigned>(ctas);
-  if (s.warp_row) {
-    if (s.vpt == 1)      k_rmsnorm_backward<1, true><<<grid, s.threads, 0, as_stream(stream)>>>(p);
-    else if (s.vpt == 2) k_rmsnorm_backward<2, true><<<grid, s.threads, 0, as_stream(stream)>>>(p);
-    else                 k_rmsnorm_backward<4, true><<<grid, s.threads, 0, as_stream(stream)>>>(p);
-  } else {
-    k_rmsnorm_backward<4, false><<<grid, s.threads, 0, as_stream(stream)>>>(p);
-  }
+  p.group = s.group;
+  const unsigned grid = static_cast<unsigned>(ctas), threads = static_cast<unsigned>(s.group * s.groups);
+  const size_t smem = want ? static_cast<size_t>(s.groups - 1) * d.cols * 4 : 0;
+  if (s.vpt == 1)      k_rmsnorm_backward<1><<<grid, threads, smem, as_stream(stream)>>>(p);
+  else if (s.vpt == 2) k_rmsnorm_backward<2><<<grid, threads, smem, as_stream(stream)>>>(p);
+  else                 k_rmsnorm_backward<4><<<grid, threads, smem, as_stream(stream)>>>(p);
   if ((st = after_launch("fp8_rmsnorm_backward launch")) != FP8T_OK) return st;
   if (want) {
     k_rmsnorm_dgamma<<<static_cast<unsigned>((d.cols + 31) / 32), 32 * kReduceWarps, 0, as_stream(stream)>>>(
