@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -236,11 +237,14 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
     if (!ws && (d.dgamma_f32 || d.dgamma_bf16)) {
       // freed on return; `workspace` keeps it from being given out again before `stream` is done with it
       const size_t bytes = lib.rmsnorm_backward_workspace_bytes(d.rows, d.cols);
-      PyObject* t = PyObject_CallFunction(lib.workspace, "KOO", static_cast<unsigned long long>(bytes), a[0],
-                                          a[9] ? a[9] : Py_None);
-      if (!t) throw Error{};
-      own = THPVariable_Unpack(t);
-      Py_DECREF(t);
+      if (a[9] && a[9] != Py_None) {
+        PyObject* t = PyObject_CallFunction(lib.workspace, "KOO", static_cast<unsigned long long>(bytes), a[0], a[9]);
+        if (!t) throw Error{};
+        own = THPVariable_Unpack(t);
+        Py_DECREF(t);
+      } else {
+        own = at::empty({static_cast<int64_t>(bytes)}, dy.options().dtype(at::kByte));
+      }
       ws = &own;
     }
     void* p = nullptr;

@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <functional>
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -70,6 +71,12 @@ template <bool NV, int BT>
 cudaError_t allow_fp4_split_smem_of() {
   return cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm_split<NV, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               fp8t::gemm::SplitShape<NV, BT>::kSmem);
+}
+template <class G>
+cudaError_t allow_fp4_wide_smem() {
+  using namespace fp8t::gemm;
+  const cudaError_t e = cudaFuncSetAttribute(k_fp4_gemm<false, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes4<false>);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_fp4_gemm<true, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes4<true>);
 }
 cudaError_t allow_fp4_split_smem() {
   cudaError_t e;
@@ -171,11 +178,9 @@ fp8t_status current_device(DeviceInfo** out) {
         (void)cudaGetLastError();
         d.mx_cast_blocks_per_sm = 1;
       }
-      e = cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               fp8t::gemm::kSmemBytes4<false>);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fp8t::gemm::kSmemBytes4<true>);
+      e = allow_fp4_wide_smem<fp8t::gemm::SmallGroup4>();
+      if (e == cudaSuccess) e = allow_fp4_wide_smem<fp8t::gemm::LargeGroup4>();
+      if (e == cudaSuccess) e = allow_fp4_wide_smem<fp8t::gemm::ListGroup4>();
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  fp8t::fp4::kCastSmemBytes);
@@ -190,7 +195,7 @@ fp8t_status current_device(DeviceInfo** out) {
       cfg.blockDim = dim3(fp8t::gemm::kThreads4, 1, 1);
       cfg.dynamicSmemBytes = fp8t::gemm::kSmemBytes4<true>;
       clusters = 0;
-      e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true, fp8t::gemm::ListGroup4>, &cfg);
       if (e != cudaSuccess || clusters < 1) {
         (void)cudaGetLastError();
         clusters = sms / 2;
@@ -1141,24 +1146,26 @@ fp8t_status encode_fp4_scales(CUtensorMap* map, const void* ptr, int64_t mn, int
   return FP8T_OK;
 }
 
-// n problems of one format on 256 x 256 pair tiles.
-fp8t_status fp4_gemm_wide(const fp8t_fp4_gemm_desc* gemms, int32_t n, const DeviceInfo* dev, cudaStream_t stream) {
+// Fills a group's problems (256 x 256 tiles) and returns the number of tiles, or -1 with *st set.
+template <class G>
+int64_t fill_fp4_group(G& g, const fp8t_fp4_gemm_desc* gemms, int32_t n, fp8t_status* st) {
   using namespace fp8t::gemm;
   EncodeTiledFn fn = encode_fn();
-  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  if (!fn) {
+    *st = fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    return -1;
+  }
   const bool nv = gemms[0].quant == FP8T_Q_NVFP4;
-  static thread_local Group group;
-  std::memset(&group, 0, sizeof(group));
-  group.n = n;
+  g.n = n;
   int64_t tiles = 0;
-  fp8t_status st;
   for (int32_t i = 0; i < n; ++i) {
     const fp8t_fp4_gemm_desc& d = gemms[i];
-    Problem& P = group.p[i];
-    if ((st = encode_kmajor(&P.a, d.A, d.M, d.K / 2, kHalf)) != FP8T_OK) return st;
-    if ((st = encode_kmajor(&P.b, d.B, d.N, d.K / 2, kHalf)) != FP8T_OK) return st;
-    if ((st = encode_fp4_scales(&P.sfa, d.A_scales, d.M, d.K, nv)) != FP8T_OK) return st;
-    if ((st = encode_fp4_scales(&P.sfb, d.B_scales, d.N, d.K, nv)) != FP8T_OK) return st;
+    Problem4& P = g.p[i];
+    if ((*st = encode_kmajor(&P.a, d.A, d.M, d.K / 2, kHalf)) != FP8T_OK ||
+        (*st = encode_kmajor(&P.b, d.B, d.N, d.K / 2, kHalf)) != FP8T_OK ||
+        (*st = encode_fp4_scales(&P.sfa, d.A_scales, d.M, d.K, nv)) != FP8T_OK ||
+        (*st = encode_fp4_scales(&P.sfb, d.B_scales, d.N, d.K, nv)) != FP8T_OK)
+      return -1;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.N), static_cast<cuuint64_t>(d.M)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.N) * 2};
     cuuint32_t box[2] = {32, 32};
@@ -1166,28 +1173,91 @@ fp8t_status fp4_gemm_wide(const fp8t_fp4_gemm_desc* gemms, int32_t n, const Devi
     CUresult r = fn(&P.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.D_bf16, dims, strides, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (D) failed (%d)", (int)r);
+    if (r != CUDA_SUCCESS) {
+      *st = fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (D) failed (%d)", (int)r);
+      return -1;
+    }
     P.sa = d.d_a_scale_inv;
     P.sb = d.d_b_scale_inv;
     P.M = static_cast<int32_t>(d.M);
     P.N = static_cast<int32_t>(d.N);
-    P.K = static_cast<int32_t>(d.K);
-    P.kb128 = static_cast<int32_t>((d.K + 255) / 256);       // this kernel's k-blocks: 256 values
-    P.sumsq_slot = -1;
+    P.num_kb = static_cast<int32_t>((d.K + 255) / 256);
     P.tiles_n = static_cast<int32_t>((d.N + kBN - 1) / kBN);
     P.tile_start = static_cast<int32_t>(tiles);
     tiles += ((d.M + kBM - 1) / kBM) * P.tiles_n;
-    if (tiles >= (int64_t(1) << 30))
-      return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
   }
-  group.total_tiles = static_cast<int32_t>(tiles);
-  const int64_t grid = 2 * std::min<int64_t>(tiles, dev->gemm_fp4_clusters);
-  build_schedule(group, static_cast<int>(grid / 2), false);
+  g.total_tiles = static_cast<int32_t>(tiles);
+  return tiles;
+}
+
+// Tiles to clusters, longest (most k-blocks) first, each to the least loaded cluster; every cluster then runs
+// its tiles in index order.
+void list_fp4_tiles(fp8t::gemm::ListGroup4& g, int clusters) {
+  std::vector<std::pair<int, int>> tiles;              // (k-blocks, tile)
+  tiles.reserve(g.total_tiles);
+  for (int p = 0; p < g.n; ++p) {
+    const int end = p + 1 < g.n ? g.p[p + 1].tile_start : g.total_tiles;
+    for (int t = g.p[p].tile_start; t < end; ++t) tiles.push_back({g.p[p].num_kb, t});
+  }
+  std::stable_sort(tiles.begin(), tiles.end(),
+                   [](const std::pair<int, int>& a, const std::pair<int, int>& b) { return a.first > b.first; });
+  std::vector<std::pair<int64_t, int>> load(clusters); // a heap of (k-blocks, cluster), least first
+  for (int c = 0; c < clusters; ++c) load[c] = {0, c};
+  std::vector<std::vector<uint16_t>> own(clusters);
+  const auto more = std::greater<std::pair<int64_t, int>>();
+  for (const auto& t : tiles) {
+    std::pop_heap(load.begin(), load.end(), more);
+    own[load.back().second].push_back(static_cast<uint16_t>(t.second));
+    load.back().first += t.first;
+    std::push_heap(load.begin(), load.end(), more);
+  }
+  int k = 0;
+  for (int c = 0; c < clusters; ++c) {
+    std::sort(own[c].begin(), own[c].end());
+    g.start[c] = static_cast<uint16_t>(k);
+    for (uint16_t t : own[c]) g.order[k++] = t;
+  }
+  g.start[clusters] = static_cast<uint16_t>(k);
+}
+
+template <class G>
+fp8t_status launch_fp4_wide(const G& g, bool nv, const DeviceInfo* dev, cudaStream_t stream) {
+  using namespace fp8t::gemm;
+  const unsigned grid = 2 * static_cast<unsigned>(std::min(g.total_tiles, dev->gemm_fp4_clusters));
   if (nv)
-    k_fp4_gemm<true><<<static_cast<unsigned>(grid), kThreads4, kSmemBytes4<true>, stream>>>(group);
+    k_fp4_gemm<true, G><<<grid, kThreads4, kSmemBytes4<true>, stream>>>(g);
   else
-    k_fp4_gemm<false><<<static_cast<unsigned>(grid), kThreads4, kSmemBytes4<false>, stream>>>(group);
+    k_fp4_gemm<false, G><<<grid, kThreads4, kSmemBytes4<false>, stream>>>(g);
   return after_launch("fp4_gemm launch");
+}
+
+// n problems of one format on 256 x 256 pair tiles. Tiles of one length (and launches of at most one tile per
+// cluster) are dealt out in turn; problems of different K get a list per cluster, where it fits.
+fp8t_status fp4_gemm_wide(const fp8t_fp4_gemm_desc* gemms, int32_t n, const DeviceInfo* dev, cudaStream_t stream) {
+  using namespace fp8t::gemm;
+  const bool nv = gemms[0].quant == FP8T_Q_NVFP4;
+  fp8t_status st = FP8T_OK;
+  int64_t tiles = 0;
+  bool uneven = false;
+  for (int32_t i = 0; i < n; ++i) {
+    tiles += (gemms[i].M + kBM - 1) / kBM * ((gemms[i].N + kBN - 1) / kBN);
+    uneven |= (gemms[i].K + 255) / 256 != (gemms[0].K + 255) / 256;
+  }
+  if (tiles >= (int64_t(1) << 30)) return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
+  if (uneven && tiles > dev->gemm_fp4_clusters && tiles <= kMaxSchedTiles && dev->gemm_fp4_clusters <= kMaxClusters) {
+    static thread_local ListGroup4 g;
+    if (fill_fp4_group(g, gemms, n, &st) < 0) return st;
+    list_fp4_tiles(g, dev->gemm_fp4_clusters);
+    return launch_fp4_wide(g, nv, dev, stream);
+  }
+  if (n <= SmallGroup4::kProblems) {
+    static thread_local SmallGroup4 g;
+    if (fill_fp4_group(g, gemms, n, &st) < 0) return st;
+    return launch_fp4_wide(g, nv, dev, stream);
+  }
+  static thread_local LargeGroup4 g;
+  if (fill_fp4_group(g, gemms, n, &st) < 0) return st;
+  return launch_fp4_wide(g, nv, dev, stream);
 }
 
 template <bool NV, int BT>
@@ -1221,8 +1291,16 @@ SplitPlan plan_fp4_split(const fp8t_fp4_gemm_desc* gemms, int32_t n, int sms) {
   p.bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   p.tiles = 0;
   for (int32_t i = 0; i < n; ++i) p.tiles += (gemms[i].N + 127) / 128;
+  // the fewest k-blocks for the SM that has most (CTAs per SM x k-blocks per CTA), within two CTAs per SM
+  int64_t best = 0;
   p.ways = 1;
-  while (p.ways < 8 && p.tiles * p.ways * 2 <= 2 * sms && p.ways * 2 <= kbs) p.ways *= 2;
+  for (int w = 1; w <= 8 && w <= kbs && (w == 1 || p.tiles * w <= 2 * sms); ++w) {
+    const int64_t most = (p.tiles * w + sms - 1) / sms * ((kbs + w - 1) / w);
+    if (w == 1 || most < best) {
+      best = most;
+      p.ways = w;
+    }
+  }
   return p;
 }
 

@@ -84,6 +84,43 @@ __device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc,
         : "memory");
 }
 
+// One GEMM of a grouped launch; tiles are numbered problem by problem.
+struct alignas(64) Problem4 {
+  CUtensorMap a, b, d;             // codes [M][K/2], [N][K/2] in 128-row boxes; D [M][N] in 32 x 32 ones
+  CUtensorMap sfa, sfb;            // scales in rows of 256 words
+  const float* sa;
+  const float* sb;
+  int32_t M, N, num_kb, tiles_n, tile_start;
+};
+// Up to NP problems; TABLE: with the host's tile list per cluster (as in the 8-bit GEMMs). A launch's
+// parameters are copied at every launch: the table and 24 problems are 26 KB, and a call of one to four
+// problems without a list takes 3 KB.
+template <int NP, bool TABLE>
+struct alignas(64) Group4 {
+  static constexpr int kProblems = NP;
+  Problem4 p[NP];
+  int32_t n, total_tiles;
+  __device__ __forceinline__ int tiles_of(int c, int clusters) const {
+    return total_tiles > c ? (total_tiles - c + clusters - 1) / clusters : 0;
+  }
+  __device__ __forceinline__ int tile_at(int c, int clusters, int i) const { return c + i * clusters; }
+  __device__ __forceinline__ const Problem4& problem(int tile) const {
+    int k = 0;
+    while (k + 1 < n && p[k + 1].tile_start <= tile) ++k;
+    return p[k];
+  }
+};
+template <int NP>
+struct alignas(64) Group4<NP, true> : Group4<NP, false> {
+  uint16_t start[kMaxClusters + 1];
+  uint16_t order[kMaxSchedTiles];    // cluster c runs order[start[c] .. start[c + 1])
+  __device__ __forceinline__ int tiles_of(int c, int) const { return start[c + 1] - start[c]; }
+  __device__ __forceinline__ int tile_at(int c, int, int i) const { return order[start[c] + i]; }
+};
+using SmallGroup4 = Group4<4, false>;
+using LargeGroup4 = Group4<kMaxProblems, false>;
+using ListGroup4 = Group4<kMaxProblems, true>;
+
 // One lane of a converged warp, the same on every call.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -109,9 +146,9 @@ struct Smem4 {
   int abort;
 };
 
-template <bool NV>
+template <bool NV, class G>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
-    k_fp4_gemm(const __grid_constant__ Group g) {
+    k_fp4_gemm(const __grid_constant__ G g) {
   constexpr int kSf = kSfBytes4<NV>, kSfRows = NV ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -124,7 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
-  const int my_tiles = tiles_of(g, cluster, n_clusters);
+  const int my_tiles = g.tiles_of(cluster, n_clusters);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages4; ++s) {
@@ -163,13 +200,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     const bool one = elect_one();
     uint32_t it = 0, issued = 0;
     for (int i = 0; i < my_tiles && !warp_aborted(abort_flag); ++i) {
-      const int tile = tile_at(g, cluster, n_clusters, i);
-      const Problem& P = g.p[find_problem(g, tile)];
+      const int tile = g.tile_at(cluster, n_clusters, i);
+      const Problem4& P = g.problem(tile);
       const int local = tile - P.tile_start, mt = local / P.tiles_n, nt = local % P.tiles_n;
       const int m0 = mt * kBM + static_cast<int>(rank) * kHalf;
       const int n0 = nt * kBN + static_cast<int>(rank) * kHalf;
       const int ra = 2 * mt + static_cast<int>(rank), rb = 2 * nt;          // 128-row blocks of the scales
-      const int num_kb = P.kb128;                                           // k-blocks of 256 values
+      const int num_kb = P.num_kb;                                           // k-blocks of 256 values
       for (int kb = 0; kb < num_kb; ++kb, ++it) {
         const uint32_t s = it % kStages4, ph = (it / kStages4) & 1;
         if (warp_aborted(abort_flag)) break;
@@ -208,9 +245,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       const bool one = elect_one();
       uint32_t it = 0;
       for (int i = 0; i < my_tiles && !warp_aborted(abort_flag); ++i) {
-        const int tile = tile_at(g, cluster, n_clusters, i);
-        const Problem& P = g.p[find_problem(g, tile)];
-        const int num_kb = P.kb128;
+        const int tile = g.tile_at(cluster, n_clusters, i);
+        const Problem4& P = g.problem(tile);
+        const int num_kb = P.num_kb;
         const uint32_t acc = i & 1, aph = (i >> 1) & 1;
         // this accumulator read by the epilogue of two tiles ago; the columns it shares with the other one
         // by the previous tile's
@@ -268,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     uint32_t chunk_count = 0;
     constexpr int kShared = static_cast<int>(kOv4<NV>) / 32;    // chunks the accumulators share
     for (int i = 0; i < my_tiles; ++i) {
-      const int tile = tile_at(g, cluster, n_clusters, i);
+      const int tile = g.tile_at(cluster, n_clusters, i);
       const uint32_t acc = i & 1, aph = (i >> 1) & 1;
       if (warp_aborted(abort_flag)) break;
       if (!warp_wait(smem_u32(&S->acc_full[acc]), aph, limit, expire_epi)) {
@@ -277,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
         break;
       }
       tc_fence_after();
-      const Problem& P = g.p[find_problem(g, tile)];
+      const Problem4& P = g.problem(tile);
       const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
       const int M = P.M, N = P.N, local = tile - P.tile_start;
       const int row0 = (local / P.tiles_n) * kBM + static_cast<int>(rank) * kHalf + quad * 32;
@@ -344,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
 // tiles for 74 pairs), and its time is that of streaming B (the weights). Here the weights are the 128-row
 // operand of a one-CTA MMA and the BT tokens the other, so a tile is 128 rows of B by all rows of A, and
 // the S CTAs of a cluster each take a contiguous part of K. Every CTA leaves its FP32
-// partial tile in the shared memory of the CTAs that own its tokens (token t belongs to rank t / (BT / S));
+// partial tile in the shared memory of the CTAs that own its tokens (token t belongs to rank t mod S);
 // after a cluster barrier each owner adds the S partials in rank order, scales, rounds and stores its
 // tokens' rows of D, 128 columns of a row at a time. No workspace, and the order of additions is fixed.
 // TMEM: accumulator (weight rows x tokens) in columns 0..BT-1, then the scales.
@@ -355,12 +392,17 @@ template <bool NV, int BT>
 struct SplitShape {
   static constexpr int kSf = (NV ? 4 : 2) * 512;                 // scale bytes per 128 rows and k-block
   static constexpr int kStage = kABytes + BT * kBK + 2 * kSf;
-  static constexpr int kStages = BT <= 64 ? 4 : 3;                // two CTAs per SM
+  static constexpr int kStages = BT <= 16 ? 4 : 3;                // two CTAs per SM
   static constexpr int kSfCols = 8;                               // TMEM columns per atom step along K
   static constexpr int kTmem = BT <= 32 ? 64 : 2 * BT;
-  static constexpr int kSmem = kStages * kStage + 1024 + 256;
+  // partials: beside the stages while two CTAs still fit an SM, so that a CTA may receive them while it
+  // computes; else over the stages, behind one more cluster barrier
+  static constexpr bool kApart = BT <= 32;
+  static constexpr int kRed = kApart ? 128 * 4 * (BT + 8) : 0;     // ceil(BT / S) * S tokens at most
+  static constexpr int kSmem = kStages * kStage + kRed + 1024 + 256;
   static_assert(BT + (NV ? 4 : 2) * kSfCols <= kTmem, "TMEM columns");
-  static_assert(128 * BT * 4 <= kStages * kStage, "the partial tiles fit the stage buffers");
+  static_assert(kApart || 128 * (BT + 8) * 4 <= kStages * kStage, "the partial tiles fit the stage buffers");
+  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
   static_assert(kStage % 1024 == 0, "stages stay 1024-byte aligned");
 };
 
@@ -407,7 +449,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     uint32_t tmem_base;
     int abort;
   };
-  Bars* S = reinterpret_cast<Bars*>(smem + Sh::kStages * Sh::kStage);
+  Bars* S = reinterpret_cast<Bars*>(smem + Sh::kStages * Sh::kStage + Sh::kRed);
   volatile int* abort_flag = &S->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank()), ways = static_cast<int>(cluster_nctarank());
@@ -420,6 +462,20 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   const int kb0 = static_cast<int>(static_cast<int64_t>(P.num_kb) * rank / ways);
   const int kb1 = static_cast<int>(static_cast<int64_t>(P.num_kb) * (rank + 1) / ways);
 
+  const uint64_t limit = wait_limit_ns();
+  const int expire = expire_mode();
+  const bool expire_main = expire == kExpireAll;
+  auto load = [&](int kb, uint32_t s) {        // one lane: a k-block into stage s
+    const uint32_t bar = smem_u32(&S->full[s]), w = smem_u32(smem + s * Sh::kStage);
+    const uint32_t t = w + kABytes, sf = t + BT * kBK;
+    mbar_arrive_expect_tx(bar, Sh::kStage);
+    tma_load_2d(w, &P.w, kb * kBK, n0, bar);
+    tma_load_2d(t, &P.t, kb * kBK, 0, bar);
+    tma_load_2d(sf, &P.sfw, 0, ((n0 >> 7) * P.num_kb + kb) * kSfRows, bar);
+    tma_load_2d(sf + kSf, &P.sft, 0, kb * kSfRows, bar);
+  };
+
+  if (ways > 1 && Sh::kApart) cluster_arrive();          // "running": waited for before the first remote store
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::kStages; ++s) {
       mbar_init(smem_u32(&S->full[s]), 1);
@@ -428,6 +484,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     mbar_init(smem_u32(&S->done), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    // the first loads need nothing but these barriers: they start before the CTA's other set-up
+    for (int kb = kb0; kb < kb1 && kb < kb0 + Sh::kStages; ++kb) load(kb, kb - kb0);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&S->tmem_base), Sh::kTmem);
@@ -437,28 +495,17 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
-  const uint64_t limit = wait_limit_ns();
-  const int expire = expire_mode();
-  const bool expire_main = expire == kExpireAll;
 
   if (warp == 0) {
     const bool one = elect_one();
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int kb = kb0 + Sh::kStages; kb < kb1; ++kb) {
       const uint32_t it = kb - kb0, s = it % Sh::kStages, ph = (it / Sh::kStages) & 1;
       if (!warp_wait(smem_u32(&S->empty[s]), ph ^ 1, limit, expire_main) || warp_aborted(abort_flag)) {
         if (one && !*abort_flag) record_error(kErrTimeout);
         *abort_flag = 1;
         break;
       }
-      if (one) {
-        const uint32_t bar = smem_u32(&S->full[s]), w = smem_u32(smem + s * Sh::kStage);
-        const uint32_t t = w + kABytes, sf = t + BT * kBK;
-        mbar_arrive_expect_tx(bar, Sh::kStage);
-        tma_load_2d(w, &P.w, kb * kBK, n0, bar);
-        tma_load_2d(t, &P.t, kb * kBK, 0, bar);
-        tma_load_2d(sf, &P.sfw, 0, ((n0 >> 7) * P.num_kb + kb) * kSfRows, bar);
-        tma_load_2d(sf + kSf, &P.sft, 0, kb * kSfRows, bar);
-      }
+      if (one) load(kb, s);
     }
   } else if (warp == 1) {
     const bool one = elect_one();
@@ -506,24 +553,32 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     mbar_wait(smem_u32(&S->done), 0, kDrainLimitNs);       // MMAs in flight, whatever the limit was
   }
   tc_fence_after();
-  __syncthreads();                           // the MMAs that read the stage buffers are done, in this CTA
-  if (ways > 1) cluster_sync();              // and in every CTA that receives partials
-  const int per_log = 31 - __clz(BT / ways), per = 1 << per_log;   // tokens per owner
-  const uint32_t red = smem_u32(smem);       // [ways][per][128] f32
+  const int per = (BT + ways - 1) / ways;    // tokens per owner
+  uint32_t red;                              // [ways][per][128] f32
+  if (Sh::kApart) {
+    red = smem_u32(smem + Sh::kStages * Sh::kStage);
+    if (ways > 1) cluster_wait();            // every CTA of the cluster runs
+  } else {
+    red = smem_u32(smem);
+    __syncthreads();                         // the MMAs that read the stage buffers are done, in this CTA
+    if (ways > 1) cluster_sync();            // and in every CTA that receives partials
+  }
+  int owner = 0, slot = 0;                   // of the token: t mod ways, t / ways
 #pragma unroll 1
-  for (int c = 0; c < BT; c += 16) {
-    if (c >= P.M) break;
+  for (int c = 0; c < BT && c < P.M; c += 16) {
     uint32_t r[16];
     tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
     tmem_ld_wait();
     tmem_reg_fence(r);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const int t = c + j;
-      if (t >= P.M) break;
+      if (c + j >= P.M) break;
       const float v = kb1 > kb0 ? __uint_as_float(r[j]) : 0.0f;
-      const uint32_t at = red + ((rank * per + (t & (per - 1))) * 128 + threadIdx.x) * 4;
-      st_cluster_f32(mapa_shared(at, t >> per_log), v);
+      st_cluster_f32(mapa_shared(red + ((rank * per + slot) * 128 + threadIdx.x) * 4, owner), v);
+      if (++owner == ways) {
+        owner = 0;
+        ++slot;
+      }
     }
   }
   tc_fence_before();
@@ -533,11 +588,11 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   if (*abort_flag) return;                   // D is incomplete; the error word says so
   const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
-  const float2* part = reinterpret_cast<const float2*>(smem);
+  const float2* part = reinterpret_cast<const float2*>(smem + (red - smem_u32(smem)));
   const int pair = threadIdx.x & 63, n = n0 + 2 * pair;
-  for (int t = threadIdx.x >> 6; t < per; t += kSplitThreads / 64) {
-    const int m = rank * per + t;
-    if (m >= P.M || n >= P.N) continue;
+  for (int t = threadIdx.x >> 6; t * ways + rank < P.M; t += kSplitThreads / 64) {
+    const int m = t * ways + rank;
+    if (n >= P.N) break;
     float2 v = part[t * 64 + pair];
     for (int s = 1; s < ways; ++s) {
       const float2 o = part[(s * per + t) * 64 + pair];
