@@ -60,6 +60,7 @@ struct DeviceInfo {
   int gemm_fp4_clusters = 0;   // ... of the 4-bit 256 x 256 kernel (fewer of its two forms)
   int mx_cast_blocks_per_sm = 0;
   int fp4_cast_blocks_per_sm = 0;
+  int fp4_cast_rows_blocks_per_sm = 0;
   int cast_blocks_per_sm = 0;
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
@@ -206,6 +207,12 @@ fp8t_status current_device(DeviceInfo** out) {
       if (e != cudaSuccess || d.fp4_cast_blocks_per_sm < 1) {
         (void)cudaGetLastError();
         d.fp4_cast_blocks_per_sm = 1;
+      }
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.fp4_cast_rows_blocks_per_sm, fp8t::fp4::k_fp4_cast_rows,
+                                                        fp8t::fp4::kCastThreads, 0);
+      if (e != cudaSuccess || d.fp4_cast_rows_blocks_per_sm < 1) {
+        (void)cudaGetLastError();
+        d.fp4_cast_rows_blocks_per_sm = 1;
       }
       e = cudaFuncSetAttribute(fp8t::cast::k_cast_transpose_amax<false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::cast::kSmemBytes);
@@ -1091,6 +1098,8 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
     std::memset(&group, 0, sizeof(group));
     group.n = b1 - b0;
     int64_t tiles = 0;
+    bool any_col = false;
+    for (int32_t i = b0; i < b1; ++i) any_col |= tensors[i].q_col != nullptr;
     for (int32_t i = b0; i < b1; ++i) {
       const fp8t_fp4_cast_tensor& t = tensors[i];
       CastTensor& T = group.t[i - b0];
@@ -1102,6 +1111,7 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
                       dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
       if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit cast input) failed (%d)", (int)r);
+      T.x = t.x_bf16;
       T.q_row = static_cast<uint8_t*>(t.q_row);
       T.sf_row = static_cast<uint8_t*>(t.scales_row);
       T.q_col = static_cast<uint8_t*>(t.q_col);
@@ -1109,14 +1119,24 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
       T.scale = t.d_scale;
       T.amax_bits = reinterpret_cast<unsigned int*>(t.d_amax_inout);
       T.scale_inv = t.d_scale_inv_out;
-      T.rows = t.rows;
-      T.cols = t.cols;
-      T.tiles_c = (t.cols + kTile - 1) / kTile;
-      T.tile_start = tiles;
+      T.rows = static_cast<int32_t>(t.rows);
+      T.cols = static_cast<int32_t>(t.cols);
+      T.tiles_c = static_cast<int32_t>((t.cols + kTile - 1) / kTile);
+      T.tile_start = static_cast<int32_t>(tiles);
       T.kind = t.quant;
       tiles += ((t.rows + kTile - 1) / kTile) * T.tiles_c;
     }
-    group.total_tiles = tiles;
+    if (tiles >= (int64_t(1) << 30)) return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_cast: too many tiles in one launch");
+    group.total_tiles = static_cast<int32_t>(tiles);
+    if (!any_col) {                    // row-wise copies only: the streaming kernel
+      int64_t most = 0;                // blocks of 32 values of the largest tensor
+      for (int32_t i = b0; i < b1; ++i) most = std::max(most, tensors[i].rows * tensors[i].cols / 32);
+      const int64_t rgrid = std::min<int64_t>((most + kCastThreads - 1) / kCastThreads,
+                                              static_cast<int64_t>(dev->sms) * dev->fp4_cast_rows_blocks_per_sm);
+      k_fp4_cast_rows<<<static_cast<unsigned>(rgrid), kCastThreads, 0, as_stream(stream)>>>(group);
+      if ((st = after_launch("fp4_cast launch")) != FP8T_OK) return st;
+      continue;
+    }
     const int64_t grid = std::min<int64_t>(tiles, static_cast<int64_t>(dev->sms) * dev->fp4_cast_blocks_per_sm);
     k_fp4_cast<<<static_cast<unsigned>(grid), kCastThreads, kCastSmemBytes, as_stream(stream)>>>(group);
     if ((st = after_launch("fp4_cast launch")) != FP8T_OK) return st;

@@ -17,6 +17,30 @@ namespace blk {
 
 enum : int { kNone = 0, kFP8 = 1, kMXFP8 = 2, kMXFP4 = 3, kNVFP4 = 4 };   // fp8t_quant
 
+// Pairs of f32 in a 64-bit register; each half is rounded as the scalar operation would be.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 // Eight f32 -> eight E2M1 codes, round to nearest even, saturating at +-6; value 0 in the low nibble.
 // (E2M1 has no NaN: a NaN value becomes a finite code, its block's scale carries the NaN.)
 __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
@@ -57,17 +81,29 @@ __device__ __forceinline__ uint8_t e8m0_scale(uint32_t amax_bits, int emax, floa
   return static_cast<uint8_t>(X + 127);
 }
 
+// E4M3 code (0 .. 0x7E) of (amax * g) / 6, or 0x7F for a NaN.
+// The division is replaced by a multiplication where that cannot change the code. Let t = amax * g and
+// p = rn(t * rn(1/6)), v = rn(t / 6); they are at most one f32 apart. The codes differ only if a
+// rounding border (a middle of two E4M3 values, an f32 of at most five significant bits) lies on one of the
+// two. v is a border only for t = 6 * border exactly (t's neighbours are 2/3 of a step of v away or more),
+// and then p is the same number: rn(1/6) is 1/6 * (1 + 2^-25), and border * (1 + 2^-25) rounds back to the
+// border. So whenever p is not a number of at most five significant bits, its code is v's.
+__device__ __forceinline__ uint32_t nvfp4_scale_code(uint32_t amax_bits, float g) {
+  const float t = __fmul_rn(__uint_as_float(amax_bits), g);
+  float p = __fmul_rn(t, 0.16666667163372040f);
+  if ((__float_as_uint(p) & 0x7FFFFu) == 0) p = __fdiv_rn(t, 6.0f);
+  return p != p ? 0x7Fu : cvt_fp8x2<0>(p, 0.0f) & 0xFFu;        // p >= 0
+}
+// g / s of a scale code (1 for the NaN code, 0 for s = 0). The E4M3 exponent and mantissa are f32's with
+// another bias; subnormals are multiples of 2^-9.
+__device__ __forceinline__ float nvfp4_factor(uint32_t c, float g) {
+  const float s = c < 8u ? static_cast<float>(c) * 0.001953125f : __uint_as_float((c << 20) + (120u << 23));
+  return c == 0x7Fu ? 1.0f : c ? __fdiv_rn(g, s) : 0.0f;
+}
 // NVFP4 block: E4M3 scale byte and factor g / s. A NaN (block maximum or g) gives the byte 0x7F.
 __device__ __forceinline__ uint8_t nvfp4_scale(uint32_t amax_bits, float g, float& factor) {
-  const float t = __fdiv_rn(__fmul_rn(__uint_as_float(amax_bits), g), 6.0f);
-  if (t != t) {
-    factor = 1.0f;
-    return 0x7F;
-  }
-  const uint32_t c = cvt_fp8x2<0>(t, 0.0f) & 0xFFu;            // t >= 0: codes 0 .. 0x7E
-  // decode: the E4M3 exponent and mantissa are f32's with another bias; subnormals are multiples of 2^-9
-  const float s = c < 8u ? static_cast<float>(c) * 0.001953125f : __uint_as_float((c << 20) + (120u << 23));
-  factor = c ? __fdiv_rn(g, s) : 0.0f;
+  const uint32_t c = nvfp4_scale_code(amax_bits, g);
+  factor = nvfp4_factor(c, g);
   return static_cast<uint8_t>(c);
 }
 

@@ -82,6 +82,22 @@ def test_cast_row_wise_any_number_of_rows(cuda_lib, kind, rows):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_cast_inputs_aligned_to_16_bytes_only(cuda_lib, kind):
+    """Every pointer at 16 bytes past a 32-byte boundary, one and both ways."""
+    bits = random_bits(96, 320, 17)
+    for col in (False, True):
+        d = cast(cuda_lib, bits, kind, 3.0, col=col)
+        for k, e in (("x", 8), ("q_row", 16), ("sf_row", 16), ("q_col", 16), ("sf_col", 16)):
+            if k in d:
+                whole = torch.empty(d[k].numel() + e, dtype=d[k].dtype, device="cuda")
+                assert whole.data_ptr() % 32 == 0
+                whole[e:] = d[k].reshape(-1)
+                d[k] = whole[e:].view(d[k].shape)
+        cuda_lib.fp4_cast_multi([d])
+        check_cast(d, bits, kind, 3.0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_cast_column_wise_only(cuda_lib, kind):
     bits = random_bits(192, 224, 5)
     d = cast(cuda_lib, bits, kind, 11.0, row=False)
