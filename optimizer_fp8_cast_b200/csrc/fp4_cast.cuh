@@ -191,11 +191,15 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
   int cur = -1;                              // tensor of the factors
   uint32_t pending = 0, pending_ph = 0;      // thread 0: loads not yet consumed, their phases
 
+  pdl_trigger();
   if (tid == 0) {
     mbar_init(smem_u32(&full[0]), 1);
     mbar_init(smem_u32(&full[1]), 1);
     fence_mbar_init();
     s_abort = 0;
+  }
+  pdl_wait();
+  if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
       const int tile = static_cast<int>(blockIdx.x) + b * stride;
       if (tile < g.total_tiles) {
@@ -373,6 +377,8 @@ __device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors) {
 
 __global__ void __launch_bounds__(kCastThreads, 4) k_fp4_cast_rows(const __grid_constant__ CastGroup g) {
   __shared__ float factors[128];
+  pdl_trigger();
+  pdl_wait();
   for (int t = 0; t < g.n; ++t) {
     if (g.t[t].kind == blk::kNVFP4) cast_rows<true>(g.t[t], factors);
     else                            cast_rows<false>(g.t[t], factors);

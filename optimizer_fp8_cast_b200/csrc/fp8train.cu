@@ -244,6 +244,29 @@ fp8t_status current_device(DeviceInfo** out) {
   return FP8T_OK;
 }
 
+// A launch that may begin while the kernel before it in the stream still runs (the kernel calls pdl_wait).
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                       const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cluster > 0) {                   // a size chosen at launch (kernels without their own)
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 fp8t_status after_launch(const char* what) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(FP8T_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -1133,12 +1156,12 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
       for (int32_t i = b0; i < b1; ++i) most = std::max(most, tensors[i].rows * tensors[i].cols / 32);
       const int64_t rgrid = std::min<int64_t>((most + kCastThreads - 1) / kCastThreads,
                                               static_cast<int64_t>(dev->sms) * dev->fp4_cast_rows_blocks_per_sm);
-      k_fp4_cast_rows<<<static_cast<unsigned>(rgrid), kCastThreads, 0, as_stream(stream)>>>(group);
+      (void)launch_pdl(k_fp4_cast_rows, rgrid, kCastThreads, 0, as_stream(stream), 0, group);
       if ((st = after_launch("fp4_cast launch")) != FP8T_OK) return st;
       continue;
     }
     const int64_t grid = std::min<int64_t>(tiles, static_cast<int64_t>(dev->sms) * dev->fp4_cast_blocks_per_sm);
-    k_fp4_cast<<<static_cast<unsigned>(grid), kCastThreads, kCastSmemBytes, as_stream(stream)>>>(group);
+    (void)launch_pdl(k_fp4_cast, grid, kCastThreads, kCastSmemBytes, as_stream(stream), 0, group);
     if ((st = after_launch("fp4_cast launch")) != FP8T_OK) return st;
   }
   return FP8T_OK;
@@ -1245,9 +1268,9 @@ fp8t_status launch_fp4_wide(const G& g, bool nv, const DeviceInfo* dev, cudaStre
   using namespace fp8t::gemm;
   const unsigned grid = 2 * static_cast<unsigned>(std::min(g.total_tiles, dev->gemm_fp4_clusters));
   if (nv)
-    k_fp4_gemm<true, G><<<grid, kThreads4, kSmemBytes4<true>, stream>>>(g);
+    (void)launch_pdl(k_fp4_gemm<true, G>, grid, kThreads4, kSmemBytes4<true>, stream, 0, g);
   else
-    k_fp4_gemm<false, G><<<grid, kThreads4, kSmemBytes4<false>, stream>>>(g);
+    (void)launch_pdl(k_fp4_gemm<false, G>, grid, kThreads4, kSmemBytes4<false>, stream, 0, g);
   return after_launch("fp4_gemm launch");
 }
 
@@ -1282,18 +1305,8 @@ fp8t_status fp4_gemm_wide(const fp8t_fp4_gemm_desc* gemms, int32_t n, const Devi
 
 template <bool NV, int BT>
 cudaError_t launch_fp4_split(const fp8t::gemm::SplitGroup& g, int64_t tiles, int ways, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ways), 1, 1);
-  cfg.blockDim = dim3(fp8t::gemm::kSplitThreads, 1, 1);
-  cfg.dynamicSmemBytes = fp8t::gemm::SplitShape<NV, BT>::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(ways);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8t::gemm::k_fp4_gemm_split<NV, BT>, g);
+  return launch_pdl(fp8t::gemm::k_fp4_gemm_split<NV, BT>, tiles * ways, fp8t::gemm::kSplitThreads,
+                    fp8t::gemm::SplitShape<NV, BT>::kSmem, stream, ways, g);
 }
 
 // Tokens per tile and CTAs per cluster of the split kernel for up to kMaxSplitProblems problems.
@@ -1469,7 +1482,7 @@ void launch_norm_as(const fp8t::norm::Fwd& p, int threads, int sms, cudaStream_t
   }
   const int64_t per_cta = WARP_ROW ? kRowsPerCta : 1;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.rows + per_cta - 1) / per_cta, static_cast<int64_t>(sms) * n));
-  k_rmsnorm_cast<VPT, WARP_ROW, Q><<<grid, threads, 0, stream>>>(p);
+  (void)launch_pdl(k_rmsnorm_cast<VPT, WARP_ROW, Q>, grid, threads, 0, stream, 0, p);
 }
 
 template <int Q>
@@ -1590,15 +1603,14 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
   p.rows = d.rows;
   p.cols = static_cast<int32_t>(d.cols);
   p.group = s.group;
-  const unsigned grid = static_cast<unsigned>(ctas), threads = static_cast<unsigned>(s.group * s.groups);
   const size_t smem = want ? static_cast<size_t>(s.groups - 1) * d.cols * 4 : 0;
-  if (s.vpt == 1)      k_rmsnorm_backward<1><<<grid, threads, smem, as_stream(stream)>>>(p);
-  else if (s.vpt == 2) k_rmsnorm_backward<2><<<grid, threads, smem, as_stream(stream)>>>(p);
-  else                 k_rmsnorm_backward<4><<<grid, threads, smem, as_stream(stream)>>>(p);
+  (void)launch_pdl(s.vpt == 1 ? k_rmsnorm_backward<1> : s.vpt == 2 ? k_rmsnorm_backward<2> : k_rmsnorm_backward<4>,
+                   ctas, s.group * s.groups, smem, as_stream(stream), 0, p);
   if ((st = after_launch("fp8_rmsnorm_backward launch")) != FP8T_OK) return st;
   if (want) {
-    k_rmsnorm_dgamma<<<static_cast<unsigned>((d.cols + 31) / 32), 32 * kReduceWarps, 0, as_stream(stream)>>>(
-        p.partials, static_cast<int>(ctas), p.cols, d.dgamma_f32, static_cast<uint16_t*>(d.dgamma_bf16));
+    (void)launch_pdl(k_rmsnorm_dgamma, (d.cols + 31) / 32, 32 * kReduceWarps, 0, as_stream(stream), 0,
+                     static_cast<const float*>(p.partials), static_cast<int>(ctas), p.cols, d.dgamma_f32,
+                     static_cast<uint16_t*>(d.dgamma_bf16));
     st = after_launch("fp8_rmsnorm_backward dgamma launch");
   }
   return st;

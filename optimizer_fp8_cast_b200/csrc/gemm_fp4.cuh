@@ -194,6 +194,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
   const int expire = expire_mode();
   const bool expire_main = expire == kExpireAll;
   const bool expire_epi = expire == kExpireAll || expire == kExpireGemmEpilogue;
+  pdl_trigger();
+  pdl_wait();
 
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs)
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     tma_load_2d(sf + kSf, &P.sft, 0, kb * kSfRows, bar);
   };
 
+  pdl_trigger();
   if (ways > 1 && Sh::kApart) cluster_arrive();          // "running": waited for before the first remote store
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::kStages; ++s) {
@@ -484,6 +487,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     mbar_init(smem_u32(&S->done), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    pdl_wait();
     // the first loads need nothing but these barriers: they start before the CTA's other set-up
     for (int kb = kb0; kb < kb1 && kb < kb0 + Sh::kStages; ++kb) load(kb, kb - kb0);
   }
@@ -495,6 +499,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
+  pdl_wait();
 
   if (warp == 0) {
     const bool one = elect_one();

@@ -298,6 +298,14 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
                : "memory");
 }
 
+// ------------------------------------------------------------------ programmatic dependent launch
+// A kernel launched with the programmatic-serialisation attribute may begin while the kernel before it
+// still runs. pdl_wait returns when that kernel (and with it all earlier ones) has completed and its writes
+// are visible: it stands before the first access to memory that another kernel may write or read.
+// pdl_trigger lets the next kernel, if it was launched so too, begin once every CTA has called it.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ FP8 conversion
 // Two f32 -> two FP8 codes, round to nearest even, saturating to +-max (cvt.rn.satfinite).
 // Byte 0 of the result holds `lo`, byte 1 holds `hi`.

@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : kMaxThreads) k_r
   const int64_t row_step = WARP_ROW ? static_cast<int64_t>(gridDim.x) * kRowsPerCta : gridDim.x;
   int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * kRowsPerCta + (threadIdx.x >> 5) : blockIdx.x;
 
+  pdl_trigger();
+  pdl_wait();
   uint4 gam[VPT];
   bool in[VPT];
 #pragma unroll
@@ -251,6 +253,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
   const int nvec = p.cols >> 3;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * groups;
 
+  pdl_trigger();
+  pdl_wait();
   uint4 gam[VPT];
   f32x2 acc[VPT][4];
   bool in[VPT];
@@ -349,6 +353,8 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
   __shared__ float sh[kReduceWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  pdl_trigger();
+  pdl_wait();
   float v[kReduceLoads];
 #pragma unroll
   for (int i = 0; i < kReduceLoads; ++i) {
