@@ -324,6 +324,10 @@ __device__ __forceinline__ uint32_t cvt_fp8x2(float lo, float hi) {
   return r;
 }
 
+// Asks for `bytes` (a multiple of 16, from a 16-byte boundary) to be brought into L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // Streaming 16-byte load (read once; do not keep in L1).
 // 16-byte asynchronous copy global -> shared (bypassing L1), grouped by commit/wait.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {

@@ -14,7 +14,9 @@
 // read once and held in registers (four 16-byte vectors per thread at most) between the sum of squares and
 // the quantisation. At 20 instructions per element the issue rate bound it instead (50% issue at 16 warps per
 // SM, 45 us for 8192 x 4096 to FP8), so arithmetic runs on pairs (f32x2 add, multiply, FMA: two elements
-// per instruction, each rounded as the scalar one) and amax is a three-input maximum.
+// per instruction, each rounded as the scalar one) and amax is a three-input maximum. A thread's loads of a row
+// come at once and then none until the next row, so one thread asks for the next row's bytes with a bulk
+// prefetch into L2: 47.2 -> 41.1 us (5.7 TB/s); two or three rows ahead gave 43.4 and 45.0.
 //
 // Backward, with xh = h * rstd and g = dy * gamma:
 //   dh = rstd * (g - xh * (sum(g * xh) / C)) (+ dres, the gradient that reaches h directly)
@@ -23,7 +25,7 @@
 // threads that share a row, with a barrier of its own); a thread owns the same columns for every row of its
 // group, so dgamma is summed in registers (f32), over the CTA's groups in shared memory, and one
 // partial row per CTA goes to the workspace; a second kernel adds the partials. Both orders are fixed: the
-// result does not depend on scheduling.
+// result does not depend on scheduling. With the same prefetch, 8192 x 4096 with dres 58.7 -> 50.7 us.
 #pragma once
 
 #include "ptx.cuh"
@@ -155,6 +157,11 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : kMaxThreads) k_r
     const int64_t base = row * nvec + tid;
     f32x2 h[VPT][4];
     float ss = 0.0f;
+    if (tid == 0 && row + row_step < p.rows) {           // the row after this one into L2
+      const int64_t next = (row + row_step) * nvec;
+      l2_prefetch(p.x + next, nvec * 16);
+      if (p.res) l2_prefetch(p.res + next, nvec * 16);
+    }
     {
       uint4 xv[VPT], rv[VPT];
 #pragma unroll
@@ -273,6 +280,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
     const float rstd = __ldg(p.rstd + row);
     const f32x2 rstd2 = pair(rstd, rstd);
     uint4 dv[VPT], hv[VPT], rv[VPT];
+    if (tid == 0 && row + row_step < p.rows) {           // the row after this one into L2
+      const int64_t next = (row + row_step) * nvec;
+      l2_prefetch(p.dy + next, nvec * 16);
+      l2_prefetch(p.h + next, nvec * 16);
+      if (p.dres) l2_prefetch(p.dres + next, nvec * 16);
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       dv[i] = load_or_zero(p.dy + base + i * nthr, in[i]);
