@@ -57,7 +57,7 @@ struct DeviceInfo {
   int gemm_wide_clusters = 0;  // ... of its wide-tile form
   int gemm_mx_clusters = 0;    // ... of its MXFP8 variant
   int gemm_mxw_clusters = 0;   // ... of the MXFP8 256 x 384 kernel
-  int gemm_fp4_clusters = 0;   // ... of the 4-bit 256 x 256 kernel (fewer of its two forms)
+  int gemm_fp4_clusters = 0;   // ... of the 4-bit tile kernel (every form: one CTA per SM)
   int mx_cast_blocks_per_sm = 0;
   int fp4_cast_blocks_per_sm = 0;
   int fp4_cast_rows_blocks_per_sm = 0;
@@ -73,11 +73,18 @@ cudaError_t allow_fp4_split_smem_of() {
   return cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm_split<NV, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               fp8t::gemm::SplitShape<NV, BT>::kSmem);
 }
+template <bool NV, bool WIDE, class G>
+cudaError_t allow_fp4_tile_smem_of() {
+  return cudaFuncSetAttribute(fp8t::gemm::k_fp4_gemm<NV, WIDE, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fp8t::gemm::kSmemBytes4<NV, WIDE>);
+}
 template <class G>
-cudaError_t allow_fp4_wide_smem() {
-  using namespace fp8t::gemm;
-  const cudaError_t e = cudaFuncSetAttribute(k_fp4_gemm<false, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes4<false>);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_fp4_gemm<true, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes4<true>);
+cudaError_t allow_fp4_tile_smem() {
+  cudaError_t e;
+  if ((e = allow_fp4_tile_smem_of<false, false, G>()) != cudaSuccess || (e = allow_fp4_tile_smem_of<true, false, G>()) != cudaSuccess ||
+      (e = allow_fp4_tile_smem_of<false, true, G>()) != cudaSuccess)
+    return e;
+  return allow_fp4_tile_smem_of<true, true, G>();
 }
 cudaError_t allow_fp4_split_smem() {
   cudaError_t e;
@@ -179,9 +186,9 @@ fp8t_status current_device(DeviceInfo** out) {
         (void)cudaGetLastError();
         d.mx_cast_blocks_per_sm = 1;
       }
-      e = allow_fp4_wide_smem<fp8t::gemm::SmallGroup4>();
-      if (e == cudaSuccess) e = allow_fp4_wide_smem<fp8t::gemm::LargeGroup4>();
-      if (e == cudaSuccess) e = allow_fp4_wide_smem<fp8t::gemm::ListGroup4>();
+      e = allow_fp4_tile_smem<fp8t::gemm::SmallGroup4>();
+      if (e == cudaSuccess) e = allow_fp4_tile_smem<fp8t::gemm::LargeGroup4>();
+      if (e == cudaSuccess) e = allow_fp4_tile_smem<fp8t::gemm::ListGroup4>();
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  fp8t::fp4::kCastSmemBytes);
@@ -194,9 +201,9 @@ fp8t_status current_device(DeviceInfo** out) {
         return fail(FP8T_ERR_CUDA, "cudaFuncSetAttribute(4-bit): %s", cudaGetErrorString(e));
       }
       cfg.blockDim = dim3(fp8t::gemm::kThreads4, 1, 1);
-      cfg.dynamicSmemBytes = fp8t::gemm::kSmemBytes4<true>;
+      cfg.dynamicSmemBytes = fp8t::gemm::kSmemBytes4<true, true>;
       clusters = 0;
-      e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true, fp8t::gemm::ListGroup4>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true, true, fp8t::gemm::ListGroup4>, &cfg);
       if (e != cudaSuccess || clusters < 1) {
         (void)cudaGetLastError();
         clusters = sms / 2;
@@ -1189,9 +1196,9 @@ fp8t_status encode_fp4_scales(CUtensorMap* map, const void* ptr, int64_t mn, int
   return FP8T_OK;
 }
 
-// Fills a group's problems (256 x 256 tiles) and returns the number of tiles, or -1 with *st set.
+// Fills a group's problems (tiles of 256 x tile_n) and returns the number of tiles, or -1 with *st set.
 template <class G>
-int64_t fill_fp4_group(G& g, const fp8t_fp4_gemm_desc* gemms, int32_t n, fp8t_status* st) {
+int64_t fill_fp4_group(G& g, const fp8t_fp4_gemm_desc* gemms, int32_t n, int tile_n, fp8t_status* st) {
   using namespace fp8t::gemm;
   EncodeTiledFn fn = encode_fn();
   if (!fn) {
@@ -1206,6 +1213,7 @@ int64_t fill_fp4_group(G& g, const fp8t_fp4_gemm_desc* gemms, int32_t n, fp8t_st
     Problem4& P = g.p[i];
     if ((*st = encode_kmajor(&P.a, d.A, d.M, d.K / 2, kHalf)) != FP8T_OK ||
         (*st = encode_kmajor(&P.b, d.B, d.N, d.K / 2, kHalf)) != FP8T_OK ||
+        (tile_n > kBN && (*st = encode_kmajor(&P.b64, d.B, d.N, d.K / 2, kHalf / 2)) != FP8T_OK) ||
         (*st = encode_fp4_scales(&P.sfa, d.A_scales, d.M, d.K, nv)) != FP8T_OK ||
         (*st = encode_fp4_scales(&P.sfb, d.B_scales, d.N, d.K, nv)) != FP8T_OK)
       return -1;
@@ -1225,7 +1233,7 @@ int64_t fill_fp4_group(G& g, const fp8t_fp4_gemm_desc* gemms, int32_t n, fp8t_st
     P.M = static_cast<int32_t>(d.M);
     P.N = static_cast<int32_t>(d.N);
     P.num_kb = static_cast<int32_t>((d.K + 255) / 256);
-    P.tiles_n = static_cast<int32_t>((d.N + kBN - 1) / kBN);
+    P.tiles_n = static_cast<int32_t>((d.N + tile_n - 1) / tile_n);
     P.tile_start = static_cast<int32_t>(tiles);
     tiles += ((d.M + kBM - 1) / kBM) * P.tiles_n;
   }
@@ -1263,44 +1271,65 @@ void list_fp4_tiles(fp8t::gemm::ListGroup4& g, int clusters) {
   g.start[clusters] = static_cast<uint16_t>(k);
 }
 
-template <class G>
-fp8t_status launch_fp4_wide(const G& g, bool nv, const DeviceInfo* dev, cudaStream_t stream) {
+template <bool WIDE, class G>
+fp8t_status launch_fp4_tiles(const G& g, bool nv, const DeviceInfo* dev, cudaStream_t stream) {
   using namespace fp8t::gemm;
-  const unsigned grid = 2 * static_cast<unsigned>(std::min(g.total_tiles, dev->gemm_fp4_clusters));
+  const int grid = 2 * std::min(g.total_tiles, dev->gemm_fp4_clusters);
   if (nv)
-    (void)launch_pdl(k_fp4_gemm<true, G>, grid, kThreads4, kSmemBytes4<true>, stream, 0, g);
+    (void)launch_pdl(k_fp4_gemm<true, WIDE, G>, grid, kThreads4, kSmemBytes4<true, WIDE>, stream, 0, g);
   else
-    (void)launch_pdl(k_fp4_gemm<false, G>, grid, kThreads4, kSmemBytes4<false>, stream, 0, g);
+    (void)launch_pdl(k_fp4_gemm<false, WIDE, G>, grid, kThreads4, kSmemBytes4<false, WIDE>, stream, 0, g);
   return after_launch("fp4_gemm launch");
 }
 
-// n problems of one format on 256 x 256 pair tiles. Tiles of one length (and launches of at most one tile per
-// cluster) are dealt out in turn; problems of different K get a list per cluster, where it fits.
-fp8t_status fp4_gemm_wide(const fp8t_fp4_gemm_desc* gemms, int32_t n, const DeviceInfo* dev, cudaStream_t stream) {
+// n problems of one format on pair tiles. 384 columns need 1.36 times the time of 256 (8.1 against 10.8 us per
+// tile of K = 4096 NVFP4, 7.6 and 10.7 MXFP4) for 1.5 times the work, so they are taken where they save
+// enough rounds: with fewer tiles than clusters, or an N just past a multiple of 384, they do not.
+// Tiles of one length (and launches of at most one tile per cluster) are dealt out in turn; problems of
+// different K get a list per cluster, where it fits.
+template <bool WIDE>
+fp8t_status fp4_gemm_tiles_as(const fp8t_fp4_gemm_desc* gemms, int32_t n, int64_t tiles, bool uneven,
+                              const DeviceInfo* dev, cudaStream_t stream) {
   using namespace fp8t::gemm;
+  constexpr int tile_n = WIDE ? kBN4w : kBN;
   const bool nv = gemms[0].quant == FP8T_Q_NVFP4;
   fp8t_status st = FP8T_OK;
-  int64_t tiles = 0;
-  bool uneven = false;
-  for (int32_t i = 0; i < n; ++i) {
-    tiles += (gemms[i].M + kBM - 1) / kBM * ((gemms[i].N + kBN - 1) / kBN);
-    uneven |= (gemms[i].K + 255) / 256 != (gemms[0].K + 255) / 256;
-  }
-  if (tiles >= (int64_t(1) << 30)) return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
   if (uneven && tiles > dev->gemm_fp4_clusters && tiles <= kMaxSchedTiles && dev->gemm_fp4_clusters <= kMaxClusters) {
     static thread_local ListGroup4 g;
-    if (fill_fp4_group(g, gemms, n, &st) < 0) return st;
+    if (fill_fp4_group(g, gemms, n, tile_n, &st) < 0) return st;
     list_fp4_tiles(g, dev->gemm_fp4_clusters);
-    return launch_fp4_wide(g, nv, dev, stream);
+    return launch_fp4_tiles<WIDE>(g, nv, dev, stream);
   }
   if (n <= SmallGroup4::kProblems) {
     static thread_local SmallGroup4 g;
-    if (fill_fp4_group(g, gemms, n, &st) < 0) return st;
-    return launch_fp4_wide(g, nv, dev, stream);
+    if (fill_fp4_group(g, gemms, n, tile_n, &st) < 0) return st;
+    return launch_fp4_tiles<WIDE>(g, nv, dev, stream);
   }
   static thread_local LargeGroup4 g;
-  if (fill_fp4_group(g, gemms, n, &st) < 0) return st;
-  return launch_fp4_wide(g, nv, dev, stream);
+  if (fill_fp4_group(g, gemms, n, tile_n, &st) < 0) return st;
+  return launch_fp4_tiles<WIDE>(g, nv, dev, stream);
+}
+
+fp8t_status fp4_gemm_tiles(const fp8t_fp4_gemm_desc* gemms, int32_t n, const DeviceInfo* dev, cudaStream_t stream) {
+  using namespace fp8t::gemm;
+  int64_t narrow = 0, wide = 0, narrow_kb = 0, wide_kb = 0;      // tiles, and k-blocks of all of them
+  bool uneven = false;
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t m = (gemms[i].M + kBM - 1) / kBM, kb = (gemms[i].K + 255) / 256;
+    const int64_t tn = m * ((gemms[i].N + kBN - 1) / kBN), tw = m * ((gemms[i].N + kBN4w - 1) / kBN4w);
+    narrow += tn;
+    wide += tw;
+    narrow_kb += tn * kb;
+    wide_kb += tw * kb;
+    uneven |= kb != (gemms[0].K + 255) / 256;
+  }
+  if (narrow >= (int64_t(1) << 30)) return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_gemm: too many tiles in one launch");
+  // rounds of tiles, or with tiles of different length the clusters' even share of k-blocks
+  const int64_t c = dev->gemm_fp4_clusters;
+  const double tn = uneven ? double(narrow_kb) / c : double((narrow + c - 1) / c);
+  const double tw = uneven ? double(wide_kb) / c : double((wide + c - 1) / c);
+  return 1.36 * tw < tn && wide > c ? fp4_gemm_tiles_as<true>(gemms, n, wide, uneven, dev, stream)
+                                    : fp4_gemm_tiles_as<false>(gemms, n, narrow, uneven, dev, stream);
 }
 
 template <bool NV, int BT>
@@ -1402,7 +1431,7 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
   fp8t_status st = current_device(&dev);
   if (st != FP8T_OK) return st;
   // consecutive problems of one format and size class share a launch: at most 128 rows (the split kernel) or
-  // more (256 x 256 tiles)
+  // more (pair tiles)
   for (int32_t b0 = 0, b1 = 0; b0 < n_gemms; b0 = b1) {
     const bool few = gemms[b0].M <= fp8t::gemm::kMaxSplitRows;
     const int most = few ? fp8t::gemm::kMaxSplitProblems : fp8t::gemm::kMaxProblems;
@@ -1410,7 +1439,7 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
                   (gemms[b1].M <= fp8t::gemm::kMaxSplitRows) == few; ++b1) {
     }
     st = few ? fp4_gemm_split(gemms + b0, b1 - b0, plan_fp4_split(gemms + b0, b1 - b0, dev->sms), as_stream(stream))
-             : fp4_gemm_wide(gemms + b0, b1 - b0, dev, as_stream(stream));
+             : fp4_gemm_tiles(gemms + b0, b1 - b0, dev, as_stream(stream));
     if (st != FP8T_OK) return st;
   }
   return FP8T_OK;

@@ -7,24 +7,32 @@
 // of an 8-bit MMA of K = 32, at twice its values. Both operands are K-major (the 4-bit kinds read no
 // other order), two values per byte. A k-block is 256 values (128 bytes per row, four MMAs).
 //
-// Large problems (k_fp4_gemm): a cluster of two CTAs computes 256 x 256 tiles, each CTA holding 128 rows of
-// A and 128 of B. Per k-block every 128 rows of A or B bring 2 (MXFP4) or 4 (NVFP4) scale atoms, stored
-// next to each other ([MN / 128][K / 256]), which arrive as one TMA box of 1 or 2 KB; each CTA takes its
-// own A rows' and all of the tile's B rows'. The MMA warp copies an atom step (A 4, B 8 TMEM columns) right
-// before the MMAs that use it.
+// Large problems (k_fp4_gemm): a cluster of two CTAs computes a tile of 256 rows by 256 or 384 columns, each CTA
+// holding 128 rows of A and 128 (192) of B. Per k-block every 128 rows of A or B bring 2 (MXFP4) or 4
+// (NVFP4) scale atoms, stored next to each other ([MN / 128][K / 256]), which arrive as one TMA box of 1 or
+// 2 KB; each CTA takes its own A rows' and all of the tile's B rows'. The MMA warp copies an atom step (A 4,
+// B 8 or 12 TMEM columns) right before the MMAs that use it.
 //
-// What bounds it. An MMA (256 x 256 x 64) takes 128 cycles, a k-block 512; a scale copy takes the copy
-// path 44-64 cycles but runs beside earlier MMAs, so MXFP4's 6 copies per k-block are hidden (519 cycles
-// measured per k-block, operands resident) and NVFP4's 12 set the pace (717). Two things make that so:
+// What bounds it. An MMA (256 x 256 x 64) takes 128 cycles, a k-block of a 256-column tile 512; a scale copy
+// takes the copy path 44-71 cycles but runs beside earlier MMAs, so MXFP4's copies are hidden (519 cycles
+// per k-block measured with operands resident, 777 for 384 columns) and NVFP4's set the pace (717, 1139).
+// Two things make that so:
 //   - the issuing warp stays converged and one elected lane issues. Issued from a lane that left its warp, a
 //     copy after an mbarrier wait did not overlap the MMAs before it: 1034 against 773 cycles for 8
 //     copies and 8 MMAs per k-block;
 //   - copies are spread between the MMAs in the order of use.
-// Two accumulators let the epilogue of a tile run beside the next tile's MMAs. Two of 256 columns and the
-// scales (24 or 48) do not fit the 512 TMEM columns, so they overlap by kOv columns: accumulator 0 at
-// 0..255, accumulator 1 at 256 - kOv, scales after it. The epilogue reads the shared columns first and
-// releases them through a barrier of their own. (With one accumulator and 256 x 384 tiles the MMAs of a
-// 16384 x 11008 x 4096 product waited about 3.3 us per tile for the epilogue: 335 us MXFP4, 441 us NVFP4.)
+// Beyond that, what the SMs take in from L2 is the bound: about 11 TB/s in both forms (35 KB per SM and k-block
+// of a 256-column tile, 44 KB of a 384-column one with half as much work again).
+//   256 columns: two accumulators let the epilogue of a tile run beside the next tile's MMAs. Two of 256 columns
+//     and the scales (24 or 48) do not fit the 512 TMEM columns, so they overlap by kOv columns: accumulator 0
+//     at 0..255, accumulator 1 at 256 - kOv, scales after it. The epilogue reads the shared columns first and
+//     releases them through a barrier of their own.
+//   384 columns (an N = 256 and an N = 128 MMA per step): one accumulator at 0..383, scales after it; the
+//     epilogue pulls it into registers, releases it, then stores. The next tile's MMAs wait for that
+//     (about 1.5 us), but the tile needs a sixth fewer operand bytes per MMA.
+// 16384 x 11008 x 4096: 288 us (MXFP4) and 308 us (NVFP4) on 256 columns, 278 and 280 on 384; in a loop long
+// enough to reach the power cap 402 against 370 us with the cast (NVFP4). 1000 x 4096 x 4096 has 64 tiles of
+// 256 columns for 74 pairs, but 44 of 384, each half as long again: the host picks by rounds of tiles.
 // Rows of a ragged edge read zero codes (TMA fill), so M and N need not be multiples of the tile; K's
 // padding has zero codes and zero scales.
 // Warp roles (320 threads): warp 0 TMA producer; warp 1 MMA issuer (even CTA), TMEM allocation; warps 2-9
@@ -36,25 +44,30 @@
 namespace fp8t {
 namespace gemm {
 
-constexpr int kStages4 = 5;
+constexpr int kBN4w = 384;                                        // the wide tile
+template <bool WIDE>
+constexpr int kStages4 = WIDE ? 4 : 5;
 template <bool NV>
 constexpr int kSfBytes4 = (NV ? 4 : 2) * 512;                     // scales of 128 rows x 256 values
-template <bool NV>
-constexpr int kStageBytes4 = kABytes + kBBytes + 3 * kSfBytes4<NV>;
+constexpr int kB1Bytes4 = (kHalf / 2) * kBK;                      // wide: 64 more rows of B per CTA
+template <bool NV, bool WIDE>
+constexpr int kStageBytes4 = kABytes + kBBytes + 3 * kSfBytes4<NV> + (WIDE ? kB1Bytes4 + kSfBytes4<NV> : 0);
 template <bool NV>
 constexpr uint32_t kOv4 = NV ? 64 : 32;                           // columns the accumulators share
 template <bool NV>
 constexpr uint32_t kAcc1Col4 = 256 - kOv4<NV>;
-template <bool NV>
-constexpr uint32_t kSfCol4 = 512 - kOv4<NV>;
+template <bool NV, bool WIDE>
+constexpr uint32_t kSfCol4 = WIDE ? kBN4w : 512 - kOv4<NV>;
 constexpr int kEpiWarps4 = 8;
 constexpr int kThreads4 = 64 + 32 * kEpiWarps4;
 constexpr int kEpiBytes4 = kEpiWarps4 * 2 * kEpiChunkBytes;
-template <bool NV>
-constexpr int kSmemBytes4 = kStages4 * kStageBytes4<NV> + kEpiBytes4 + 1024 + 256;
-static_assert(kStageBytes4<false> % 1024 == 0 && kStageBytes4<true> % 1024 == 0, "stages stay 1024-byte aligned");
-static_assert(kSmemBytes4<true> <= 232448, "shared memory of an SM");
-static_assert(kSfCol4<false> + 2 * 12 <= 512 && kSfCol4<true> + 4 * 12 <= 512, "TMEM columns");
+template <bool NV, bool WIDE>
+constexpr int kSmemBytes4 = kStages4<WIDE> * kStageBytes4<NV, WIDE> + kEpiBytes4 + 1024 + 256;
+static_assert(kStageBytes4<false, false> % 1024 == 0 && kStageBytes4<true, false> % 1024 == 0 &&
+              kStageBytes4<false, true> % 1024 == 0 && kStageBytes4<true, true> % 1024 == 0, "stages stay 1024-byte aligned");
+static_assert(kSmemBytes4<true, false> <= 232448 && kSmemBytes4<true, true> <= 232448, "shared memory of an SM");
+static_assert(kSfCol4<false, false> + 2 * 12 <= 512 && kSfCol4<true, false> + 4 * 12 <= 512 &&
+              kSfCol4<true, true> + 4 * 16 <= 512, "TMEM columns");
 
 // Block-scaled instruction descriptor of the 4-bit kinds: E2M1 operands, K-major, scale type (bit 23:
 // 1 E8M0, 0 E4M3), scale-factor ids of A and B.
@@ -87,6 +100,7 @@ __device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc,
 // One GEMM of a grouped launch; tiles are numbered problem by problem.
 struct alignas(64) Problem4 {
   CUtensorMap a, b, d;             // codes [M][K/2], [N][K/2] in 128-row boxes; D [M][N] in 32 x 32 ones
+  CUtensorMap b64;                 // wide tiles: B in 64-row boxes
   CUtensorMap sfa, sfb;            // scales in rows of 256 words
   const float* sa;
   const float* sb;
@@ -136,9 +150,9 @@ __device__ __forceinline__ bool warp_aborted(const volatile int* flag) {
 }
 
 struct Smem4 {
-  uint64_t full[kStages4];      // even CTA: both CTAs' loads of a stage have landed
-  uint64_t empty[kStages4];     // both CTAs: the pair MMA has consumed a stage
-  uint64_t acc_full[2];         // both CTAs: an accumulator holds a finished tile
+  uint64_t full[5];             // even CTA: both CTAs' loads of a stage have landed
+  uint64_t empty[5];            // both CTAs: the pair MMA has consumed a stage
+  uint64_t acc_full[2];         // both CTAs: an accumulator holds a finished tile (wide: only the first)
   uint64_t acc_empty[2];        // even CTA: every epilogue warp of both CTAs has read an accumulator
   uint64_t acc_shared_free;     // even CTA: the warps that read the shared columns have
   uint64_t mma_done;            // even CTA: every issued MMA has completed
@@ -146,14 +160,42 @@ struct Smem4 {
   int abort;
 };
 
-template <bool NV, class G>
+// A packed 32 x 32 chunk (a row per lane) into the warp's swizzled staging buffer and out by TMA.
+__device__ __forceinline__ void store_chunk4(const CUtensorMap* map, uint8_t* my_buf, uint32_t& chunk_count,
+                                             const uint32_t (&w)[16], int lane, int n, int row0) {
+  uint8_t* buf = my_buf + (chunk_count & 1) * kEpiChunkBytes;
+  ++chunk_count;
+  if (lane == 0) bulk_wait_group_read<1>();                // the store that last used buf has read it
+  __syncwarp();
+  // row `lane` of the chunk: four 16-byte pieces, 64-byte swizzle, matching the store's map
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + (p ^ ((lane >> 1) & 3)) * 16) =
+        make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, smem_u32(buf), n, row0);
+    bulk_commit_group();
+  }
+}
+// 32 accumulator columns of this lane, scaled and packed as BF16.
+__device__ __forceinline__ void pack_chunk4(const uint32_t (&r)[32], float alpha, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    w[j] = pack_bf16x2(__fmul_rn(__uint_as_float(r[2 * j]), alpha), __fmul_rn(__uint_as_float(r[2 * j + 1]), alpha));
+}
+
+template <bool NV, bool WIDE, class G>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     k_fp4_gemm(const __grid_constant__ G g) {
   constexpr int kSf = kSfBytes4<NV>, kSfRows = NV ? 2 : 1;
+  constexpr int kStages = kStages4<WIDE>, kStage = kStageBytes4<NV, WIDE>, kTileN = WIDE ? kBN4w : kBN;
+  constexpr int kB = kBBytes + (WIDE ? kB1Bytes4 : 0), kStep = WIDE ? 16 : 12;   // B bytes; scale columns per step
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  // stage s: [A 128 x 128 B][B 128 x 128 B][scales of A | B rows 0..127 | B rows 128..255]
-  uint8_t* sEpi = smem + kStages4 * kStageBytes4<NV>;
+  // stage s: [A 128 x 128 B][B 128 x 128 B][wide: B 64 x 128 B][scales of A | B rows 0.. | 128.. | 256..]
+  uint8_t* sEpi = smem + kStages * kStage;
   Smem4* S = reinterpret_cast<Smem4*>(sEpi + kEpiBytes4);
   volatile int* abort_flag = &S->abort;
 
@@ -164,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
   const int my_tiles = g.tiles_of(cluster, n_clusters);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages4; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&S->full[s]), 1);
       mbar_init(smem_u32(&S->empty[s]), 1);
     }
@@ -206,11 +248,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       const Problem4& P = g.problem(tile);
       const int local = tile - P.tile_start, mt = local / P.tiles_n, nt = local % P.tiles_n;
       const int m0 = mt * kBM + static_cast<int>(rank) * kHalf;
-      const int n0 = nt * kBN + static_cast<int>(rank) * kHalf;
-      const int ra = 2 * mt + static_cast<int>(rank), rb = 2 * nt;          // 128-row blocks of the scales
+      const int n0 = nt * kTileN + static_cast<int>(rank) * kHalf;
+      const int n1 = nt * kTileN + 256 + static_cast<int>(rank) * (kHalf / 2);
+      const bool second = WIDE && nt * kTileN + 256 < P.N;                  // the N = 128 MMA has columns
+      const uint32_t tx = 2u * (kStage - (WIDE && !second ? kB1Bytes4 + kSf : 0));
+      const int ra = 2 * mt + static_cast<int>(rank), rb = (kTileN / 128) * nt;   // 128-row blocks of the scales
       const int num_kb = P.num_kb;                                           // k-blocks of 256 values
       for (int kb = 0; kb < num_kb; ++kb, ++it) {
-        const uint32_t s = it % kStages4, ph = (it / kStages4) & 1;
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
         if (warp_aborted(abort_flag)) break;
         if (!warp_wait(smem_u32(&S->empty[s]), ph ^ 1, limit, expire_main)) {
           *abort_flag = 1;
@@ -219,14 +264,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
         }
         if (one) {
           const uint32_t full_leader = mapa_shared(smem_u32(&S->full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), 2 * kStageBytes4<NV>);
-          const uint32_t a_dst = smem_u32(smem + s * kStageBytes4<NV>), b_dst = a_dst + kABytes;
-          const uint32_t sf_dst = b_dst + kBBytes;
+          if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), tx);
+          const uint32_t a_dst = smem_u32(smem + s * kStage), b_dst = a_dst + kABytes;
+          const uint32_t sf_dst = b_dst + kB;
           tma_load_2d_pair(a_dst, &P.a, kb * kBK, m0, full_leader);
           tma_load_2d_pair(b_dst, &P.b, kb * kBK, n0, full_leader);
           tma_load_2d_pair(sf_dst, &P.sfa, 0, (ra * num_kb + kb) * kSfRows, full_leader);
           tma_load_2d_pair(sf_dst + kSf, &P.sfb, 0, (rb * num_kb + kb) * kSfRows, full_leader);
           tma_load_2d_pair(sf_dst + 2 * kSf, &P.sfb, 0, ((rb + 1) * num_kb + kb) * kSfRows, full_leader);
+          if (second) {
+            tma_load_2d_pair(b_dst + kBBytes, &P.b64, kb * kBK, n1, full_leader);
+            tma_load_2d_pair(sf_dst + 3 * kSf, &P.sfb, 0, ((rb + 2) * num_kb + kb) * kSfRows, full_leader);
+          }
         }
         ++issued;
       }
@@ -235,10 +284,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     // an abort a stage may miss the peer's bytes, and the settle delay below covers loads in flight)
     if (leader) {
       const uint64_t t0 = globaltimer_ns();
-      for (uint32_t i = issued > kStages4 ? issued - kStages4 : 0; i < issued; ++i) {
+      for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
         const uint64_t spent = globaltimer_ns() - t0;
         if (spent >= kPairDrainNs) break;
-        mbar_wait(smem_u32(&S->full[i % kStages4]), (i / kStages4) & 1, kPairDrainNs - spent);
+        mbar_wait(smem_u32(&S->full[i % kStages]), (i / kStages) & 1, kPairDrainNs - spent);
       }
     }
   } else if (warp == 1) {
@@ -250,11 +299,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
         const int tile = g.tile_at(cluster, n_clusters, i);
         const Problem4& P = g.problem(tile);
         const int num_kb = P.num_kb;
-        const uint32_t acc = i & 1, aph = (i >> 1) & 1;
-        // this accumulator read by the epilogue of two tiles ago; the columns it shares with the other one
-        // by the previous tile's
+        const bool second = WIDE && (tile - P.tile_start) % P.tiles_n * kTileN + 256 < P.N;
+        const uint32_t acc = WIDE ? 0 : i & 1, aph = WIDE ? i & 1 : (i >> 1) & 1;
+        // this accumulator read by the epilogue of two tiles ago (wide: of the last); the columns it shares with
+        // the other one by the previous tile's
         if (!warp_wait(smem_u32(&S->acc_empty[acc]), aph ^ 1, limit, expire_main) ||
-            (i > 0 && !warp_wait(smem_u32(&S->acc_shared_free), (i - 1) & 1, limit, expire_main))) {
+            (!WIDE && i > 0 && !warp_wait(smem_u32(&S->acc_shared_free), (i - 1) & 1, limit, expire_main))) {
           *abort_flag = 1;
           if (one) record_error(kErrTimeout);
           break;
@@ -263,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
         const uint32_t d_tmem = tmem + acc * kAcc1Col4<NV>;
         bool ok = true;
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
-          const uint32_t s = it % kStages4, ph = (it / kStages4) & 1;
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
           if (!warp_wait(smem_u32(&S->full[s]), ph, limit, expire_main) || warp_aborted(abort_flag)) {
             if (one && !*abort_flag) record_error(kErrTimeout);
             *abort_flag = 1;
@@ -271,21 +321,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
             break;
           }
           if (one) {
-            const uint32_t a_base = smem_u32(smem + s * kStageBytes4<NV>), b_base = a_base + kABytes;
-            const uint32_t sf = b_base + kBBytes;
+            const uint32_t a_base = smem_u32(smem + s * kStage), b_base = a_base + kABytes;
+            const uint32_t sf = b_base + kB;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               // MXFP4: two scales per 64 values, so an atom step serves two MMAs (scale ids 0 and 2)
               const int a = NV ? k : k >> 1;
-              const uint32_t sc = tmem + kSfCol4<NV> + a * 12, id = NV ? 0 : (k & 1) * 2;
+              const uint32_t sc = tmem + kSfCol4<NV, WIDE> + a * kStep, id = NV ? 0 : (k & 1) * 2;
               if (NV || (k & 1) == 0) {
                 tc_cp_32x128b_warpx4_pair(sc, make_sf_desc(sf + a * 512));
                 tc_cp_32x128b_warpx4_pair(sc + 4, make_sf_desc(sf + kSf + a * 512));
                 tc_cp_32x128b_warpx4_pair(sc + 8, make_sf_desc(sf + 2 * kSf + a * 512));
+                if (second) tc_cp_32x128b_warpx4_pair(sc + 12, make_sf_desc(sf + 3 * kSf + a * 512));
               }
               tc_mma_fp4_pair<NV>(d_tmem, make_sw128_desc(a_base + k * kUmmaK), make_sw128_desc(b_base + k * kUmmaK),
                                   make_idesc_fp4<NV>(kBM, kBN, id), sc | id << 30, (sc + 4) | id << 30,
                                   (kb | k) != 0 ? 1u : 0u);
+              if (second)
+                tc_mma_fp4_pair<NV>(d_tmem + 256, make_sw128_desc(a_base + k * kUmmaK),
+                                    make_sw128_desc(b_base + kBBytes + k * kUmmaK), make_idesc_fp4<NV>(kBM, 128, id),
+                                    sc | id << 30, (sc + 12) | id << 30, (kb | k) != 0 ? 1u : 0u);
             }
             tc_commit_pair_mc(smem_u32(&S->empty[s]), 0x3);
           }
@@ -305,10 +360,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* my_buf = sEpi + (warp - 2) * 2 * kEpiChunkBytes;
     uint32_t chunk_count = 0;
-    constexpr int kShared = static_cast<int>(kOv4<NV>) / 32;    // chunks the accumulators share
+    [[maybe_unused]] constexpr int kShared = static_cast<int>(kOv4<NV>) / 32;    // chunks the accumulators share
     for (int i = 0; i < my_tiles; ++i) {
       const int tile = g.tile_at(cluster, n_clusters, i);
-      const uint32_t acc = i & 1, aph = (i >> 1) & 1;
+      const uint32_t acc = WIDE ? 0 : i & 1, aph = WIDE ? i & 1 : (i >> 1) & 1;
       if (warp_aborted(abort_flag)) break;
       if (!warp_wait(smem_u32(&S->acc_full[acc]), aph, limit, expire_epi)) {
         *abort_flag = 1;
@@ -320,46 +375,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
       const int M = P.M, N = P.N, local = tile - P.tile_start;
       const int row0 = (local / P.tiles_n) * kBM + static_cast<int>(rank) * kHalf + quad * 32;
-      const int n0 = (local % P.tiles_n) * kBN;
+      const int n0 = (local % P.tiles_n) * kTileN;
       const uint32_t t_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kAcc1Col4<NV>;
-      // the shared columns come first: accumulator 0's last chunks (half 1, walking down), accumulator
-      // 1's first (half 0, walking up)
+      if constexpr (WIDE) {
+        // this half's 192 columns into registers, then the accumulator is free
+        uint32_t w[kBN4w / 64][16];
+#pragma unroll
+        for (int s = 0; s < kBN4w / 64; ++s) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_base + (half * (kBN4w / 64) + s) * 32, r);
+          tmem_ld_wait();
+          tmem_reg_fence(r);
+          pack_chunk4(r, alpha, w[s]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_empty[0]), 0));
+#pragma unroll
+        for (int s = 0; s < kBN4w / 64; ++s) {
+          const int n = n0 + (half * (kBN4w / 64) + s) * 32;
+          if (n < N && row0 < M) store_chunk4(&P.d, my_buf, chunk_count, w[s], lane, n, row0);
+        }
+      } else {
+        // the shared columns come first: accumulator 0's last chunks (half 1, walking down), accumulator
+        // 1's first (half 0, walking up)
 #pragma unroll 1
-      for (int step = 0; step < 4; ++step) {
-        const int c = half * 4 + (acc == 0 ? 3 - step : step);
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t_base + c * 32, r);
-        tmem_ld_wait();
-        tmem_reg_fence(r);
-        if (step == kShared - 1 && half == (acc == 0 ? 1 : 0)) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_shared_free), 0));
-        }
-        if (step == 3) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_empty[acc]), 0));
-        }
-        if (n0 + c * 32 >= N || row0 >= M) continue;       // chunk entirely outside the matrix
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          w[j] = pack_bf16x2(__fmul_rn(__uint_as_float(r[2 * j]), alpha), __fmul_rn(__uint_as_float(r[2 * j + 1]), alpha));
-        uint8_t* buf = my_buf + (chunk_count & 1) * kEpiChunkBytes;
-        ++chunk_count;
-        if (lane == 0) bulk_wait_group_read<1>();          // the store that last used buf has read it
-        __syncwarp();
-        // row `lane` of the chunk: four 16-byte pieces, 64-byte swizzle, matching the store's map
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          *reinterpret_cast<uint4*>(buf + lane * 64 + (p ^ ((lane >> 1) & 3)) * 16) =
-              make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&P.d, smem_u32(buf), n0 + c * 32, row0);
-          bulk_commit_group();
+        for (int step = 0; step < 4; ++step) {
+          const int c = half * 4 + (acc == 0 ? 3 - step : step);
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_base + c * 32, r);
+          tmem_ld_wait();
+          tmem_reg_fence(r);
+          if (step == kShared - 1 && half == (acc == 0 ? 1 : 0)) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_shared_free), 0));
+          }
+          if (step == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_empty[acc]), 0));
+          }
+          if (n0 + c * 32 >= N || row0 >= M) continue;     // chunk entirely outside the matrix
+          uint32_t w[16];
+          pack_chunk4(r, alpha, w);
+          store_chunk4(&P.d, my_buf, chunk_count, w, lane, n0 + c * 32, row0);
         }
       }
     }

@@ -186,6 +186,33 @@ def test_gemm_between(cuda_lib, kind, M, N, K):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(2100, 4104, 544), (2304, 4224, 96), (2049, 4544, 32), (1281, 6536, 800)])
+def test_gemm_wide_tiles(cuda_lib, kind, M, N, K):
+    """Sizes that take 384-column tiles: a last column tile of 264, 384, 320 (its N = 128 MMA partly outside) and
+    8 columns (without that MMA), rows that leave one row or one CTA's half of a tile."""
+    check_gemm(cuda_lib, M, N, K, kind, seed=11)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shapes", [
+    [(700, 2000, 288), (900, 1544, 1088), (300, 2056, 96), (1100, 1280, 32), (200, 776, 2048)],     # 256 columns, lists
+    [(1536, 4104, 64), (1300, 3864, 576), (520, 1160, 1024)],                                       # 384 columns, lists
+    [(1300, 1160, 160)] * 6])                                                                       # more than four
+def test_gemm_grouped_large(cuda_lib, kind, shapes):
+    descs, refs = [], []
+    for i, (M, N, K) in enumerate(shapes):
+        A, sa, a = operand(M, K, kind, i)
+        B, sb, b = operand(N, K, kind, 50 + i)
+        D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        descs.append(dict(A=A, a_sf=sa, B=B, b_sf=sb, quant=kind, D=D, b_scale_inv=f32(0.25)))
+        refs.append(reference(a, b, 0.25))
+    cuda_lib.fp4_gemm_multi(descs)
+    cuda_lib.fp8t_check_device_error()
+    for d, (R, ab) in zip(descs, refs):
+        assert gemm_within_tolerance(bf16_bits(d["D"]), R, ab).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_gemm_scales_missing_means_one(cuda_lib, kind):
     A, sa, a = operand(40, 256, kind, 1)
     B, sb, b = operand(64, 256, kind, 2)
