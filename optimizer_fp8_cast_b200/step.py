@@ -23,10 +23,17 @@ for the next step with that step's scale, which the cast launch's update has alr
 the cast launch then carries only the scale update of W (its amax came from AdamW), and W is
 never read by a cast. The first step's W cast happens once, at construction (prime). All
 scalars stay on the device; nothing in a step synchronises with the host.
+
+Other recipes: "current" (every scale from the tensor's own amax), "mxfp8" (block scales, both
+orientations cast, block-scaled GEMMs) and the 4-bit forms "mxfp4" and "nvfp4": X, W and dY cast along
+both of their axes in one launch (the column-wise copies transposed), the three products in another,
+AdamW with its norm pass. "nvfp4" has a per-tensor scale beside the block scales, delayed like the FP8
+ones (its update follows the casts, with 448 * 6 as the format's largest value).
 """
 import torch
 
-from . import (AMAX_MAX, AMAX_MOST_RECENT, CURRENT_WORKSPACE_BYTES, E4M3, E5M2, FP8_MAX,
+from . import (AMAX_MAX, AMAX_MOST_RECENT, CURRENT_WORKSPACE_BYTES, E4M3, E5M2, FP4_MAX, FP8_MAX,
+               Q_MXFP4, Q_NVFP4, fp4_cast_multi, fp4_gemm_multi, fp4_scale_bytes,
                fp8_cast_transpose_amax, fp8_cast_transpose_amax_current_multi,
                fp8_cast_transpose_amax_multi, fp8_cast_transpose_amax_update_multi,
                fp8_gemm_multi, fp8_gemm_multi_sumsq, fp8_gemm_sumsq_workspace_bytes,
@@ -105,12 +112,25 @@ class Fp8LinearStep:
         self.adamw_ticket = torch.zeros(1, dtype=torch.int32, device=self.device)
         # current scaling: every scale from the tensor's own amax (no history, no delayed update)
         # mxfp8: E4M3 codes with a scale per 32 values, both orientations, block-scaled GEMMs
-        assert recipe in ("delayed", "current", "mxfp8")
+        # mxfp4, nvfp4: E2M1 codes, both orientations, 4-bit GEMMs; AdamW sums the gradient squares itself
+        assert recipe in ("delayed", "current", "mxfp8", "mxfp4", "nvfp4")
         self.recipe = recipe
+        self.quant = {"mxfp4": Q_MXFP4, "nvfp4": Q_NVFP4}.get(recipe)
         self.current_ws = torch.zeros(CURRENT_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         if recipe != "delayed":
             fused_update = fused_wcast = False
             self.fused_update = False
+        if self.quant is not None:
+            self.fused_norm = fused_norm = False
+            self.fp8_max.fill_(FP4_MAX)
+            u8 = dict(dtype=torch.uint8, device=self.device)
+            for L in self.layers:
+                shapes = dict(X=(tokens, L.fin), W=(L.fin, L.fout), dY=(tokens, L.fout))
+                L.fp4 = {}
+                for name, (r, c) in shapes.items():
+                    L.fp4[name] = dict(q_row=torch.empty(r, c // 2, **u8), q_col=torch.empty(c, r // 2, **u8),
+                                       sf_row=torch.empty(fp4_scale_bytes(r, c, self.quant), **u8),
+                                       sf_col=torch.empty(fp4_scale_bytes(c, r, self.quant), **u8))
         if recipe == "mxfp8":
             u8 = dict(dtype=torch.uint8, device=self.device)
             for L in self.layers:
@@ -210,6 +230,34 @@ class Fp8LinearStep:
         else:
             fp8_mx_gemm_multi(self.mx_gemm_descs(), stream=stream)
 
+    def _fp4_scalars(self, k, role, names):
+        """NVFP4's per-tensor scalars of one tensor (MXFP4 has none): argument name -> slot."""
+        if self.recipe != "nvfp4":
+            return {}
+        return {arg: self._slot(getattr(self, t), 3 * k + role) for arg, t in names.items()}
+
+    def fp4_cast_all(self, xs, dys, stream=None):
+        """4-bit: X, W and dY along both of their axes, as the products read them."""
+        casts = []
+        for k, L in enumerate(self.layers):
+            for role, name, src in ((ROLE_X, "X", xs[k]), (ROLE_W, "W", L.W), (ROLE_DY, "dY", dys[k])):
+                casts.append(dict(x=src, quant=self.quant, **L.fp4[name],
+                                  **self._fp4_scalars(k, role, dict(scale="scale", amax="amax", scale_inv="sinv_used"))))
+        fp4_cast_multi(casts, stream=stream)
+
+    def fp4_gemm_all(self, stream=None):
+        """The 4-bit fprop, dgrad and wgrad of every layer in one grouped call."""
+        out = []
+        for k, L in enumerate(self.layers):
+            for a, aw, ra, b, bw, rb, D in (("X", "row", ROLE_X, "W", "col", ROLE_W, L.Y),
+                                            ("dY", "row", ROLE_DY, "W", "row", ROLE_W, L.dX),
+                                            ("X", "col", ROLE_X, "dY", "col", ROLE_DY, L.dW)):
+                out.append(dict(A=L.fp4[a]["q_" + aw], a_sf=L.fp4[a]["sf_" + aw], B=L.fp4[b]["q_" + bw],
+                                b_sf=L.fp4[b]["sf_" + bw], quant=self.quant, D=D,
+                                **self._fp4_scalars(k, ra, dict(a_scale_inv="sinv_used")),
+                                **self._fp4_scalars(k, rb, dict(b_scale_inv="sinv_used"))))
+        fp4_gemm_multi(out, stream=stream)
+
     def cast_all_current(self, xs, dys, stream=None):
         """Current scaling: the X, W and dY scales from their own amax, then the casts."""
         descs = []
@@ -307,6 +355,13 @@ class Fp8LinearStep:
             self.mx_gemm_all(stream, sumsq=self.fused_norm)
             self.adamw(stream, presummed=self.fused_norm)
             return
+        if self.quant is not None:
+            self.fp4_cast_all(xs, dys, stream)
+            if self.recipe == "nvfp4":
+                self.scale_update(stream)          # the products read sinv_used, not what this writes
+            self.fp4_gemm_all(stream)
+            self.adamw(stream)
+            return
         if self.recipe == "current":
             self.amax.zero_()                  # amax slots report this step's tensors only
             self.cast_all_current(xs, dys, stream)
@@ -373,6 +428,15 @@ class Fp8LinearStep:
         if self.recipe == "mxfp8":
             return ((3 * len(self.layers) + 7) // 8 + (3 * len(self.layers) + 23) // 24 +
                     (1 if self.fused_norm else 2) * n_adamw_batches)
+        if self.quant is not None:
+            # the products share launches in runs of one size class: up to 4 of at most 128 rows, up to 24 of more
+            n, run, last = 0, 0, None
+            for rows in (r for L in self.layers for r in (self.tokens, self.tokens, L.fin)):
+                few = rows <= 128
+                if few != last or run == (4 if few else 24):
+                    n, run, last = n + 1, 0, few
+                run += 1
+            return (3 * len(self.layers) + 7) // 8 + (self.recipe == "nvfp4") + n + 2 * n_adamw_batches
         n_scale_launches = 0 if (self.fused_update and not self.side_update) or self.recipe == "current" else 1
         if self.recipe == "current":
             n_cast_launches *= 2                   # an amax launch before each cast launch
