@@ -443,13 +443,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
 // tiles for 74 pairs), and its time is that of streaming B (the weights). Here the weights are the 128-row
 // operand of a one-CTA MMA and the BT tokens the other, so a tile is 128 rows of B by all rows of A, and
 // the S CTAs of a cluster each take a contiguous part of K. Every CTA leaves its FP32
-// partial tile in the shared memory of the CTAs that own its tokens (token t belongs to rank t mod S);
-// after a cluster barrier each owner adds the S partials in rank order, scales, rounds and stores its
-// tokens' rows of D, 128 columns of a row at a time. No workspace, and the order of additions is fixed.
+// partial tile in the shared memory of the CTAs that own its tokens (groups of four: group j belongs to rank
+// j mod S, 16 bytes of a weight row at a time); after a cluster barrier each owner adds the S partials in rank
+// order, scales, rounds and stores its tokens' rows of D, 128 columns of a row at a time. No workspace, and
+// the order of additions is fixed.
 // TMEM: accumulator (weight rows x tokens) in columns 0..BT-1, then the scales.
 constexpr int kSplitThreads = 128;
 constexpr int kMaxSplitProblems = 4;
 constexpr int64_t kMaxSplitRows = 128;
+// The most slots that `groups` of four tokens take over 1 .. 8 owners: S * ceil(groups / S).
+constexpr int split_slots(int groups) {
+  int most = 0;
+  for (int s = 1; s <= 8; ++s) most = s * ((groups + s - 1) / s) > most ? s * ((groups + s - 1) / s) : most;
+  return most;
+}
 template <bool NV, int BT>
 struct SplitShape {
   static constexpr int kSf = (NV ? 4 : 2) * 512;                 // scale bytes per 128 rows and k-block
@@ -460,10 +467,11 @@ struct SplitShape {
   // partials: beside the stages while two CTAs still fit an SM, so that a CTA may receive them while it
   // computes; else over the stages, behind one more cluster barrier
   static constexpr bool kApart = BT <= 32;
-  static constexpr int kRed = kApart ? 128 * 4 * (BT + 8) : 0;     // ceil(BT / S) * S tokens at most
+  static constexpr int kRedBytes = split_slots(BT / 4) * 128 * 16;
+  static constexpr int kRed = kApart ? kRedBytes : 0;
   static constexpr int kSmem = kStages * kStage + kRed + 1024 + 256;
   static_assert(BT + (NV ? 4 : 2) * kSfCols <= kTmem, "TMEM columns");
-  static_assert(kApart || 128 * (BT + 8) * 4 <= kStages * kStage, "the partial tiles fit the stage buffers");
+  static_assert(kApart || kRedBytes <= kStages * kStage, "the partial tiles fit the stage buffers");
   static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
   static_assert(kStage % 1024 == 0, "stages stay 1024-byte aligned");
 };
@@ -618,8 +626,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     mbar_wait(smem_u32(&S->done), 0, kDrainLimitNs);       // MMAs in flight, whatever the limit was
   }
   tc_fence_after();
-  const int per = (BT + ways - 1) / ways;    // tokens per owner
-  uint32_t red;                              // [ways][per][128] f32
+  const int per = (BT / 4 + ways - 1) / ways;   // slots: groups of four tokens per owner
+  uint32_t red;                                 // [ways][per][128] x 4 f32
   if (Sh::kApart) {
     red = smem_u32(smem + Sh::kStages * Sh::kStage);
     if (ways > 1) cluster_wait();            // every CTA of the cluster runs
@@ -628,7 +636,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     __syncthreads();                         // the MMAs that read the stage buffers are done, in this CTA
     if (ways > 1) cluster_sync();            // and in every CTA that receives partials
   }
-  int owner = 0, slot = 0;                   // of the token: t mod ways, t / ways
+  int owner = 0, slot = 0;                      // of the group: j mod ways, j / ways
 #pragma unroll 1
   for (int c = 0; c < BT && c < P.M; c += 16) {
     uint32_t r[16];
@@ -636,10 +644,11 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     tmem_ld_wait();
     tmem_reg_fence(r);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (c + j >= P.M) break;
-      const float v = kb1 > kb0 ? __uint_as_float(r[j]) : 0.0f;
-      st_cluster_f32(mapa_shared(red + ((rank * per + slot) * 128 + threadIdx.x) * 4, owner), v);
+    for (int j = 0; j < 4; ++j) {
+      if (c + 4 * j >= P.M) break;
+      if (kb1 == kb0) r[4 * j] = r[4 * j + 1] = r[4 * j + 2] = r[4 * j + 3] = 0u;
+      st_cluster_v4(mapa_shared(red + ((rank * per + slot) * 128 + threadIdx.x) * 16, owner), r[4 * j], r[4 * j + 1],
+                    r[4 * j + 2], r[4 * j + 3]);
       if (++owner == ways) {
         owner = 0;
         ++slot;
@@ -653,19 +662,24 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   if (*abort_flag) return;                   // D is incomplete; the error word says so
   const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
-  const float2* part = reinterpret_cast<const float2*>(smem + (red - smem_u32(smem)));
-  const int pair = threadIdx.x & 63, n = n0 + 2 * pair;
-  for (int t = threadIdx.x >> 6; t * ways + rank < P.M; t += kSplitThreads / 64) {
-    const int m = t * ways + rank;
+  const float4* part = reinterpret_cast<const float4*>(smem + (red - smem_u32(smem)));
+  const int pair = threadIdx.x & 63, n = n0 + 2 * pair;      // two weight rows: adjacent columns of D
+  for (int s = threadIdx.x >> 6; (s * ways + rank) * 4 < P.M; s += kSplitThreads / 64) {
     if (n >= P.N) break;
-    float2 v = part[t * 64 + pair];
-    for (int s = 1; s < ways; ++s) {
-      const float2 o = part[(s * per + t) * 64 + pair];
-      v.x = __fadd_rn(v.x, o.x);
-      v.y = __fadd_rn(v.y, o.y);
+    float4 x = part[s * 128 + 2 * pair], y = part[s * 128 + 2 * pair + 1];
+    for (int w = 1; w < ways; ++w) {
+      const float4 u = part[(w * per + s) * 128 + 2 * pair], v = part[(w * per + s) * 128 + 2 * pair + 1];
+      x.x = __fadd_rn(x.x, u.x); x.y = __fadd_rn(x.y, u.y); x.z = __fadd_rn(x.z, u.z); x.w = __fadd_rn(x.w, u.w);
+      y.x = __fadd_rn(y.x, v.x); y.y = __fadd_rn(y.y, v.y); y.z = __fadd_rn(y.z, v.z); y.w = __fadd_rn(y.w, v.w);
     }
-    *reinterpret_cast<uint32_t*>(P.D + static_cast<int64_t>(m) * P.N + n) =
-        pack_bf16x2(__fmul_rn(v.x, alpha), __fmul_rn(v.y, alpha));
+    const int m = (s * ways + rank) * 4;
+    const uint32_t o[4] = {pack_bf16x2(__fmul_rn(x.x, alpha), __fmul_rn(y.x, alpha)),
+                           pack_bf16x2(__fmul_rn(x.y, alpha), __fmul_rn(y.y, alpha)),
+                           pack_bf16x2(__fmul_rn(x.z, alpha), __fmul_rn(y.z, alpha)),
+                           pack_bf16x2(__fmul_rn(x.w, alpha), __fmul_rn(y.w, alpha))};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (m + k < P.M) *reinterpret_cast<uint32_t*>(P.D + static_cast<int64_t>(m + k) * P.N + n) = o[k];
   }
 }
 
