@@ -68,10 +68,13 @@ __device__ __forceinline__ int cast_tensor_of(const CastGroup& g, int tile) {
   return ti;
 }
 
-__device__ __forceinline__ void issue_cast_tile(const CastGroup& g, int tile, uint32_t dst, uint32_t bar) {
-  const CastTensor& T = g.t[cast_tensor_of(g, tile)];
-  const int local = tile - T.tile_start, rt = local / T.tiles_c;
-  const int r0 = rt * kTile, c0 = (local - rt * T.tiles_c) * kTile;
+// One thread: the loads of a tile, and its tensor, row tile and column tile for the CTA.
+__device__ __forceinline__ void issue_cast_tile(const CastGroup& g, int tile, uint32_t dst, uint32_t bar, int4& at) {
+  const int ti = cast_tensor_of(g, tile);
+  const CastTensor& T = g.t[ti];
+  const int local = tile - T.tile_start, rt = local / T.tiles_c, ct = local - rt * T.tiles_c;
+  const int r0 = rt * kTile, c0 = ct * kTile;
+  at = make_int4(ti, rt, ct, 0);
   mbar_arrive_expect_tx(bar, kXBytes);               // out-of-range parts are zero-filled
   tma_load_2d(dst, &T.x_map, c0, r0, bar);
   tma_load_2d(dst + kHalfBytes, &T.x_map, c0 + 64, r0, bar);
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
   uint64_t* full = reinterpret_cast<uint64_t*>(atom_c + kAtomBytes);
   __shared__ int s_abort;
   __shared__ float factors[128];             // NVFP4: g / s of the current tensor
+  __shared__ int4 where[2];                  // per buffer: tensor, row tile, column tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int stride = static_cast<int>(gridDim.x);
   int cur = -1;                              // tensor of the factors
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
     for (int b = 0; b < 2; ++b) {
       const int tile = static_cast<int>(blockIdx.x) + b * stride;
       if (tile < g.total_tiles) {
-        issue_cast_tile(g, tile, smem_u32(xbuf + b * kXBytes), smem_u32(&full[b]));
+        issue_cast_tile(g, tile, smem_u32(xbuf + b * kXBytes), smem_u32(&full[b]), where[b]);
         pending |= 1u << b;
       }
     }
@@ -222,16 +226,20 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
         pending &= ~(1u << buf);
       }
     }
-    const int ti = cast_tensor_of(g, tile);
-    const CastTensor& T = g.t[ti];
-    const bool nv = T.kind == blk::kNVFP4;
-    const float gs = nv ? __ldg(T.scale) : 1.0f;
-    if (nv && ti != cur) fill_factors(factors, gs);   // the last reads are behind the previous tile's barrier
-    cur = ti;
     __syncthreads();                          // tile landed; the previous tile's atoms written
     if (s_abort) break;
-    const int local = tile - T.tile_start, rt = local / T.tiles_c, ct = local - rt * T.tiles_c;
-    const int r0 = rt * kTile, c0 = ct * kTile, rows = T.rows, cols = T.cols;
+    const int4 at = where[buf];
+    const CastTensor& T = g.t[at.x];
+    const int rt = at.y, ct = at.z, r0 = rt * kTile, c0 = ct * kTile, rows = T.rows, cols = T.cols;
+    const bool nv = T.kind == blk::kNVFP4;
+    const float gs = nv ? __ldg(T.scale) : 1.0f;
+    if (at.x != cur) {                        // the same in every thread; the factors of the last are read
+      cur = at.x;
+      if (nv) {
+        fill_factors(factors, gs);
+        __syncthreads();
+      }
+    }
     const uint8_t* xs = xbuf + buf * kXBytes;
 
     if (T.q_col) {
@@ -249,7 +257,7 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
     if (T.q_row || T.amax_bits) {
       const int b = lane >> 3;
       uint32_t top = 0;
-#pragma unroll 1
+#pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int row = 64 * u + 8 * warp + (lane & 7);
         uint4 out;
@@ -267,10 +275,10 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
     }
     __syncthreads();                          // input tile consumed; the atoms complete
     if (tid == 0) {                           // refill the buffer just consumed
-      if (T.scale_inv && local == 0) *T.scale_inv = __fdiv_rn(1.0f, gs);
+      if (T.scale_inv && rt == 0 && ct == 0) *T.scale_inv = __fdiv_rn(1.0f, gs);
       const int next = tile + 2 * stride;
       if (next < g.total_tiles) {
-        issue_cast_tile(g, next, smem_u32(xbuf + buf * kXBytes), smem_u32(&full[buf]));
+        issue_cast_tile(g, next, smem_u32(xbuf + buf * kXBytes), smem_u32(&full[buf]), where[buf]);
         pending |= 1u << buf;
         pending_ph = (pending_ph & ~(1u << buf)) | (static_cast<uint32_t>(((i + 2) >> 1) & 1) << buf);
       }

@@ -56,29 +56,19 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
   return r;
 }
 
-// Shared exponent of a block from the bit pattern of its largest f32 magnitude; NaN is the caller's.
-__device__ __forceinline__ int e8m0_exponent(uint32_t m, int emax) {
-  if (m == 0) return -127;
-  if (m >= 0x7F800000u) return 127;
-  const int e = static_cast<int>(m >> 23);
-  const int fl = e ? e - 127 : (31 - __clz(m)) - 149;         // floor(log2) of normal / subnormal
-  return max(-127, min(127, fl - emax));
-}
-// 2^-X (2^-127 is the subnormal 0x00400000).
-__device__ __forceinline__ float pow2_neg(int X) {
-  return X == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - X) << 23);
-}
-
-// E8M0 block: the scale byte and the factor the block's values are multiplied by. A NaN in the block
-// gives the byte 0xFF and unit scale.
+// E8M0 block: the scale byte X + 127 of the largest f32 magnitude's bit pattern, and the factor 2^-X that the
+// block's values are multiplied by. With e the pattern's exponent field, floor(log2 amax) is e - 127 for a normal
+// amax, so the byte is e - emax, clamped at 0 (X = -127); a subnormal or zero amax (e = 0) clamps there too.
+// An infinity gives 254 (X = 127; 2^-127 is the subnormal 0x00400000), a NaN 0xFF and unit scale.
 __device__ __forceinline__ uint8_t e8m0_scale(uint32_t amax_bits, int emax, float& factor) {
-  if (amax_bits > 0x7F800000u) {
-    factor = 1.0f;
-    return 0xFF;
+  uint32_t byte = static_cast<uint32_t>(max(static_cast<int>(amax_bits >> 23) - emax, 0));
+  uint32_t f = (254u - byte) << 23;
+  if (amax_bits >= 0x7F800000u) {
+    byte = amax_bits > 0x7F800000u ? 255u : 254u;
+    f = amax_bits > 0x7F800000u ? 0x3F800000u : 0x00400000u;
   }
-  const int X = e8m0_exponent(amax_bits, emax);
-  factor = pow2_neg(X);
-  return static_cast<uint8_t>(X + 127);
+  factor = __uint_as_float(f);
+  return static_cast<uint8_t>(byte);
 }
 
 // E4M3 code (0 .. 0x7E) of (amax * g) / 6, or 0x7F for a NaN.
