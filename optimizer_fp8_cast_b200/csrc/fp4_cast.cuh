@@ -13,7 +13,9 @@
 // quantise to zero codes and the scales of an all-zero block, so the atoms of a ragged edge are complete.
 // Every warp does an eighth of both copies:
 //   column-wise: two adjacent columns of 32 rows per thread (one 4-byte shared load per row, a warp covers the
-//     64 columns of a box row: no bank conflicts), 16 bytes of codes to each of the two transposed rows;
+//     64 columns of a box row: no bank conflicts), 16 bytes of codes for each of the two transposed rows, staged
+//     in shared memory (64-byte swizzle) and stored by one TMA box per tile (straight 16-byte stores, each half
+//     a sector, cost 3.5 of 28 us on 8192 x 4096);
 //   row-wise: a quarter-warp per block of 8 consecutive rows, 16 bytes of codes per block.
 // Bound: HBM, 2 B read + 0.5 B per copy written (+ 1/32 B MXFP4, 1/16 B NVFP4 of scales) per element; with both
 // copies every element is quantised twice, and the instructions per element (BF16 pairs compared as pairs,
@@ -34,10 +36,12 @@ constexpr int kCastTensors = 8;
 constexpr int kHalfBytes = kTile * 64 * 2;                 // one 128-row x 64-column BF16 box
 constexpr int kXBytes = 2 * kHalfBytes;
 constexpr int kAtomBytes = 2 * 512;                        // atoms of a tile and orientation (NVFP4: 2)
-constexpr int kCastSmemBytes = 2 * kXBytes + 2 * kAtomBytes + 64 + 1024 /*alignment*/;
+constexpr int kStageBytes = kTile * kTile / 2;             // column-wise codes of a tile: 128 rows of 64 bytes
+constexpr int kCastSmemBytes = 2 * kXBytes + kStageBytes + 2 * kAtomBytes + 64 + 1024 /*alignment*/;
 
 struct alignas(64) CastTensor {
   CUtensorMap x_map;               // BF16 [rows][cols], 64 x 128 boxes, 128-byte swizzle
+  CUtensorMap qc_map;              // q_col as bytes [cols][rows / 2], 64 x 128 boxes, 64-byte swizzle
   const void* x;
   uint8_t* q_row;                  // [rows][cols / 2] (may be null)
   uint8_t* sf_row;                 // atoms [rows / 128][K = cols]
@@ -180,11 +184,12 @@ __device__ __forceinline__ uint32_t row_block(const uint8_t* xs, int row, int b3
   return top;
 }
 
-__global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_constant__ CastGroup g) {
+__global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_constant__ CastGroup g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* xbuf = smem;                                             // [2][2 boxes][128][128 B]
-  uint8_t* atom_r = smem + 2 * kXBytes;
+  uint8_t* stage = smem + 2 * kXBytes;                              // [128 columns][64 B], swizzled
+  uint8_t* atom_r = stage + kStageBytes;
   uint8_t* atom_c = atom_r + kAtomBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(atom_c + kAtomBytes);
   __shared__ int s_abort;
@@ -225,6 +230,7 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
       } else {
         pending &= ~(1u << buf);
       }
+      bulk_wait_group_read<0>();              // the previous tile's staged codes are stored
     }
     __syncthreads();                          // tile landed; the previous tile's atoms written
     if (s_abort) break;
@@ -248,11 +254,10 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
       uint4 out[2];
       if (nv) col_block<true>(xs, rb, col, gs, factors, out, atom_c);
       else    col_block<false>(xs, rb, col, gs, factors, out, atom_c);
-      if (r0 + 32 * rb < rows && c0 + col < cols) {   // rows, cols are multiples of 32: whole blocks
-        uint8_t* dst = T.q_col + static_cast<int64_t>(c0 + col) * (rows >> 1) + ((r0 + 32 * rb) >> 1);
-        *reinterpret_cast<uint4*>(dst) = out[0];
-        *reinterpret_cast<uint4*>(dst + (rows >> 1)) = out[1];
-      }
+      uint8_t* s = stage + col * 64 + ((rb ^ (lane & 3)) << 4);      // (col >> 1) & 3 = lane & 3, also for col + 1
+      *reinterpret_cast<uint4*>(s) = out[0];
+      *reinterpret_cast<uint4*>(s + 64) = out[1];
+      fence_proxy_async_smem();                                      // visible to the TMA store
     }
     if (T.q_row || T.amax_bits) {
       const int b = lane >> 3;
@@ -275,6 +280,10 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
     }
     __syncthreads();                          // input tile consumed; the atoms complete
     if (tid == 0) {                           // refill the buffer just consumed
+      if (T.q_col) {                          // clipped at the matrix edges
+        tma_store_2d(&T.qc_map, smem_u32(stage), r0 >> 1, c0);
+        bulk_commit_group();
+      }
       if (T.scale_inv && rt == 0 && ct == 0) *T.scale_inv = __fdiv_rn(1.0f, gs);
       const int next = tile + 2 * stride;
       if (next < g.total_tiles) {
@@ -304,6 +313,7 @@ __global__ void __launch_bounds__(kCastThreads, 3) k_fp4_cast(const __grid_const
     // loads still in flight after an abort must land before shared memory is released
     for (int b = 0; b < 2; ++b)
       if (pending & (1u << b)) mbar_wait(smem_u32(&full[b]), (pending_ph >> b) & 1u, kDrainLimitNs);
+    bulk_wait_group<0>();                     // stores complete before the CTA exits
   }
 }
 

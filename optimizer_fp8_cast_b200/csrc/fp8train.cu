@@ -1141,6 +1141,15 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
                       dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
       if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit cast input) failed (%d)", (int)r);
+      if (t.q_col) {
+        cuuint64_t qdims[2] = {static_cast<cuuint64_t>(t.rows / 2), static_cast<cuuint64_t>(t.cols)};
+        cuuint64_t qstrides[1] = {static_cast<cuuint64_t>(t.rows / 2)};
+        cuuint32_t qbox[2] = {static_cast<cuuint32_t>(kTile / 2), static_cast<cuuint32_t>(kTile)};
+        r = fn(&T.qc_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, t.q_col, qdims, qstrides, qbox, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit column codes) failed (%d)", (int)r);
+      }
       T.x = t.x_bf16;
       T.q_row = static_cast<uint8_t*>(t.q_row);
       T.sf_row = static_cast<uint8_t*>(t.scales_row);
