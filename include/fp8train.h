@@ -363,8 +363,8 @@ typedef enum fp8t_quant {
  *          infinite: 127), scale byte X + 127, code = e2m1(x * 2^-X). A NaN in the block gives the byte
  *          0xFF (E2M1 has no NaN; the codes of such a block are those at unit scale, a NaN becomes 6).
  *   NVFP4: g is the tensor's f32 scale, s = e4m3((amax * g) / 6) of the block's 16 values, saturating at
- *          448, code = e2m1(x * (g / s)), every f32 operation rounded separately; s = 0 gives zero codes;
- *          a NaN gives the byte 0x7F. The tensor stands for code * s / g. A g of 2688 / amax (= 448 * 6 /
+ *          448, code = e2m1(x * (g / s)), every f32 operation rounded separately; s = 0 gives zero codes, and
+ *          so does a g below 0 (s has no sign); a NaN gives the byte 0x7F. The tensor stands for code * s / g. A g of 2688 / amax (= 448 * 6 /
  *          amax) uses the whole range: fp8_scale_update with d_fp8_max = 2688 gives it under delayed
  *          scaling.
  * Scale layout: the 512-byte atoms of MXFP8 (128 rows x 4 consecutive scales: byte (i % 32) * 16 +

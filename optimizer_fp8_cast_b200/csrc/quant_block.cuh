@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t nvfp4_scale_code(uint32_t amax_bits, float g
   const float t = __fmul_rn(__uint_as_float(amax_bits), g);
   float p = __fmul_rn(t, 0.16666667163372040f);
   if ((__float_as_uint(p) & 0x7FFFFu) == 0) p = __fdiv_rn(t, 6.0f);
-  return p != p ? 0x7Fu : cvt_fp8x2<0>(p, 0.0f) & 0xFFu;        // p >= 0
+  return p > 0.0f ? cvt_fp8x2<0>(p, 0.0f) & 0xFFu : p != p ? 0x7Fu : 0u;      // a g below 0 counts as 0
 }
 // g / s of a scale code (1 for the NaN code, 0 for s = 0). The E4M3 exponent and mantissa are f32's with
 // another bias; subnormals are multiples of 2^-9.
