@@ -252,7 +252,9 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
       // column-wise: rows 32 * (warp % 4) .. + 31, columns 2 * lane (+1) of box warp / 4
       const int rb = warp & 3, col = 64 * (warp >> 2) + 2 * lane;
       uint4 out[2];
-      if (nv) col_block<true>(xs, rb, col, gs, factors, out, atom_c);
+      // a block past the matrix has zero values; under g = 0 its scale is 0 also where gs is not finite
+      const float ge = r0 + 32 * rb < rows && c0 + col < cols ? gs : 0.0f;
+      if (nv) col_block<true>(xs, rb, col, ge, factors, out, atom_c);
       else    col_block<false>(xs, rb, col, gs, factors, out, atom_c);
       uint8_t* s = stage + col * 64 + ((rb ^ (lane & 3)) << 4);      // (col >> 1) & 3 = lane & 3, also for col + 1
       *reinterpret_cast<uint4*>(s) = out[0];
@@ -266,10 +268,11 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
       for (int u = 0; u < 2; ++u) {
         const int row = 64 * u + 8 * warp + (lane & 7);
         uint4 out;
-        const uint32_t m = nv ? row_block<true>(xs, row, b, gs, factors, out, atom_r)
+        const bool in = r0 + row < rows && c0 + 32 * b < cols;  // cols is a multiple of 32
+        const uint32_t m = nv ? row_block<true>(xs, row, b, in ? gs : 0.0f, factors, out, atom_r)
                               : row_block<false>(xs, row, b, gs, factors, out, atom_r);
         top = max(top, m);
-        if (T.q_row && r0 + row < rows && c0 + 32 * b < cols)   // cols is a multiple of 32
+        if (T.q_row && in)
           *reinterpret_cast<uint4*>(T.q_row + static_cast<int64_t>(r0 + row) * (cols >> 1) + ((c0 + 32 * b) >> 1)) = out;
       }
       if (T.amax_bits) {

@@ -30,6 +30,18 @@ def test_nvfp4_scale_not_above_zero_gives_zero_codes(cuda_lib, g):
         assert d["amax"].item() == bq.bf16_f64(bits & 0x7FFF).max()
 
 
+@pytest.mark.parametrize("g", [np.inf, np.nan])
+def test_nvfp4_scale_not_finite(cuda_lib, g):
+    """An infinite g saturates the block scales (NaN where the block is zero), a NaN one makes them NaN."""
+    bits = random_bits(64, 96, 22)
+    bits[:, :16] = 0
+    d = cast(cuda_lib, bits, bq.NVFP4, g, scale_inv=None)
+    cuda_lib.fp4_cast_multi([d])
+    for q, sf, b in ((d["q_row"], d["sf_row"], bits), (d["q_col"], d["sf_col"], np.ascontiguousarray(bits.T))):
+        codes, s = bq.quantise(b, bq.NVFP4, g)
+        assert np.array_equal(bq.unpack(u8(q)), codes) and np.array_equal(u8(sf), bq.atoms(s, bq.NVFP4))
+
+
 @pytest.mark.parametrize("g", [0.0, -0.0, -2.0, np.nan])
 @pytest.mark.parametrize("cols", [96, 2080])
 def test_norm_nvfp4_scale_without_a_positive_value(cuda_lib, g, cols):
