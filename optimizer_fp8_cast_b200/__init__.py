@@ -290,7 +290,7 @@ def _load_binding():
     lib = load()
     m.bind(*(C.cast(getattr(lib, f), C.c_void_p).value for f in
              ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes", "fp4_cast_multi",
-              "fp4_gemm_multi", "fp4_scale_bytes")), _check, _workspace)
+              "fp4_gemm_multi")), _check, _workspace)
     return m
 
 

@@ -36,7 +36,6 @@ struct Library {
   decltype(&fp8_rmsnorm_backward_workspace_bytes) rmsnorm_backward_workspace_bytes = nullptr;
   decltype(&fp4_cast_multi) cast_multi = nullptr;
   decltype(&fp4_gemm_multi) gemm_multi = nullptr;
-  decltype(&fp4_scale_bytes) scale_bytes = nullptr;
   PyObject* check = nullptr;                // check(status, where) raises
   PyObject* workspace = nullptr;            // workspace(bytes, like, stream) -> uint8 tensor
 } lib;
@@ -115,6 +114,7 @@ int integer(PyObject* o, int otherwise) {
   if (!o || o == Py_None) return otherwise;
   const long v = PyLong_AsLong(o);
   if (v == -1 && PyErr_Occurred()) throw Error{};
+  if (v != static_cast<int>(v)) value_error("quant and fmt", "a constant of the package");
   return static_cast<int>(v);
 }
 
@@ -344,17 +344,16 @@ PyObject* gemm_multi(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* k
   });
 }
 
-// bind(rmsnorm_cast, rmsnorm_backward, workspace_bytes, cast_multi, gemm_multi, scale_bytes, check, workspace)
+// bind(rmsnorm_cast, rmsnorm_backward, workspace_bytes, cast_multi, gemm_multi, check, workspace)
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[6];
+  unsigned long long p[5];
   PyObject *check, *workspace;
-  if (!PyArg_ParseTuple(args, "KKKKKKOO", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &check, &workspace)) return nullptr;
+  if (!PyArg_ParseTuple(args, "KKKKKOO", &p[0], &p[1], &p[2], &p[3], &p[4], &check, &workspace)) return nullptr;
   lib.rmsnorm_cast = reinterpret_cast<decltype(lib.rmsnorm_cast)>(p[0]);
   lib.rmsnorm_backward = reinterpret_cast<decltype(lib.rmsnorm_backward)>(p[1]);
   lib.rmsnorm_backward_workspace_bytes = reinterpret_cast<decltype(lib.rmsnorm_backward_workspace_bytes)>(p[2]);
   lib.cast_multi = reinterpret_cast<decltype(lib.cast_multi)>(p[3]);
   lib.gemm_multi = reinterpret_cast<decltype(lib.gemm_multi)>(p[4]);
-  lib.scale_bytes = reinterpret_cast<decltype(lib.scale_bytes)>(p[5]);
   Py_INCREF(check);
   Py_INCREF(workspace);
   lib.check = check;

@@ -28,12 +28,13 @@ Other recipes: "current" (every scale from the tensor's own amax), "mxfp8" (bloc
 orientations cast, block-scaled GEMMs) and the 4-bit forms "mxfp4" and "nvfp4": X, W and dY cast along
 both of their axes in one launch (the column-wise copies transposed), the three products in another,
 AdamW with its norm pass. "nvfp4" has a per-tensor scale beside the block scales, delayed like the FP8
-ones (its update follows the casts, with 448 * 6 as the format's largest value).
+ones (its update follows the casts, with 448 * 6 as the format's largest value; as there, the first step runs
+on a scale of 1, under which blocks smaller than about 2^-7.5 quantise to zero).
 """
 import torch
 
 from . import (AMAX_MAX, AMAX_MOST_RECENT, CURRENT_WORKSPACE_BYTES, E4M3, E5M2, FP4_MAX, FP8_MAX,
-               Q_MXFP4, Q_NVFP4, fp4_cast_multi, fp4_gemm_multi, fp4_scale_bytes,
+               Q_MXFP4, Q_NVFP4, fp4_scale_bytes,
                fp8_cast_transpose_amax, fp8_cast_transpose_amax_current_multi,
                fp8_cast_transpose_amax_multi, fp8_cast_transpose_amax_update_multi,
                fp8_gemm_multi, fp8_gemm_multi_sumsq, fp8_gemm_sumsq_workspace_bytes,
@@ -238,6 +239,7 @@ class Fp8LinearStep:
 
     def fp4_cast_all(self, xs, dys, stream=None):
         """4-bit: X, W and dY along both of their axes, as the products read them."""
+        from . import fp4_cast_multi           # loads the library: not while this module is imported
         casts = []
         for k, L in enumerate(self.layers):
             for role, name, src in ((ROLE_X, "X", xs[k]), (ROLE_W, "W", L.W), (ROLE_DY, "dY", dys[k])):
@@ -247,6 +249,7 @@ class Fp8LinearStep:
 
     def fp4_gemm_all(self, stream=None):
         """The 4-bit fprop, dgrad and wgrad of every layer in one grouped call."""
+        from . import fp4_gemm_multi
         out = []
         for k, L in enumerate(self.layers):
             for a, aw, ra, b, bw, rb, D in (("X", "row", ROLE_X, "W", "col", ROLE_W, L.Y),

@@ -1,6 +1,9 @@
 """Refusals of the norm and 4-bit entry points: every invalid argument is found on the host, before any
 CUDA call (addresses here are dummies that nothing dereferences)."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -155,3 +158,17 @@ def test_binding_documents_its_calls(lib):
     for f in (fp8.fp8_rmsnorm_cast, fp8.fp8_rmsnorm_backward, fp8.fp4_cast_multi, fp8.fp4_gemm_multi):
         assert f.__doc__ and f.__text_signature__
     assert all(hasattr(fp8, n) for n in fp8.__all__)
+
+
+def test_binding_refuses_integers_that_would_wrap(lib):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="constant of the package"):
+        fp8.fp8_rmsnorm_cast(x, x[0], 1e-5, quant=(1 << 32) + fp8.Q_FP8)
+    with pytest.raises(ValueError, match="constant of the package"):
+        fp8.fp4_cast_multi([dict(x=x, quant=(1 << 32) + fp8.Q_MXFP4)])
+
+
+def test_importing_the_step_driver_loads_no_library():
+    code = ("import sys, optimizer_fp8_cast_b200.step as s, optimizer_fp8_cast_b200 as p;"
+            "assert p._lib is None and not any(m.endswith('._binding') for m in sys.modules)")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(__file__)))
