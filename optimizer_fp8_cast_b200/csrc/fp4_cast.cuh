@@ -17,9 +17,12 @@
 //     in shared memory (64-byte swizzle) and stored by one TMA box per tile (straight 16-byte stores, each half
 //     a sector, cost 3.5 of 28 us on 8192 x 4096);
 //   row-wise: a quarter-warp per block of 8 consecutive rows, 16 bytes of codes per block.
+// NVFP4's amax is kept per thread from tile to tile and leaves the CTA by one atomic per tensor: one per warp and
+// tile, all to one address, made 16384 x 11008 both ways 237 instead of 114 us.
 // Bound: HBM, 2 B read + 0.5 B per copy written (+ 1/32 B MXFP4, 1/16 B NVFP4 of scales) per element; with both
 // copies every element is quantised twice, and the instructions per element (BF16 pairs compared as pairs,
-// multiplied as f32x2 pairs) come close to it.
+// multiplied as f32x2 pairs) come close to it: 8192 x 4096 both ways 21 us (MXFP4) and 26 (NVFP4), row-wise 14.6 and 16.1
+(tiles with one copy: 16.2 and 18.8), 16384 x 11008 both ways 92 and 114, inputs and outputs of three calls in turn.
 #pragma once
 
 #include "ptx.cuh"
@@ -197,7 +200,9 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
   __shared__ int4 where[2];                  // per buffer: tensor, row tile, column tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int stride = static_cast<int>(gridDim.x);
+  __shared__ uint32_t tops[kCastThreads / 32];
   int cur = -1;                              // tensor of the factors
+  uint32_t top = 0;                          // its largest magnitude pattern in this thread's tiles
   uint32_t pending = 0, pending_ph = 0;      // thread 0: loads not yet consumed, their phases
 
   pdl_trigger();
@@ -240,7 +245,9 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
     const bool nv = T.kind == blk::kNVFP4;
     const float gs = nv ? __ldg(T.scale) : 1.0f;
     if (at.x != cur) {                        // the same in every thread; the factors of the last are read
+      if (cur >= 0 && g.t[cur].amax_bits) blk::cta_amax(g.t[cur].amax_bits, top << 16, tops);
       cur = at.x;
+      top = 0;
       if (nv) {
         fill_factors(factors, gs);
         __syncthreads();
@@ -263,7 +270,6 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
     }
     if (T.q_row || T.amax_bits) {
       const int b = lane >> 3;
-      uint32_t top = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int row = 64 * u + 8 * warp + (lane & 7);
@@ -274,11 +280,6 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
         top = max(top, m);
         if (T.q_row && in)
           *reinterpret_cast<uint4*>(T.q_row + static_cast<int64_t>(r0 + row) * (cols >> 1) + ((c0 + 32 * b) >> 1)) = out;
-      }
-      if (T.amax_bits) {
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top > 0x7F80u) top = 0x7FC0u;     // canonical NaN
-        if (lane == 0 && top) atomicMax(T.amax_bits, top << 16);
       }
     }
     __syncthreads();                          // input tile consumed; the atoms complete
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
       else if (r0 + kTile >= rows && rt * per + t / 32 < words) dst[t] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
+  if (cur >= 0 && g.t[cur].amax_bits) blk::cta_amax(g.t[cur].amax_bits, top << 16, tops);
   if (tid == 0) {
     // loads still in flight after an abort must land before shared memory is released
     for (int b = 0; b < 2; ++b)
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
 
 // Row-wise copies alone: blocks of 32 values numbered through the matrix, a thread each.
 template <bool NV>
-__device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors) {
+__device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors, uint32_t* tops) {
   constexpr int kN = NV ? 2 : 1, kV = 4 / kN;              // scales per 32 values, and vectors of 8 per scale
   const uint32_t per_row = static_cast<uint32_t>(T.cols) >> 5;
   const int words = ((T.cols + 255) >> 8) * 2 * kN;        // atom words per row
@@ -376,33 +378,46 @@ __device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors) {
       ++row;
     }
   }
+  if (NV) {
+    // one atomic per CTA, by its last warp (no barrier: one here made the loop above spill, 0.15 us of 2.2)
+    if (T.amax_bits) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((threadIdx.x & 31) == 0) {
+        atomicMax(&tops[0], top);
+        __threadfence_block();
+        if (atomicAdd(&tops[1], 1u) == kCastThreads / 32 - 1) {
+          __threadfence_block();
+          top = atomicExch(&tops[0], 0u);
+          tops[1] = 0;
+          if (top) atomicMax(T.amax_bits, top > 0x7F80u ? 0x7FC00000u : top << 16);
+        }
+      }
+    }
+    if (T.scale_inv && first == 0) *T.scale_inv = __fdiv_rn(1.0f, g);
+  }
   // zero scales: K's padding of each row, and the rows that fill up the last atoms
   const int pad = words * 4 - kN * static_cast<int>(per_row);
+#pragma unroll 1
   for (int64_t i = first; i < static_cast<int64_t>(T.rows) * pad; i += stride) {
     const int64_t r = i / pad;
     const int j = kN * static_cast<int>(per_row) + static_cast<int>(i - r * pad);
     sf[blk::atom_word(r, j >> 2, words) + (j & 3)] = 0;
   }
   const int64_t fill = (T.rows + 127) / 128 * 128 - T.rows;
+#pragma unroll 1
   for (int64_t i = first; i < fill * words; i += stride)
     *reinterpret_cast<uint32_t*>(sf + blk::atom_word(T.rows + i / words, i % words, words)) = 0u;
-  if (NV) {
-    if (T.amax_bits) {
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (top > 0x7F80u) top = 0x7FC0u;                    // canonical NaN
-      if ((threadIdx.x & 31) == 0 && top) atomicMax(T.amax_bits, top << 16);
-    }
-    if (T.scale_inv && first == 0) *T.scale_inv = __fdiv_rn(1.0f, g);
-  }
 }
 
 __global__ void __launch_bounds__(kCastThreads, 4) k_fp4_cast_rows(const __grid_constant__ CastGroup g) {
   __shared__ float factors[128];
+  __shared__ uint32_t tops[2];               // NVFP4: the CTA's largest magnitude, and how many warps have added theirs
+  if (threadIdx.x < 2) tops[threadIdx.x] = 0;
   pdl_trigger();
   pdl_wait();
   for (int t = 0; t < g.n; ++t) {
-    if (g.t[t].kind == blk::kNVFP4) cast_rows<true>(g.t[t], factors);
-    else                            cast_rows<false>(g.t[t], factors);
+    if (g.t[t].kind == blk::kNVFP4) cast_rows<true>(g.t[t], factors, tops);
+    else                            cast_rows<false>(g.t[t], factors, tops);
   }
 }
 

@@ -193,7 +193,8 @@ fp8t_status current_device(DeviceInfo** out) {
         e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  fp8t::fp4::kCastSmemBytes);
       if (e == cudaSuccess) e = allow_fp4_split_smem();
-      for (auto* k : {fp8t::norm::k_rmsnorm_backward<1>, fp8t::norm::k_rmsnorm_backward<2>, fp8t::norm::k_rmsnorm_backward<4>})
+      for (auto* k : {fp8t::norm::k_rmsnorm_backward<1>, fp8t::norm::k_rmsnorm_backward<2>, fp8t::norm::k_rmsnorm_backward<3>,
+                      fp8t::norm::k_rmsnorm_backward<4>})
         if (e == cudaSuccess)
           e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::norm::kBwdMaxSmem);
       if (e != cudaSuccess) {
@@ -1168,8 +1169,14 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
     if (tiles >= (int64_t(1) << 30)) return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_cast: too many tiles in one launch");
     group.total_tiles = static_cast<int32_t>(tiles);
     if (!any_col) {                    // row-wise copies only: the streaming kernel
-      int64_t most = 0;                // blocks of 32 values of the largest tensor
-      for (int32_t i = b0; i < b1; ++i) most = std::max(most, tensors[i].rows * tensors[i].cols / 32);
+      // blocks of 32 values of the largest tensor, or the words that fill up its last atoms (one row of 4096 on
+      // the CTAs of its blocks alone: 4.2 and 6.9 us, on those of the words 2.1 and 2.6)
+      int64_t most = 0;
+      for (int32_t i = b0; i < b1; ++i) {
+        const fp8t_fp4_cast_tensor& t = tensors[i];
+        const int64_t words = ((t.rows + 127) / 128 * 128 - t.rows) * fp8t::blk::atoms_per_row(t.cols, t.quant);
+        most = std::max({most, t.rows * t.cols / 32, words});
+      }
       const int64_t rgrid = std::min<int64_t>((most + kCastThreads - 1) / kCastThreads,
                                               static_cast<int64_t>(dev->sms) * dev->fp4_cast_rows_blocks_per_sm);
       (void)launch_pdl(k_fp4_cast_rows, rgrid, kCastThreads, 0, as_stream(stream), 0, group);
@@ -1460,8 +1467,9 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
 namespace {
 
 // Threads and vectors per thread of a forward launch. Rows of up to 1024 columns take a warp each, four to a
-// CTA. Wider rows take a CTA: with rows enough to fill the GPU, the vectors per thread that leave few threads
-// to sum over; else the fewest that 512 threads hold.
+// CTA (16384 x 1024 to FP8: 21.9 us either way; 1000 x 1024: 3.4 us, on a CTA each 3.6). Wider rows take a CTA: with
+// rows enough to fill the GPU two vectors per thread, so that fewer threads are summed over (one / two: 1000 x 4096
+// 8.1 / 6.3 us, 8192 x 4096 45.2 / 40.8), else the fewest that 512 threads hold (1 x 2048 2.3 / 2.4, to NVFP4 2.6 / 2.9).
 struct NormShape {
   bool warp_row;
   int vpt, threads;
@@ -1492,7 +1500,9 @@ NormBwdShape norm_backward_shape(int64_t rows, int64_t cols) {
   using namespace fp8t::norm;
   const int nvec = static_cast<int>(cols / 8);
   NormBwdShape s;
-  s.vpt = nvec <= 32 ? 1 : nvec <= kBwdThreads ? 2 : 4;     // two row groups or more while two vectors do
+  // the fewest vectors that 512 threads hold, but two where that leaves a row group a warp or more. 8192 rows, one /
+  // two / three vectors: 2048 columns 33 / 27 us, 2816 - / 38 / 46, 5120 - / 73 / 80
+  s.vpt = nvec <= 32 ? 1 : nvec <= 2 * kBwdThreads ? 2 : nvec <= 3 * kBwdThreads ? 3 : 4;
   s.group = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
   const int most = std::min(kBwdThreads / s.group, s.group == 32 ? 16 : 15);      // barrier ids 1..15
   s.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (rows + kBwdCtas - 1) / kBwdCtas)));
@@ -1642,7 +1652,8 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
   p.cols = static_cast<int32_t>(d.cols);
   p.group = s.group;
   const size_t smem = want ? static_cast<size_t>(s.groups - 1) * d.cols * 4 : 0;
-  (void)launch_pdl(s.vpt == 1 ? k_rmsnorm_backward<1> : s.vpt == 2 ? k_rmsnorm_backward<2> : k_rmsnorm_backward<4>,
+  (void)launch_pdl(s.vpt == 1 ? k_rmsnorm_backward<1> : s.vpt == 2 ? k_rmsnorm_backward<2>
+             : s.vpt == 3 ? k_rmsnorm_backward<3> : k_rmsnorm_backward<4>,
                    ctas, s.group * s.groups, smem, as_stream(stream), 0, p);
   if ((st = after_launch("fp8_rmsnorm_backward launch")) != FP8T_OK) return st;
   if (want) {

@@ -25,7 +25,9 @@
 // threads that share a row, with a barrier of its own); a thread owns the same columns for every row of its
 // group, so dgamma is summed in registers (f32), over the CTA's groups in shared memory, and one
 // partial row per CTA goes to the workspace; a second kernel adds the partials. Both orders are fixed: the
-// result does not depend on scheduling. With the same prefetch, 8192 x 4096 with dres 58.7 -> 50.7 us.
+// result does not depend on scheduling. With the same prefetch, 8192 x 4096 with dres 58.7 -> 48.5 us. Of rows
+wider than 8192 columns gamma is re-read for every row (from L1) and dres once the row's sum is known, since three or
+four vectors of all inputs per thread spill: 8192 x 8192 on two vectors 92 us (on four 143), 4096 x 16384 122 (147).
 #pragma once
 
 #include "ptx.cuh"
@@ -242,9 +244,8 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : kMaxThreads) k_r
   }
   if (Q == blk::kFP8 || Q == blk::kNVFP4) {
     if (p.amax_bits) {
-      uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-      if (a > 0x7F800000u) a = 0x7FC00000u;            // canonical NaN
-      if (lane == 0 && a) atomicMax(p.amax_bits, a);
+      __shared__ uint32_t tops[kMaxThreads / 32];
+      blk::cta_amax(p.amax_bits, __float_as_uint(amax), tops);
     }
     if (p.scale_inv && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_inv = __fdiv_rn(1.0f, scale);
   }
@@ -262,16 +263,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
 
   pdl_trigger();
   pdl_wait();
-  uint4 gam[VPT];
+  constexpr bool kHold = VPT < 3;          // gamma and dres in registers (three vectors or more would spill)
+  uint4 gam[kHold ? VPT : 1];
   f32x2 acc[VPT][4];
   bool in[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     in[i] = i * nthr + tid < nvec;
-    gam[i] = in[i] ? __ldg(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
+    if (kHold) gam[i] = in[i] ? __ldg(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
   }
+  auto gamma = [&](int i) {
+    return kHold ? gam[i] : in[i] ? __ldg(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
+  };
   const float inv_c = __fdiv_rn(1.0f, static_cast<float>(p.cols));
 
   int it = 0;
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
     const int64_t base = row * nvec + tid;
     const float rstd = __ldg(p.rstd + row);
     const f32x2 rstd2 = pair(rstd, rstd);
-    uint4 dv[VPT], hv[VPT], rv[VPT];
+    uint4 dv[VPT], hv[VPT], rv[kHold ? VPT : 1];
     if (tid == 0 && row + row_step < p.rows) {           // the row after this one into L2
       const int64_t next = (row + row_step) * nvec;
       l2_prefetch(p.dy + next, nvec * 16);
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
       dv[i] = load_or_zero(p.dy + base + i * nthr, in[i]);
       hv[i] = load_or_zero(p.h + base + i * nthr, in[i]);
     }
-    if (p.dres) {
+    if (kHold && p.dres) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) rv[i] = load_or_zero(p.dres + base + i * nthr, in[i]);
     }
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
       f32x2 d[4], h[4], gm[4];
       unpack8(dv[i], d);
       unpack8(hv[i], h);
-      unpack8(gam[i], gm);
+      unpack8(gamma(i), gm);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f32x2 xh = mul2(h[j], rstd2);
@@ -316,11 +321,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
       f32x2 d[4], h[4], gm[4];
       unpack8(dv[i], d);
       unpack8(hv[i], h);
-      unpack8(gam[i], gm);
+      unpack8(gamma(i), gm);
 #pragma unroll
       for (int j = 0; j < 4; ++j) d[j] = mul2(rstd2, fma2(mul2(h[j], rstd2), ms2, mul2(d[j], gm[j])));
       if (p.dres) {
-        unpack8(rv[i], h);
+        unpack8(kHold ? rv[i] : load_or_zero(p.dres + base + i * nthr, in[i]), h);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = add2(d[j], h[j]);
       }
