@@ -26,8 +26,8 @@
 // group, so dgamma is summed in registers (f32), over the CTA's groups in shared memory, and one
 // partial row per CTA goes to the workspace; a second kernel adds the partials. Both orders are fixed: the
 // result does not depend on scheduling. With the same prefetch, 8192 x 4096 with dres 58.7 -> 48.5 us. Of rows
-wider than 8192 columns gamma is re-read for every row (from L1) and dres once the row's sum is known, since three or
-four vectors of all inputs per thread spill: 8192 x 8192 on two vectors 92 us (on four 143), 4096 x 16384 122 (147).
+// wider than 8192 columns gamma is re-read for every row (from L1) and dres once the row's sum is known, since three or
+// four vectors of all inputs per thread spill: 8192 x 8192 on two vectors 92 us (on four 143), 4096 x 16384 122 (147).
 #pragma once
 
 #include "ptx.cuh"
