@@ -5,6 +5,10 @@ sm_100a). Each function takes torch CUDA tensors, passes their device pointers a
 CUDA stream to the C entry point of the same name, and raises ``Fp8TrainError`` on a non-OK
 status. Every step of the path runs in the library's kernels; there is no CPU or PyTorch
 fallback, and a missing library is an error.
+
+The norm and 4-bit calls (``fp8_rmsnorm_cast``, ``fp8_rmsnorm_backward``, ``fp4_cast_multi``,
+``fp4_gemm_multi``) are made per layer on as little as one token; their binding is compiled
+(``csrc/binding.cpp``, ``_binding.so``) and is loaded when one of them is first asked for.
 """
 import ctypes as C
 import importlib.util
