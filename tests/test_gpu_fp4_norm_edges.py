@@ -9,7 +9,7 @@ from tests import _block_quant as bq
 from tests._gpu import bf16_bits, bf16_from_bits, u8
 from tests._pins import gemm_within_tolerance
 from tests.test_gpu_fp4 import KINDS, cast, check_cast, operand, random_bits, reference
-from tests.test_gpu_rmsnorm import MXFP4, NVFP4, U, check, make, run
+from tests.test_gpu_rmsnorm import MXFP4, NVFP4, U, bf, check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -65,6 +65,22 @@ def test_cast_list_of_one_and_two_way_tensors(cuda_lib):
         ref.append((bits, kind, 2.0 + i))
     cuda_lib.fp4_cast_multi(ds)
     cuda_lib.fp8t_check_device_error()
+    for d, r in zip(ds, ref):
+        check_cast(d, *r)
+
+
+def test_cast_list_of_row_wise_tensors(cuda_lib):
+    """Row-wise copies alone over two launches, each tensor with an amax slot of its own: from one row (one CTA's
+    work, many to fill up its atoms) to many, and an all-zero one among them."""
+    ds, ref = [], []
+    for i, (rows, cols) in enumerate([(1, 4096), (3, 32), (700, 288), (128, 64), (1, 32), (2049, 1056), (64, 512), (5, 96), (300, 800)]):
+        kind = bq.MXFP4 if i % 4 == 1 else bq.NVFP4
+        bits = random_bits(rows, cols, 400 + i)
+        if i == 6:
+            bits[:] = 0
+        ds.append(cast(cuda_lib, bits, kind, 0.5 + i, col=False))
+        ref.append((bits, kind, 0.5 + i))
+    cuda_lib.fp4_cast_multi(ds)
     for d, r in zip(ds, ref):
         check_cast(d, *r)
 
@@ -195,6 +211,39 @@ def test_backward_captured_with_a_workspace_of_the_call(cuda_lib):
 
 
 # ------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("rows,cols", [(700, 8192), (310, 8208), (160, 12288), (333, 12304), (299, 16384), (40000, 16)])
+def test_backward_of_wide_and_short_rows(cuda_lib, rows, cols):
+    """Two, three and four vectors per thread with dres, and the shortest rows; dh over dy and over dres."""
+    h, r, gamma = make(rows, cols, rows)
+    rng = np.random.default_rng(cols)
+    dy, dres = bf(rng.standard_normal((rows, cols))), bf(rng.standard_normal((rows, cols)))
+    H, G, DY, DR = (bq.bf16_f64(v) for v in (h, gamma, dy, dres))
+    rstd = bq.rmsnorm(H, None, G, 1e-5)[1].astype(np.float32).astype(np.float64)
+    want, wantg = bq.rmsnorm_grad(DY, H, G, rstd, DR)
+    xh = H * rstd[:, None]
+    terms = rstd[:, None] * (np.abs(DY * G) + np.abs(xh) * np.abs(DY * G * xh).mean(1, keepdims=True)) + np.abs(DR)
+    first = None
+    for place in ("own", "dy", "dres"):
+        t = dict(dy=bf16_from_bits(dy), dres=bf16_from_bits(dres))
+        t["own"] = torch.full_like(t["dy"], float("nan"))
+        dg = torch.full((cols,), float("nan"), device="cuda")
+        cuda_lib.fp8_rmsnorm_backward(t["dy"], bf16_from_bits(h), bf16_from_bits(gamma),
+                                      torch.from_numpy(rstd.astype(np.float32)).cuda(), t[place], dres=t["dres"], dgamma=dg)
+        if first is None:
+            first = t[place], dg
+            assert (np.abs(bq.bf16_f64(bf16_bits(t[place])) - want) <= 2.0 ** -8 * np.abs(want) + 64 * U * terms).all()
+            # a column: rows / 148 additions or fewer in a thread's chain, at most 16 groups, 148 partials
+            bound = (rows // 148 + 1 + 16 + 148 // 16 + 1 + 16 + 8) * U * np.abs(DY * xh).sum(0)
+            assert (np.abs(dg.cpu().numpy() - wantg) <= bound).all()
+        assert torch.equal(t[place].view(torch.int16), first[0].view(torch.int16)) and torch.equal(dg, first[1])
+
+
+@pytest.mark.parametrize("quant", [1, MXFP4])
+def test_norm_of_many_short_rows(cuda_lib, quant):
+    x, r, gamma = make(40000, 32, 6)
+    check(run(cuda_lib, x, r, gamma, 1e-5, quant), x, r, gamma, 1e-5, quant)
+
+
 def some_rows(rows, n=24):
     """Rows to check: the first and last, those around 2^31 elements' border and random ones."""
     rng = np.random.default_rng(rows)
