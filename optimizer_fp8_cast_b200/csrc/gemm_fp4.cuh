@@ -445,8 +445,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
 // the S CTAs of a cluster each take a contiguous part of K. Every CTA leaves its FP32
 // partial tile in the shared memory of the CTAs that own its tokens (groups of four: group j belongs to rank
 // j mod S, 16 bytes of a weight row at a time); after a cluster barrier each owner adds the S partials in rank
-// order, scales, rounds and stores its tokens' rows of D, 128 columns of a row at a time. No workspace, and
-// the order of additions is fixed.
+// order, scales, rounds and stores its tokens' rows of D, 128 columns of a row at a time (a warp per group of tokens, four
+// columns per lane: 128 x 4096 x 4096 9.7 -> 9.1 us against two columns per lane of 64). No workspace, and the order
+// of additions is fixed. For many tokens the exchange counts: remote stores leave an SM at about 15 bytes per cycle, 1.7
+// of the 9.1 us above (measured with all of them kept in the CTA).
 // TMEM: accumulator (weight rows x tokens) in columns 0..BT-1, then the scales.
 constexpr int kSplitThreads = 128;
 constexpr int kMaxSplitProblems = 4;
@@ -636,6 +638,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     __syncthreads();                         // the MMAs that read the stage buffers are done, in this CTA
     if (ways > 1) cluster_sync();            // and in every CTA that receives partials
   }
+  // a weight row's place in its 128, such that eight lanes that read every fourth row (the sum below) meet all banks
+  auto place = [](int row) { return row ^ ((row >> 3) & 3); };
   int owner = 0, slot = 0;                      // of the group: j mod ways, j / ways
 #pragma unroll 1
   for (int c = 0; c < BT && c < P.M; c += 16) {
@@ -647,8 +651,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     for (int j = 0; j < 4; ++j) {
       if (c + 4 * j >= P.M) break;
       if (kb1 == kb0) r[4 * j] = r[4 * j + 1] = r[4 * j + 2] = r[4 * j + 3] = 0u;
-      st_cluster_v4(mapa_shared(red + ((rank * per + slot) * 128 + threadIdx.x) * 16, owner), r[4 * j], r[4 * j + 1],
-                    r[4 * j + 2], r[4 * j + 3]);
+      const uint32_t to = red + ((rank * per + slot) * 128 + place(threadIdx.x)) * 16;
+      st_cluster_v4(mapa_shared(to, owner), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
       if (++owner == ways) {
         owner = 0;
         ++slot;
@@ -663,23 +667,33 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   if (*abort_flag) return;                   // D is incomplete; the error word says so
   const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
   const float4* part = reinterpret_cast<const float4*>(smem + (red - smem_u32(smem)));
-  const int pair = threadIdx.x & 63, n = n0 + 2 * pair;      // two weight rows: adjacent columns of D
-  for (int s = threadIdx.x >> 6; (s * ways + rank) * 4 < P.M; s += kSplitThreads / 64) {
-    if (n >= P.N) break;
-    float4 x = part[s * 128 + 2 * pair], y = part[s * 128 + 2 * pair + 1];
+  const int n = n0 + 4 * lane;                 // four weight rows: adjacent columns of D; a group of tokens per warp
+  if (n >= P.N) return;                        // N is a multiple of 8
+  const int M = P.M, N = P.N;
+  uint16_t* D = P.D + n;
+  for (int s = warp; (s * ways + rank) * 4 < M; s += kSplitThreads / 32) {
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = part[s * 128 + place(4 * lane + i)];
+#pragma unroll 1
     for (int w = 1; w < ways; ++w) {
-      const float4 u = part[(w * per + s) * 128 + 2 * pair], v = part[(w * per + s) * 128 + 2 * pair + 1];
-      x.x = __fadd_rn(x.x, u.x); x.y = __fadd_rn(x.y, u.y); x.z = __fadd_rn(x.z, u.z); x.w = __fadd_rn(x.w, u.w);
-      y.x = __fadd_rn(y.x, v.x); y.y = __fadd_rn(y.y, v.y); y.z = __fadd_rn(y.z, v.z); y.w = __fadd_rn(y.w, v.w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 u = part[(w * per + s) * 128 + place(4 * lane + i)];
+        x[i].x = __fadd_rn(x[i].x, u.x); x[i].y = __fadd_rn(x[i].y, u.y);
+        x[i].z = __fadd_rn(x[i].z, u.z); x[i].w = __fadd_rn(x[i].w, u.w);
+      }
     }
     const int m = (s * ways + rank) * 4;
-    const uint32_t o[4] = {pack_bf16x2(__fmul_rn(x.x, alpha), __fmul_rn(y.x, alpha)),
-                           pack_bf16x2(__fmul_rn(x.y, alpha), __fmul_rn(y.y, alpha)),
-                           pack_bf16x2(__fmul_rn(x.z, alpha), __fmul_rn(y.z, alpha)),
-                           pack_bf16x2(__fmul_rn(x.w, alpha), __fmul_rn(y.w, alpha))};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (m + k < P.M) *reinterpret_cast<uint32_t*>(P.D + static_cast<int64_t>(m + k) * P.N + n) = o[k];
+    auto store = [&](int k, float a, float b, float c, float d) {
+      if (m + k < M)
+        *reinterpret_cast<uint2*>(D + static_cast<int64_t>(m + k) * N) =
+            make_uint2(pack_bf16x2(__fmul_rn(a, alpha), __fmul_rn(b, alpha)), pack_bf16x2(__fmul_rn(c, alpha), __fmul_rn(d, alpha)));
+    };
+    store(0, x[0].x, x[1].x, x[2].x, x[3].x);
+    store(1, x[0].y, x[1].y, x[2].y, x[3].y);
+    store(2, x[0].z, x[1].z, x[2].z, x[3].z);
+    store(3, x[0].w, x[1].w, x[2].w, x[3].w);
   }
 }
 
