@@ -418,10 +418,11 @@ typedef struct fp8t_fp4_gemm_desc {
 
 /*
  * fp4_gemm_multi — 4-bit block-scaled GEMMs on the block-scaled tensor cores (FP32 accumulation, BF16
- * output), grouped: consecutive descriptors with the same quant share a launch (up to 24). The
- * accumulation order over k is unspecified but fixed for given sizes: the result is the same on every
- * run, and within 2 BF16 ulp + 1e-5 * sum_k |a b| * scales of the exact value. The scales of rows past M
- * or N are read but do not matter; those of K's padding must be zero bytes (the casts write them).
+ * output), grouped: consecutive descriptors of one quant share a launch, up to 4 of at most 128 rows or up to
+ * 24 of more. The accumulation order over k is unspecified but fixed for a given list of sizes: the same
+ * call gives the same result on every run (a problem may round differently in another list), within 2 BF16
+ * ulp + 1e-5 * sum_k |a b| * scales of the exact value. The scales of rows past M or N are read but do not
+ * matter; those of K's padding must be zero bytes (the casts write them).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED (pointers 16-byte aligned, scale inverses 4), CUDA.
  */
 fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, void* stream);
