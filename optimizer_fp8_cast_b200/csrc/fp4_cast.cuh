@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
     const CastTensor& T = g.t[at.x];
     const int rt = at.y, ct = at.z, r0 = rt * kTile, c0 = ct * kTile, rows = T.rows, cols = T.cols;
     const bool nv = T.kind == blk::kNVFP4;
-    const float gs = nv ? __ldg(T.scale) : 1.0f;
+    const float gs = nv ? ld_dep(T.scale) : 1.0f;
     if (at.x != cur) {                        // the same in every thread; the factors of the last are read
       if (cur >= 0 && g.t[cur].amax_bits) blk::cta_amax(g.t[cur].amax_bits, top << 16, tops);
       cur = at.x;
@@ -330,7 +330,7 @@ __device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors, u
   const int words = ((T.cols + 255) >> 8) * 2 * kN;        // atom words per row
   const int64_t n = static_cast<int64_t>(T.rows) * per_row, stride = static_cast<int64_t>(gridDim.x) * kCastThreads;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x;
-  const float g = NV ? __ldg(T.scale) : 1.0f;
+  const float g = NV ? ld_dep(T.scale) : 1.0f;
   if (NV) {
     __syncthreads();                                       // the previous tensor's factors are read
     fill_factors(factors, g);

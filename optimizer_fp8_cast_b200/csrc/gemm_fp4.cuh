@@ -372,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       }
       tc_fence_after();
       const Problem4& P = g.problem(tile);
-      const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
+      const float alpha = __fmul_rn(P.sa ? ld_dep(P.sa) : 1.0f, P.sb ? ld_dep(P.sb) : 1.0f);
       const int M = P.M, N = P.N, local = tile - P.tile_start;
       const int row0 = (local / P.tiles_n) * kBM + static_cast<int>(rank) * kHalf + quad * 32;
       const int n0 = (local % P.tiles_n) * kTileN;
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   if (*abort_flag) return;                   // D is incomplete; the error word says so
-  const float alpha = __fmul_rn(P.sa ? __ldg(P.sa) : 1.0f, P.sb ? __ldg(P.sb) : 1.0f);
+  const float alpha = __fmul_rn(P.sa ? ld_dep(P.sa) : 1.0f, P.sb ? ld_dep(P.sb) : 1.0f);
   const float4* part = reinterpret_cast<const float4*>(smem + (red - smem_u32(smem)));
   const int n = n0 + 4 * lane;                 // four weight rows: adjacent columns of D; a group of tokens per warp
   if (n >= P.N) return;                        // N is a multiple of 8

@@ -306,6 +306,19 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
 // pdl_trigger lets the next kernel, if it was launched so too, begin once every CTA has called it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Loads of memory that the kernel before this one may write. Such a kernel runs while this one is already resident, so
+// the memory is not read-only for this one's lifetime, as the non-coherent path (__ldg, const __restrict__) needs it
+// to be; volatile asm also keeps them behind pdl_wait.
+__device__ __forceinline__ float ld_dep(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_dep(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 // ------------------------------------------------------------------ FP8 conversion
 // Two f32 -> two FP8 codes, round to nearest even, saturating to +-max (cvt.rn.satfinite).

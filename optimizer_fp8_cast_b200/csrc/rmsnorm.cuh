@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : kMaxThreads) k_r
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     in[i] = i * nthr + tid < nvec;
-    gam[i] = in[i] ? __ldg(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
+    gam[i] = in[i] ? ld_dep(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
   }
-  const float scale = Q == blk::kFP8 || Q == blk::kNVFP4 ? __ldg(p.scale) : 1.0f;
+  const float scale = Q == blk::kFP8 || Q == blk::kNVFP4 ? ld_dep(p.scale) : 1.0f;
   const int emax = Q == blk::kMXFP4 ? 2 : (p.fmt == 0 ? 8 : 15);
   const float inv_c = __fdiv_rn(1.0f, static_cast<float>(p.cols));
   float amax = 0.0f;
@@ -270,19 +270,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     in[i] = i * nthr + tid < nvec;
-    if (kHold) gam[i] = in[i] ? __ldg(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
+    if (kHold) gam[i] = in[i] ? ld_dep(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
   }
   auto gamma = [&](int i) {
-    return kHold ? gam[i] : in[i] ? __ldg(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
+    return kHold ? gam[i] : in[i] ? ld_dep(p.gamma + i * nthr + tid) : make_uint4(0u, 0u, 0u, 0u);
   };
   const float inv_c = __fdiv_rn(1.0f, static_cast<float>(p.cols));
 
   int it = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g; row < p.rows; row += row_step, ++it) {
     const int64_t base = row * nvec + tid;
-    const float rstd = __ldg(p.rstd + row);
+    const float rstd = ld_dep(p.rstd + row);
     const f32x2 rstd2 = pair(rstd, rstd);
     uint4 dv[VPT], hv[VPT], rv[kHold ? VPT : 1];
     if (tid == 0 && row + row_step < p.rows) {           // the row after this one into L2
@@ -366,8 +366,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
 constexpr int kReduceWarps = 16;
 constexpr int kReduceLoads = (kBwdCtas + kReduceWarps - 1) / kReduceWarps;
 __global__ void __launch_bounds__(32 * kReduceWarps)
-    k_rmsnorm_dgamma(const float* __restrict__ partials, int n, int cols, float* __restrict__ out_f32,
-                     uint16_t* __restrict__ out_bf16) {
+    k_rmsnorm_dgamma(const float* partials, int n, int cols, float* out_f32, uint16_t* out_bf16) {
   __shared__ float sh[kReduceWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
