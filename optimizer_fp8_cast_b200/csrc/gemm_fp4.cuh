@@ -403,6 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
         for (int step = 0; step < 4; ++step) {
           const int c = half * 4 + (acc == 0 ? 3 - step : step);
           uint32_t r[32];
+          __syncwarp();                                    // one lane stored the chunk before
           tmem_ld_32x32b_x32(t_base + c * 32, r);
           tmem_ld_wait();
           tmem_reg_fence(r);
@@ -622,11 +623,12 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     }
   }
   __syncwarp();
-  if (!mbar_wait(smem_u32(&S->done), 0, limit, expire != kExpireNone)) {
+  if (!warp_wait(smem_u32(&S->done), 0, limit, expire != kExpireNone)) {
     if (lane == 0) record_error(kErrTimeout);
     *abort_flag = 1;
-    mbar_wait(smem_u32(&S->done), 0, kDrainLimitNs);       // MMAs in flight, whatever the limit was
+    warp_wait(smem_u32(&S->done), 0, kDrainLimitNs);       // MMAs in flight, whatever the limit was
   }
+  __syncwarp();                                            // TMEM loads follow
   tc_fence_after();
   const int per = (BT / 4 + ways - 1) / ways;   // slots: groups of four tokens per owner
   uint32_t red;                                 // [ways][per][128] x 4 f32

@@ -26,3 +26,30 @@ def test_no_non_coherent_loads(name):
     scale inverses, rstd and partial rows while this one is resident."""
     text = code(name)
     assert "__ldg(" not in text and "__restrict__" not in text and "ld.global.nc" not in text
+
+
+def body(text, head):
+    """The braces after the first place that `head` matches."""
+    at = text.index("{", re.search(head, text).end())
+    depth, i = 1, at + 1
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+    return text[at:i]
+
+
+@pytest.mark.parametrize("name", ["cluster_sync", "cluster_arrive", "cluster_wait"])
+def test_cluster_barriers_converge_their_warps(name):
+    """barrier.cluster in its .aligned forms is undefined for a warp whose lanes come one by one."""
+    assert re.match(r"\{\s*__syncwarp\(\);\s*asm", body(code("ptx.cuh"), r"void " + name + r"\(\)"))
+
+
+def test_split_product_waits_as_whole_warps():
+    """tcgen05.ld.sync.aligned follows these waits, so a lane may not leave one alone."""
+    split = body(code("gemm_fp4.cuh"), r"k_fp4_gemm_split\(const __grid_constant__ SplitGroup g\)")
+    assert "warp_wait(" in split and not re.search(r"\bmbar_wait\(", split)
+
+
+def test_tile_product_converges_before_each_chunk():
+    tile = body(code("gemm_fp4.cuh"), r"k_fp4_gemm\(const __grid_constant__ G g\)")
+    assert re.search(r"__syncwarp\(\);\s*tmem_ld_32x32b_x32\(t_base \+ c \* 32, r\);", tile)
