@@ -548,7 +548,6 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
     tma_load_2d(sf + kSf, &P.sft, 0, kb * kSfRows, bar);
   };
 
-  pdl_trigger();
   if (ways > 1 && Sh::kApart) cluster_arrive();          // "running": waited for before the first remote store
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::kStages; ++s) {
@@ -565,6 +564,9 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   if (warp == 1) {
     tmem_alloc(smem_u32(&S->tmem_base), Sh::kTmem);
     tmem_relinquish();
+    // Only now may the next kernel start: one that took this SM's tensor memory first would hold it until this
+    // grid has ended, and this CTA would wait for it.
+    pdl_trigger();
   }
   tc_fence_before();
   __syncthreads();

@@ -53,3 +53,12 @@ def test_split_product_waits_as_whole_warps():
 def test_tile_product_converges_before_each_chunk():
     tile = body(code("gemm_fp4.cuh"), r"k_fp4_gemm\(const __grid_constant__ G g\)")
     assert re.search(r"__syncwarp\(\);\s*tmem_ld_32x32b_x32\(t_base \+ c \* 32, r\);", tile)
+
+
+@pytest.mark.parametrize("head,alloc", [(r"k_fp4_gemm\(const __grid_constant__ G g\)", "tmem_alloc_pair("),
+                                        (r"k_fp4_gemm_split\(const __grid_constant__ SplitGroup g\)", "tmem_alloc(")])
+def test_tensor_memory_is_taken_before_the_next_kernel_may_start(head, alloc):
+    """A dependent kernel waits for this grid's end with what it has allocated: if it could take an SM's tensor
+    memory before this grid's CTA there, neither would go on."""
+    text = body(code("gemm_fp4.cuh"), head)
+    assert text.count("pdl_trigger()") == 1 and text.index(alloc) < text.index("pdl_trigger()")
