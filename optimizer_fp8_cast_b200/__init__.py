@@ -276,13 +276,6 @@ def fp8_rmsnorm_backward_workspace_bytes(rows, cols):
     return int(load().fp8_rmsnorm_backward_workspace_bytes(int(rows), int(cols)))
 
 
-def _workspace(n, like, stream):
-    t = torch.empty(n, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)      # freed when the call returns, read by kernels of that stream
-    return t
-
-
 def _load_binding():
     """The calls of csrc/binding.cpp (norm and 4-bit entry points), with the library's addresses."""
     spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
@@ -294,7 +287,7 @@ def _load_binding():
     lib = load()
     m.bind(*(C.cast(getattr(lib, f), C.c_void_p).value for f in
              ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes", "fp4_cast_multi",
-              "fp4_gemm_multi")), _check, _workspace)
+              "fp4_gemm_multi")), _check)
     return m
 
 

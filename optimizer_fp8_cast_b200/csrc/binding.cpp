@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -37,7 +38,6 @@ struct Library {
   decltype(&fp4_cast_multi) cast_multi = nullptr;
   decltype(&fp4_gemm_multi) gemm_multi = nullptr;
   PyObject* check = nullptr;                // check(status, where) raises
-  PyObject* workspace = nullptr;            // workspace(bytes, like, stream) -> uint8 tensor
 } lib;
 
 void check_status(fp8t_status status, const char* where) {
@@ -232,19 +232,17 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
     d.dres_bf16 = c.bf16(a[5], d.rows, d.cols, "dres");
     d.dgamma_f32 = c.f32(a[6], d.cols, "dgamma");
     d.dgamma_bf16 = c.bf16(a[7], d.cols, "dgamma_bf16");
+    void* stream = c.stream(a[9]);
     const at::Tensor* ws = tensor(a[8], "workspace");
     at::Tensor own;
     if (!ws && (d.dgamma_f32 || d.dgamma_bf16)) {
-      // freed on return; `workspace` keeps it from being given out again before `stream` is done with it
-      const size_t bytes = lib.rmsnorm_backward_workspace_bytes(d.rows, d.cols);
-      if (a[9] && a[9] != Py_None) {
-        PyObject* t = PyObject_CallFunction(lib.workspace, "KOO", static_cast<unsigned long long>(bytes), a[0], a[9]);
-        if (!t) throw Error{};
-        own = THPVariable_Unpack(t);
-        Py_DECREF(t);
-      } else {
-        own = at::empty({static_cast<int64_t>(bytes)}, dy.options().dtype(at::kByte));
-      }
+      // Memory of the stream that the kernels run on, freed on return for that stream's later work: a block of another
+      // stream's may still be in use by what is queued there, and nothing orders this call behind it.
+      c10::cuda::OptionalCUDAStreamGuard on;
+      if (a[9] && a[9] != Py_None)
+        on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), c.device));
+      own = at::empty({static_cast<int64_t>(lib.rmsnorm_backward_workspace_bytes(d.rows, d.cols))},
+                      dy.options().dtype(at::kByte));
       ws = &own;
     }
     void* p = nullptr;
@@ -254,7 +252,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyObj
       p = c.address(*ws, "workspace");
       bytes = static_cast<size_t>(ws->numel());
     }
-    check_status(lib.rmsnorm_backward(&d, p, bytes, c.stream(a[9])), "fp8_rmsnorm_backward");
+    check_status(lib.rmsnorm_backward(&d, p, bytes, stream), "fp8_rmsnorm_backward");
   });
 }
 
@@ -344,20 +342,18 @@ PyObject* gemm_multi(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* k
   });
 }
 
-// bind(rmsnorm_cast, rmsnorm_backward, workspace_bytes, cast_multi, gemm_multi, check, workspace)
+// bind(rmsnorm_cast, rmsnorm_backward, workspace_bytes, cast_multi, gemm_multi, check)
 PyObject* bind(PyObject*, PyObject* args) {
   unsigned long long p[5];
-  PyObject *check, *workspace;
-  if (!PyArg_ParseTuple(args, "KKKKKOO", &p[0], &p[1], &p[2], &p[3], &p[4], &check, &workspace)) return nullptr;
+  PyObject* check;
+  if (!PyArg_ParseTuple(args, "KKKKKO", &p[0], &p[1], &p[2], &p[3], &p[4], &check)) return nullptr;
   lib.rmsnorm_cast = reinterpret_cast<decltype(lib.rmsnorm_cast)>(p[0]);
   lib.rmsnorm_backward = reinterpret_cast<decltype(lib.rmsnorm_backward)>(p[1]);
   lib.rmsnorm_backward_workspace_bytes = reinterpret_cast<decltype(lib.rmsnorm_backward_workspace_bytes)>(p[2]);
   lib.cast_multi = reinterpret_cast<decltype(lib.cast_multi)>(p[3]);
   lib.gemm_multi = reinterpret_cast<decltype(lib.gemm_multi)>(p[4]);
   Py_INCREF(check);
-  Py_INCREF(workspace);
   lib.check = check;
-  lib.workspace = workspace;
   Py_RETURN_NONE;
 }
 

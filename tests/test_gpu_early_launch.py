@@ -80,3 +80,53 @@ def test_scalars_rewritten_between_replays(cuda_lib, rows):
     for w, o in zip(want, got):
         for a, c in zip(w, o):
             assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+
+
+def backward_inputs(rows, cols):
+    g = torch.Generator().manual_seed(rows)
+    h, dy = (torch.randn(rows, cols, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    gamma = (1 + 0.1 * torch.randn(cols, generator=g)).to(torch.bfloat16).cuda()
+    rstd = (torch.rand(rows, generator=g) + 0.5).cuda()
+    return dy, h, gamma, rstd, torch.empty_like(h)
+
+
+def test_backward_takes_its_workspace_from_the_stream_it_runs_on(cuda_lib):
+    """The allocator keeps freed blocks per stream: a block that the current stream freed may still be in use there, so
+    a call on another stream must not be given it."""
+    rows, cols = 700, 1024
+    args = backward_inputs(rows, cols)
+    need = cuda_lib.fp8_rmsnorm_backward_workspace_bytes(rows, cols)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def bytes_reserved(stream):
+        return sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == stream.cuda_stream)
+    before = bytes_reserved(side)
+    assert before == 0
+    cuda_lib.fp8_rmsnorm_backward(*args, dgamma=torch.empty(cols, device="cuda"), stream=side)
+    torch.cuda.synchronize()
+    assert bytes_reserved(side) >= need
+
+
+def test_backward_beside_work_on_just_freed_memory(cuda_lib):
+    """The current stream is busy with temporaries of the workspace's size that Python has freed already; neither they
+    nor dgamma of the call on another stream may change."""
+    rows, cols = 700, 1024
+    args = backward_inputs(rows, cols)
+    n = cuda_lib.fp8_rmsnorm_backward_workspace_bytes(rows, cols)
+    want = torch.empty(cols, device="cuda")
+    cuda_lib.fp8_rmsnorm_backward(*args, dgamma=want)
+    side = torch.cuda.Stream()
+    got = [torch.empty(cols, device="cuda") for _ in range(8)]
+    sums = torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(8):
+        t = torch.full((n // 4,), float(i + 1), device="cuda")
+        torch.cuda._sleep(2_000_000)                     # about a millisecond: t is read long after it was freed
+        sums[i] = t.min() + t.max()
+        del t
+        cuda_lib.fp8_rmsnorm_backward(*args, dgamma=got[i], stream=side)
+    torch.cuda.synchronize()
+    cuda_lib.fp8t_check_device_error()
+    assert sums.tolist() == [2.0 * (i + 1) for i in range(8)]
+    assert all(torch.equal(g, want) for g in got)
