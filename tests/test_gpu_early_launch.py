@@ -96,13 +96,12 @@ def test_backward_takes_its_workspace_from_the_stream_it_runs_on(cuda_lib):
     rows, cols = 700, 1024
     args = backward_inputs(rows, cols)
     need = cuda_lib.fp8_rmsnorm_backward_workspace_bytes(rows, cols)
-    side = torch.cuda.Stream()
-    torch.cuda.synchronize()
 
     def bytes_reserved(stream):
         return sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == stream.cuda_stream)
-    before = bytes_reserved(side)
-    assert before == 0
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = next(s for s in (torch.cuda.Stream() for _ in range(64)) if bytes_reserved(s) == 0)
     cuda_lib.fp8_rmsnorm_backward(*args, dgamma=torch.empty(cols, device="cuda"), stream=side)
     torch.cuda.synchronize()
     assert bytes_reserved(side) >= need
