@@ -9,6 +9,7 @@ single symbol. No fast-math: the quantise, scale and AdamW arithmetic relies on 
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -60,8 +61,8 @@ def needs_build() -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    build_binding(force)
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """Compile the C library (it needs nvcc only)."""
     if not force and not needs_build():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
@@ -72,6 +73,18 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         cmd[1:1] = ["-Xptxas", "-v"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """Build what is out of date and return the library's path. Where the extension cannot be built (no C++ compiler,
+    no CUDA build of torch) the library stands all the same, with a warning: only the calls that the extension binds
+    are missing then, and they raise."""
+    build_library(force, verbose_ptxas)
+    try:
+        build_binding(force)
+    except (OSError, subprocess.CalledProcessError, ImportError) as e:
+        warnings.warn(f"{BINDING} could not be built, so the norm and 4-bit calls are missing: {e}", RuntimeWarning)
     return LIB
 
 
