@@ -278,12 +278,17 @@ def fp8_rmsnorm_backward_workspace_bytes(rows, cols):
 
 def _load_binding():
     """The calls of csrc/binding.cpp (norm and 4-bit entry points), with the library's addresses."""
+    how = ("run `python -c \"import __graft_entry__ as g; g.build()\"` or "
+           "`python -m optimizer_fp8_cast_b200.build`")
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is not built: {how}")
     spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
-    if spec is None or not os.path.exists(BINDING_PATH):
-        raise RuntimeError(f"{BINDING_PATH} is not built: run `python -c \"import __graft_entry__ as g; g.build()\"` "
-                           "or `python -m optimizer_fp8_cast_b200.build`")
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
+    from .build import binding_key
+    if getattr(m, "built_for", None) != binding_key():
+        raise RuntimeError(f"{BINDING_PATH} was built for {getattr(m, 'built_for', 'another version')!r}, this is "
+                           f"{binding_key()!r}: {how}")
     lib = load()
     m.bind(*(C.cast(getattr(lib, f), C.c_void_p).value for f in
              ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes", "fp4_cast_multi",

@@ -9,6 +9,7 @@ single symbol. No fast-math: the quantise, scale and AdamW arithmetic relies on 
 import os
 import subprocess
 import sys
+import sysconfig
 import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,19 +32,33 @@ def _sources():
     return out
 
 
+def binding_key() -> str:
+    """What the extension is compiled against: torch's C++ objects and Python's have other layouts in other versions."""
+    import torch
+    return "fp8t-binding torch %s cxx11abi %d %s" % (torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                                                     sysconfig.get_config_var("SOABI"))
+
+
+def binding_current() -> bool:
+    """Whether the extension is there, newer than its sources, and built for this torch and Python."""
+    if not os.path.exists(BINDING) or \
+            os.path.getmtime(BINDING) < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(HEADER)):
+        return False
+    with open(BINDING, "rb") as f:
+        return binding_key().encode() in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     """Compile the extension against the installed torch's headers (it is loaded after torch, whose
     libraries give its symbols)."""
-    if not force and os.path.exists(BINDING) and \
-            os.path.getmtime(BINDING) >= max(os.path.getmtime(BINDING_SRC), os.path.getmtime(HEADER)):
+    if not force and binding_current():
         return BINDING
-    import sysconfig
-
     import torch
     base = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp.%d" % os.getpid()
     subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                     "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                    '-DFP8T_BUILT_FOR="%s"' % binding_key(),
                     "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
                     "-isystem", os.path.join(base, "include"),
                     "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),

@@ -38,3 +38,28 @@ def test_library_that_cannot_be_built_is_an_error(commands):
     with pytest.raises(FileNotFoundError):
         build.build()
     assert seen == [build.NVCC]
+
+
+def test_extension_is_rebuilt_for_another_torch(commands, monkeypatch):
+    """It is compiled against torch's private C++ headers: a newer file alone does not make it the right one."""
+    seen, _ = commands
+    build.build_binding()
+    with open(build.BINDING, "wb") as f:                 # what the compiler writes holds the versions
+        f.write(b"\x7fELF " + build.binding_key().encode() + b"\0")
+    build.build_binding()
+    assert seen == [build.CXX]                           # current: not compiled again
+    import torch
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    build.build_binding()
+    assert seen == [build.CXX] * 2
+
+
+def test_extension_of_another_torch_is_refused(monkeypatch):
+    import optimizer_fp8_cast_b200 as fp8
+    build.build_library()
+    build.build_binding()
+    import torch
+    assert fp8._load_binding().built_for == build.binding_key()
+    monkeypatch.setattr(torch, "__version__", "0.0.other")
+    with pytest.raises(RuntimeError, match="was built for"):
+        fp8._load_binding()
