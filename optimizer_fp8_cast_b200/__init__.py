@@ -8,10 +8,12 @@ fallback, and a missing library is an error.
 
 The norm and 4-bit calls (``fp8_rmsnorm_cast``, ``fp8_rmsnorm_backward``, ``fp4_cast_multi``,
 ``fp4_gemm_multi``) are made per layer on as little as one token; their binding is compiled
-(``csrc/binding.cpp``, ``_binding.so``) and is loaded when one of them is first asked for.
+(``csrc/binding.cpp``, ``_binding.so``) and is loaded when one of them is first called.
 """
 import ctypes as C
+import functools
 import importlib.util
+import inspect
 import os
 
 import torch
@@ -296,17 +298,60 @@ def _load_binding():
     return m
 
 
-_BOUND = ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp4_cast_multi", "fp4_gemm_multi")
+_functions = {}
 
 
-def __getattr__(name):
-    # the calls of the compiled binding, loaded at their first use
-    if name in _BOUND:
-        m = _load_binding()
-        for f in _BOUND:
-            globals()[f] = getattr(m, f)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+def _compiled(declared):
+    """A call of the compiled binding as the package holds it until the first of them is made: that one loads the
+    binding and puts its functions in the package, so naming or importing them needs no library."""
+    name = declared.__name__
+
+    @functools.wraps(declared)
+    def call(*args, **kwargs):
+        if not _functions:
+            m = _load_binding()
+            found = {f: getattr(m, f) for f in ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp4_cast_multi",
+                                                "fp4_gemm_multi")}
+            _functions.update(found)
+            globals().update(found)
+        return _functions[name](*args, **kwargs)
+    call.__text_signature__ = str(inspect.signature(declared))
+    return call
+
+
+@_compiled
+def fp8_rmsnorm_cast(x, gamma, eps, *, residual=None, h=None, rstd=None, y=None, quant=Q_NONE, fmt=E4M3, q=None, sf=None,
+                     scale=None, amax=None, scale_inv=None, stream=None):
+    """h = bf16(x + residual); y = h / sqrt(mean(h^2) + eps) * gamma for each row of x (BF16 [rows, cols]).
+
+    Writes h (BF16, with a residual; may be x or residual), rstd (float32 [rows], for the backward pass), y
+    (BF16) and, as quant says, y's codes q (uint8): Q_FP8 with scale, amax (max-accumulated) and scale_inv
+    (float32 [1] each), Q_MXFP8 / Q_MXFP4 / Q_NVFP4 with sf (uint8 scale atoms along the rows), Q_NVFP4 also
+    with scale and optionally amax and scale_inv."""
+
+
+@_compiled
+def fp8_rmsnorm_backward(dy, h, gamma, rstd, dh, *, dres=None, dgamma=None, dgamma_bf16=None, workspace=None, stream=None):
+    """Gradients of fp8_rmsnorm_cast: dh (BF16 [rows, cols]; may be dy or dres) from dy and the forward pass's h
+    and rstd, with dres added where given; dgamma (float32 [cols]) and / or dgamma_bf16.
+
+    workspace is a uint8 CUDA tensor of at least fp8_rmsnorm_backward_workspace_bytes bytes (allocated per
+    call where it is missing)."""
+
+
+@_compiled
+def fp4_cast_multi(casts, stream=None):
+    """4-bit quantisation. casts: a list of dicts with x (BF16 [rows, cols]), quant (Q_MXFP4 or Q_NVFP4), q_row
+    (uint8 [rows, cols / 2]) / sf_row and / or q_col (uint8 [cols, rows / 2]: transposed) / sf_col, scales uint8
+    tensors of fp4_scale_bytes; for NVFP4 also scale (float32 [1]) and optionally amax (max-accumulated) and
+    scale_inv."""
+
+
+@_compiled
+def fp4_gemm_multi(gemms, stream=None):
+    """4-bit block-scaled GEMMs: a list of dicts with A (uint8 [M, K / 2]), a_sf, B (uint8 [N, K / 2]), b_sf, quant,
+    D (BF16 [M, N]) and optionally a_scale_inv, b_scale_inv (float32 [1]); D = bf16(A . B^T) with the operands'
+    block scales, times the scale inverses."""
 
 
 def fp8_scale_update(amax, history, fp8_max, algo, margin, scale, scale_inv, stream=None):

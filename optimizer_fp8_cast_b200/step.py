@@ -239,7 +239,7 @@ class Fp8LinearStep:
 
     def fp4_cast_all(self, xs, dys, stream=None):
         """4-bit: X, W and dY along both of their axes, as the products read them."""
-        from . import fp4_cast_multi           # loads the library: not while this module is imported
+        from . import fp4_cast_multi           # here: the compiled function itself from the second call on
         casts = []
         for k, L in enumerate(self.layers):
             for role, name, src in ((ROLE_X, "X", xs[k]), (ROLE_W, "W", L.W), (ROLE_DY, "dY", dys[k])):
