@@ -57,13 +57,15 @@ struct DeviceInfo {
   int gemm_wide_clusters = 0;  // ... of its wide-tile form
   int gemm_mx_clusters = 0;    // ... of its MXFP8 variant
   int gemm_mxw_clusters = 0;   // ... of the MXFP8 256 x 384 kernel
-  int gemm_fp4_clusters = 0;   // ... of the 4-bit tile kernel (every form: one CTA per SM)
   int mx_cast_blocks_per_sm = 0;
-  int fp4_cast_blocks_per_sm = 0;
-  int fp4_cast_rows_blocks_per_sm = 0;
   int cast_blocks_per_sm = 0;
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
+  // set up by their own first calls, so that no other call loads these kernels or fails with them
+  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false};
+  int fp4_cast_blocks_per_sm = 0;
+  int fp4_cast_rows_blocks_per_sm = 0;
+  int gemm_fp4_clusters = 0;         // co-resident clusters of the 4-bit tile kernel (every form: one CTA per SM)
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mutex;
@@ -186,42 +188,6 @@ fp8t_status current_device(DeviceInfo** out) {
         (void)cudaGetLastError();
         d.mx_cast_blocks_per_sm = 1;
       }
-      e = allow_fp4_tile_smem<fp8t::gemm::SmallGroup4>();
-      if (e == cudaSuccess) e = allow_fp4_tile_smem<fp8t::gemm::LargeGroup4>();
-      if (e == cudaSuccess) e = allow_fp4_tile_smem<fp8t::gemm::ListGroup4>();
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fp8t::fp4::k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fp8t::fp4::kCastSmemBytes);
-      if (e == cudaSuccess) e = allow_fp4_split_smem();
-      for (auto* k : {fp8t::norm::k_rmsnorm_backward<1>, fp8t::norm::k_rmsnorm_backward<2>, fp8t::norm::k_rmsnorm_backward<3>,
-                      fp8t::norm::k_rmsnorm_backward<4>})
-        if (e == cudaSuccess)
-          e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::norm::kBwdMaxSmem);
-      if (e != cudaSuccess) {
-        d.state = 0;
-        return fail(FP8T_ERR_CUDA, "cudaFuncSetAttribute(4-bit): %s", cudaGetErrorString(e));
-      }
-      cfg.blockDim = dim3(fp8t::gemm::kThreads4, 1, 1);
-      cfg.dynamicSmemBytes = fp8t::gemm::kSmemBytes4<true, true>;
-      clusters = 0;
-      e = cudaOccupancyMaxActiveClusters(&clusters, fp8t::gemm::k_fp4_gemm<true, true, fp8t::gemm::ListGroup4>, &cfg);
-      if (e != cudaSuccess || clusters < 1) {
-        (void)cudaGetLastError();
-        clusters = sms / 2;
-      }
-      d.gemm_fp4_clusters = clusters;
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.fp4_cast_blocks_per_sm, fp8t::fp4::k_fp4_cast,
-                                                        fp8t::fp4::kCastThreads, fp8t::fp4::kCastSmemBytes);
-      if (e != cudaSuccess || d.fp4_cast_blocks_per_sm < 1) {
-        (void)cudaGetLastError();
-        d.fp4_cast_blocks_per_sm = 1;
-      }
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.fp4_cast_rows_blocks_per_sm, fp8t::fp4::k_fp4_cast_rows,
-                                                        fp8t::fp4::kCastThreads, 0);
-      if (e != cudaSuccess || d.fp4_cast_rows_blocks_per_sm < 1) {
-        (void)cudaGetLastError();
-        d.fp4_cast_rows_blocks_per_sm = 1;
-      }
       e = cudaFuncSetAttribute(fp8t::cast::k_cast_transpose_amax<false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::cast::kSmemBytes);
       if (e == cudaSuccess)
@@ -250,6 +216,69 @@ fp8t_status current_device(DeviceInfo** out) {
   if (d.state != 1) return fail(FP8T_ERR_UNSUPPORTED_DEVICE, "device %d is not sm_100", dev);
   *out = &d;
   return FP8T_OK;
+}
+
+// Runs `set_up` (a cudaError_t) once per device for the calls that need it; a failure is tried again by the next call.
+template <class F>
+fp8t_status once_per_device(std::atomic<bool>& ready, const char* what, F&& set_up) {
+  if (ready.load(std::memory_order_acquire)) return FP8T_OK;
+  std::lock_guard<std::mutex> lock(g_dev_mutex);
+  if (ready.load(std::memory_order_relaxed)) return FP8T_OK;
+  const cudaError_t e = set_up();
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(FP8T_ERR_CUDA, "%s: setting up its kernels: %s", what, cudaGetErrorString(e));
+  }
+  ready.store(true, std::memory_order_release);
+  return FP8T_OK;
+}
+template <class K>
+int resident_blocks(K* kernel, int threads, int smem) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) == cudaSuccess && n > 0) return n;
+  (void)cudaGetLastError();
+  return 1;
+}
+fp8t_status ready_fp4_cast(DeviceInfo* d) {
+  using namespace fp8t::fp4;
+  return once_per_device(d->fp4_cast_ready, "fp4_cast", [&] {
+    const cudaError_t e = cudaFuncSetAttribute(k_fp4_cast, cudaFuncAttributeMaxDynamicSharedMemorySize, kCastSmemBytes);
+    if (e == cudaSuccess) {
+      d->fp4_cast_blocks_per_sm = resident_blocks(k_fp4_cast, kCastThreads, kCastSmemBytes);
+      d->fp4_cast_rows_blocks_per_sm = resident_blocks(k_fp4_cast_rows, kCastThreads, 0);
+    }
+    return e;
+  });
+}
+fp8t_status ready_fp4_gemm(DeviceInfo* d) {
+  using namespace fp8t::gemm;
+  return once_per_device(d->fp4_gemm_ready, "fp4_gemm", [&] {
+    cudaError_t e = allow_fp4_tile_smem<SmallGroup4>();
+    if (e == cudaSuccess) e = allow_fp4_tile_smem<LargeGroup4>();
+    if (e == cudaSuccess) e = allow_fp4_tile_smem<ListGroup4>();
+    if (e == cudaSuccess) e = allow_fp4_split_smem();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (d->sms / 2), 1, 1);
+    cfg.blockDim = dim3(kThreads4, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes4<true, true>;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, k_fp4_gemm<true, true, ListGroup4>, &cfg) != cudaSuccess || clusters < 1) {
+      (void)cudaGetLastError();
+      clusters = d->sms / 2;
+    }
+    d->gemm_fp4_clusters = clusters;
+    return cudaSuccess;
+  });
+}
+fp8t_status ready_norm_backward(DeviceInfo* d) {
+  using namespace fp8t::norm;
+  return once_per_device(d->norm_backward_ready, "fp8_rmsnorm_backward", [] {
+    cudaError_t e = cudaSuccess;
+    for (auto* k : {k_rmsnorm_backward<1>, k_rmsnorm_backward<2>, k_rmsnorm_backward<3>, k_rmsnorm_backward<4>})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdMaxSmem);
+    return e;
+  });
 }
 
 // A launch that may begin while the kernel before it in the stream still runs (the kernel calls pdl_wait).
@@ -1119,7 +1148,7 @@ fp8t_status fp4_cast_multi(const fp8t_fp4_cast_tensor* tensors, int32_t n_tensor
   }
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
-  if (st != FP8T_OK) return st;
+  if (st != FP8T_OK || (st = ready_fp4_cast(dev)) != FP8T_OK) return st;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   using namespace fp8t::fp4;
@@ -1447,7 +1476,7 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
   }
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
-  if (st != FP8T_OK) return st;
+  if (st != FP8T_OK || (st = ready_fp4_gemm(dev)) != FP8T_OK) return st;
   // consecutive problems of one format and size class share a launch: at most 128 rows (the split kernel) or more
   // (pair tiles). Split / tiles, NVFP4: 1 x 4096 x 4096 5.0 / 10.4 us, 128 x 4096 x 4096 8.8 / 11.2, 128 x 11008 x 4096
   // 10.8 / 12.0, 128 x 4096 x 256 4.9 / 6.4. With several tiles of tokens the split kernel took 7.2 to 33 us over 19
@@ -1642,7 +1671,7 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
                 static_cast<size_t>(ctas * d.cols * 4));
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
-  if (st != FP8T_OK) return st;
+  if (st != FP8T_OK || (st = ready_norm_backward(dev)) != FP8T_OK) return st;
   using namespace fp8t::norm;
   Bwd p = {};
   p.dy = static_cast<const uint4*>(d.dy_bf16);
