@@ -76,6 +76,8 @@ class Fp8LinearStep:
                  w_init=None, device="cuda", counters=False, device_step=False, fused_update=True,
                  fused_norm=True, fused_wcast=True, transposes=False, recipe="delayed",
                  side_update=False):
+        if counters and recipe in ("mxfp4", "nvfp4"):
+            raise ValueError(f"recipe {recipe!r} keeps no counters: the 4-bit casts count nothing")
         self.device = torch.device(device)
         self.tokens = tokens
         self.algo = AMAX_MAX if algo == "max" else AMAX_MOST_RECENT

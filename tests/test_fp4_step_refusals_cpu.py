@@ -1,0 +1,20 @@
+"""What the step driver's 4-bit recipes do not do is refused or left out, not silently empty (no kernel runs)."""
+import pytest
+import torch
+
+from optimizer_fp8_cast_b200.step import Fp8LinearStep
+from tests.test_step_config_cpu import HP
+
+FOUR = ("mxfp4", "nvfp4")
+
+
+def make(recipe, fin=256, fout=160, tokens=192, **kw):
+    return Fp8LinearStep([(fin, fout)], tokens, 16, adamw=HP, w_init=[torch.zeros(fin, fout)], device="cpu",
+                         recipe=recipe, **kw)
+
+
+@pytest.mark.parametrize("recipe", FOUR)
+def test_counters_are_refused(recipe):
+    with pytest.raises(ValueError, match="counters"):
+        make(recipe, counters=True)
+    assert make(recipe).counters is None and make("delayed", counters=True).counters is not None
