@@ -78,6 +78,9 @@ class Fp8LinearStep:
                  side_update=False):
         if counters and recipe in ("mxfp4", "nvfp4"):
             raise ValueError(f"recipe {recipe!r} keeps no counters: the 4-bit casts count nothing")
+        if recipe in ("mxfp4", "nvfp4") and any(n % 32 for n in (tokens, *(f for s in layer_shapes for f in s))):
+            raise ValueError(f"recipe {recipe!r} needs tokens and layer sizes that are multiples of 32 (every one of them "
+                             "is some product's contraction)")
         self.device = torch.device(device)
         self.tokens = tokens
         self.algo = AMAX_MAX if algo == "max" else AMAX_MOST_RECENT

@@ -18,3 +18,11 @@ def test_counters_are_refused(recipe):
     with pytest.raises(ValueError, match="counters"):
         make(recipe, counters=True)
     assert make(recipe).counters is None and make("delayed", counters=True).counters is not None
+
+
+@pytest.mark.parametrize("recipe", FOUR)
+@pytest.mark.parametrize("size", [dict(fin=144), dict(fout=48), dict(tokens=200)])
+def test_sizes_are_refused_at_construction(recipe, size):
+    with pytest.raises(ValueError, match="multiples of 32"):
+        make(recipe, **size)
+    make(recipe, fin=32, fout=96, tokens=32)
