@@ -48,7 +48,7 @@ ROLE_FMT = (E4M3, E4M3, E5M2)
 
 
 class LinearLayerBuffers:
-    def __init__(self, fin, fout, tokens, w_init, device, transposes=False):
+    def __init__(self, fin, fout, tokens, w_init, device, transposes=False, codes8=True):
         u8 = dict(dtype=torch.uint8, device=device)
         bf = dict(dtype=torch.bfloat16, device=device)
         self.fin, self.fout, self.tokens = fin, fout, tokens
@@ -56,12 +56,13 @@ class LinearLayerBuffers:
         self.master = self.W.float()
         self.m = torch.zeros_like(self.master)
         self.v = torch.zeros_like(self.master)
-        self.Xq = torch.empty(tokens, fin, **u8)
-        self.Wq = torch.empty(fin, fout, **u8)
-        self.dYq = torch.empty(tokens, fout, **u8)
-        self.XqT = torch.empty(fin, tokens, **u8) if transposes else None
-        self.WqT = torch.empty(fout, fin, **u8) if transposes else None
-        self.dYqT = torch.empty(fout, tokens, **u8) if transposes else None
+        # 8-bit codes; a recipe with formats of its own (codes8=False) has none
+        self.Xq = torch.empty(tokens, fin, **u8) if codes8 else None
+        self.Wq = torch.empty(fin, fout, **u8) if codes8 else None
+        self.dYq = torch.empty(tokens, fout, **u8) if codes8 else None
+        self.XqT = torch.empty(fin, tokens, **u8) if codes8 and transposes else None
+        self.WqT = torch.empty(fout, fin, **u8) if codes8 and transposes else None
+        self.dYqT = torch.empty(fout, tokens, **u8) if codes8 and transposes else None
         self.Y = torch.empty(tokens, fout, **bf)
         self.dX = torch.empty(tokens, fin, **bf)
         self.dW = torch.empty(fin, fout, **bf)
@@ -100,7 +101,8 @@ class Fp8LinearStep:
         self.fp8_max = torch.tensor([FP8_MAX[ROLE_FMT[i % 3]] for i in range(n)], **f32)
         self.counters = torch.zeros(n, 3, dtype=torch.int64, device=self.device) if counters else None
         self.transposes = transposes
-        self.layers = [LinearLayerBuffers(fi, fo, tokens, w_init[k], self.device, transposes)
+        self.layers = [LinearLayerBuffers(fi, fo, tokens, w_init[k], self.device, transposes,
+                                          codes8=recipe not in ("mxfp4", "nvfp4"))
                        for k, (fi, fo) in enumerate(layer_shapes)]
         self.grad_norm = torch.zeros(1, **f32)
         self.skipped = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -113,8 +115,9 @@ class Fp8LinearStep:
         # gradient sum of squares from the wgrad epilogues (fused_norm)
         self.fused_norm = fused_norm
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.device)
-        gws = fp8_gemm_sumsq_workspace_bytes(self._gemm_descs(sumsq=True))
-        self.gemm_workspace = torch.zeros(gws, dtype=torch.uint8, device=self.device)
+        if recipe not in ("mxfp4", "nvfp4"):
+            gws = fp8_gemm_sumsq_workspace_bytes(self._gemm_descs(sumsq=True))
+            self.gemm_workspace = torch.zeros(gws, dtype=torch.uint8, device=self.device)
         self.adamw_ticket = torch.zeros(1, dtype=torch.int32, device=self.device)
         # current scaling: every scale from the tensor's own amax (no history, no delayed update)
         # mxfp8: E4M3 codes with a scale per 32 values, both orientations, block-scaled GEMMs

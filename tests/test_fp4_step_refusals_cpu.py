@@ -26,3 +26,13 @@ def test_sizes_are_refused_at_construction(recipe, size):
     with pytest.raises(ValueError, match="multiples of 32"):
         make(recipe, **size)
     make(recipe, fin=32, fout=96, tokens=32)
+
+
+@pytest.mark.parametrize("recipe", FOUR)
+@pytest.mark.parametrize("transposes", [False, True])
+def test_no_8_bit_buffers(recipe, transposes):
+    st = make(recipe, transposes=transposes)
+    L = st.layers[0]
+    assert all(getattr(L, n) is None for n in ("Xq", "Wq", "dYq", "XqT", "WqT", "dYqT"))
+    assert not hasattr(st, "gemm_workspace") and L.dW.shape == (256, 160)
+    assert make("delayed").layers[0].Xq.numel() == 256 * 192 and make("delayed").gemm_workspace.numel() > 0
