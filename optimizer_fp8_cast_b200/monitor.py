@@ -45,10 +45,11 @@ class HealthMonitor:
         return ev
 
     def maybe_check(self, st):
-        """Every `every` steps of an Fp8LinearStep: read its buffers and check them."""
+        """Every `every` steps of an Fp8LinearStep: read its buffers and check them. A recipe that keeps no amax
+        (mxfp8, mxfp4) has the gradient norm and the skip flag checked and no amax taken for one."""
         if st.t % self.every:
             return []
-        amax = st.history[:, 0].tolist()
+        amax = st.history[:, 0].tolist() if st.keeps_amax else []
         return self.check(st.t, amax, float(st.grad_norm.item()), int(st.skipped.item()),
                           scale=st.scale.tolist(),
                           counters=st.counters.tolist() if st.counters is not None else None,

@@ -125,6 +125,8 @@ class Fp8LinearStep:
         assert recipe in ("delayed", "current", "mxfp8", "mxfp4", "nvfp4")
         self.recipe = recipe
         self.quant = {"mxfp4": Q_MXFP4, "nvfp4": Q_NVFP4}.get(recipe)
+        # block scales alone need no amax of a tensor: its slots and history stay zero
+        self.keeps_amax = recipe not in ("mxfp8", "mxfp4")
         self.current_ws = torch.zeros(CURRENT_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         if recipe != "delayed":
             fused_update = fused_wcast = False

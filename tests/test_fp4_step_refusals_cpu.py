@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from optimizer_fp8_cast_b200.monitor import HealthMonitor
 from optimizer_fp8_cast_b200.step import Fp8LinearStep
 from tests.test_step_config_cpu import HP
 
@@ -36,3 +37,15 @@ def test_no_8_bit_buffers(recipe, transposes):
     assert all(getattr(L, n) is None for n in ("Xq", "Wq", "dYq", "XqT", "WqT", "dYqT"))
     assert not hasattr(st, "gemm_workspace") and L.dW.shape == (256, 160)
     assert make("delayed").layers[0].Xq.numel() == 256 * 192 and make("delayed").gemm_workspace.numel() > 0
+
+
+@pytest.mark.parametrize("recipe,kept", [("mxfp4", False), ("mxfp8", False), ("nvfp4", True), ("delayed", True)])
+def test_monitor_takes_no_amax_that_is_not_kept(recipe, kept):
+    """The zeros of a history that nothing fills are no amax: a monitor that averages them looks as if it watched."""
+    st = make(recipe)
+    mon = HealthMonitor(n_tensors=3, every=1, window=2)
+    for st.t in range(4):
+        assert mon.maybe_check(st) == []
+    assert [len(r) for r in mon.recent] == [2 * kept] * 3
+    st.skipped.fill_(1)
+    assert [e[0] for e in mon.maybe_check(st)] == ["skip"]
