@@ -49,7 +49,7 @@ class HealthMonitor:
         (mxfp8, mxfp4) has the gradient norm and the skip flag checked and no amax taken for one."""
         if st.t % self.every:
             return []
-        amax = st.history[:, 0].tolist() if st.keeps_amax else []
+        amax = st.history[:, 0].tolist() if getattr(st, "keeps_amax", True) else []
         return self.check(st.t, amax, float(st.grad_norm.item()), int(st.skipped.item()),
                           scale=st.scale.tolist(),
                           counters=st.counters.tolist() if st.counters is not None else None,
