@@ -28,8 +28,10 @@ Other recipes: "current" (every scale from the tensor's own amax), "mxfp8" (bloc
 orientations cast, block-scaled GEMMs) and the 4-bit forms "mxfp4" and "nvfp4": X, W and dY cast along
 both of their axes in one launch (the column-wise copies transposed), the three products in another,
 AdamW with its norm pass. "nvfp4" has a per-tensor scale beside the block scales, delayed like the FP8
-ones (its update follows the casts, with 448 * 6 as the format's largest value; as there, the first step runs
-on a scale of 1, under which blocks smaller than about 2^-7.5 quantise to zero).
+ones (its update follows the casts, with 448 * 6 as the format's largest value). Its block scales span 2^18 (of
+E5M2's 2^32), so a first step on scales of 1 would quantise every block below 2^-7.4, most gradients, to zero. W's
+first scale is that of its own amax, dY's NVFP4_FIRST_DY, and prime_scales(xs, dys) gives every tensor the one
+of its own amax.
 """
 import torch
 
@@ -45,6 +47,9 @@ from . import (AMAX_MAX, AMAX_MOST_RECENT, CURRENT_WORKSPACE_BYTES, E4M3, E5M2, 
 
 ROLE_X, ROLE_W, ROLE_DY = 0, 1, 2
 ROLE_FMT = (E4M3, E4M3, E5M2)
+# nvfp4's scale of dY before any amax is known: blocks from 6 * 2^-10 / 512 = 1.1e-5 (1.8e-4 with normal scales) up
+# to 2688 / 512 = 5.25 are represented, larger ones saturate there
+NVFP4_FIRST_DY = 512.0
 
 
 class LinearLayerBuffers:
@@ -165,6 +170,27 @@ class Fp8LinearStep:
             self._update_done = torch.cuda.Event()
         if self.fused_wcast and self.device.type == "cuda":
             self.prime()
+        if recipe == "nvfp4":
+            self.scale[ROLE_DY::3] = NVFP4_FIRST_DY
+            self.scale_inv[ROLE_DY::3] = 1.0 / NVFP4_FIRST_DY
+            if self.device.type == "cuda":
+                self._prime_weight_scales()
+
+    def _prime_weight_scales(self):
+        """nvfp4: every W's scale from its own amax."""
+        from . import fp4_cast_multi
+        fp4_cast_multi([self._fp4_cast_desc(k, ROLE_W, "W", L.W) for k, L in enumerate(self.layers)])
+        for i in range(ROLE_W, 3 * len(self.layers), 3):
+            fp8_scale_update(self._slot(self.amax, i), self.history[i:i + 1], self._slot(self.fp8_max, i), self.algo,
+                             self.margin, self._slot(self.scale, i), self._slot(self.scale_inv, i))
+
+    def prime_scales(self, xs, dys, stream=None):
+        """nvfp4, before the first step: the scales of X, W and dY from the amax of these tensors (xs and dys as step
+        takes them), so that the first step already runs on its own tensors' scales."""
+        if self.recipe != "nvfp4":
+            raise ValueError(f"prime_scales: recipe {self.recipe!r} has no delayed 4-bit scales")
+        self.fp4_cast_all(xs, dys, stream)
+        self.scale_update(stream)
 
     def prime(self):
         """Cast every W with its current scale (codes, transposed codes, amax, scale inverse), as
@@ -247,14 +273,17 @@ class Fp8LinearStep:
             return {}
         return {arg: self._slot(getattr(self, t), 3 * k + role) for arg, t in names.items()}
 
+    def _fp4_cast_desc(self, k, role, name, src):
+        return dict(x=src, quant=self.quant, **self.layers[k].fp4[name],
+                    **self._fp4_scalars(k, role, dict(scale="scale", amax="amax", scale_inv="sinv_used")))
+
     def fp4_cast_all(self, xs, dys, stream=None):
         """4-bit: X, W and dY along both of their axes, as the products read them."""
         from . import fp4_cast_multi           # here: the compiled function itself from the second call on
         casts = []
         for k, L in enumerate(self.layers):
             for role, name, src in ((ROLE_X, "X", xs[k]), (ROLE_W, "W", L.W), (ROLE_DY, "dY", dys[k])):
-                casts.append(dict(x=src, quant=self.quant, **L.fp4[name],
-                                  **self._fp4_scalars(k, role, dict(scale="scale", amax="amax", scale_inv="sinv_used"))))
+                casts.append(self._fp4_cast_desc(k, role, name, src))
         fp4_cast_multi(casts, stream=stream)
 
     def fp4_gemm_all(self, stream=None):
