@@ -564,12 +564,12 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_gemm_split(const __grid_c
   if (warp == 1) {
     tmem_alloc(smem_u32(&S->tmem_base), Sh::kTmem);
     tmem_relinquish();
-    // Only now may the next kernel start: one that took this SM's tensor memory first would hold it until this
-    // grid has ended, and this CTA would wait for it.
-    pdl_trigger();
   }
   tc_fence_before();
   __syncthreads();
+  // Only now may the next kernel start: one that took this SM's tensor memory first would hold it until this grid has
+  // ended, and this CTA would wait for it. By every thread: 128 x 4096 x 4096 7.8 us, by the allocating warp alone 9.2.
+  pdl_trigger();
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
   pdl_wait();
