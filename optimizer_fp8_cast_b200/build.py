@@ -99,6 +99,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     try:
         build_binding(force)
     except (OSError, subprocess.CalledProcessError, ImportError) as e:
+        if os.path.exists(BINDING):            # an older one may pass structures of an older header
+            os.remove(BINDING)
         warnings.warn(f"{BINDING} could not be built, so the norm and 4-bit calls are missing: {e}", RuntimeWarning)
     return LIB
 

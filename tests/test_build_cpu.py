@@ -1,4 +1,5 @@
 """The build's parts do not stand in one another's way (nothing is compiled here)."""
+import os
 import subprocess
 
 import pytest
@@ -30,6 +31,17 @@ def test_library_is_built_where_the_extension_cannot_be(commands):
     with pytest.warns(RuntimeWarning, match="norm and 4-bit calls are missing"):
         assert build.build() == build.LIB
     assert seen == [build.NVCC, build.CXX]
+
+
+def test_an_extension_that_cannot_be_rebuilt_does_not_stay(commands):
+    """Its calls raise then, instead of passing the new library structures of an older header."""
+    _, missing = commands
+    with open(build.BINDING, "wb") as f:
+        f.write(b"older")
+    missing.add(build.CXX)
+    with pytest.warns(RuntimeWarning):
+        build.build()
+    assert not os.path.exists(build.BINDING)
 
 
 def test_library_that_cannot_be_built_is_an_error(commands):
