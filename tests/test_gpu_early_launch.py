@@ -129,3 +129,22 @@ def test_backward_beside_work_on_just_freed_memory(cuda_lib):
     cuda_lib.fp8t_check_device_error()
     assert sums.tolist() == [2.0 * (i + 1) for i in range(8)]
     assert all(torch.equal(g, want) for g in got)
+
+
+def test_backward_captured_on_the_stream_it_is_given(cuda_lib):
+    """The workspace is then the graph's; eager calls on the same stream between replays change nothing."""
+    rows, cols = 700, 1024
+    args, other = backward_inputs(rows, cols), backward_inputs(rows, cols)
+    want, got, eager = (torch.empty(cols, device="cuda") for _ in range(3))
+    cuda_lib.fp8_rmsnorm_backward(*args, dgamma=want)
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        cuda_lib.fp8_rmsnorm_backward(*args, dgamma=got, stream=s)
+    for _ in range(3):
+        got.fill_(float("nan"))
+        graph.replay()
+        s.wait_stream(torch.cuda.current_stream())
+        cuda_lib.fp8_rmsnorm_backward(other[1], other[0], *other[2:], dgamma=eager, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
