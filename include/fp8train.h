@@ -434,11 +434,14 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
  *   h    = bf16(f32(x) + f32(residual))         (h = x without a residual)
  *   rstd = 1 / sqrt(sum_c h^2 / cols + eps)
  *   y    = (f32(h) * rstd) * f32(gamma)          f32, statistics in f32
+ * (the mean here and in the backward pass is the sum times the f32 nearest to 1 / cols: one rounding more than a quotient)
  * y is written as BF16 (y_bf16) and / or quantised from its f32 value (q): FP8T_Q_FP8 as
  * fp8_cast_transpose_amax (d_scale, d_amax_inout, d_scale_inv_out; the amax is max|y| in f32), the
  * block formats along each row as fp8_mx_cast_multi's and fp4_cast_multi's row-wise copies, with amax and
  * exponents of the f32 values. (A column-wise copy, for wgrad, is a cast of y_bf16.)
  * A row with an infinite or NaN element, or whose sum of squares overflows f32, follows the formula.
+ * Any number of rows is quantised. The products that read the codes: fp4_gemm_multi any number of rows,
+ * fp8_gemm_multi multiples of 16, fp8_mx_gemm_multi multiples of 128.
  */
 typedef struct fp8t_rmsnorm {
     const void* x_bf16;             /* rows x cols                                                  */

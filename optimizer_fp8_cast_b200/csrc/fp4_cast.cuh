@@ -19,9 +19,10 @@
 //   row-wise: a quarter-warp per block of 8 consecutive rows, 16 bytes of codes per block.
 // NVFP4's amax is kept per thread from tile to tile and leaves the CTA by one atomic per tensor: one per warp and
 // tile, all to one address, made 16384 x 11008 both ways 237 instead of 114 us.
-// Bound: HBM, 2 B read + 0.5 B per copy written (+ 1/32 B MXFP4, 1/16 B NVFP4 of scales) per element; with both
-// copies every element is quantised twice, and the instructions per element (BF16 pairs compared as pairs,
-// multiplied as f32x2 pairs) come close to it: 8192 x 4096 both ways 21 us (MXFP4) and 26 (NVFP4), row-wise 14.6 and 16.1
+// Bound: HBM, 2 B read + 0.5 B per copy written (+ 1/32 B MXFP4, 1/16 B NVFP4 of scales) per element. With both
+// copies every element is quantised twice (BF16 pairs compared as pairs, multiplied as f32x2 pairs) and latency comes
+// first: the 16 warps per SM that 127 registers leave use half of the issue slots and half of DRAM, stalled by turns on
+// shared memory, dependencies and a tile's two barriers: 8192 x 4096 both ways 21 us (MXFP4) and 26 (NVFP4), row-wise 14.6 and 16.1
 // (tiles with one copy: 16.2 and 18.8), 16384 x 11008 both ways 92 and 114, inputs and outputs of three calls in turn.
 #pragma once
 

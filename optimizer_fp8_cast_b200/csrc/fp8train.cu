@@ -1478,8 +1478,8 @@ fp8t_status fp4_gemm_multi(const fp8t_fp4_gemm_desc* gemms, int32_t n_gemms, voi
   fp8t_status st = current_device(&dev);
   if (st != FP8T_OK || (st = ready_fp4_gemm(dev)) != FP8T_OK) return st;
   // consecutive problems of one format and size class share a launch: at most 128 rows (the split kernel) or more
-  // (pair tiles). Split / tiles, NVFP4: 1 x 4096 x 4096 5.0 / 10.4 us, 128 x 4096 x 4096 8.8 / 11.2, 128 x 11008 x 4096
-  // 10.8 / 12.0, 128 x 4096 x 256 4.9 / 6.4. With several tiles of tokens the split kernel took 7.2 to 33 us over 19
+  // (pair tiles). Split / tiles, NVFP4: 1 x 4096 x 4096 4.7 / 10.4 us, 128 x 4096 x 4096 7.3 / 11.2, 128 x 11008 x 4096
+  // 10.6 / 12.0, 128 x 4096 x 256 4.8 / 6.4. With several tiles of tokens the split kernel took 7.2 to 33 us over 19
   // sizes of 200 to 8000 rows, pair tiles 5.7 to 12.5 (it won at 300 x 1024 x 4096 only)
   for (int32_t b0 = 0, b1 = 0; b0 < n_gemms; b0 = b1) {
     const bool few = gemms[b0].M <= fp8t::gemm::kMaxSplitRows;

@@ -21,8 +21,9 @@
 //     copy after an mbarrier wait did not overlap the MMAs before it: 1034 against 773 cycles for 8
 //     copies and 8 MMAs per k-block;
 //   - copies are spread between the MMAs in the order of use.
-// Beyond that, what the SMs take in from L2 is the bound: about 11 TB/s in both forms (35 KB per SM and k-block
-// of a 256-column tile, 44 KB of a 384-column one with half as much work again).
+// Beyond that, L2 is the bound: 12 TB/s through it in a profile of 16384 x 11008 x 4096 (operands, their way from DRAM and
+// D), of it 10 to 11 of operands that the SMs take in (35 KB per SM and k-block of a 256-column tile, 44 KB of a
+// 384-column one with half as much work again).
 //   256 columns: two accumulators let the epilogue of a tile run beside the next tile's MMAs. Two of 256 columns
 //     and the scales (24 or 48) do not fit the 512 TMEM columns, so they overlap by kOv columns: accumulator 0
 //     at 0..255, accumulator 1 at 256 - kOv, scales after it. The epilogue reads the shared columns first and
@@ -447,9 +448,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
 // partial tile in the shared memory of the CTAs that own its tokens (groups of four: group j belongs to rank
 // j mod S, 16 bytes of a weight row at a time); after a cluster barrier each owner adds the S partials in rank
 // order, scales, rounds and stores its tokens' rows of D, 128 columns of a row at a time (a warp per group of tokens, four
-// columns per lane: 128 x 4096 x 4096 9.7 -> 9.1 us against two columns per lane of 64). No workspace, and the order
-// of additions is fixed. For many tokens the exchange counts: remote stores leave an SM at about 15 bytes per cycle, 1.7
-// of the 9.1 us above (measured with all of them kept in the CTA).
+// columns per lane: 128 x 4096 x 4096 9.7 -> 9.1 us against two columns per lane of 64, and 7.8 since the next kernel
+// is let in behind the set-up). No workspace, and the order of additions is fixed. For many tokens the exchange counts:
+// remote stores leave an SM at about 15 bytes per cycle, 1.7 us of these (measured with all of them kept in the CTA).
 // TMEM: accumulator (weight rows x tokens) in columns 0..BT-1, then the scales.
 constexpr int kSplitThreads = 128;
 constexpr int kMaxSplitProblems = 4;

@@ -12,8 +12,8 @@
 //
 // What bounds it: HBM, 2 B (x) + 2 B (residual) read and 2 B (h) + code bytes written per element. A row is
 // read once and held in registers (four 16-byte vectors per thread at most) between the sum of squares and
-// the quantisation. At 20 instructions per element the issue rate bound it instead (50% issue at 16 warps per
-// SM, 45 us for 8192 x 4096 to FP8), so arithmetic runs on pairs (f32x2 add, multiply, FMA: two elements
+// the quantisation. Scalar arithmetic, 20 instructions per element, kept the loads waiting (45 us for 8192 x 4096 to
+// FP8, half of the issue slots used by 16 warps per SM), so it runs on pairs (f32x2 add, multiply, FMA: two elements
 // per instruction, each rounded as the scalar one) and amax is a three-input maximum. A thread's loads of a row
 // come at once and then none until the next row, so one thread asks for the next row's bytes with a bulk
 // prefetch into L2: 47.2 -> 41.1 us (5.7 TB/s); two or three rows ahead gave 43.4 and 45.0.
@@ -27,7 +27,8 @@
 // partial row per CTA goes to the workspace; a second kernel adds the partials. Both orders are fixed: the
 // result does not depend on scheduling. With the same prefetch, 8192 x 4096 with dres 58.7 -> 48.5 us. Of rows
 // wider than 8192 columns gamma is re-read for every row (from L1) and dres once the row's sum is known, since three or
-// four vectors of all inputs per thread spill: 8192 x 8192 on two vectors 92 us (on four 143), 4096 x 16384 122 (147).
+// four vectors of all inputs per thread spill: 8192 x 8192 on two vectors 92 us (on four 143), 4096 x 16384 121 (147; of
+// more than 12288 columns, four vectors, 40 bytes of a thread still spill). Means are the sum times rn(1 / C).
 #pragma once
 
 #include "ptx.cuh"
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rmsnorm_backward(const Bwd p
 
   pdl_trigger();
   pdl_wait();
-  constexpr bool kHold = VPT < 3;          // gamma and dres in registers (three vectors or more would spill)
+  constexpr bool kHold = VPT < 3;          // gamma and dres in registers (three vectors would spill, four do all the same)
   uint4 gam[kHold ? VPT : 1];
   f32x2 acc[VPT][4];
   bool in[VPT];
