@@ -115,6 +115,12 @@ __device__ __forceinline__ void fill_factors(float* factors, float g) {
   if (threadIdx.x < 128) factors[threadIdx.x] = blk::nvfp4_factor(threadIdx.x, g);
 }
 
+// Atom words of a row of K values, K padded to 256: 2 (MXFP4) or 4 (NVFP4) per 256. K goes up to 2^31 - 1, so the sum is
+// unsigned.
+__device__ __forceinline__ int atom_words(int K, int scales_per_32) {
+  return static_cast<int>(((static_cast<uint32_t>(K) + 255u) >> 8) * 2u * scales_per_32);
+}
+
 // Position of scale j (0..7) of row r in a tile's one or two atoms.
 __device__ __forceinline__ uint32_t atom_off(int r, int j) {
   return (j >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (j & 3);
@@ -301,17 +307,17 @@ __global__ void __launch_bounds__(kCastThreads, 2) k_fp4_cast(const __grid_const
     // pad K to a multiple of 256
     const int per = nv ? 2 : 1;
     if (T.q_row && tid < 128) {
-      const int words = ((cols + 255) >> 8) * 2 * per;
+      const int words = atom_words(cols, per);
       uint4* dst = reinterpret_cast<uint4*>(T.sf_row + (static_cast<int64_t>(rt) * words + ct * per) * 512);
       if (tid < 32 * per) dst[tid] = reinterpret_cast<const uint4*>(atom_r)[tid];
       else if (ct == T.tiles_c - 1 && ct * per + tid / 32 < words) dst[tid] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (T.q_col && tid >= 128) {
       const int t = tid - 128;
-      const int words = ((rows + 255) >> 8) * 2 * per;
+      const int words = atom_words(rows, per);
       uint4* dst = reinterpret_cast<uint4*>(T.sf_col + (static_cast<int64_t>(ct) * words + rt * per) * 512);
       if (t < 32 * per) dst[t] = reinterpret_cast<const uint4*>(atom_c)[t];
-      else if (r0 + kTile >= rows && rt * per + t / 32 < words) dst[t] = make_uint4(0u, 0u, 0u, 0u);
+      else if (rows - r0 <= kTile && rt * per + t / 32 < words) dst[t] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   if (cur >= 0 && g.t[cur].amax_bits) blk::cta_amax(g.t[cur].amax_bits, top << 16, tops);
@@ -328,7 +334,7 @@ template <bool NV>
 __device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors, uint32_t* tops) {
   constexpr int kN = NV ? 2 : 1, kV = 4 / kN;              // scales per 32 values, and vectors of 8 per scale
   const uint32_t per_row = static_cast<uint32_t>(T.cols) >> 5;
-  const int words = ((T.cols + 255) >> 8) * 2 * kN;        // atom words per row
+  const int words = atom_words(T.cols, kN);
   const int64_t n = static_cast<int64_t>(T.rows) * per_row, stride = static_cast<int64_t>(gridDim.x) * kCastThreads;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x;
   const float g = NV ? ld_dep(T.scale) : 1.0f;
@@ -404,9 +410,9 @@ __device__ __forceinline__ void cast_rows(const CastTensor& T, float* factors, u
     const int j = kN * static_cast<int>(per_row) + static_cast<int>(i - r * pad);
     sf[blk::atom_word(r, j >> 2, words) + (j & 3)] = 0;
   }
-  const int64_t fill = (T.rows + 127) / 128 * 128 - T.rows;
+  const uint32_t fill = (128u - (static_cast<uint32_t>(T.rows) & 127u)) & 127u;
 #pragma unroll 1
-  for (int64_t i = first; i < fill * words; i += stride)
+  for (int64_t i = first; i < static_cast<int64_t>(fill) * words; i += stride)
     *reinterpret_cast<uint32_t*>(sf + blk::atom_word(T.rows + i / words, i % words, words)) = 0u;
 }
 
