@@ -19,7 +19,9 @@
  * plus current scaling (fp8_cast_transpose_amax_current_multi), MXFP8 block scaling
  * (fp8_mx_cast_multi, fp8_mx_gemm_multi), its 4-bit forms (fp4_cast_multi, fp4_gemm_multi) and the
  * root-mean-square norm in front of a Linear, quantising its output (fp8_rmsnorm_cast), with its
- * backward pass (fp8_rmsnorm_backward).
+ * backward pass (fp8_rmsnorm_backward); and for a feed-forward block its gated form in one product
+ * (fp8_gated_gemm) with the gradient (fp8_gated_gemm_backward), the Muon step of its matrices
+ * (fused_muon_multi_tensor, muon_orthogonalize) and 4-bit weights times a few tokens (fp4_matvec).
  *
  * Sources, cited by page title and section:
  *   [P1] "算子与编译器：FP8 训练与优化器 Kernel" (charles2530.github.io)
@@ -497,6 +499,140 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
 
 /* Scratch bytes fp8_rmsnorm_backward needs (0 on invalid input). */
 size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Activation of a gated feed-forward block: act(g) = g * sigmoid(w(g)). */
+typedef enum fp8t_act {
+    FP8T_ACT_NONE = 0,             /* fp4_matvec only: no gate                                      */
+    FP8T_ACT_SILU = 1,             /* w = g                                                         */
+    FP8T_ACT_GELU = 2              /* w = 2 sqrt(2 / pi) (g + 0.044715 g^3): GELU in its tanh form  */
+} fp8t_act;
+
+/*
+ * fp8_gated_gemm — the gate and up projections of a feed-forward block, the activation and the product in
+ * one kernel:
+ *   [G | U] = (A . B^T) * a_scale_inv * b_scale_inv,   h = act(G) * U
+ * FP8 operands, FP32 accumulation; h is formed in f32 from the accumulators. B holds both projections,
+ * the gate's N output features first, then the up projection's N, under one scale; as fp8_gemm's operand
+ * it is stored [2N][K] (FP8T_K_MAJOR) or, as weights in x out, [K][2N] (FP8T_MN_MAJOR).
+ * Any number of rows M. Errors: INVALID_ARG (NULL operand, no output, codes without their scale or the
+ * reverse, unknown enum), UNSUPPORTED_SHAPE, MISALIGNED (matrices 16 bytes, scalars 4), CUDA.
+ */
+typedef struct fp8t_gated {
+    const void* A;                 /* M x K codes                                                   */
+    fp8t_format a_fmt;
+    const void* B;                 /* 2N x K codes, or K x 2N                                       */
+    fp8t_format b_fmt;
+    fp8t_layout b_layout;
+    int64_t M, N, K;               /* M > 0 any; N and K multiples of 16                            */
+    const float* d_a_scale_inv;    /* 1 float each                                                  */
+    const float* d_b_scale_inv;
+    fp8t_act act;                  /* SILU or GELU                                                  */
+    void* gu_bf16;                 /* M x 2N: [G | U] rounded, for the backward pass, or NULL       */
+    void* h_bf16;                  /* M x N, or NULL                                                */
+    void* q;                       /* M x N codes of h * scale (saturating), or NULL                */
+    fp8t_format q_fmt;
+    const float* d_scale;          /* with q: 1 float                                               */
+    float* d_amax_inout;           /* 1 float, max-accumulated with max |h| (f32), or NULL          */
+    float* d_scale_inv_out;        /* with q: 1 float, 1 / scale, or NULL                           */
+} fp8t_gated;
+fp8t_status fp8_gated_gemm(const fp8t_gated* desc, void* stream);
+
+/*
+ * fp8_gated_gemm_backward — the gradient of h = act(G) * U inside the product that brings it:
+ *   dH = (A . B^T) * a_scale_inv * b_scale_inv       (A the gradient of the block's output, M x K; B the
+ *                                                     down projection, N x K: weights in x out as stored)
+ *   dG = dH * U * act'(G),   dU = dH * act(G)        with G and U as fp8_gated_gemm kept them
+ * [dG | dU] (M x 2N) is written as BF16 and / or as codes under ONE scale, so that with W = [Wg | Wu] the
+ * input's gradient ([dG | dU] . W^T) and the weights' (X^T . [dG | dU]) are one product each. dH itself
+ * is never stored. Errors as fp8_gated_gemm.
+ */
+typedef struct fp8t_gated_grad {
+    const void* A;                 /* M x K codes                                                   */
+    fp8t_format a_fmt;
+    const void* B;                 /* N x K codes, or K x N                                         */
+    fp8t_format b_fmt;
+    fp8t_layout b_layout;
+    int64_t M, N, K;               /* M > 0 any; N and K multiples of 16                            */
+    const float* d_a_scale_inv;    /* 1 float each                                                  */
+    const float* d_b_scale_inv;
+    fp8t_act act;                  /* SILU or GELU                                                  */
+    const void* gu_bf16;           /* M x 2N: the forward pass's [G | U]                            */
+    void* dgu_bf16;                /* M x 2N, or NULL; may be gu itself                             */
+    void* q;                       /* M x 2N codes, or NULL                                         */
+    fp8t_format q_fmt;
+    const float* d_scale;          /* with q: 1 float                                               */
+    float* d_amax_inout;           /* 1 float, max-accumulated with max |[dG | dU]| (f32), or NULL  */
+    float* d_scale_inv_out;        /* with q: 1 float, 1 / scale, or NULL                           */
+} fp8t_gated_grad;
+fp8t_status fp8_gated_gemm_backward(const fp8t_gated_grad* desc, void* stream);
+
+/*
+ * fp4_matvec — 4-bit weights times one to eight rows of BF16 activations (weights as fp4_cast_multi writes
+ * them row-wise; x is not quantised):
+ *   y = (x . W^T) * w_scale_inv                                     act NONE, W [N][K]
+ *   y = act(g) * u, [g | u] = (x . W^T) * w_scale_inv               else, W [2N][K]: gate rows, then up rows
+ * FP32 accumulation in an order fixed by the sizes, one rounding to BF16. More rows: fp4_gemm_multi.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (rows above 8, N not a multiple of 8 or K of 32), MISALIGNED
+ * (matrices and scales 16 bytes), CUDA.
+ */
+typedef struct fp8t_fp4_matvec {
+    const void* x_bf16;            /* rows x K                                                      */
+    int64_t rows, N, K;            /* rows 1 .. 8, N a multiple of 8, K of 32                       */
+    const void* q;                 /* N (2N with an act) x K/2 bytes                                */
+    const void* scales;            /* fp4_scale_bytes(N or 2N, K, quant)                            */
+    fp8t_quant quant;              /* FP8T_Q_MXFP4 or FP8T_Q_NVFP4                                  */
+    const float* d_w_scale_inv;    /* 1 float, or NULL for 1: the inverse of NVFP4's tensor scale   */
+    fp8t_act act;
+    void* y_bf16;                  /* rows x N                                                      */
+} fp8t_fp4_matvec;
+fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream);
+
+/*
+ * muon_orthogonalize — for each matrix X0 (BF16 or f32), out = bf16(X) after `steps` Newton-Schulz steps
+ *   X = X0 / |X0|_F;   A = X X^T,  X <- a X + (b A + c A A) X       (a, b, c) = (3.4445, -4.775, 2.0315)
+ * which leaves X0's singular vectors and moves its singular values towards 1 (into about 0.68 .. 1.21). FP16
+ * products under a factor of 2^10 with FP32 accumulation, |X0|_F in FP64. A zero matrix stays zero; one
+ * with a non-finite element becomes NaN. Any sizes from 1 x 1 up to 65536 each way.
+ *   x_f32          0: X0 is BF16, 1: f32
+ *   steps          1 .. 16
+ *   d_workspace    muon_workspace_bytes of the sizes, 256-byte aligned, contents on entry ignored. Calls that may run
+ *                  at the same time need their own.
+ * out may be a BF16 X0 itself. Errors: INVALID_ARG (also two outputs at one address), UNSUPPORTED_SHAPE,
+ * MISALIGNED (16 bytes), CUDA.
+ */
+typedef struct fp8t_orth_matrix {
+    const void* x;                 /* rows x cols                                                   */
+    void* out_bf16;                /* rows x cols                                                   */
+    int64_t rows, cols;
+} fp8t_orth_matrix;
+fp8t_status muon_orthogonalize(const fp8t_orth_matrix* matrices, int32_t n_matrices, int32_t x_f32, int32_t steps,
+                               void* d_workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fused_muon_multi_tensor — one Muon step over a list of matrices (the optimiser beside fused_adamw_* for the
+ * two-dimensional weights):
+ *   g = f32(grad) * (1 / loss_scale),   m <- beta m + g,   u = g + beta m (nesterov) or m
+ *   O = the orthogonal factor of u as muon_orthogonalize forms it
+ *   master <- master (1 - lr weight_decay) - lr update_rms sqrt(max(rows, cols)) O,   weight = bf16(master)
+ * (O's entries have a root mean square of about 1 / sqrt(max(rows, cols)), so the update's is lr * update_rms;
+ * 0.2 is about AdamW's). If any u has a non-finite norm nothing is changed and *d_skipped_out (int32, or
+ * NULL) is 1, else 0. There is no clipping: O does not depend on the gradient's size.
+ * Tensors must not overlap. Errors and workspace as muon_orthogonalize; hyperparameters finite, loss_scale > 0.
+ */
+typedef struct fp8t_muon_tensor {
+    float* master;                 /* rows x cols                                                   */
+    float* momentum;               /* rows x cols                                                   */
+    const void* grad_bf16;         /* rows x cols                                                   */
+    void* weight_bf16;             /* rows x cols, written                                          */
+    int64_t rows, cols;
+} fp8t_muon_tensor;
+fp8t_status fused_muon_multi_tensor(const fp8t_muon_tensor* tensors, int32_t n_tensors, float lr, float beta,
+                                    float weight_decay, float update_rms, float loss_scale, int32_t nesterov,
+                                    int32_t steps, int32_t* d_skipped_out, void* d_workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Scratch bytes of both calls for matrices of these sizes (0 on invalid input). */
+size_t muon_workspace_bytes(const int64_t* rows, const int64_t* cols, int32_t n_matrices);
 
 /*
  * fp8_scale_update — roll each tensor's amax history and compute the next scale

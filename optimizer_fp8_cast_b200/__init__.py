@@ -6,8 +6,8 @@ CUDA stream to the C entry point of the same name, and raises ``Fp8TrainError`` 
 status. Every step of the path runs in the library's kernels; there is no CPU or PyTorch
 fallback, and a missing library is an error.
 
-The norm and 4-bit calls (``fp8_rmsnorm_cast``, ``fp8_rmsnorm_backward``, ``fp4_cast_multi``,
-``fp4_gemm_multi``) are made per layer on as little as one token; their binding is compiled
+The norm, 4-bit and gated calls (``fp8_rmsnorm_cast``, ``fp8_rmsnorm_backward``, ``fp4_cast_multi``,
+``fp4_gemm_multi``, ``fp4_matvec``, ``fp8_gated_gemm``, ``fp8_gated_gemm_backward``) are made per layer on as little as one token; their binding is compiled
 (``csrc/binding.cpp``, ``_binding.so``) and is loaded when one of them is first called.
 """
 import ctypes as C
@@ -29,6 +29,8 @@ __all__ = ["fp8_cast_transpose_amax", "fp8_cast_transpose_amax_multi",
            "fp8_mx_gemm_multi_sumsq", "fp8_mx_gemm_sumsq_workspace_bytes",
            "mx_scale_bytes", "fp4_scale_bytes", "fp4_cast_multi", "fp4_gemm_multi", "fp8_rmsnorm_cast",
            "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes",
+           "fp8_gated_gemm", "fp8_gated_gemm_backward", "fp4_matvec", "muon_orthogonalize", "fused_muon_multi_tensor",
+           "muon_workspace_bytes", "ACT_NONE", "ACT_SILU", "ACT_GELU",
            "Q_NONE", "Q_FP8", "Q_MXFP8", "Q_MXFP4", "Q_NVFP4", "FP4_MAX",
            "fp8t_check_device_error", "fp8t_debug_expire_waits", "fp8t_set_wait_timeout_ns",
            "Fp8TrainError", "E4M3", "E5M2", "K_MAJOR", "MN_MAJOR", "AMAX_MAX", "AMAX_MOST_RECENT", "FP8_MAX", "load",
@@ -38,6 +40,7 @@ E4M3, E5M2 = 0, 1
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 K_MAJOR, MN_MAJOR = 0, 1
 Q_NONE, Q_FP8, Q_MXFP8, Q_MXFP4, Q_NVFP4 = 0, 1, 2, 3, 4
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 FP8_MAX = {E4M3: 448.0, E5M2: 57344.0}
 FP4_MAX = 448.0 * 6.0        # NVFP4's largest scale times its largest value (fp8_max of its scale update)
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8train.so")
@@ -279,7 +282,7 @@ def fp8_rmsnorm_backward_workspace_bytes(rows, cols):
 
 
 def _load_binding():
-    """The calls of csrc/binding.cpp (norm and 4-bit entry points), with the library's addresses."""
+    """The calls of csrc/binding.cpp (norm, 4-bit and gated entry points), with the library's addresses."""
     how = ("run `python -c \"import __graft_entry__ as g; g.build()\"` or "
            "`python -m optimizer_fp8_cast_b200.build`")
     if not os.path.exists(BINDING_PATH):
@@ -294,7 +297,7 @@ def _load_binding():
     lib = load()
     m.bind(*(C.cast(getattr(lib, f), C.c_void_p).value for f in
              ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp8_rmsnorm_backward_workspace_bytes", "fp4_cast_multi",
-              "fp4_gemm_multi")), _check)
+              "fp4_gemm_multi", "fp8_gated_gemm", "fp8_gated_gemm_backward", "fp4_matvec")), _check)
     return m
 
 
@@ -311,7 +314,7 @@ def _compiled(declared):
         if not _functions:
             m = _load_binding()
             found = {f: getattr(m, f) for f in ("fp8_rmsnorm_cast", "fp8_rmsnorm_backward", "fp4_cast_multi",
-                                                "fp4_gemm_multi")}
+                                                "fp4_gemm_multi", "fp8_gated_gemm", "fp8_gated_gemm_backward", "fp4_matvec")}
             _functions.update(found)
             globals().update(found)
         return _functions[name](*args, **kwargs)
@@ -352,6 +355,38 @@ def fp4_gemm_multi(gemms, stream=None):
     """4-bit block-scaled GEMMs: a list of dicts with A (uint8 [M, K / 2]), a_sf, B (uint8 [N, K / 2]), b_sf, quant,
     D (BF16 [M, N]) and optionally a_scale_inv, b_scale_inv (float32 [1]); D = bf16(A . B^T) with the operands'
     block scales, times the scale inverses."""
+
+
+@_compiled
+def fp8_gated_gemm(A, a_fmt, B, b_fmt, a_scale_inv, b_scale_inv, *, act=ACT_SILU, b_mn=False, gu=None, h=None, q=None,
+                   q_fmt=E4M3, scale=None, amax=None, scale_inv=None, stream=None):
+    """[G | U] = (A . B^T) * a_scale_inv * b_scale_inv; h = act(G) * U: both projections of a gated feed-forward block, its
+    activation and product in one kernel.
+
+    A: FP8 codes (uint8 [M, K], any M); B: codes of the gate's and the up projection's weights side by side, [2N, K], or [K, 2N]
+    with b_mn (weights in x out). act: ACT_SILU or ACT_GELU (tanh form). Writes gu (BF16 [M, 2N], for the backward pass), h
+    (BF16 [M, N]) and / or q (uint8 [M, N]: codes of h * scale in q_fmt, with scale and optionally scale_inv), and
+    max-accumulates max|h| into amax (float32 [1] each)."""
+
+
+@_compiled
+def fp8_gated_gemm_backward(A, a_fmt, B, b_fmt, a_scale_inv, b_scale_inv, gu, *, act=ACT_SILU, b_mn=False, dgu=None,
+                            q=None, q_fmt=E5M2, scale=None, amax=None, scale_inv=None, stream=None):
+    """Gradient of fp8_gated_gemm inside the product that brings it: dH = (A . B^T) * a_scale_inv * b_scale_inv with A the
+    output's gradient (codes [M, K]) and B the down projection (codes [N, K], or [K, N] with b_mn), then dG = dH * U * act'(G)
+    and dU = dH * act(G) of gu (BF16 [M, 2N], the forward pass's).
+
+    Writes [dG | dU] as dgu (BF16 [M, 2N]; may be gu) and / or q (uint8 [M, 2N] in q_fmt under one scale, with scale and
+    optionally scale_inv), and max-accumulates its magnitude into amax (float32 [1] each)."""
+
+
+@_compiled
+def fp4_matvec(x, q, sf, quant, y, *, w_scale_inv=None, act=ACT_NONE, stream=None):
+    """y = (x . W^T) * w_scale_inv for one to eight rows x (BF16 [rows, K]) and 4-bit weights W as fp4_cast_multi writes them
+    row-wise: q (uint8 [N, K / 2]), sf, quant (Q_MXFP4 or Q_NVFP4).
+
+    With act (ACT_SILU or ACT_GELU) W holds gate and up features, q is [2N, K / 2] and y = act(g) * u. y: BF16 [rows, N];
+    w_scale_inv: float32 [1], the inverse of NVFP4's tensor scale."""
 
 
 def fp8_scale_update(amax, history, fp8_max, algo, margin, scale, scale_inv, stream=None):
@@ -450,6 +485,82 @@ def fused_adamw_multi_tensor_noalloc(master, m, v, grads, weights, *, lr, beta1,
                                                    float(max_grad_norm),
                                                    _ptr(grad_norm), _ptr(skipped), _stream(stream)),
            "fused_adamw_multi_tensor_noalloc")
+
+
+def _rows_cols(t, what):
+    if t.dim() != 2 or t.size(0) < 1 or t.size(1) < 1:
+        raise ValueError(f"{what}: must be a matrix of at least one element")
+    return int(t.size(0)), int(t.size(1))
+
+
+def muon_workspace_bytes(shapes):
+    """Scratch bytes of muon_orthogonalize and fused_muon_multi_tensor for matrices of these (rows, cols)."""
+    n = len(shapes)
+    rows, cols = (C.c_int64 * n)(*[int(s[0]) for s in shapes]), (C.c_int64 * n)(*[int(s[1]) for s in shapes])
+    return int(load().muon_workspace_bytes(rows, cols, n))
+
+
+def _muon_call(shapes, tensors, workspace, stream, call, name):
+    """Checks devices and the workspace (allocated on the call's stream where it is missing), and calls."""
+    device = torch.device("cuda", torch.cuda.current_device())
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"{name}: tensors must be on the current device")
+    if workspace is None:
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+            workspace = torch.empty(muon_workspace_bytes(shapes), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.device != device:
+        raise ValueError(f"{name}: workspace must be a uint8 tensor on the current device")
+    _check(call(_ptr(workspace), workspace.numel(), _stream(stream)), name)
+
+
+def muon_orthogonalize(xs, outs, *, steps=5, workspace=None, stream=None):
+    """The nearest-orthogonal factor of each matrix of ``xs`` (all BF16 or all float32) into ``outs`` (BF16 of the same
+    shape; may be the BF16 input itself) by ``steps`` Newton-Schulz steps: X = x / |x|_F, then
+    X <- aX + (bA + cA^2) X with A = X X^T and (a, b, c) = (3.4445, -4.775, 2.0315); singular values end in about 0.68 to
+    1.21. ``workspace``: a uint8 CUDA tensor of muon_workspace_bytes (allocated per call where it is missing)."""
+    if not xs or len(xs) != len(outs):
+        raise ValueError("xs and outs must be lists of the same length, not empty")
+    f32 = xs[0].dtype == torch.float32
+    arr, shapes = (_abi.OrthMatrix * len(xs))(), []
+    for i, (x, o) in enumerate(zip(xs, outs)):
+        if x.dtype != (torch.float32 if f32 else torch.bfloat16) or o.dtype != torch.bfloat16:
+            raise ValueError("xs must be all bfloat16 or all float32, outs bfloat16")
+        shapes.append(_rows_cols(x, "xs"))
+        if o.shape != x.shape:
+            raise ValueError("outs must have the shapes of xs")
+        arr[i] = _abi.OrthMatrix(_ptr(x), _ptr(o), *shapes[-1])
+    _muon_call(shapes, [*xs, *outs], workspace, stream,
+               lambda w, n, s: load().muon_orthogonalize(arr, len(xs), int(f32), int(steps), w, n, s),
+               "muon_orthogonalize")
+
+
+def fused_muon_multi_tensor(master, momentum, grads, weights, *, lr, beta=0.95, weight_decay=0.0, update_rms=0.2,
+                            loss_scale=1.0, nesterov=True, steps=5, skipped=None, workspace=None, stream=None):
+    """One Muon step over lists of matrices (float32 master and momentum, BF16 gradients and weights):
+
+    g = grad / loss_scale; momentum <- beta * momentum + g; u = g + beta * momentum (``nesterov``) or momentum;
+    master <- master * (1 - lr * weight_decay) - lr * update_rms * sqrt(max(rows, cols)) * O with O the orthogonal factor
+    of u (muon_orthogonalize); weights = BF16 of master. A non-finite u changes nothing and sets ``skipped`` (int32 [1]).
+    ``workspace``: a uint8 CUDA tensor of muon_workspace_bytes (allocated per call where it is missing)."""
+    n = len(master)
+    if not n or not n == len(momentum) == len(grads) == len(weights):
+        raise ValueError("master, momentum, grads and weights must be lists of the same length, not empty")
+    arr, shapes = (_abi.MuonTensor * n)(), []
+    for i, (p, m, g, w) in enumerate(zip(master, momentum, grads, weights)):
+        if p.dtype != torch.float32 or m.dtype != torch.float32 or g.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+            raise ValueError("master and momentum must be float32, grads and weights bfloat16")
+        shapes.append(_rows_cols(p, "master"))
+        if not p.shape == m.shape == g.shape == w.shape:
+            raise ValueError("master, momentum, grads and weights must have the same shapes")
+        arr[i] = _abi.MuonTensor(_ptr(p), _ptr(m), _ptr(g), _ptr(w), *shapes[-1])
+    if skipped is not None and (skipped.dtype != torch.int32 or skipped.numel() < 1):
+        raise ValueError("skipped must be int32 [1]")
+    _muon_call(shapes, [*master, *momentum, *grads, *weights] + ([] if skipped is None else [skipped]), workspace, stream,
+               lambda ws, b, s: load().fused_muon_multi_tensor(arr, n, float(lr), float(beta), float(weight_decay),
+                                                               float(update_rms), float(loss_scale), int(bool(nesterov)),
+                                                               int(steps), _ptr(skipped), ws, b, s),
+               "fused_muon_multi_tensor")
 
 
 def fp8t_check_device_error(stream=None):

@@ -89,6 +89,42 @@ class RmsNormGrad(C.Structure):
                 ("dh_bf16", C.c_void_p), ("dgamma_f32", C.c_void_p), ("dgamma_bf16", C.c_void_p)]
 
 
+class Gated(C.Structure):
+    """fp8t_gated."""
+    _fields_ = [("A", C.c_void_p), ("a_fmt", C.c_int), ("B", C.c_void_p), ("b_fmt", C.c_int), ("b_layout", C.c_int),
+                ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("d_a_scale_inv", C.c_void_p),
+                ("d_b_scale_inv", C.c_void_p), ("act", C.c_int), ("gu_bf16", C.c_void_p), ("h_bf16", C.c_void_p),
+                ("q", C.c_void_p), ("q_fmt", C.c_int), ("d_scale", C.c_void_p), ("d_amax_inout", C.c_void_p),
+                ("d_scale_inv_out", C.c_void_p)]
+
+
+class GatedGrad(C.Structure):
+    """fp8t_gated_grad."""
+    _fields_ = [("A", C.c_void_p), ("a_fmt", C.c_int), ("B", C.c_void_p), ("b_fmt", C.c_int), ("b_layout", C.c_int),
+                ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("d_a_scale_inv", C.c_void_p),
+                ("d_b_scale_inv", C.c_void_p), ("act", C.c_int), ("gu_bf16", C.c_void_p), ("dgu_bf16", C.c_void_p),
+                ("q", C.c_void_p), ("q_fmt", C.c_int), ("d_scale", C.c_void_p), ("d_amax_inout", C.c_void_p),
+                ("d_scale_inv_out", C.c_void_p)]
+
+
+class Fp4Matvec(C.Structure):
+    """fp8t_fp4_matvec."""
+    _fields_ = [("x_bf16", C.c_void_p), ("rows", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("q", C.c_void_p),
+                ("scales", C.c_void_p), ("quant", C.c_int), ("d_w_scale_inv", C.c_void_p), ("act", C.c_int),
+                ("y_bf16", C.c_void_p)]
+
+
+class OrthMatrix(C.Structure):
+    """fp8t_orth_matrix."""
+    _fields_ = [("x", C.c_void_p), ("out_bf16", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64)]
+
+
+class MuonTensor(C.Structure):
+    """fp8t_muon_tensor."""
+    _fields_ = [("master", C.c_void_p), ("momentum", C.c_void_p), ("grad_bf16", C.c_void_p), ("weight_bf16", C.c_void_p),
+                ("rows", C.c_int64), ("cols", C.c_int64)]
+
+
 def declare(L):
     vp, i32, i64, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_float
     L.fp8_cast_transpose_amax.restype = C.c_int
@@ -133,6 +169,19 @@ def declare(L):
     L.fp8_rmsnorm_backward.argtypes = [C.POINTER(RmsNormGrad), vp, C.c_size_t, vp]
     L.fp8_rmsnorm_backward_workspace_bytes.restype = C.c_size_t
     L.fp8_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.fp8_gated_gemm.restype = C.c_int
+    L.fp8_gated_gemm.argtypes = [C.POINTER(Gated), vp]
+    L.fp8_gated_gemm_backward.restype = C.c_int
+    L.fp8_gated_gemm_backward.argtypes = [C.POINTER(GatedGrad), vp]
+    L.fp4_matvec.restype = C.c_int
+    L.fp4_matvec.argtypes = [C.POINTER(Fp4Matvec), vp]
+    L.muon_orthogonalize.restype = C.c_int
+    L.muon_orthogonalize.argtypes = [C.POINTER(OrthMatrix), i32, i32, i32, vp, C.c_size_t, vp]
+    L.fused_muon_multi_tensor.restype = C.c_int
+    L.fused_muon_multi_tensor.argtypes = [C.POINTER(MuonTensor), i32, f32, f32, f32, f32, f32, i32, i32, vp, vp,
+                                          C.c_size_t, vp]
+    L.muon_workspace_bytes.restype = C.c_size_t
+    L.muon_workspace_bytes.argtypes = [C.POINTER(i64), C.POINTER(i64), i32]
     L.fp8_gemm.restype = C.c_int
     L.fp8_gemm.argtypes = [vp, C.c_int, vp, C.c_int, i64, i64, i64, vp, vp, vp, vp]
     L.fp8_scale_update.restype = C.c_int

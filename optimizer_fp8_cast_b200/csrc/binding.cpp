@@ -1,4 +1,4 @@
-// binding.cpp — the Python binding of the norm and 4-bit entry points as a CPython extension.
+// binding.cpp — the Python binding of the norm, 4-bit and gated entry points as a CPython extension.
 //
 // These calls are made per layer on as little as one token, where the GPU needs 3 to 10 us and a ctypes
 // call with its checks in Python needs 10 (norm) to 22 us (norm and product): the host would be what
@@ -37,6 +37,9 @@ struct Library {
   decltype(&fp8_rmsnorm_backward_workspace_bytes) rmsnorm_backward_workspace_bytes = nullptr;
   decltype(&fp4_cast_multi) cast_multi = nullptr;
   decltype(&fp4_gemm_multi) gemm_multi = nullptr;
+  decltype(&fp8_gated_gemm) gated_gemm = nullptr;
+  decltype(&fp8_gated_gemm_backward) gated_backward = nullptr;
+  decltype(&fp4_matvec) matvec = nullptr;
   PyObject* check = nullptr;                // check(status, where) raises
 } lib;
 
@@ -342,16 +345,128 @@ PyObject* gemm_multi(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* k
   });
 }
 
-// bind(rmsnorm_cast, rmsnorm_backward, workspace_bytes, cast_multi, gemm_multi, check)
+// Truth of a flag that may be missing.
+bool flag(PyObject* o) {
+  const int v = o ? PyObject_IsTrue(o) : 0;
+  if (v < 0) throw Error{};
+  return v != 0;
+}
+// Codes of an operand: a uint8 matrix.
+const at::Tensor& codes(PyObject* o, const char* what) {
+  const at::Tensor& t = matrix(o, what);
+  if (t.scalar_type() != at::kByte) value_error(what, "a uint8 matrix of codes");
+  return t;
+}
+// What both gated calls have in their first six arguments, act and b_mn; `halves`: the column blocks of B.
+template <class D>
+void gated_operands(Call& c, D& d, PyObject* const* a, PyObject* act, PyObject* b_mn, int64_t halves) {
+  const at::Tensor &A = codes(a[0], "A"), &B = codes(a[2], "B");
+  const bool mn = flag(b_mn);
+  d.M = A.size(0);
+  d.K = A.size(1);
+  if (B.size(mn ? 0 : 1) != d.K || B.size(mn ? 1 : 0) % halves)
+    value_error("B", "codes [features, K] (or [K, features] with b_mn) of A's K, gate and up features alike");
+  d.N = B.size(mn ? 1 : 0) / halves;
+  d.A = c.address(A, "A");
+  d.B = c.address(B, "B");
+  d.a_fmt = static_cast<fp8t_format>(integer(a[1], -1));
+  d.b_fmt = static_cast<fp8t_format>(integer(a[3], -1));
+  d.b_layout = mn ? FP8T_MN_MAJOR : FP8T_K_MAJOR;
+  d.d_a_scale_inv = c.f32(a[4], 1, "a_scale_inv");
+  d.d_b_scale_inv = c.f32(a[5], 1, "b_scale_inv");
+  d.act = static_cast<fp8t_act>(integer(act, FP8T_ACT_SILU));
+}
+void* code_output(Call& c, PyObject* o, int64_t rows, int64_t cols) {
+  const at::Tensor* t = tensor(o, "q");
+  if (!t) return nullptr;
+  if (t->scalar_type() != at::kByte || t->dim() != 2 || t->size(0) != rows || t->size(1) != cols)
+    value_error("q", "a uint8 matrix of the output's rows and columns");
+  return c.address(*t, "q");
+}
+
+PyObject* gated_gemm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const Names<16> names({"A", "a_fmt", "B", "b_fmt", "a_scale_inv", "b_scale_inv", "act", "b_mn", "gu", "h", "q", "q_fmt",
+                                "scale", "amax", "scale_inv", "stream"});
+  return guarded([&] {
+    PyObject* a[16];
+    parse(args, n, kw, names.v, 6, "fp8_gated_gemm", a);
+    for (int i = 0; i < 6; ++i) required(a[i], "fp8_gated_gemm", "A, a_fmt, B, b_fmt, a_scale_inv or b_scale_inv");
+    Call c;
+    fp8t_gated d = {};
+    gated_operands(c, d, a, a[6], a[7], 2);
+    d.gu_bf16 = c.bf16(a[8], d.M, 2 * d.N, "gu");
+    d.h_bf16 = c.bf16(a[9], d.M, d.N, "h");
+    d.q = code_output(c, a[10], d.M, d.N);
+    d.q_fmt = static_cast<fp8t_format>(integer(a[11], FP8T_E4M3));
+    d.d_scale = c.f32(a[12], 1, "scale");
+    d.d_amax_inout = c.f32(a[13], 1, "amax");
+    d.d_scale_inv_out = c.f32(a[14], 1, "scale_inv");
+    check_status(lib.gated_gemm(&d, c.stream(a[15])), "fp8_gated_gemm");
+  });
+}
+
+PyObject* gated_backward(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const Names<16> names({"A", "a_fmt", "B", "b_fmt", "a_scale_inv", "b_scale_inv", "gu", "act", "b_mn", "dgu", "q", "q_fmt",
+                                "scale", "amax", "scale_inv", "stream"});
+  return guarded([&] {
+    PyObject* a[16];
+    parse(args, n, kw, names.v, 7, "fp8_gated_gemm_backward", a);
+    for (int i = 0; i < 7; ++i)
+      required(a[i], "fp8_gated_gemm_backward", "A, a_fmt, B, b_fmt, a_scale_inv, b_scale_inv or gu");
+    Call c;
+    fp8t_gated_grad d = {};
+    gated_operands(c, d, a, a[7], a[8], 1);
+    d.gu_bf16 = c.bf16(a[6], d.M, 2 * d.N, "gu");
+    d.dgu_bf16 = c.bf16(a[9], d.M, 2 * d.N, "dgu");
+    d.q = code_output(c, a[10], d.M, 2 * d.N);
+    d.q_fmt = static_cast<fp8t_format>(integer(a[11], FP8T_E5M2));
+    d.d_scale = c.f32(a[12], 1, "scale");
+    d.d_amax_inout = c.f32(a[13], 1, "amax");
+    d.d_scale_inv_out = c.f32(a[14], 1, "scale_inv");
+    check_status(lib.gated_backward(&d, c.stream(a[15])), "fp8_gated_gemm_backward");
+  });
+}
+
+PyObject* matvec(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const Names<8> names({"x", "q", "sf", "quant", "y", "w_scale_inv", "act", "stream"});
+  return guarded([&] {
+    PyObject* a[8];
+    parse(args, n, kw, names.v, 5, "fp4_matvec", a);
+    for (int i = 0; i < 5; ++i) required(a[i], "fp4_matvec", "x, q, sf, quant or y");
+    Call c;
+    const at::Tensor &x = matrix(a[0], "x"), &q = codes(a[1], "q");
+    fp8t_fp4_matvec d = {};
+    const int quant = integer(a[3], -1);
+    d.rows = x.size(0);
+    d.K = x.size(1);
+    d.act = static_cast<fp8t_act>(integer(a[6], FP8T_ACT_NONE));
+    const int64_t halves = d.act == FP8T_ACT_NONE ? 1 : 2;
+    if (2 * q.size(1) != d.K || q.size(0) % halves)
+      value_error("q", "codes [features, K / 2] of x's K, gate and up features alike with an act");
+    d.N = q.size(0) / halves;
+    d.quant = static_cast<fp8t_quant>(quant);
+    d.x_bf16 = c.bf16(a[0], d.rows, d.K, "x");
+    d.q = c.address(q, "q");
+    d.scales = c.bytes(a[2], fp4_sf_bytes(q.size(0), d.K, quant), "sf");
+    d.y_bf16 = c.bf16(a[4], d.rows, d.N, "y");
+    d.d_w_scale_inv = c.f32(a[5], 1, "w_scale_inv");
+    check_status(lib.matvec(&d, c.stream(a[7])), "fp4_matvec");
+  });
+}
+
+// bind(rmsnorm_cast, rmsnorm_backward, workspace_bytes, cast_multi, gemm_multi, gated_gemm, gated_backward, matvec, check)
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[5];
+  unsigned long long p[8];
   PyObject* check;
-  if (!PyArg_ParseTuple(args, "KKKKKO", &p[0], &p[1], &p[2], &p[3], &p[4], &check)) return nullptr;
+  if (!PyArg_ParseTuple(args, "KKKKKKKKO", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &check)) return nullptr;
   lib.rmsnorm_cast = reinterpret_cast<decltype(lib.rmsnorm_cast)>(p[0]);
   lib.rmsnorm_backward = reinterpret_cast<decltype(lib.rmsnorm_backward)>(p[1]);
   lib.rmsnorm_backward_workspace_bytes = reinterpret_cast<decltype(lib.rmsnorm_backward_workspace_bytes)>(p[2]);
   lib.cast_multi = reinterpret_cast<decltype(lib.cast_multi)>(p[3]);
   lib.gemm_multi = reinterpret_cast<decltype(lib.gemm_multi)>(p[4]);
+  lib.gated_gemm = reinterpret_cast<decltype(lib.gated_gemm)>(p[5]);
+  lib.gated_backward = reinterpret_cast<decltype(lib.gated_backward)>(p[6]);
+  lib.matvec = reinterpret_cast<decltype(lib.matvec)>(p[7]);
   Py_INCREF(check);
   lib.check = check;
   Py_RETURN_NONE;
@@ -385,6 +500,30 @@ PyMethodDef methods[] = {
      "4-bit block-scaled GEMMs: a list of dicts with A (uint8 [M, K / 2]), a_sf, B (uint8 [N, K / 2]), b_sf, quant,\n"
      "D (BF16 [M, N]) and optionally a_scale_inv, b_scale_inv (float32 [1]); D = bf16(A . B^T) with the operands'\n"
      "block scales, times the scale inverses."},
+    {"fp8_gated_gemm", FAST(gated_gemm),
+     "fp8_gated_gemm(A, a_fmt, B, b_fmt, a_scale_inv, b_scale_inv, *, act=1, b_mn=False, gu=None, h=None, q=None, q_fmt=0, scale=None, amax=None, scale_inv=None, stream=None)\n--\n\n"
+     "[G | U] = (A . B^T) * a_scale_inv * b_scale_inv; h = act(G) * U: both projections of a gated feed-forward block, its\n"
+     "activation and product in one kernel.\n"
+     "\n"
+     "A: FP8 codes (uint8 [M, K], any M); B: codes of the gate's and the up projection's weights side by side, [2N, K], or [K, 2N]\n"
+     "with b_mn (weights in x out). act: ACT_SILU or ACT_GELU (tanh form). Writes gu (BF16 [M, 2N], for the backward pass), h\n"
+     "(BF16 [M, N]) and / or q (uint8 [M, N]: codes of h * scale in q_fmt, with scale and optionally scale_inv), and\n"
+     "max-accumulates max|h| into amax (float32 [1] each)."},
+    {"fp8_gated_gemm_backward", FAST(gated_backward),
+     "fp8_gated_gemm_backward(A, a_fmt, B, b_fmt, a_scale_inv, b_scale_inv, gu, *, act=1, b_mn=False, dgu=None, q=None, q_fmt=1, scale=None, amax=None, scale_inv=None, stream=None)\n--\n\n"
+     "Gradient of fp8_gated_gemm inside the product that brings it: dH = (A . B^T) * a_scale_inv * b_scale_inv with A the\n"
+     "output's gradient (codes [M, K]) and B the down projection (codes [N, K], or [K, N] with b_mn), then dG = dH * U * act'(G)\n"
+     "and dU = dH * act(G) of gu (BF16 [M, 2N], the forward pass's).\n"
+     "\n"
+     "Writes [dG | dU] as dgu (BF16 [M, 2N]; may be gu) and / or q (uint8 [M, 2N] in q_fmt under one scale, with scale and\n"
+     "optionally scale_inv), and max-accumulates its magnitude into amax (float32 [1] each)."},
+    {"fp4_matvec", FAST(matvec),
+     "fp4_matvec(x, q, sf, quant, y, *, w_scale_inv=None, act=0, stream=None)\n--\n\n"
+     "y = (x . W^T) * w_scale_inv for one to eight rows x (BF16 [rows, K]) and 4-bit weights W as fp4_cast_multi writes them\n"
+     "row-wise: q (uint8 [N, K / 2]), sf, quant (Q_MXFP4 or Q_NVFP4).\n"
+     "\n"
+     "With act (ACT_SILU or ACT_GELU) W holds gate and up features, q is [2N, K / 2] and y = act(g) * u. y: BF16 [rows, N];\n"
+     "w_scale_inv: float32 [1], the inverse of NVFP4's tensor scale."},
     {"bind", bind, METH_VARARGS, "Hands over the library's entry points and the Python callables."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -25,6 +25,9 @@
 #include "gemm_tcgen05.cuh"
 #include "gemm_mx_wide.cuh"
 #include "gemm_fp4.cuh"
+#include "fp4_matvec.cuh"
+#include "gated.cuh"
+#include "muon.cuh"
 #include "mx_cast.cuh"
 #include "rmsnorm.cuh"
 #include "scale_update.cuh"
@@ -62,9 +65,10 @@ struct DeviceInfo {
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
   // set up by their own first calls, so that no other call loads these kernels or fails with them
-  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false};
+  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false};
   int fp4_cast_blocks_per_sm = 0;
   int fp4_cast_rows_blocks_per_sm = 0;
+  int pair_clusters = 0;             // co-resident clusters of the pair-tile products (one CTA per SM)
   int gemm_fp4_clusters = 0;         // co-resident clusters of the 4-bit tile kernel (every form: one CTA per SM)
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -1696,6 +1700,514 @@ fp8t_status fp8_rmsnorm_backward(const fp8t_rmsnorm_grad* desc, void* d_workspac
     st = after_launch("fp8_rmsnorm_backward dgamma launch");
   }
   return st;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ gated feed-forward
+namespace {
+
+template <class Op>
+cudaError_t allow_pair_smem() {
+  return cudaFuncSetAttribute(fp8t::pair::k_pair_gemm<Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fp8t::pair::kPairSmemBytes);
+}
+using fp8t::gated::kGelu;
+using fp8t::gated::kSilu;
+fp8t_status ready_pair(DeviceInfo* d) {
+  using namespace fp8t;
+  return once_per_device(d->pair_ready, "pair products", [&] {
+    cudaError_t e;
+    if ((e = allow_pair_smem<gated::Forward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Forward<kGelu>>()) != cudaSuccess ||
+        (e = allow_pair_smem<gated::Backward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Backward<kGelu>>()) != cudaSuccess ||
+        (e = allow_pair_smem<muon::Product<4>>()) != cudaSuccess ||
+        (e = allow_pair_smem<muon::Product<muon::kMaxMatrices>>()) != cudaSuccess)
+      return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (d->sms / 2), 1, 1);
+    cfg.blockDim = dim3(pair::kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = pair::kPairSmemBytes;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, pair::k_pair_gemm<gated::Forward<kSilu>>, &cfg) != cudaSuccess || clusters < 1) {
+      (void)cudaGetLastError();
+      clusters = d->sms / 2;
+    }
+    d->pair_clusters = clusters;
+    return cudaSuccess;
+  });
+}
+
+// rows x cols elements of `bytes` each, row pitch in elements: boxes of box_rows x box_cols, zero fill.
+fp8t_status encode_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t pitch, int bytes,
+                      uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch * bytes)};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(map, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(ptr),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FP8T_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return FP8T_OK;
+}
+
+// What the forward and the backward call share; `width`: rows of B as [rows][K], columns of the codes.
+struct GatedCall {
+  const char* name;
+  const void *A, *B;
+  fp8t_format a_fmt, b_fmt;
+  fp8t_layout b_layout;
+  int64_t M, N, K, b_rows;
+  const float *sa, *sb;
+  fp8t_act act;
+  const void *gu, *out16, *q;      // out16, q: M x (N or 2N)
+  fp8t_format q_fmt;
+  const float* scale;
+  float *amax, *scale_inv;
+};
+fp8t_status check_gated(const GatedCall& c) {
+  if (!c.A || !c.B || !c.sa || !c.sb) return fail(FP8T_ERR_INVALID_ARG, "%s: NULL operand or scale inverse", c.name);
+  for (int f : {c.a_fmt, c.b_fmt, c.q ? c.q_fmt : FP8T_E4M3})
+    if (f != FP8T_E4M3 && f != FP8T_E5M2) return fail(FP8T_ERR_INVALID_ARG, "%s: unknown format %d", c.name, f);
+  if (c.b_layout != FP8T_K_MAJOR && c.b_layout != FP8T_MN_MAJOR)
+    return fail(FP8T_ERR_INVALID_ARG, "%s: unknown operand layout", c.name);
+  if (c.act != FP8T_ACT_SILU && c.act != FP8T_ACT_GELU)
+    return fail(FP8T_ERR_INVALID_ARG, "%s: act must be SILU or GELU", c.name);
+  if ((c.q != nullptr) != (c.scale != nullptr) || (c.scale_inv && !c.q))
+    return fail(FP8T_ERR_INVALID_ARG, "%s: codes need a scale, and scale and scale_inv go with codes", c.name);
+  if (c.M <= 0 || c.N <= 0 || c.K <= 0) return fail(FP8T_ERR_INVALID_ARG, "%s: M, N, K must be > 0", c.name);
+  const int64_t lim = int64_t(1) << 30;
+  if (c.N % 16 || c.K % 16 || c.M >= lim || c.N >= lim || c.K >= lim ||
+      (c.M + 255) / 256 * ((c.N + 127) / 128) >= lim)
+    return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "%s: N and K must be multiples of 16, all sizes below 2^30", c.name);
+  if (!aligned(c.A, 16) || !aligned(c.B, 16) || !aligned(c.gu, 16) || !aligned(c.out16, 16) || !aligned(c.q, 16) ||
+      !aligned(c.sa, 4) || !aligned(c.sb, 4) || !aligned(c.scale, 4) || !aligned(c.amax, 4) || !aligned(c.scale_inv, 4))
+    return fail(FP8T_ERR_MISALIGNED, "%s: misaligned pointer", c.name);
+  return FP8T_OK;
+}
+// Operands, sizes and scalars.
+fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int tile_n) {
+  using namespace fp8t::gemm;
+  const bool mn = c.b_layout == FP8T_MN_MAJOR;
+  fp8t_status st = encode_kmajor(&p.a, c.A, c.M, c.K, kHalf);
+  if (st == FP8T_OK) st = mn ? encode_kmajor(&p.b, c.B, c.K, c.b_rows, kBK) : encode_kmajor(&p.b, c.B, c.b_rows, c.K, kHalf);
+  p.sa = c.sa;
+  p.sb = c.sb;
+  p.scale = c.scale;
+  p.amax_bits = reinterpret_cast<unsigned int*>(c.amax);
+  p.scale_inv = c.scale_inv;
+  p.M = static_cast<int32_t>(c.M);
+  p.N = static_cast<int32_t>(c.N);
+  p.tiles_m = static_cast<int32_t>((c.M + kBM - 1) / kBM);
+  p.tiles_n = static_cast<int32_t>((c.N + tile_n - 1) / tile_n);
+  p.total_tiles = p.tiles_m * p.tiles_n;
+  p.num_kb = static_cast<int32_t>((c.K + kBK - 1) / kBK);
+  p.b_mn = mn ? 1 : 0;
+  p.idesc = make_idesc(c.a_fmt, c.b_fmt, 0, p.b_mn);
+  p.act = c.act;
+  p.fmt = c.q_fmt;
+  p.has_q = c.q != nullptr;
+  return st;
+}
+template <class Op, class P>
+fp8t_status launch_pair(const P& p, const DeviceInfo* dev, const char* what, cudaStream_t stream) {
+  const int64_t grid = 2 * std::min<int64_t>(p.total_tiles, dev->pair_clusters);
+  (void)launch_pdl(fp8t::pair::k_pair_gemm<Op>, grid, fp8t::pair::kPairThreads, fp8t::pair::kPairSmemBytes, stream, 0, p);
+  return after_launch(what);
+}
+// Groups of 16 rows per CTA, chunks in flight and most warps of a matrix-vector launch.
+template <bool NV, int R, int U, int W>
+void launch_matvec_as(const fp8t::mv::Params& p, cudaStream_t stream) {
+  const int64_t per = static_cast<int64_t>(R) * (p.act ? 8 : 16);
+  const int warps = std::min(W, (p.K + 127) / 128);
+  (void)launch_pdl(fp8t::mv::k_fp4_matvec<NV, R, U, W>, (p.N + per - 1) / per, 32 * warps, 0, stream, 0, p);
+}
+template <bool NV>
+void launch_matvec_of(const fp8t::mv::Params& p, cudaStream_t stream) {
+  if (p.rows <= 2) launch_matvec_as<NV, 1, 4, 8>(p, stream);
+  else launch_matvec_as<NV, 2, 2, 16>(p, stream);
+}
+void launch_matvec(const fp8t::mv::Params& p, bool nv, cudaStream_t stream) {
+  nv ? launch_matvec_of<true>(p, stream) : launch_matvec_of<false>(p, stream);
+}
+
+constexpr CUtensorMapSwizzle kSwizzle16 = CU_TENSOR_MAP_SWIZZLE_64B, kSwizzle8 = CU_TENSOR_MAP_SWIZZLE_32B;
+
+}  // namespace
+
+extern "C" {
+
+fp8t_status fp8_gated_gemm(const fp8t_gated* desc, void* stream) {
+  t_last_error.clear();
+  if (!desc) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm: desc NULL");
+  const fp8t_gated& d = *desc;
+  const GatedCall c = {"fp8_gated_gemm", d.A, d.B, d.a_fmt, d.b_fmt, d.b_layout, d.M, d.N, d.K, 2 * d.N, d.d_a_scale_inv,
+                       d.d_b_scale_inv, d.act, d.gu_bf16, d.h_bf16, d.q, d.q_fmt, d.d_scale, d.d_amax_inout, d.d_scale_inv_out};
+  fp8t_status st = check_gated(c);
+  if (st != FP8T_OK) return st;
+  if (!d.gu_bf16 && !d.h_bf16 && !d.q) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm: no output asked for");
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != FP8T_OK || (st = ready_pair(dev)) != FP8T_OK) return st;
+  fp8t::gated::Params p = {};
+  if ((st = fill_gated(p, c, 128)) != FP8T_OK) return st;
+  p.keep = d.gu_bf16 != nullptr;
+  p.has_h = d.h_bf16 != nullptr;
+  if (p.keep && ((st = encode_2d(&p.o0, d.gu_bf16, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK ||
+                 (st = encode_2d(&p.o1, static_cast<const uint16_t*>(d.gu_bf16) + d.N, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK))
+    return st;
+  if (p.has_h && (st = encode_2d(&p.h, d.h_bf16, d.M, d.N, d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK) return st;
+  if (p.has_q && (st = encode_2d(&p.q0, d.q, d.M, d.N, d.N, 1, 32, 32, kSwizzle8)) != FP8T_OK) return st;
+  using namespace fp8t::gated;
+  return d.act == FP8T_ACT_SILU ? launch_pair<Forward<kSilu>>(p, dev, "fp8_gated_gemm launch", as_stream(stream))
+                                : launch_pair<Forward<kGelu>>(p, dev, "fp8_gated_gemm launch", as_stream(stream));
+}
+
+fp8t_status fp8_gated_gemm_backward(const fp8t_gated_grad* desc, void* stream) {
+  t_last_error.clear();
+  if (!desc) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm_backward: desc NULL");
+  const fp8t_gated_grad& d = *desc;
+  const GatedCall c = {"fp8_gated_gemm_backward", d.A, d.B, d.a_fmt, d.b_fmt, d.b_layout, d.M, d.N, d.K, d.N, d.d_a_scale_inv,
+                       d.d_b_scale_inv, d.act, d.gu_bf16, d.dgu_bf16, d.q, d.q_fmt, d.d_scale, d.d_amax_inout, d.d_scale_inv_out};
+  fp8t_status st = check_gated(c);
+  if (st != FP8T_OK) return st;
+  if (!d.gu_bf16) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm_backward: gu NULL");
+  if (!d.dgu_bf16 && !d.q) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm_backward: no output asked for");
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != FP8T_OK || (st = ready_pair(dev)) != FP8T_OK) return st;
+  fp8t::gated::Params p = {};
+  if ((st = fill_gated(p, c, fp8t::gemm::kBN)) != FP8T_OK) return st;
+  p.gu = static_cast<const uint16_t*>(d.gu_bf16);
+  p.keep = d.dgu_bf16 != nullptr;
+  if (p.keep && ((st = encode_2d(&p.o0, d.dgu_bf16, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK ||
+                 (st = encode_2d(&p.o1, static_cast<const uint16_t*>(d.dgu_bf16) + d.N, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK))
+    return st;
+  if (p.has_q && ((st = encode_2d(&p.q0, d.q, d.M, d.N, 2 * d.N, 1, 32, 32, kSwizzle8)) != FP8T_OK ||
+                  (st = encode_2d(&p.q1, static_cast<const uint8_t*>(d.q) + d.N, d.M, d.N, 2 * d.N, 1, 32, 32, kSwizzle8)) != FP8T_OK))
+    return st;
+  using namespace fp8t::gated;
+  return d.act == FP8T_ACT_SILU ? launch_pair<Backward<kSilu>>(p, dev, "fp8_gated_gemm_backward launch", as_stream(stream))
+                                : launch_pair<Backward<kGelu>>(p, dev, "fp8_gated_gemm_backward launch", as_stream(stream));
+}
+
+// ------------------------------------------------------------------ 4-bit weights times a few tokens
+fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream) {
+  t_last_error.clear();
+  if (!desc) return fail(FP8T_ERR_INVALID_ARG, "fp4_matvec: desc NULL");
+  const fp8t_fp4_matvec& d = *desc;
+  if (!d.x_bf16 || !d.q || !d.scales || !d.y_bf16) return fail(FP8T_ERR_INVALID_ARG, "fp4_matvec: NULL pointer");
+  if (d.quant != FP8T_Q_MXFP4 && d.quant != FP8T_Q_NVFP4)
+    return fail(FP8T_ERR_INVALID_ARG, "fp4_matvec: quant must be MXFP4 or NVFP4");
+  if (d.act < FP8T_ACT_NONE || d.act > FP8T_ACT_GELU) return fail(FP8T_ERR_INVALID_ARG, "fp4_matvec: unknown act %d", (int)d.act);
+  if (d.rows <= 0 || d.N <= 0 || d.K <= 0) return fail(FP8T_ERR_INVALID_ARG, "fp4_matvec: rows, N, K must be > 0");
+  const int64_t lim = int64_t(1) << 30;
+  if (d.rows > fp8t::mv::kMaxRows || d.N % 8 || d.K % 32 || d.N >= lim || d.K >= lim)
+    return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "fp4_matvec: at most 8 rows, N a multiple of 8 and K of 32, both below 2^30");
+  if (!aligned(d.x_bf16, 16) || !aligned(d.q, 16) || !aligned(d.scales, 16) || !aligned(d.y_bf16, 16) ||
+      !aligned(d.d_w_scale_inv, 4))
+    return fail(FP8T_ERR_MISALIGNED, "fp4_matvec: misaligned pointer");
+  DeviceInfo* dev = nullptr;
+  fp8t_status st = current_device(&dev);
+  if (st != FP8T_OK) return st;
+  fp8t::mv::Params p = {};
+  p.x = static_cast<const uint16_t*>(d.x_bf16);
+  p.q = static_cast<const uint8_t*>(d.q);
+  p.sf = static_cast<const uint8_t*>(d.scales);
+  p.factor = d.d_w_scale_inv;
+  p.y = static_cast<uint16_t*>(d.y_bf16);
+  p.rows = static_cast<int32_t>(d.rows);
+  p.N = static_cast<int32_t>(d.N);
+  p.K = static_cast<int32_t>(d.K);
+  const bool nv = d.quant == FP8T_Q_NVFP4;
+  p.words = static_cast<int32_t>(fp8t::blk::atoms_per_row(d.K, nv ? fp8t::blk::kNVFP4 : fp8t::blk::kMXFP4));
+  p.act = d.act;
+  launch_matvec(p, nv, as_stream(stream));
+  return after_launch("fp4_matvec launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ Newton-Schulz and Muon
+namespace {
+
+constexpr int64_t kMaxMuonSide = 65536;
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// Where a matrix's FP16 copies lie in a batch's part of the workspace: X twice, A and B.
+struct MuonSizes {
+  int64_t rows, cols, side, pitch_x, pitch_s;
+  size_t x, s;                     // bytes of X, of A
+  MuonSizes(int64_t r, int64_t c) : rows(r), cols(c), side(std::min(r, c)), pitch_x(round_up(c, 8)), pitch_s(round_up(side, 8)) {
+    x = static_cast<size_t>(round_up(rows * pitch_x * 2, 256));
+    s = static_cast<size_t>(round_up(side * pitch_s * 2, 256));
+  }
+  size_t bytes() const { return 2 * x + 2 * s; }
+  int64_t chunks() const { return (rows * cols + fp8t::muon::kChunk - 1) / fp8t::muon::kChunk; }
+};
+// The workspace: a norm per matrix, the partial sums of the largest batch, the copies of the largest batch.
+struct MuonPlan {
+  size_t norms = 0, partials = 0, copies = 0;
+  bool ok = true;
+  template <class Shape>
+  MuonPlan(int32_t n, Shape&& shape) {
+    for (int32_t b0 = 0; b0 < n && ok; b0 += fp8t::muon::kMaxMatrices) {
+      size_t copy = 0;
+      int64_t chunks = 0;
+      for (int32_t i = b0; i < std::min<int32_t>(n, b0 + fp8t::muon::kMaxMatrices); ++i) {
+        const std::pair<int64_t, int64_t> v = shape(i);
+        if (v.first <= 0 || v.second <= 0 || v.first > kMaxMuonSide || v.second > kMaxMuonSide) {
+          ok = false;
+          return;
+        }
+        const MuonSizes s(v.first, v.second);
+        copy += s.bytes();
+        chunks += s.chunks();
+      }
+      copies = std::max(copies, copy);
+      partials = std::max(partials, static_cast<size_t>(round_up(chunks * 8, 256)));
+    }
+    norms = static_cast<size_t>(round_up(static_cast<int64_t>(n) * sizeof(fp8t::muon::Norm) + 4, 256));   // and a word
+  }
+  size_t bytes() const { return norms + partials + copies; }
+};
+
+// A matrix's tensor maps: X (two copies) as K-major and as MN-major operand and as output, A and B as operand and output.
+struct MuonMaps {
+  CUtensorMap xk[2], xm[2], xd[2], sk[2], sd[2];
+  uint16_t* s[2];
+  fp8t_status encode(const MuonSizes& z, char* at) {
+    const CUtensorMapSwizzle in = CU_TENSOR_MAP_SWIZZLE_128B;
+    fp8t_status st = FP8T_OK;
+    for (int i = 0; i < 2 && st == FP8T_OK; ++i) {
+      const char* x = at + i * z.x;
+      s[i] = reinterpret_cast<uint16_t*>(at + 2 * z.x + i * z.s);
+      if ((st = encode_2d(&xk[i], x, z.rows, z.cols, z.pitch_x, 2, 128, 64, in)) == FP8T_OK &&
+          (st = encode_2d(&xm[i], x, z.rows, z.cols, z.pitch_x, 2, 64, 64, in)) == FP8T_OK &&
+          (st = encode_2d(&xd[i], x, z.rows, z.cols, z.pitch_x, 2, 32, 32, kSwizzle16)) == FP8T_OK &&
+          (st = encode_2d(&sk[i], s[i], z.side, z.side, z.pitch_s, 2, 128, 64, in)) == FP8T_OK)
+        st = encode_2d(&sd[i], s[i], z.side, z.side, z.pitch_s, 2, 32, 32, kSwizzle16);
+    }
+    return st;
+  }
+};
+
+// Product `phase` (0 A, 1 B, 2 X) of a step whose X is copy `cur`; returns its tiles.
+int32_t fill_muon_product(fp8t::muon::Matmul& p, const MuonSizes& z, const MuonMaps& m, int phase, int cur, int32_t start) {
+  using namespace fp8t::muon;
+  const bool wide = z.cols >= z.rows;
+  const float back = 1.0f / kFactor;
+  const int32_t side = static_cast<int32_t>(z.side);
+  p = Matmul{};
+  p.M = p.N = side;
+  int64_t k = side;
+  if (phase == 0) {                // wide: rows of X, K-major; tall: columns
+    p.a = p.b = wide ? m.xk[cur] : m.xm[cur];
+    p.a_mn = p.b_mn = wide ? 0 : 1;
+    p.d = m.sd[0];
+    k = wide ? z.cols : z.rows;
+    p.alpha = back;
+  } else if (phase == 1) {
+    p.a = p.b = m.sk[0];
+    p.d = m.sd[1];
+    p.c = m.s[0];
+    p.ldc = static_cast<int32_t>(z.pitch_s);
+    p.alpha = 2.0315f * back;
+    p.beta = -4.7750f;
+    p.diagonal = 3.4445f * kFactor;
+  } else {                         // wide: B X, B's rows by X's columns; tall: X B
+    p.a = wide ? m.sk[1] : m.xk[cur];
+    p.b = wide ? m.xm[cur] : m.sk[1];
+    p.b_mn = wide ? 1 : 0;
+    p.d = m.xd[cur ^ 1];
+    p.M = static_cast<int32_t>(z.rows);
+    p.N = static_cast<int32_t>(z.cols);
+    p.alpha = back;
+  }
+  p.symmetric = phase < 2 ? 1 : 0;
+  p.num_kb = static_cast<int32_t>((k + 63) / 64);
+  p.idesc = fp8t::pair::make_idesc_f16(p.a_mn, p.b_mn);
+  p.tiles_n = (p.N + 255) / 256;
+  p.tile_start = start;
+  const int32_t tiles_m = (p.M + 255) / 256;
+  return p.symmetric ? tiles_m * (tiles_m + 1) / 2 : tiles_m * p.tiles_n;
+}
+template <int NP>
+fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<MuonMaps>& m, int32_t steps,
+                          int32_t* expired, const DeviceInfo* dev, cudaStream_t stream) {
+  static thread_local fp8t::muon::Group<NP> g;
+  g.n = static_cast<int32_t>(z.size());
+  g.expired = expired;
+  for (int32_t i = 0; i < steps; ++i)
+    for (int phase = 0; phase < 3; ++phase) {
+      g.total_tiles = 0;
+      for (int32_t k = 0; k < g.n; ++k) g.total_tiles += fill_muon_product(g.p[k], z[k], m[k], phase, i & 1, g.total_tiles);
+      const fp8t_status st = launch_pair<fp8t::muon::Product<NP>>(g, dev, "Newton-Schulz product launch", stream);
+      if (st != FP8T_OK) return st;
+    }
+  return FP8T_OK;
+}
+
+// Both calls; `get(i)` gives the kernels' view of matrix i (x, chunk_start and pitch are filled here).
+template <int MODE, class Get>
+fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Table& t, void* d_workspace, size_t workspace_bytes,
+                      cudaStream_t stream, Get&& get) {
+  using namespace fp8t::muon;
+  auto shape = [&](int32_t i) {
+    int64_t r, c;
+    Tensor T;
+    get(i, T, r, c);
+    return std::make_pair(r, c);
+  };
+  const MuonPlan plan(n, shape);
+  if (!plan.ok) return fail(FP8T_ERR_UNSUPPORTED_SHAPE, "%s: rows and cols must be 1 to 65536", name);
+  if (!d_workspace || workspace_bytes < plan.bytes())
+    return fail(FP8T_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", name, plan.bytes());
+  if (!aligned(d_workspace, 256)) return fail(FP8T_ERR_MISALIGNED, "%s: misaligned workspace", name);
+  DeviceInfo* dev = nullptr;
+  fp8t_status st = current_device(&dev);
+  if (st != FP8T_OK || (st = ready_pair(dev)) != FP8T_OK) return st;
+  char* ws = static_cast<char*>(d_workspace);
+  t.norms = reinterpret_cast<Norm*>(ws);
+  t.expired = reinterpret_cast<int32_t*>(t.norms + n);
+  t.partials = reinterpret_cast<double*>(ws + plan.norms);
+  char* copies = ws + plan.norms + plan.partials;
+  t.all = n;
+  std::vector<MuonSizes> sizes;
+  auto table = [&](int32_t b0) {
+    const int32_t b1 = std::min<int32_t>(n, b0 + kMaxMatrices);
+    sizes.clear();
+    t.n = b1 - b0;
+    t.first = b0;
+    t.chunks = 0;
+    char* at = copies;
+    for (int32_t i = b0; i < b1; ++i) {
+      Tensor& T = t.t[i - b0];
+      int64_t r, c;
+      get(i, T, r, c);
+      sizes.emplace_back(r, c);
+      T.x = reinterpret_cast<uint16_t*>(at);
+      T.numel = r * c;
+      T.cols = static_cast<int32_t>(c);
+      T.pitch = static_cast<int32_t>(sizes.back().pitch_x);
+      T.chunk_start = t.chunks;
+      t.chunks += static_cast<int32_t>(sizes.back().chunks());
+      at += sizes.back().bytes();
+    }
+  };
+  // every norm before the first write: a non-finite one anywhere leaves all matrices as they are
+  for (int32_t b0 = 0; b0 < n; b0 += kMaxMatrices) {
+    table(b0);
+    (void)launch_pdl(k_muon_sumsq<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
+    if ((st = after_launch(name)) != FP8T_OK) return st;
+    (void)launch_pdl(k_muon_norms, t.n, kPassThreads, 0, stream, 0, t);
+    if ((st = after_launch(name)) != FP8T_OK) return st;
+  }
+  for (int32_t b0 = 0; b0 < n; b0 += kMaxMatrices) {
+    if (n > kMaxMatrices) table(b0);
+    std::vector<MuonMaps> maps(t.n);
+    for (int32_t i = 0; i < t.n; ++i)
+      if ((st = maps[i].encode(sizes[i], reinterpret_cast<char*>(t.t[i].x))) != FP8T_OK) return st;
+    (void)launch_pdl(k_muon_scale<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
+    if ((st = after_launch(name)) != FP8T_OK) return st;
+    st = t.n <= 4 ? newton_schulz<4>(sizes, maps, steps, t.expired, dev, stream)
+                  : newton_schulz<kMaxMatrices>(sizes, maps, steps, t.expired, dev, stream);
+    if (st != FP8T_OK) return st;
+    if (steps & 1)                 // the result is in the second copy
+      for (int32_t i = 0; i < t.n; ++i) t.t[i].x += sizes[i].x / 2;
+    (void)launch_pdl(k_muon_apply<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
+    if ((st = after_launch(name)) != FP8T_OK) return st;
+  }
+  return FP8T_OK;
+}
+
+// Whether two of the addresses are the same.
+bool any_twice(std::vector<const void*>& v) {
+  std::sort(v.begin(), v.end());
+  return std::adjacent_find(v.begin(), v.end()) != v.end();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t muon_workspace_bytes(const int64_t* rows, const int64_t* cols, int32_t n_matrices) {
+  if (!rows || !cols || n_matrices < 1 || n_matrices > 4096) return 0;
+  const MuonPlan plan(n_matrices, [&](int32_t i) { return std::make_pair(rows[i], cols[i]); });
+  return plan.ok ? plan.bytes() : 0;
+}
+
+fp8t_status muon_orthogonalize(const fp8t_orth_matrix* matrices, int32_t n_matrices, int32_t x_f32, int32_t steps,
+                               void* d_workspace, size_t workspace_bytes, void* stream) {
+  t_last_error.clear();
+  if (!matrices || n_matrices < 1 || n_matrices > 4096)
+    return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrices NULL or n_matrices out of range");
+  if (steps < 1 || steps > 16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: steps in 1..16");
+  std::vector<const void*> outs;
+  for (int32_t i = 0; i < n_matrices; ++i) {
+    const fp8t_orth_matrix& m = matrices[i];
+    if (!m.x || !m.out_bf16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrix %d: NULL pointer", i);
+    if (x_f32 && m.x == m.out_bf16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrix %d: out is the f32 input", i);
+    if (!aligned(m.x, 16) || !aligned(m.out_bf16, 16))
+      return fail(FP8T_ERR_MISALIGNED, "muon_orthogonalize: matrix %d: misaligned pointer", i);
+    outs.push_back(m.out_bf16);
+  }
+  if (any_twice(outs)) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: two results at one address");
+  fp8t::muon::Table t = {};
+  auto get = [&](int32_t i, fp8t::muon::Tensor& T, int64_t& r, int64_t& c) {
+    T = {};
+    T.g = matrices[i].x;
+    T.w = static_cast<uint16_t*>(matrices[i].out_bf16);
+    r = matrices[i].rows;
+    c = matrices[i].cols;
+  };
+  return x_f32 ? muon_call<fp8t::muon::kOrthF32>("muon_orthogonalize", n_matrices, steps, t, d_workspace, workspace_bytes, as_stream(stream), get)
+               : muon_call<fp8t::muon::kOrthBf16>("muon_orthogonalize", n_matrices, steps, t, d_workspace, workspace_bytes, as_stream(stream), get);
+}
+
+fp8t_status fused_muon_multi_tensor(const fp8t_muon_tensor* tensors, int32_t n_tensors, float lr, float beta,
+                                    float weight_decay, float update_rms, float loss_scale, int32_t nesterov,
+                                    int32_t steps, int32_t* d_skipped_out, void* d_workspace, size_t workspace_bytes,
+                                    void* stream) {
+  t_last_error.clear();
+  if (!tensors || n_tensors < 1 || n_tensors > 4096)
+    return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: tensors NULL or n_tensors out of range");
+  if (steps < 1 || steps > 16) return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: steps in 1..16");
+  if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale) || !std::isfinite(lr) || !std::isfinite(beta) ||
+      !std::isfinite(weight_decay) || !std::isfinite(update_rms))
+    return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: non-finite hyperparameter or loss_scale <= 0");
+  std::vector<const void*> outs;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const fp8t_muon_tensor& m = tensors[i];
+    if (!m.master || !m.momentum || !m.grad_bf16 || !m.weight_bf16)
+      return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: tensor %d: NULL pointer", i);
+    if (!aligned(m.master, 16) || !aligned(m.momentum, 16) || !aligned(m.grad_bf16, 16) || !aligned(m.weight_bf16, 16))
+      return fail(FP8T_ERR_MISALIGNED, "fused_muon_multi_tensor: tensor %d: misaligned pointer", i);
+    outs.push_back(m.master);
+    outs.push_back(m.momentum);
+    outs.push_back(m.weight_bf16);
+  }
+  if (any_twice(outs)) return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: a tensor is given twice");
+  if (!aligned(d_skipped_out, 4)) return fail(FP8T_ERR_MISALIGNED, "fused_muon_multi_tensor: misaligned skipped");
+  fp8t::muon::Table t = {};
+  t.beta = beta;
+  t.inv_scale = static_cast<float>(1.0 / static_cast<double>(loss_scale));
+  t.keep = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
+  t.nesterov = nesterov ? 1 : 0;
+  t.skipped = d_skipped_out;
+  auto get = [&](int32_t i, fp8t::muon::Tensor& T, int64_t& r, int64_t& c) {
+    const fp8t_muon_tensor& m = tensors[i];
+    T = {};
+    T.p = m.master;
+    T.m = m.momentum;
+    T.g = m.grad_bf16;
+    T.w = static_cast<uint16_t*>(m.weight_bf16);
+    r = m.rows;
+    c = m.cols;
+    T.rate = static_cast<float>(static_cast<double>(lr) * static_cast<double>(update_rms) *
+                                std::sqrt(static_cast<double>(std::max(r, c))));
+  };
+  return muon_call<fp8t::muon::kMuon>("fused_muon_multi_tensor", n_tensors, steps, t, d_workspace, workspace_bytes, as_stream(stream), get);
 }
 
 // ------------------------------------------------------------------ scale update

@@ -258,6 +258,16 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with FP16 (or, by the descriptor, BF16) operands, K = 16 per MMA.
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Block-scaled pair MMA (MXFP8): as tc_mma_f8_pair, with one E8M0 scale per 32 K values of
 // every row of A and of B read from tensor memory at sfa_tmem / sfb_tmem (the byte of each
 // 32-bit scale column selected by the descriptor's scale-factor ids).
@@ -310,6 +320,11 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
 // pdl_trigger lets the next kernel, if it was launched so too, begin once every CTA has called it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Both, for a kernel that has set up all it needs: the next kernel may begin, this one waits for those before it.
+__device__ __forceinline__ void pdl_enter() {
+  pdl_trigger();
+  pdl_wait();
+}
 // Loads of memory that the kernel before this one may write. Such a kernel runs while this one is already resident, so
 // the memory is not read-only for this one's lifetime, as the non-coherent path (__ldg, const __restrict__) needs it
 // to be; volatile asm also keeps them behind pdl_wait.
@@ -321,6 +336,27 @@ __device__ __forceinline__ float ld_dep(const float* p) {
 __device__ __forceinline__ uint4 ld_dep(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint2 ld_dep(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_dep(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int32_t ld_dep(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ double ld_dep(const double* p) {
+  double v;
+  asm volatile("ld.global.f64 %0, [%1];" : "=d"(v) : "l"(p));
   return v;
 }
 
