@@ -7,15 +7,15 @@
 //   - a weight under its scale is a BF16 number exactly (2 significant bits times a power of two, or times 4 bits). A
 //     code's three magnitude bits, put where BF16 has its low exponent bits and its first mantissa bit, are the value times
 //     2^-126, subnormals included; one BF16 multiplication by the scale times 2^124 (E4M3: 2^117), both to stay in range, makes
-//     two weights. Two shifts, two logic operations and one multiplication for two weights.
+//     two weights.
 //   - products and sums are mma.sync m16n8k16: 16 rows of W, 8 tokens, FP32 accumulators. An FMA per weight and token
 //     would cost as much as the decoding for one token and eight times that for eight. A tcgen05 tile would need the decoded
 //     weights in shared memory and a 128-row tile's set-up, and would still be bound by the bytes.
 // A lane holds 32 consecutive codes (16 bytes) of row g and of row g + 8, lanes 4g .. 4g + 3 the 128 values of a chunk; which of
 // the lane's own values goes into which k of an MMA is free as long as x is taken in the same order: the code
 // pairs (i, i + 4) of a word. The gated form takes the up row of the same output for row g + 8, so a lane has both.
-// A CTA takes 16 rows (8 gated outputs), its warps the chunks of K in turn, all of a warp's loads of a round in flight; the
-// warps' sums are added in shared memory in warp order.
+// A group is 16 rows (8 gated outputs); the warps of a CTA take its chunks of K in turn, and their sums are added in shared
+// memory in warp order.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -34,6 +34,7 @@ struct Params {
   int32_t rows, N, K;              // N: outputs
   int32_t words;                   // scale words of a row (atoms of a row block)
   int32_t act;                     // 0: W has N rows; else 2N
+  int32_t ways;                    // warps that share a group's K
 };
 constexpr int kMaxRows = 8;
 
@@ -48,18 +49,21 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Codes i and i + 4 of a word as BF16 values times 2^-126.
+// Codes I and I + 4 of a word (I = 0 or 1) as BF16 values times 2^-126. The two nibbles times 2^6 + 2^12 (I = 1: 2^2 + 2^8) put the
+// magnitude at bits 6 to 8 and the sign at bit 15; the two copies of a nibble do not meet, and what else there is of them is
+// masked away. The multiplication leaves the two logic operations to the pipe that is short here: shifts run on
+// the same half-rate pipe as logic does.
 template <int I>
 __device__ __forceinline__ uint32_t raw_pair(uint32_t w) {
-  const uint32_t mag = I <= 1 ? w << (6 - 4 * I) : w >> (4 * I - 6);
-  const uint32_t sign = w << (12 - 4 * I);
-  return (mag & 0x01C001C0u) | (sign & 0x80008000u);
+  return (w & (0x000F000Fu << (4 * I))) * (I == 0 ? 0x1040u : 0x104u) & 0x81C081C0u;
 }
 // What multiplies the raw pairs of the lane's 32 codes. E8M0 code c: 2^(c - 127 + 124) as the BF16 exponent field c + 124, so
-// that a weight is kept at a quarter (6 * 2^127 would not fit; 0.5 * 2^-127 * 2^-2 still does, as a subnormal), and above
-// what that field holds a second power of two (blocks of values of 2^4 and more).
-__device__ __forceinline__ uint32_t e8m0_factor(uint32_t c, uint32_t& more) {
-  more = c > 130u ? (c - 3u) << 7 : 0x3F80u;
+// that a weight is kept at a quarter (6 * 2^127 would not fit; 0.5 * 2^-127 * 2^-2 still does, as a subnormal). Above c = 130
+// (blocks of values of 2^4 and more) the field is full and a second power of two is needed; 255 is NaN.
+constexpr uint32_t kOneE8m0 = 130;
+__device__ __forceinline__ uint32_t e8m0_factor(uint32_t c) { return c * 0x00800080u + 0x3E003E00u; }
+__device__ __forceinline__ uint32_t e8m0_large(uint32_t c, uint32_t& more) {
+  more = c > kOneE8m0 ? (c - 3u) << 7 : 0x3F80u;
   uint32_t f = min(c + 124u, 254u) << 7;
   if (c == 255u) f = 0x7FC0u, more = 0x3F80u;
   more |= more << 16;
@@ -75,49 +79,40 @@ __device__ __forceinline__ void e4m3_factors(uint32_t c, uint32_t& f0, uint32_t&
   f1 = __byte_perm(__float_as_uint(f.y * up), 0, 0x3232);
 }
 
-// A row's 32 codes and their scale bytes, as loaded.
+// A row's 32 codes of a chunk and their scales: E4M3 two bytes, E8M0 the pair of bytes that holds the lane's (16 bits are
+// loaded as aligned).
 struct Piece {
   uint4 q;
   uint32_t s;
 };
-template <bool NV>
-__device__ __forceinline__ Piece load_piece(const Params& p, int row, bool in, int k, int t, int chunk) {
-  Piece r = {make_uint4(0, 0, 0, 0), 0u};
-  if (in) {
-    r.q = ld_dep(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(row) * (p.K / 2) + k / 2));
-    if constexpr (NV) {
-      const uint8_t* at = p.sf + blk::atom_word(row, 2 * chunk + (t >> 1), p.words) + (t & 1) * 2;
-      r.s = ld_dep(reinterpret_cast<const uint16_t*>(at));
-    } else {
-      uint16_t both;                                       // the byte's pair: 16 bits are loaded as aligned
-      const uint8_t* at = p.sf + blk::atom_word(row, chunk, p.words) + (t & 2);
-      both = ld_dep(reinterpret_cast<const uint16_t*>(at));
-      r.s = (both >> ((t & 1) * 8)) & 0xFFu;
-    }
-  }
-  return r;
-}
+
 // 8 codes of a row: four BF16 pairs.
 __device__ __forceinline__ void decode(uint32_t w, uint32_t f, uint32_t (&v)[4]) {
   v[0] = mul_bf16x2(raw_pair<0>(w), f);
   v[1] = mul_bf16x2(raw_pair<1>(w), f);
-  v[2] = mul_bf16x2(raw_pair<2>(w), f);
-  v[3] = mul_bf16x2(raw_pair<3>(w), f);
+  v[2] = mul_bf16x2(raw_pair<0>(w >> 8), f);
+  v[3] = mul_bf16x2(raw_pair<1>(w >> 8), f);
 }
 
 // One chunk of 16 rows: 8 MMAs.
 template <bool NV>
-__device__ __forceinline__ void chunk_mma(float (&acc)[4], const Piece& a, const Piece& b, const uint32_t (&x)[16]) {
+__device__ __forceinline__ void chunk_mma(float (&acc)[4], const Piece& a, const Piece& b, const uint4 (&xv)[4], int t) {
   uint32_t fa[2], fb[2], ma = 0x3F803F80u, mb = 0x3F803F80u;
+  bool large = false;
   if constexpr (NV) {
     e4m3_factors(a.s, fa[0], fa[1]);
     e4m3_factors(b.s, fb[0], fb[1]);
   } else {
-    fa[0] = fa[1] = e8m0_factor(a.s, ma);
-    fb[0] = fb[1] = e8m0_factor(b.s, mb);
+    const uint32_t ca = (a.s >> ((t & 1) * 8)) & 0xFFu, cb = (b.s >> ((t & 1) * 8)) & 0xFFu;
+    fa[0] = fa[1] = e8m0_factor(ca);
+    fb[0] = fb[1] = e8m0_factor(cb);
+    large = __any_sync(0xffffffffu, max(ca, cb) > kOneE8m0);
+    if (large) {
+      fa[0] = fa[1] = e8m0_large(ca, ma);
+      fb[0] = fb[1] = e8m0_large(cb, mb);
+    }
   }
   const uint32_t qa[4] = {a.q.x, a.q.y, a.q.z, a.q.w}, qb[4] = {b.q.x, b.q.y, b.q.z, b.q.w};
-  const bool large = !NV && __any_sync(0xffffffffu, ma != 0x3F803F80u || mb != 0x3F803F80u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t va[4], vb[4];
@@ -130,80 +125,141 @@ __device__ __forceinline__ void chunk_mma(float (&acc)[4], const Piece& a, const
         vb[j] = mul_bf16x2(vb[j], mb);
       }
     }
-    mma_bf16(acc, va[0], vb[0], va[1], vb[1], x[4 * i], x[4 * i + 1]);
-    mma_bf16(acc, va[2], vb[2], va[3], vb[3], x[4 * i + 2], x[4 * i + 3]);
+    mma_bf16(acc, va[0], vb[0], va[1], vb[1], xv[i].x, xv[i].y);
+    mma_bf16(acc, va[2], vb[2], va[3], vb[3], xv[i].z, xv[i].w);
   }
 }
 
-// R: groups of 16 rows of a CTA, which share the loads of x; U: chunks in flight; W: most warps.
-template <bool NV, int R, int U, int W>
-__global__ void __launch_bounds__(32 * W) k_fp4_matvec(const __grid_constant__ Params p) {
-  __shared__ float part[W][R][4][33];                      // [warp][group][accumulator][lane]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+// Eight consecutive values of x in the order of the code pairs: (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ uint4 in_pairs(uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
+}
+// Bytes of a token's x in shared memory: 256 a chunk, [8 values of each lane][lane], and half a bank round more, so that the
+// 16-byte reads of two tokens' four lanes meet no bank twice.
+__host__ __device__ __forceinline__ int64_t x_stride(int64_t K) { return (K + 127) / 128 * 256 + 64; }
+constexpr int64_t kMaxXBytes = 200 * 1024;
+constexpr int kWarps = 16, kAhead = 3;
+
+// Persistent: a CTA per SM, whose 16 warps take 16 / p.ways groups of 16 rows at a time, `ways` warps (a power of two) a group:
+// they take its chunks in turn, kAhead of a warp's in flight across the groups' borders, and add up in shared memory behind
+// a barrier of their own. XS: x fits shared memory and is put there once; else it is read as it is needed.
+template <bool NV, bool XS>
+__global__ void __launch_bounds__(32 * kWarps, 1) k_fp4_matvec(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t sx[];
+  __shared__ float part[2][kWarps][4][33];                 // [group's parity][warp][accumulator][lane]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  const int ways = p.ways, first = warp & (ways - 1), slot = warp / ways;   // this warp's first chunk; its group among the CTA's
   const int per = p.act ? 8 : 16;                          // outputs of a group
   const int chunks = (p.K + 127) / 128;
-  float acc[R][4];
-#pragma unroll
-  for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
+  const int groups = (p.N + per - 1) / per;
+  const int step = gridDim.x * (kWarps / ways);
+  const int64_t row_bytes = p.K / 2, sf_step = (NV ? 1024 : 512) * ways;
+  const int q_step = 64 * ways;
+  const uint16_t* x = p.x + static_cast<int64_t>(min(g, p.rows - 1)) * p.K + t * 32;   // tokens past the last: not stored
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  Piece a[kAhead], b[kAhead];
+  int lg = blockIdx.x * (kWarps / ways) + slot, lc = chunks;   // the next piece to load; its group's pointers are not set
+  const uint8_t *qa = nullptr, *qb = nullptr, *sa = nullptr, *sb = nullptr;
+  int group = lg, c = first;                               // the piece in hand
+  lg -= step;
+  auto load = [&](Piece& pa, Piece& pb) {
+    if (lc >= chunks) {                                    // the next group
+      lg += step;
+      if (lg >= groups || first >= chunks) {
+        lg -= step;                                        // stays past the end
+        return;
+      }
+      lc = first;
+      // rows past N are loaded as the last one: what they give is not stored
+      const int n = lg * per + g;
+      const int64_t ra = n, rb = p.act ? p.N + n : min(n + 8, p.N - 1);
+      qa = p.q + ra * row_bytes + t * 16 + lc * 64;
+      qb = p.q + rb * row_bytes + t * 16 + lc * 64;
+      const int at = NV ? (t >> 1) * 512 + (t & 1) * 2 : t & 2;
+      sa = p.sf + blk::atom_word(ra, NV ? 2 * lc : lc, p.words) + at;
+      sb = p.sf + blk::atom_word(rb, NV ? 2 * lc : lc, p.words) + at;
+    }
+    if (lc * 128 + t * 32 < p.K) {                         // K is a multiple of 32
+      pa.q = ld_dep(reinterpret_cast<const uint4*>(qa));
+      pb.q = ld_dep(reinterpret_cast<const uint4*>(qb));
+      pa.s = ld_dep(reinterpret_cast<const uint16_t*>(sa));
+      pb.s = ld_dep(reinterpret_cast<const uint16_t*>(sb));
+    } else {
+      pa = pb = {make_uint4(0, 0, 0, 0), 0u};
+    }
+    lc += ways;
+    qa += q_step;
+    qb += q_step;
+    sa += sf_step;
+    sb += sf_step;
+  };
   pdl_enter();
-  for (int c0 = warp; c0 < chunks; c0 += U * warps) {
-    Piece a[U][R], b[U][R];
-    uint4 xv[U][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * warps, k = c * 128 + t * 32;
-      const bool in = k < p.K;                             // K is a multiple of 32
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int n = (blockIdx.x * R + r) * per + g, second = p.act ? p.N + n : n + 8;
-        a[u][r] = load_piece<NV>(p, n, in && n < p.N, k, t, c);
-        b[u][r] = load_piece<NV>(p, second, in && (p.act ? n : n + 8) < p.N, k, t, c);
+  for (int u = 0; u < kAhead; ++u) load(a[u], b[u]);
+  const int stride = static_cast<int>(x_stride(p.K));
+  if constexpr (XS) {
+    const int vecs = chunks * 16;                          // of 8 values, of a token
+    for (int token = 0; token < p.rows; ++token)
+      for (int v = threadIdx.x; v < vecs; v += 32 * kWarps) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (v * 8 < p.K) w = ld_dep(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(token) * p.K + v * 8));
+        *reinterpret_cast<uint4*>(sx + token * stride + (v >> 4) * 256 + (v & 3) * 64 + ((v >> 2) & 3) * 16) = in_pairs(w);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xv[u][i] = make_uint4(0, 0, 0, 0);
-        if (in && g < p.rows) xv[u][i] = ld_dep(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(g) * p.K + k) + i);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c0 + u * warps >= chunks) break;                 // the same for the warp
-      uint32_t x[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {                        // values (0, 4), (1, 5), (2, 6), (3, 7)
-        const uint4 v = xv[u][i];
-        x[4 * i] = __byte_perm(v.x, v.z, 0x5410);
-        x[4 * i + 1] = __byte_perm(v.x, v.z, 0x7632);
-        x[4 * i + 2] = __byte_perm(v.y, v.w, 0x5410);
-        x[4 * i + 3] = __byte_perm(v.y, v.w, 0x7632);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) chunk_mma<NV>(acc[r], a[u][r], b[u][r], x);
-    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[warp][r][j][lane] = acc[r][j];
-  __syncthreads();
-  // accumulator j of lane 4g + t: row g (j < 2) or its second row, token 2t + (j & 1)
+  const uint8_t* mine = sx + min(g, p.rows - 1) * stride + t * 16;
   const float factor = (p.factor ? ld_dep(p.factor) : 1.0f) * (NV ? 512.0f : 4.0f);
-  for (int i = threadIdx.x; i < R * per * kMaxRows; i += blockDim.x) {
-    const int token = i / (R * per), o = i - token * R * per, r = o / per, row = o - r * per;
-    const int n = (blockIdx.x * R + r) * per + row;
-    if (token >= p.rows || n >= p.N) continue;
-    const int l = (row & 7) * 4 + (token >> 1), j = (token & 1) + (row >> 3) * 2;
-    float v = 0.0f, w = 0.0f;
-    for (int s = 0; s < warps; ++s) {
-      v += part[s][r][j][l];
-      if (p.act) w += part[s][r][j + 2][l];
+  int parity = 0;
+  // the group's last chunk of this warp is done: its warps' sums, added in warp order
+  auto finish = [&] {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      part[parity][warp][j][lane] = acc[j];
+      acc[j] = 0.0f;
     }
-    v *= factor;
-    if (p.act) v = v * (p.act == gated::kSilu ? gated::gate<gated::kSilu>(v) : gated::gate<gated::kGelu>(v)) * (w * factor);
-    uint16_t h;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
-    p.y[static_cast<int64_t>(token) * p.N + n] = h;
+    __syncwarp();
+    if (ways > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(32 * ways) : "memory");
+    // accumulator j of lane 4g + t: row g (j < 2) or its second row, token 2t + (j & 1)
+    for (int i = first * 32 + lane; i < per * p.rows; i += 32 * ways) {
+      const int token = p.act ? i >> 3 : i >> 4, row = i & (per - 1), n = group * per + row;
+      if (n >= p.N) continue;
+      const int l = (row & 7) * 4 + (token >> 1), j = (token & 1) + (row >> 3) * 2;
+      float v = 0.0f, w = 0.0f;
+      for (int s = slot * ways; s < (slot + 1) * ways; ++s) {
+        v += part[parity][s][j][l];
+        if (p.act) w += part[parity][s][j + 2][l];
+      }
+      v *= factor;
+      if (p.act) v = v * (p.act == gated::kSilu ? gated::gate<gated::kSilu>(v) : gated::gate<gated::kGelu>(v)) * (w * factor);
+      uint16_t h;
+      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+      p.y[static_cast<int64_t>(token) * p.N + n] = h;
+    }
+    parity ^= 1;                                           // the other half is free: all have passed this group's barrier
+    group += step;
+    c = first;
+  };
+  while (group < groups) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (group >= groups) break;
+      if (c < chunks) {
+        uint4 xv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (XS) xv[i] = *reinterpret_cast<const uint4*>(mine + c * 256 + i * 64);
+          else xv[i] = c * 128 + t * 32 < p.K ? in_pairs(ld_dep(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(c) * 128) + i))
+                                              : make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();                                      // the MMA's and the vote's lanes together
+        chunk_mma<NV>(acc, a[u], b[u], xv, t);
+        load(a[u], b[u]);
+        c += ways;
+      }
+      if (c >= chunks) finish();
+    }
   }
 }
 

@@ -65,7 +65,7 @@ struct DeviceInfo {
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
   // set up by their own first calls, so that no other call loads these kernels or fails with them
-  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false};
+  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false}, matvec_ready{false};
   int fp4_cast_blocks_per_sm = 0;
   int fp4_cast_rows_blocks_per_sm = 0;
   int pair_clusters = 0;             // co-resident clusters of the pair-tile products (one CTA per SM)
@@ -1710,7 +1710,7 @@ namespace {
 template <class Op>
 cudaError_t allow_pair_smem() {
   return cudaFuncSetAttribute(fp8t::pair::k_pair_gemm<Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fp8t::pair::kPairSmemBytes);
+                              fp8t::pair::kPairSmemBytes<Op>);
 }
 using fp8t::gated::kGelu;
 using fp8t::gated::kSilu;
@@ -1720,13 +1720,13 @@ fp8t_status ready_pair(DeviceInfo* d) {
     cudaError_t e;
     if ((e = allow_pair_smem<gated::Forward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Forward<kGelu>>()) != cudaSuccess ||
         (e = allow_pair_smem<gated::Backward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Backward<kGelu>>()) != cudaSuccess ||
-        (e = allow_pair_smem<muon::Product<4>>()) != cudaSuccess ||
-        (e = allow_pair_smem<muon::Product<muon::kMaxMatrices>>()) != cudaSuccess)
+        (e = allow_pair_smem<muon::Steps<4>>()) != cudaSuccess ||
+        (e = allow_pair_smem<muon::Steps<muon::kMaxMatrices>>()) != cudaSuccess)
       return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (d->sms / 2), 1, 1);
     cfg.blockDim = dim3(pair::kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = pair::kPairSmemBytes;
+    cfg.dynamicSmemBytes = pair::kPairSmemBytes<gated::Forward<kSilu>>;
     int clusters = 0;
     if (cudaOccupancyMaxActiveClusters(&clusters, pair::k_pair_gemm<gated::Forward<kSilu>>, &cfg) != cudaSuccess || clusters < 1) {
       (void)cudaGetLastError();
@@ -1814,23 +1814,31 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int tile_n) {
 template <class Op, class P>
 fp8t_status launch_pair(const P& p, const DeviceInfo* dev, const char* what, cudaStream_t stream) {
   const int64_t grid = 2 * std::min<int64_t>(p.total_tiles, dev->pair_clusters);
-  (void)launch_pdl(fp8t::pair::k_pair_gemm<Op>, grid, fp8t::pair::kPairThreads, fp8t::pair::kPairSmemBytes, stream, 0, p);
+  (void)launch_pdl(fp8t::pair::k_pair_gemm<Op>, grid, fp8t::pair::kPairThreads, fp8t::pair::kPairSmemBytes<Op>, stream, 0, p);
   return after_launch(what);
 }
-// Groups of 16 rows per CTA, chunks in flight and most warps of a matrix-vector launch.
-template <bool NV, int R, int U, int W>
-void launch_matvec_as(const fp8t::mv::Params& p, cudaStream_t stream) {
-  const int64_t per = static_cast<int64_t>(R) * (p.act ? 8 : 16);
-  const int warps = std::min(W, (p.K + 127) / 128);
-  (void)launch_pdl(fp8t::mv::k_fp4_matvec<NV, R, U, W>, (p.N + per - 1) / per, 32 * warps, 0, stream, 0, p);
+fp8t_status ready_matvec(DeviceInfo* d) {
+  return once_per_device(d->matvec_ready, "fp4_matvec", [] {
+    const cudaError_t e = cudaFuncSetAttribute(fp8t::mv::k_fp4_matvec<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(fp8t::mv::kMaxXBytes));
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(fp8t::mv::k_fp4_matvec<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(fp8t::mv::kMaxXBytes));
+  });
 }
-template <bool NV>
-void launch_matvec_of(const fp8t::mv::Params& p, cudaStream_t stream) {
-  if (p.rows <= 2) launch_matvec_as<NV, 1, 4, 8>(p, stream);
-  else launch_matvec_as<NV, 2, 2, 16>(p, stream);
-}
-void launch_matvec(const fp8t::mv::Params& p, bool nv, cudaStream_t stream) {
-  nv ? launch_matvec_of<true>(p, stream) : launch_matvec_of<false>(p, stream);
+void launch_matvec(fp8t::mv::Params& p, bool nv, int sms, cudaStream_t stream) {
+  using namespace fp8t::mv;
+  const int64_t per = p.act ? 8 : 16, groups = (p.N + per - 1) / per;
+  static const int forced = getenv("MV") ? atoi(getenv("MV")) : 0;
+  p.ways = kWarps;
+  while (p.ways > 1 && groups * p.ways >= 4 * kWarps * static_cast<int64_t>(sms)) p.ways /= 2;
+  if (forced) p.ways = forced;
+  const int64_t grid = std::min<int64_t>((groups * p.ways + kWarps - 1) / kWarps, sms);
+  const int64_t x = p.rows * x_stride(p.K);
+  const bool fits = x <= kMaxXBytes;
+  auto* kernel = nv ? (fits ? k_fp4_matvec<true, true> : k_fp4_matvec<true, false>)
+                    : (fits ? k_fp4_matvec<false, true> : k_fp4_matvec<false, false>);
+  (void)launch_pdl(kernel, grid, 32 * kWarps, fits ? static_cast<size_t>(x) : 0, stream, 0, p);
 }
 
 constexpr CUtensorMapSwizzle kSwizzle16 = CU_TENSOR_MAP_SWIZZLE_64B, kSwizzle8 = CU_TENSOR_MAP_SWIZZLE_32B;
@@ -1878,7 +1886,9 @@ fp8t_status fp8_gated_gemm_backward(const fp8t_gated_grad* desc, void* stream) {
   if ((st = current_device(&dev)) != FP8T_OK || (st = ready_pair(dev)) != FP8T_OK) return st;
   fp8t::gated::Params p = {};
   if ((st = fill_gated(p, c, fp8t::gemm::kBN)) != FP8T_OK) return st;
-  p.gu = static_cast<const uint16_t*>(d.gu_bf16);
+  if ((st = encode_2d(&p.g, d.gu_bf16, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK ||
+      (st = encode_2d(&p.u, static_cast<const uint16_t*>(d.gu_bf16) + d.N, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK)
+    return st;
   p.keep = d.dgu_bf16 != nullptr;
   if (p.keep && ((st = encode_2d(&p.o0, d.dgu_bf16, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK ||
                  (st = encode_2d(&p.o1, static_cast<const uint16_t*>(d.dgu_bf16) + d.N, d.M, d.N, 2 * d.N, 2, 32, 32, kSwizzle16)) != FP8T_OK))
@@ -1909,7 +1919,7 @@ fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream) {
     return fail(FP8T_ERR_MISALIGNED, "fp4_matvec: misaligned pointer");
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
-  if (st != FP8T_OK) return st;
+  if (st != FP8T_OK || (st = ready_matvec(dev)) != FP8T_OK) return st;
   fp8t::mv::Params p = {};
   p.x = static_cast<const uint16_t*>(d.x_bf16);
   p.q = static_cast<const uint8_t*>(d.q);
@@ -1922,7 +1932,7 @@ fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream) {
   const bool nv = d.quant == FP8T_Q_NVFP4;
   p.words = static_cast<int32_t>(fp8t::blk::atoms_per_row(d.K, nv ? fp8t::blk::kNVFP4 : fp8t::blk::kMXFP4));
   p.act = d.act;
-  launch_matvec(p, nv, as_stream(stream));
+  launch_matvec(p, nv, dev->sms, as_stream(stream));
   return after_launch("fp4_matvec launch");
 }
 
@@ -1967,85 +1977,57 @@ struct MuonPlan {
       copies = std::max(copies, copy);
       partials = std::max(partials, static_cast<size_t>(round_up(chunks * 8, 256)));
     }
-    norms = static_cast<size_t>(round_up(static_cast<int64_t>(n) * sizeof(fp8t::muon::Norm) + 4, 256));   // and a word
+    norms = static_cast<size_t>(round_up(static_cast<int64_t>(n) * sizeof(fp8t::muon::Norm) + 8, 256));   // and two words
   }
   size_t bytes() const { return norms + partials + copies; }
 };
 
-// A matrix's tensor maps: X (two copies) as K-major and as MN-major operand and as output, A and B as operand and output.
-struct MuonMaps {
-  CUtensorMap xk[2], xm[2], xd[2], sk[2], sd[2];
-  uint16_t* s[2];
-  fp8t_status encode(const MuonSizes& z, char* at) {
-    const CUtensorMapSwizzle in = CU_TENSOR_MAP_SWIZZLE_128B;
-    fp8t_status st = FP8T_OK;
-    for (int i = 0; i < 2 && st == FP8T_OK; ++i) {
-      const char* x = at + i * z.x;
-      s[i] = reinterpret_cast<uint16_t*>(at + 2 * z.x + i * z.s);
-      if ((st = encode_2d(&xk[i], x, z.rows, z.cols, z.pitch_x, 2, 128, 64, in)) == FP8T_OK &&
-          (st = encode_2d(&xm[i], x, z.rows, z.cols, z.pitch_x, 2, 64, 64, in)) == FP8T_OK &&
-          (st = encode_2d(&xd[i], x, z.rows, z.cols, z.pitch_x, 2, 32, 32, kSwizzle16)) == FP8T_OK &&
-          (st = encode_2d(&sk[i], s[i], z.side, z.side, z.pitch_s, 2, 128, 64, in)) == FP8T_OK)
-        st = encode_2d(&sd[i], s[i], z.side, z.side, z.pitch_s, 2, 32, 32, kSwizzle16);
-    }
-    return st;
+// A matrix's tensor maps and tiles. Only the tiles of A and B on and above the diagonal count.
+fp8t_status fill_muon_matrix(fp8t::muon::Matrix& m, const MuonSizes& z, char* at, int32_t& sym_tiles, int32_t& x_tiles) {
+  fp8t_status st = FP8T_OK;
+  for (int i = 0; i < 2; ++i) {
+    char *x = at + i * z.x, *s = at + 2 * z.x + i * z.s;
+    if ((st = encode_2d(&m.x[i], x, z.rows, z.cols, z.pitch_x, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != FP8T_OK ||
+        (st = encode_2d(&m.s[i], s, z.side, z.side, z.pitch_s, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != FP8T_OK ||
+        (st = encode_2d(&m.xd[i], x, z.rows, z.cols, z.pitch_x, 2, 32, 32, kSwizzle16)) != FP8T_OK ||
+        (st = encode_2d(&m.sd[i], s, z.side, z.side, z.pitch_s, 2, 32, 32, kSwizzle16)) != FP8T_OK)
+      return st;
   }
-};
-
-// Product `phase` (0 A, 1 B, 2 X) of a step whose X is copy `cur`; returns its tiles.
-int32_t fill_muon_product(fp8t::muon::Matmul& p, const MuonSizes& z, const MuonMaps& m, int phase, int cur, int32_t start) {
-  using namespace fp8t::muon;
-  const bool wide = z.cols >= z.rows;
-  const float back = 1.0f / kFactor;
-  const int32_t side = static_cast<int32_t>(z.side);
-  p = Matmul{};
-  p.M = p.N = side;
-  int64_t k = side;
-  if (phase == 0) {                // wide: rows of X, K-major; tall: columns
-    p.a = p.b = wide ? m.xk[cur] : m.xm[cur];
-    p.a_mn = p.b_mn = wide ? 0 : 1;
-    p.d = m.sd[0];
-    k = wide ? z.cols : z.rows;
-    p.alpha = back;
-  } else if (phase == 1) {
-    p.a = p.b = m.sk[0];
-    p.d = m.sd[1];
-    p.c = m.s[0];
-    p.ldc = static_cast<int32_t>(z.pitch_s);
-    p.alpha = 2.0315f * back;
-    p.beta = -4.7750f;
-    p.diagonal = 3.4445f * kFactor;
-  } else {                         // wide: B X, B's rows by X's columns; tall: X B
-    p.a = wide ? m.sk[1] : m.xk[cur];
-    p.b = wide ? m.xm[cur] : m.sk[1];
-    p.b_mn = wide ? 1 : 0;
-    p.d = m.xd[cur ^ 1];
-    p.M = static_cast<int32_t>(z.rows);
-    p.N = static_cast<int32_t>(z.cols);
-    p.alpha = back;
-  }
-  p.symmetric = phase < 2 ? 1 : 0;
-  p.num_kb = static_cast<int32_t>((k + 63) / 64);
-  p.idesc = fp8t::pair::make_idesc_f16(p.a_mn, p.b_mn);
-  p.tiles_n = (p.N + 255) / 256;
-  p.tile_start = start;
-  const int32_t tiles_m = (p.M + 255) / 256;
-  return p.symmetric ? tiles_m * (tiles_m + 1) / 2 : tiles_m * p.tiles_n;
+  m.rows = static_cast<int32_t>(z.rows);
+  m.cols = static_cast<int32_t>(z.cols);
+  m.sym_start = sym_tiles;
+  m.x_start = x_tiles;
+  const int32_t side = static_cast<int32_t>((z.side + 255) / 256);
+  sym_tiles += side * (side + 1) / 2;
+  x_tiles += static_cast<int32_t>((z.rows + 255) / 256 * ((z.cols + 255) / 256));
+  return st;
 }
 template <int NP>
-fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<MuonMaps>& m, int32_t steps,
-                          int32_t* expired, const DeviceInfo* dev, cudaStream_t stream) {
+fp8t_status newton_schulz(const std::vector<MuonSizes>& z, char* copies, int32_t steps, const fp8t::pair::Grid& grid,
+                          const DeviceInfo* dev, cudaStream_t stream) {
+  using Op = fp8t::muon::Steps<NP>;
   static thread_local fp8t::muon::Group<NP> g;
   g.n = static_cast<int32_t>(z.size());
-  g.expired = expired;
-  for (int32_t i = 0; i < steps; ++i)
-    for (int phase = 0; phase < 3; ++phase) {
-      g.total_tiles = 0;
-      for (int32_t k = 0; k < g.n; ++k) g.total_tiles += fill_muon_product(g.p[k], z[k], m[k], phase, i & 1, g.total_tiles);
-      const fp8t_status st = launch_pair<fp8t::muon::Product<NP>>(g, dev, "Newton-Schulz product launch", stream);
-      if (st != FP8T_OK) return st;
-    }
-  return FP8T_OK;
+  g.steps = steps;
+  g.sym_tiles = g.x_tiles = 0;
+  g.grid = grid;
+  for (int32_t k = 0; k < g.n; copies += z[k].bytes(), ++k) {
+    const fp8t_status st = fill_muon_matrix(g.m[k], z[k], copies, g.sym_tiles, g.x_tiles);
+    if (st != FP8T_OK) return st;
+  }
+  // its CTAs wait for one another: a cooperative launch has them all resident or fails
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(std::max(g.sym_tiles, g.x_tiles), dev->pair_clusters)), 1, 1);
+  cfg.blockDim = dim3(fp8t::pair::kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = fp8t::pair::kPairSmemBytes<Op>;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  (void)cudaLaunchKernelEx(&cfg, fp8t::pair::k_pair_gemm<Op>, g);
+  return after_launch("Newton-Schulz products launch");
 }
 
 // Both calls; `get(i)` gives the kernels' view of matrix i (x, chunk_start and pitch are filled here).
@@ -2069,7 +2051,8 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
   if (st != FP8T_OK || (st = ready_pair(dev)) != FP8T_OK) return st;
   char* ws = static_cast<char*>(d_workspace);
   t.norms = reinterpret_cast<Norm*>(ws);
-  t.expired = reinterpret_cast<int32_t*>(t.norms + n);
+  t.grid.counter = reinterpret_cast<unsigned int*>(t.norms + n);
+  t.grid.expired = reinterpret_cast<int32_t*>(t.norms + n) + 1;
   t.partials = reinterpret_cast<double*>(ws + plan.norms);
   char* copies = ws + plan.norms + plan.partials;
   t.all = n;
@@ -2105,13 +2088,10 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
   }
   for (int32_t b0 = 0; b0 < n; b0 += kMaxMatrices) {
     if (n > kMaxMatrices) table(b0);
-    std::vector<MuonMaps> maps(t.n);
-    for (int32_t i = 0; i < t.n; ++i)
-      if ((st = maps[i].encode(sizes[i], reinterpret_cast<char*>(t.t[i].x))) != FP8T_OK) return st;
     (void)launch_pdl(k_muon_scale<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
     if ((st = after_launch(name)) != FP8T_OK) return st;
-    st = t.n <= 4 ? newton_schulz<4>(sizes, maps, steps, t.expired, dev, stream)
-                  : newton_schulz<kMaxMatrices>(sizes, maps, steps, t.expired, dev, stream);
+    st = t.n <= 4 ? newton_schulz<4>(sizes, copies, steps, t.grid, dev, stream)
+                  : newton_schulz<kMaxMatrices>(sizes, copies, steps, t.grid, dev, stream);
     if (st != FP8T_OK) return st;
     if (steps & 1)                 // the result is in the second copy
       for (int32_t i = 0; i < t.n; ++i) t.t[i].x += sizes[i].x / 2;

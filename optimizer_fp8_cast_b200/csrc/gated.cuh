@@ -15,6 +15,7 @@
 #pragma once
 
 #include "gemm_pair.cuh"
+#include "quant_block.cuh"
 
 namespace fp8t {
 namespace gated {
@@ -26,11 +27,11 @@ enum : int { kSilu = 1, kGelu = 2 };                       // fp8t_act
 struct alignas(64) Params {
   CUtensorMap a, b;                // A in 128-row boxes (or [K][M]), B
   CUtensorMap o0, o1;              // 16-bit outputs: G and U (forward), dG and dU (backward)
+  CUtensorMap g, u;                // backward: the kept G and U
   CUtensorMap h;                   // forward: h as BF16
   CUtensorMap q0, q1;              // codes: h (forward), dG and dU (backward)
   const float* sa;
   const float* sb;
-  const uint16_t* gu;              // backward: [M][2N] BF16
   const float* scale;              // of the codes
   unsigned int* amax_bits;
   float* scale_inv;
@@ -40,22 +41,43 @@ struct alignas(64) Params {
   uint32_t idesc;
   int32_t act, fmt;                // fmt of the codes
   int32_t keep, has_h, has_q;      // which outputs are written
-  int32_t tile_start;              // 0
-  __device__ __forceinline__ const Params& problem(int) const { return *this; }
 };
 
-// sigmoid(w(g)) and w'(g).
+// Pairs of values: each half is rounded as the scalar operation would be, at half the instructions.
+using blk::f32x2;
+__device__ __forceinline__ f32x2 both(float v) { return blk::pair(v, v); }
+__device__ __forceinline__ float ex2(float x) {            // 2^x, to 2 ulp; infinity and 0 where it leaves the range
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {            // 1 / x, to 1 ulp; 0 for infinity
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// Sigmoid of w(g), and w'(g) where the operator needs it (1 for SiLU). g^2 is held to 10^12, far past where the sigmoid is 0 or
+// 1 in f32, so that w' stays finite.
 template <int ACT>
-__device__ __forceinline__ float gate(float g, float* dw = nullptr) {
-  float w = g;
+__device__ __forceinline__ f32x2 gate(f32x2 g, f32x2& dw) {
+  using namespace blk;
+  f32x2 x;                                                 // -w log2(e)
   if constexpr (ACT == kGelu) {
-    const float g2 = g * g;
-    w = 1.5957691216057308f * g * fmaf(0.044715f, g2, 1.0f);
-    if (dw) *dw = 1.5957691216057308f * fmaf(0.134145f, g2, 1.0f);
-  } else if (dw) {
-    *dw = 1.0f;
+    f32x2 g2 = mul2(g, g);
+    g2 = blk::pair(fminf(lo(g2), 1e12f), fminf(hi(g2), 1e12f));
+    x = mul2(mul2(g, both(-1.5957691216057308f * kLog2e)), fma2(g2, both(0.044715f), both(1.0f)));
+    dw = mul2(fma2(g2, both(0.134145f), both(1.0f)), both(1.5957691216057308f));
+  } else {
+    x = mul2(g, both(-kLog2e));
   }
-  return __fdividef(1.0f, 1.0f + __expf(-w));              // exp overflows to infinity where sigmoid is 0
+  const f32x2 d = add2(blk::pair(ex2(lo(x)), ex2(hi(x))), both(1.0f));
+  return blk::pair(rcp(lo(d)), rcp(hi(d)));
+}
+template <int ACT>
+__device__ __forceinline__ float gate(float g) {
+  f32x2 dw;
+  return blk::lo(gate<ACT>(both(g), dw));
 }
 
 // Runs of `kRun` row tiles share their column tiles, so that the weights a wave of tiles reads are read by several rows
@@ -68,35 +90,71 @@ __device__ __forceinline__ void place_in_runs(int tiles_m, int tiles_n, int loca
   mt = run * kRun + in - nt * rows;
 }
 
-__device__ __forceinline__ void note(uint32_t& top, float v, bool valid) {
-  if (valid) top = max(top, __float_as_uint(v) & 0x7FFFFFFFu);
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
-// Codes of 32 values of a row under `scale`.
-__device__ __forceinline__ void codes32(const float (&v)[32], float scale, int fmt, uint32_t (&q)[8]) {
+// The largest magnitude of a row's 32 values. Rows past M and columns past N stay out of it: an infinite weight makes NaN of
+// their zeros. N is a multiple of 16.
+__device__ __forceinline__ void note(Out& o, const f32x2 (&v)[16], bool row, bool whole) {
+  float a = 0.0f, b = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float a = __fmul_rn(v[4 * j], scale), b = __fmul_rn(v[4 * j + 1], scale);
-    const float c = __fmul_rn(v[4 * j + 2], scale), d = __fmul_rn(v[4 * j + 3], scale);
-    q[j] = fmt == 0 ? cvt_fp8x2<0>(a, b) | cvt_fp8x2<0>(c, d) << 16 : cvt_fp8x2<1>(a, b) | cvt_fp8x2<1>(c, d) << 16;
+    a = max_abs(a, blk::lo(v[j]), blk::hi(v[j]));
+    b = max_abs(b, blk::lo(v[8 + j]), blk::hi(v[8 + j]));
+  }
+  if (row) o.amax = max(o.amax, max(__float_as_uint(a), whole ? __float_as_uint(b) : 0u) & 0x7FFFFFFFu);
+}
+// Codes of 32 values of a row under `scale`.
+__device__ __forceinline__ void codes32(const f32x2 (&v)[16], f32x2 scale, int fmt, uint32_t (&q)[8]) {
+  using namespace blk;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const f32x2 a = mul2(v[2 * j], scale), b = mul2(v[2 * j + 1], scale);
+    q[j] = fmt == 0 ? cvt_fp8x2<0>(lo(a), hi(a)) | cvt_fp8x2<0>(lo(b), hi(b)) << 16
+                    : cvt_fp8x2<1>(lo(a), hi(a)) | cvt_fp8x2<1>(lo(b), hi(b)) << 16;
   }
 }
-__device__ __forceinline__ void pack16(const float (&v)[32], uint32_t (&w)[16]) {
+__device__ __forceinline__ void pack16(const f32x2 (&v)[16], uint32_t (&w)[16]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(blk::lo(v[j]), blk::hi(v[j]));
+}
+// 32 accumulator columns times alpha.
+__device__ __forceinline__ void scaled(const uint32_t (&r)[32], f32x2 alpha, f32x2 (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = blk::mul2(blk::pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), alpha);
 }
 
 struct Scalars {
-  float alpha, scale;
+  f32x2 alpha, scale;
 };
 struct Base {
   using Params = gated::Params;
   using Scalars = gated::Scalars;
-  static constexpr bool kF16 = false, kAmax = true;
-  static __device__ __forceinline__ void place(const Params& P, int local, int& mt, int& nt) {
-    place_in_runs(P.tiles_m, P.tiles_n, local, mt, nt);
+  static constexpr bool kF16 = false, kAmax = true, kPhased = false;
+  static __device__ __forceinline__ int phases(const Params&) { return 1; }
+  static __device__ __forceinline__ int tiles(const Params& g, int) { return g.total_tiles; }
+  static __device__ __forceinline__ bool reads(int) { return false; }
+  static __device__ __forceinline__ Grid grid(const Params&) { return {}; }
+  // b_step: rows of B from one column tile to the next; b_other: from the even CTA's to the odd CTA's
+  static __device__ __forceinline__ Work work_of(const Params& g, int tile, int rank, int b_step, int b_other) {
+    Work w;
+    place_in_runs(g.tiles_m, g.tiles_n, tile, w.mt, w.nt);
+    w.a = &g.a;
+    w.b = &g.b;
+    w.a_row = w.mt * kBM + rank * kHalf;
+    w.b_row = w.nt * b_step + rank * b_other;
+    w.num_kb = g.num_kb;
+    w.a_mn = 0;
+    w.b_mn = g.b_mn;
+    w.idesc = g.idesc;
+    w.which = 0;
+    return w;
   }
   static __device__ __forceinline__ Scalars scalars(const Params& g) {
-    return {__fmul_rn(ld_dep(g.sa), ld_dep(g.sb)), g.scale ? ld_dep(g.scale) : 1.0f};
+    return {both(__fmul_rn(ld_dep(g.sa), ld_dep(g.sb))), both(g.scale ? ld_dep(g.scale) : 1.0f)};
   }
   // A CTA whose waits expired has not seen all of its tiles: its amax is a NaN, so that the next scale stays as it is.
   static __device__ __forceinline__ void finish(const Params& g, uint32_t top, bool aborted) {
@@ -108,13 +166,15 @@ struct Base {
 
 template <int ACT>
 struct Forward : Base {
-  static __device__ __forceinline__ int b_row(const Params& P, int nt, int rank) { return nt * 128 + rank * P.N; }
-  template <class Release>
-  static __device__ __forceinline__ void epilogue(const Params& g, const Params&, const Scalars& k, Out& o, int, int nt,
-                                                  int row0, int half, uint32_t t_base, Release&& release) {
+  static constexpr int kLoads = 0;
+  static __device__ __forceinline__ void prefetch(const Params&, const Work&, int, Out&, int, int) {}
+  static __device__ __forceinline__ Work work(const Params& g, int, int tile, int rank) { return work_of(g, tile, rank, 128, g.N); }
+  template <class Release, class Ahead>
+  static __device__ __forceinline__ bool epilogue(const Params& g, const Work& w, int, const Scalars& k, Out& o, int row0, int half,
+                                                  uint32_t t_base, Release&& release, Ahead&&) {
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
-      const int c = half * 64 + s * 32, n = nt * 128 + c;
+      const int c = half * 64 + s * 32, n = w.nt * 128 + c;
       uint32_t rg[32], ru[32];
       __syncwarp();                                        // one lane stored the chunk before
       tmem_ld_32x32b_x32(t_base + c, rg);
@@ -124,31 +184,26 @@ struct Forward : Base {
       tmem_reg_fence(ru);
       if (s == 1) release();
       if (n >= g.N || row0 >= g.M) continue;               // chunk entirely outside the matrix
-      float gv[32], uv[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        gv[j] = __fmul_rn(__uint_as_float(rg[j]), k.alpha);
-        uv[j] = __fmul_rn(__uint_as_float(ru[j]), k.alpha);
-      }
+      f32x2 gv[16], uv[16];
+      scaled(rg, k.alpha, gv);
+      scaled(ru, k.alpha, uv);
       if (g.keep) {
-        uint32_t w[16];
-        pack16(gv, w);
-        store16(o, &g.o0, w, n, row0);
-        pack16(uv, w);
-        store16(o, &g.o1, w, n, row0);
+        uint32_t v[16];
+        pack16(gv, v);
+        store16(o, &g.o0, v, n, row0);
+        pack16(uv, v);
+        store16(o, &g.o1, v, n, row0);
       }
-      // rows past M and columns past N (whose gate is a column of the up projection) stay out of amax: an infinite weight
-      // makes NaN of their zeros. N is a multiple of 16
-      const bool in = row0 + o.lane < g.M, all = in && n + 16 < g.N;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        gv[j] = gv[j] * gate<ACT>(gv[j]) * uv[j];
-        note(o.amax, gv[j], j < 16 ? in : all);
+      for (int j = 0; j < 16; ++j) {
+        f32x2 dw;
+        gv[j] = blk::mul2(blk::mul2(gv[j], gate<ACT>(gv[j], dw)), uv[j]);
       }
+      note(o, gv, row0 + o.lane < g.M, n + 16 < g.N);
       if (g.has_h) {
-        uint32_t w[16];
-        pack16(gv, w);
-        store16(o, &g.h, w, n, row0);
+        uint32_t v[16];
+        pack16(gv, v);
+        store16(o, &g.h, v, n, row0);
       }
       if (g.has_q) {
         uint32_t q[8];
@@ -156,39 +211,37 @@ struct Forward : Base {
         store8(o, &g.q0, q, n, row0);
       }
     }
+    return true;
   }
 };
 
-// 32 BF16 values of a row (four 16-byte loads where they lie within it).
-__device__ __forceinline__ void load32(const uint16_t* p, int left, bool row, float (&v)[32]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (row && 8 * c < left) x = ld_dep(reinterpret_cast<const uint4*>(p + 8 * c));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * c + 2 * j] = __uint_as_float(w[j] << 16);
-      v[8 * c + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  }
-}
+__device__ __forceinline__ f32x2 pair_of(uint32_t w) { return blk::pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
 template <int ACT>
 struct Backward : Base {
-  static __device__ __forceinline__ int b_row(const Params&, int nt, int rank) { return nt * kBN + rank * kHalf; }
-  template <class Release>
-  static __device__ __forceinline__ void epilogue(const Params& g, const Params&, const Scalars& k, Out& o, int, int nt,
-                                                  int row0, int half, uint32_t t_base, Release&& release) {
-    const int row = row0 + o.lane;
-    const bool in = row < g.M;
-    const uint16_t* line = g.gu + static_cast<int64_t>(row) * 2 * g.N;
+  static constexpr int kLoads = 2;
+  static __device__ __forceinline__ void fetch_at(const Params& g, Out& o, int row0, int n) {
+    const CUtensorMap* const maps[2] = {&g.g, &g.u};
+    const int x[2] = {n, n};
+    fetch(o, maps, x, row0);
+  }
+  static __device__ __forceinline__ void prefetch(const Params& g, const Work& w, int, Out& o, int row0, int half) {
+    fetch_at(g, o, row0, w.nt * kBN + half * 128);
+  }
+  static __device__ __forceinline__ Work work(const Params& g, int, int tile, int rank) { return work_of(g, tile, rank, kBN, kHalf); }
+  template <class Release, class Ahead>
+  static __device__ __forceinline__ bool epilogue(const Params& g, const Work& w, int, const Scalars& k, Out& o, int row0, int half,
+                                                  uint32_t t_base, Release&& release, Ahead&& ahead) {
+    const bool in = row0 + o.lane < g.M;
 #pragma unroll 1
     for (int s = 0; s < 4; ++s) {
-      const int c = half * 128 + s * 32, n = nt * kBN + c;
-      float gv[32], uv[32];
-      load32(line + n, g.N - n, in, gv);
-      load32(line + g.N + n, g.N - n, in, uv);
+      const int c = half * 128 + s * 32, n = w.nt * kBN + c;
+      uint4 gw[4], uw[4];
+      if (!fetched(o)) return false;
+      chunk_row(o, 0, gw);
+      chunk_row(o, 1, uw);
+      if (s < 3) fetch_at(g, o, row0, n + 32);
+      else ahead();
       uint32_t r[32];
       __syncwarp();
       tmem_ld_32x32b_x32(t_base + c, r);
@@ -196,27 +249,32 @@ struct Backward : Base {
       tmem_reg_fence(r);
       if (s == 3) release();
       if (n >= g.N || row0 >= g.M) continue;
-      const bool all = in && n + 16 < g.N;
+      f32x2 gv[16], uv[16], dh[16];
+      scaled(r, k.alpha, dh);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float dh = __fmul_rn(__uint_as_float(r[j]), k.alpha);
-        float dw;
-        const float sg = gate<ACT>(gv[j], &dw);
-        const float rest = sg * (1.0f - sg);
-        // where sigmoid is 0 or 1 its slope is 0 whatever g and w'(g) are (they may be infinite)
-        const float slope = rest == 0.0f ? 0.0f : gv[j] * rest * dw;
-        const float du = dh * (gv[j] * sg);
-        gv[j] = dh * uv[j] * (sg + slope);
-        uv[j] = du;
-        note(o.amax, gv[j], j < 16 ? in : all);
-        note(o.amax, uv[j], j < 16 ? in : all);
+      for (int j = 0; j < 16; ++j) {
+        gv[j] = pair_of((&gw[j >> 2].x)[j & 3]);
+        uv[j] = pair_of((&uw[j >> 2].x)[j & 3]);
       }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        using namespace blk;
+        f32x2 dw;
+        const f32x2 sg = gate<ACT>(gv[j], dw), gs = mul2(gv[j], sg);
+        // g s (1 - s) w': where the sigmoid is 0 or 1 the product is 0 before the finite w' comes in
+        f32x2 slope = mul2(gs, fma2(sg, both(-1.0f), both(1.0f)));
+        if constexpr (ACT == kGelu) slope = mul2(slope, dw);
+        gv[j] = mul2(mul2(dh[j], uv[j]), add2(sg, slope));
+        uv[j] = mul2(dh[j], gs);
+      }
+      note(o, gv, in, n + 16 < g.N);
+      note(o, uv, in, n + 16 < g.N);
       if (g.keep) {
-        uint32_t w[16];
-        pack16(gv, w);
-        store16(o, &g.o0, w, n, row0);
-        pack16(uv, w);
-        store16(o, &g.o1, w, n, row0);
+        uint32_t v[16];
+        pack16(gv, v);
+        store16(o, &g.o0, v, n, row0);
+        pack16(uv, v);
+        store16(o, &g.o1, v, n, row0);
       }
       if (g.has_q) {
         uint32_t q[8];
@@ -226,6 +284,7 @@ struct Backward : Base {
         store8(o, &g.q1, q, n, row0);
       }
     }
+    return true;
   }
 };
 

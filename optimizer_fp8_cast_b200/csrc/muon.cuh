@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include "gemm_pair.cuh"
+#include "quant_block.cuh"
 
 namespace fp8t {
 namespace muon {
@@ -31,62 +32,102 @@ using namespace pair;
 constexpr float kFactor = 1024.0f;                         // of X, A and B
 
 // ------------------------------------------------------------------ the products
-struct alignas(64) Matmul {
-  CUtensorMap a, b, d;             // operands in 128-byte boxes, D in 32 x 32 ones
-  const uint16_t* c;               // FP16 [M][ldc] added with factor beta, or NULL
-  float alpha, beta, diagonal;     // D = alpha acc + beta c + diagonal I
-  int32_t M, N, num_kb, ldc;
-  int32_t tiles_n, symmetric, tile_start;
-  int32_t a_mn, b_mn;
-  uint32_t idesc;
+// All of a table's steps are one launch: three phases a step (A, B, X) behind barriers of the grid. A launch of each phase
+// took 9.5 us for a 256 x 256 matrix, of which the products are one (set-up 0.8 us, first loads 1.4, stores 0.9, launch 2).
+struct alignas(64) Matrix {
+  CUtensorMap x[2], s[2];          // operands in boxes of 64 rows x 64 values: X (two copies), A and B
+  CUtensorMap xd[2], sd[2];        // the same as outputs, in boxes of 32 x 32
+  int32_t rows, cols;
+  int32_t sym_start, x_start;      // first tile in the phases of A and B, and of X
 };
 constexpr int kMaxMatrices = 24;
-// Up to NP products; a launch's parameters are copied at every launch, and most calls have few matrices.
+// Up to NP matrices: a launch's parameters are copied at every launch, and most calls have few matrices.
 template <int NP>
 struct alignas(64) Group {
-  Matmul p[NP];
-  int32_t n, total_tiles;
-  int32_t* expired;                // set by a CTA whose waits expired
-  __device__ __forceinline__ const Matmul& problem(int tile) const {
-    int k = 0;
-    while (k + 1 < n && p[k + 1].tile_start <= tile) ++k;
-    return p[k];
-  }
+  Matrix m[NP];
+  int32_t n, steps;
+  int32_t sym_tiles, x_tiles;      // of the phases
+  Grid grid;
 };
 
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+
 template <int NP>
-struct Product {
+struct Steps {
   using Params = Group<NP>;
   struct Scalars {};
-  static constexpr bool kF16 = true, kAmax = false;
+  static constexpr bool kF16 = true, kAmax = false, kPhased = true;
+  static constexpr int kLoads = 1;
   static __device__ __forceinline__ Scalars scalars(const Params&) { return {}; }
+  static __device__ __forceinline__ Grid grid(const Params& g) { return g.grid; }
+  static __device__ __forceinline__ int phases(const Params& g) { return 3 * g.steps; }
+  static __device__ __forceinline__ int tiles(const Params& g, int ph) { return ph % 3 == 2 ? g.x_tiles : g.sym_tiles; }
+  static __device__ __forceinline__ bool reads(int ph) { return ph % 3 == 1; }      // B's epilogue reads A
   static __device__ __forceinline__ void finish(const Params& g, uint32_t, bool aborted) {
-    if (aborted) atomicExch(g.expired, 1);
+    if (aborted) atomicExch(g.grid.expired, 1);
   }
-  static __device__ __forceinline__ int b_row(const Matmul&, int nt, int rank) { return nt * kBN + rank * kHalf; }
-  static __device__ __forceinline__ void place(const Matmul& P, int local, int& mt, int& nt) {
-    if (!P.symmetric) {
-      mt = local / P.tiles_n;
-      nt = local - mt * P.tiles_n;
-      return;
+  static __device__ __forceinline__ Work work(const Params& g, int ph, int tile, int rank) {
+    const int phase = ph % 3, cur = (ph / 3) & 1;          // X is copy `cur`, the step's result the other
+    int k = 0;
+    if (phase == 2) {
+      while (k + 1 < g.n && g.m[k + 1].x_start <= tile) ++k;
+    } else {
+      while (k + 1 < g.n && g.m[k + 1].sym_start <= tile) ++k;
     }
-    mt = 0;                                                // rows of the upper triangle: tiles_n, tiles_n - 1, ...
-    while (local >= P.tiles_n - mt) local -= P.tiles_n - mt++;
-    nt = mt + local;
+    const Matrix& m = g.m[k];
+    const bool wide = m.cols >= m.rows;
+    const int side = wide ? m.rows : m.cols, lengthwise = wide ? m.cols : m.rows;
+    Work w;
+    w.which = k;
+    w.a_mn = w.b_mn = 0;
+    int inner = side;
+    if (phase == 2) {                                      // wide: B X; tall: X B
+      const int tiles_n = (m.cols + kBN - 1) / kBN, local = tile - m.x_start;
+      w.mt = local / tiles_n;
+      w.nt = local - w.mt * tiles_n;
+      w.a = wide ? &m.s[1] : &m.x[cur];
+      w.b = wide ? &m.x[cur] : &m.s[1];
+      w.b_mn = wide ? 1 : 0;
+    } else {                                               // the tiles on and above the diagonal: rows of n, n - 1, ...
+      int local = tile - m.sym_start, n = (side + kBN - 1) / kBN;
+      w.mt = 0;
+      while (local >= n) local -= n--, ++w.mt;
+      w.nt = w.mt + local;
+      w.a = w.b = phase == 0 ? &m.x[cur] : &m.s[0];
+      if (phase == 0) {                                    // wide: rows of X; tall: its columns
+        inner = lengthwise;
+        w.a_mn = w.b_mn = wide ? 0 : 1;
+      }
+    }
+    w.a_row = w.mt * kBM + rank * kHalf;
+    w.b_row = w.nt * kBN + rank * kHalf;
+    w.num_kb = (inner + 63) / 64;
+    w.idesc = make_idesc_f16(w.a_mn, w.b_mn);
+    return w;
   }
-  template <class Release>
-  static __device__ __forceinline__ void epilogue(const Params&, const Matmul& P, const Scalars&, Out& o, int mt, int nt,
-                                                  int row0, int half, uint32_t t_base, Release&& release) {
-    const int row = row0 + o.lane;
+  static __device__ __forceinline__ void fetch_at(const Params& g, const Work& w, Out& o, int row0, int n) {
+    const CUtensorMap* const maps[1] = {&g.m[w.which].sd[0]};
+    const int x[1] = {n};
+    fetch(o, maps, x, row0);
+  }
+  static __device__ __forceinline__ void prefetch(const Params& g, const Work& w, int ph, Out& o, int row0, int half) {
+    if (reads(ph)) fetch_at(g, w, o, row0, w.nt * kBN + half * 128);
+  }
+  // 32 columns of the accumulator, times alpha: with READ also kB times A's values and a I.
+  template <bool READ, class Release, class Ahead>
+  static __device__ __forceinline__ bool chunks(const Params& g, const Work& w, const CUtensorMap* d, Out& o, int row0, int half,
+                                                int M, int N, bool mirrored, float alpha, uint32_t t_base, Release&& release,
+                                                Ahead&& ahead) {
+    using namespace blk;
 #pragma unroll 1
     for (int s = 0; s < 4; ++s) {
-      const int c = half * 128 + s * 32, n = nt * kBN + c;
-      uint4 cv[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        cv[p] = make_uint4(0, 0, 0, 0);
-        if (P.c && row < P.M && n + 8 * p < P.N)            // ldc is a multiple of 8, at least N
-          cv[p] = ld_dep(reinterpret_cast<const uint4*>(P.c + static_cast<int64_t>(row) * P.ldc + n + 8 * p));
+      const int c = half * 128 + s * 32, n = w.nt * kBN + c;
+      uint4 av[4];
+      if constexpr (READ) {
+        if (!fetched(o)) return false;
+        chunk_row(o, 0, av);
+        if (s < 3) fetch_at(g, w, o, row0, n + 32);
+        else ahead();
       }
       uint32_t r[32];
       __syncwarp();
@@ -94,22 +135,41 @@ struct Product {
       tmem_ld_wait();
       tmem_reg_fence(r);
       if (s == 3) release();
-      if (n >= P.N || row0 >= P.M) continue;
-      uint32_t w[16];
+      if (n >= N || row0 >= M) continue;
+      const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
+      f32x2 v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const uint32_t h = (&cv[j >> 2].x)[j & 3];
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        float lo = __fmul_rn(__uint_as_float(r[2 * j]), P.alpha), hi = __fmul_rn(__uint_as_float(r[2 * j + 1]), P.alpha);
-        lo = fmaf(P.beta, f.x, lo);
-        hi = fmaf(P.beta, f.y, hi);
-        if (row == n + 2 * j) lo += P.diagonal;
-        if (row == n + 2 * j + 1) hi += P.diagonal;
-        w[j] = pack_f16x2(lo, hi);
+        v[j] = mul2(blk::pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), al);
+        if constexpr (READ) {
+          const uint32_t h = (&av[j >> 2].x)[j & 3];
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          v[j] = fma2(be, blk::pair(f.x, f.y), v[j]);
+        }
       }
-      store16(o, &P.d, w, n, row0);
-      if (P.symmetric && mt != nt) store16_transposed(o, &P.d, w, row0, n);
+      uint32_t q[16];
+      if (READ && row0 == n) {                             // the diagonal runs through this chunk
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          q[j] = pack_f16x2(lo(v[j]) + (o.lane == 2 * j ? kA * kFactor : 0.0f), hi(v[j]) + (o.lane == 2 * j + 1 ? kA * kFactor : 0.0f));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) q[j] = pack_f16x2(lo(v[j]), hi(v[j]));
+      }
+      store16(o, d, q, n, row0);
+      if (mirrored) store16_transposed(o, d, q, row0, n);
     }
+    return true;
+  }
+  template <class Release, class Ahead>
+  static __device__ __forceinline__ bool epilogue(const Params& g, const Work& w, int ph, const Scalars&, Out& o, int row0, int half,
+                                                  uint32_t t_base, Release&& release, Ahead&& ahead) {
+    const Matrix& m = g.m[w.which];
+    const int phase = ph % 3, side = min(m.rows, m.cols);
+    if (phase == 1) return chunks<true>(g, w, &m.sd[1], o, row0, half, side, side, w.mt != w.nt, kC / kFactor, t_base, release, ahead);
+    const bool sym = phase == 0;
+    return chunks<false>(g, w, sym ? &m.sd[0] : &m.xd[((ph / 3) & 1) ^ 1], o, row0, half, sym ? side : m.rows, sym ? side : m.cols,
+                         sym && w.mt != w.nt, 1.0f / kFactor, t_base, release, ahead);
   }
 };
 
@@ -141,7 +201,7 @@ struct Table {
   int32_t nesterov;
   double* partials;                // one a chunk, of this table
   Norm* norms;                     // one a tensor, of the call
-  int32_t* expired;                // a product of this table gave up waiting: its X is not to be used
+  Grid grid;                       // of the products; expired: one gave up waiting, and X is not to be used
   int32_t* skipped;
 };
 constexpr int kPassThreads = 256, kVec = 8, kChunk = kPassThreads * kVec * 4;   // elements of a CTA's chunk
@@ -280,7 +340,7 @@ __device__ __forceinline__ bool all_finite(const Table& t) {
 template <int MODE>
 __global__ void __launch_bounds__(kPassThreads) k_muon_scale(const __grid_constant__ Table t) {
   pdl_enter();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *t.expired = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *t.grid.counter = 0, *t.grid.expired = 0;
   if (MODE == kMuon) {
     const bool go = all_finite(t);
     if (blockIdx.x == 0 && threadIdx.x == 0 && t.skipped) *t.skipped = go ? 0 : 1;
@@ -327,7 +387,7 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_scale(const __grid_consta
 template <int MODE>
 __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_constant__ Table t) {
   pdl_enter();
-  const bool expired = ld_dep(t.expired) != 0;
+  const bool expired = ld_dep(t.grid.expired) != 0;
   if (MODE == kMuon && !all_finite(t)) return;
   if (MODE == kMuon && expired) {                          // m is new, p and w stay
     if (blockIdx.x == 0 && threadIdx.x == 0 && t.skipped) *t.skipped = 1;
