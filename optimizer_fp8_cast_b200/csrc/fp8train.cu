@@ -2011,8 +2011,16 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, char* copies, int32_t
   g.steps = steps;
   g.sym_tiles = g.x_tiles = 0;
   g.grid = grid;
+  // the longest first: a cluster takes every n-th tile, and the phase of A ends with the shortest (its K is the longer side)
+  std::vector<int32_t> order(z.size());
+  std::vector<char*> at(z.size());
   for (int32_t k = 0; k < g.n; copies += z[k].bytes(), ++k) {
-    const fp8t_status st = fill_muon_matrix(g.m[k], z[k], copies, g.sym_tiles, g.x_tiles);
+    order[k] = k;
+    at[k] = copies;
+  }
+  std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return std::max(z[a].rows, z[a].cols) > std::max(z[b].rows, z[b].cols); });
+  for (int32_t k = 0; k < g.n; ++k) {
+    const fp8t_status st = fill_muon_matrix(g.m[k], z[order[k]], at[order[k]], g.sym_tiles, g.x_tiles);
     if (st != FP8T_OK) return st;
   }
   // its CTAs wait for one another: a cooperative launch has them all resident or fails
@@ -2021,10 +2029,10 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, char* copies, int32_t
   cfg.blockDim = dim3(fp8t::pair::kPairThreads, 1, 1);
   cfg.dynamicSmemBytes = fp8t::pair::kPairSmemBytes<Op>;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeCooperative;
-  at[0].val.cooperative = 1;
-  cfg.attrs = at;
+  cudaLaunchAttribute together[1];
+  together[0].id = cudaLaunchAttributeCooperative;
+  together[0].val.cooperative = 1;
+  cfg.attrs = together;
   cfg.numAttrs = 1;
   (void)cudaLaunchKernelEx(&cfg, fp8t::pair::k_pair_gemm<Op>, g);
   return after_launch("Newton-Schulz products launch");

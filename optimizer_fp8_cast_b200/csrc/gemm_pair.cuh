@@ -181,11 +181,11 @@ __device__ __forceinline__ void grid_arrive(const Grid& g, unsigned int* warps_d
   if (lane == 0) {
     bulk_wait_group<0>();
     fence_proxy_async_all();
-    __threadfence();
-    if (atomicAdd(warps_done, 1u) % kPairEpiWarps == kPairEpiWarps - 1) {
-      __threadfence();
+    // every warp releases, so that the last one's arrival carries the others' stores
+    unsigned int before;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(warps_done)) : "memory");
+    if (before % kPairEpiWarps == kPairEpiWarps - 1)
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.counter) : "memory");
-    }
   }
   __syncwarp();
 }
@@ -194,11 +194,11 @@ __device__ __forceinline__ bool grid_wait(const Grid& g, unsigned int target, ui
   bool ok = true;
   if (lane == 0) {
     const uint64_t t0 = globaltimer_ns();
-    while (expire || ld_acquire(g.counter) < target) {
-      if (*reinterpret_cast<volatile int32_t*>(g.expired) != 0 || globaltimer_ns() - t0 > limit) {
-        ok = false;
-        break;
-      }
+    while (ok && (expire || ld_acquire(g.counter) < target)) {
+      // the clock and the other word only now and then: each is a round trip that would delay the next look at the counter
+      int looks = 0;
+      while (looks < 16 && (expire || ld_acquire(g.counter) < target)) ++looks;
+      if (looks == 16 && (*reinterpret_cast<volatile int32_t*>(g.expired) != 0 || globaltimer_ns() - t0 > limit)) ok = false;
     }
     fence_proxy_async_all();
   }
