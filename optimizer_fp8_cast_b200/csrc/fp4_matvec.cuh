@@ -16,6 +16,11 @@
 // pairs (i, i + 4) of a word. The gated form takes the up row of the same output for row g + 8, so a lane has both.
 // A group is 16 rows (8 gated outputs); the warps of a CTA take its chunks of K in turn, and their sums are added in shared
 // memory in warp order.
+// What bounds it: for few weights the launch and one trip to memory (1 x 4096 x 4096 4.6 us, 1.4 of them its bytes); for many the
+// issue of about 4.3 instructions a weight and lane at 24 warps an SM, and the logic pipe, which takes two cycles an operation
+// (4 x 4096 x 2 x 11008 NVFP4 18.2 us, 7.8 its bytes). Measured and not kept: a persistent form with three chunks of a warp in
+// flight and x in shared memory in the order of the MMAs (21.9 us, and 8 x 11008 x 4096 17.5: filling 176 KB of x is in
+// nobody's shadow).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -34,7 +39,6 @@ struct Params {
   int32_t rows, N, K;              // N: outputs
   int32_t words;                   // scale words of a row (atoms of a row block)
   int32_t act;                     // 0: W has N rows; else 2N
-  int32_t ways;                    // warps that share a group's K
 };
 constexpr int kMaxRows = 8;
 
@@ -135,131 +139,99 @@ __device__ __forceinline__ uint4 in_pairs(uint4 v) {
   return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                     __byte_perm(v.y, v.w, 0x7632));
 }
-// Bytes of a token's x in shared memory: 256 a chunk, [8 values of each lane][lane], and half a bank round more, so that the
-// 16-byte reads of two tokens' four lanes meet no bank twice.
-__host__ __device__ __forceinline__ int64_t x_stride(int64_t K) { return (K + 127) / 128 * 256 + 64; }
-constexpr int64_t kMaxXBytes = 200 * 1024;
-constexpr int kWarps = 16, kAhead = 3;
 
-// Persistent: a CTA per SM, whose 16 warps take 16 / p.ways groups of 16 rows at a time, `ways` warps (a power of two) a group:
-// they take its chunks in turn, kAhead of a warp's in flight across the groups' borders, and add up in shared memory behind
-// a barrier of their own. XS: x fits shared memory and is put there once; else it is read as it is needed.
-template <bool NV, bool XS>
-__global__ void __launch_bounds__(32 * kWarps, 1) k_fp4_matvec(const __grid_constant__ Params p) {
-  extern __shared__ uint8_t sx[];
-  __shared__ float part[2][kWarps][4][33];                 // [group's parity][warp][accumulator][lane]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// W: most warps; B: CTAs that an SM is to hold; AHEAD: the next chunk is loaded before a chunk's arithmetic. A warp takes two
+// groups, which share its x (one: 4 x 4096 x 2 x 11008 21.2 us for 18.2, 8 x 11008 x 4096 12.1 for 11.0).
+constexpr int kGroups = 2;
+template <bool NV, int W, int B, bool AHEAD>
+__global__ void __launch_bounds__(32 * W, B) k_fp4_matvec(const __grid_constant__ Params p) {
+  constexpr int R = kGroups;
+  __shared__ float part[W][R][4][33];                      // [warp][group][accumulator][lane]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int ways = p.ways, first = warp & (ways - 1), slot = warp / ways;   // this warp's first chunk; its group among the CTA's
-  const int per = p.act ? 8 : 16;                          // outputs of a group
+  const int per = p.act ? 8 : 16, n0 = blockIdx.x * per * R;   // outputs of a group; this CTA's first
   const int chunks = (p.K + 127) / 128;
-  const int groups = (p.N + per - 1) / per;
-  const int step = gridDim.x * (kWarps / ways);
-  const int64_t row_bytes = p.K / 2, sf_step = (NV ? 1024 : 512) * ways;
-  const int q_step = 64 * ways;
-  const uint16_t* x = p.x + static_cast<int64_t>(min(g, p.rows - 1)) * p.K + t * 32;   // tokens past the last: not stored
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  Piece a[kAhead], b[kAhead];
-  int lg = blockIdx.x * (kWarps / ways) + slot, lc = chunks;   // the next piece to load; its group's pointers are not set
-  const uint8_t *qa = nullptr, *qb = nullptr, *sa = nullptr, *sb = nullptr;
-  int group = lg, c = first;                               // the piece in hand
-  lg -= step;
-  auto load = [&](Piece& pa, Piece& pb) {
-    if (lc >= chunks) {                                    // the next group
-      lg += step;
-      if (lg >= groups || first >= chunks) {
-        lg -= step;                                        // stays past the end
-        return;
-      }
-      lc = first;
-      // rows past N are loaded as the last one: what they give is not stored
-      const int n = lg * per + g;
-      const int64_t ra = n, rb = p.act ? p.N + n : min(n + 8, p.N - 1);
-      qa = p.q + ra * row_bytes + t * 16 + lc * 64;
-      qb = p.q + rb * row_bytes + t * 16 + lc * 64;
-      const int at = NV ? (t >> 1) * 512 + (t & 1) * 2 : t & 2;
-      sa = p.sf + blk::atom_word(ra, NV ? 2 * lc : lc, p.words) + at;
-      sb = p.sf + blk::atom_word(rb, NV ? 2 * lc : lc, p.words) + at;
-    }
-    if (lc * 128 + t * 32 < p.K) {                         // K is a multiple of 32
-      pa.q = ld_dep(reinterpret_cast<const uint4*>(qa));
-      pb.q = ld_dep(reinterpret_cast<const uint4*>(qb));
-      pa.s = ld_dep(reinterpret_cast<const uint16_t*>(sa));
-      pb.s = ld_dep(reinterpret_cast<const uint16_t*>(sb));
-    } else {
-      pa = pb = {make_uint4(0, 0, 0, 0), 0u};
-    }
-    lc += ways;
-    qa += q_step;
-    qb += q_step;
-    sa += sf_step;
-    sb += sf_step;
-  };
-  pdl_enter();
+  // Rows past N and tokens past the last are loaded as the last one: what they give is not stored.
+  const uint8_t *q[R][2], *s[R][2];
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(a[u], b[u]);
-  const int stride = static_cast<int>(x_stride(p.K));
-  if constexpr (XS) {
-    const int vecs = chunks * 16;                          // of 8 values, of a token
-    for (int token = 0; token < p.rows; ++token)
-      for (int v = threadIdx.x; v < vecs; v += 32 * kWarps) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (v * 8 < p.K) w = ld_dep(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(token) * p.K + v * 8));
-        *reinterpret_cast<uint4*>(sx + token * stride + (v >> 4) * 256 + (v & 3) * 64 + ((v >> 2) & 3) * 16) = in_pairs(w);
-      }
-    __syncthreads();
+  for (int r = 0; r < R; ++r) {
+    const int n = min(n0 + r * per + g, p.N - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t row = h == 0 ? n : p.act ? p.N + n : min(n + 8, p.N - 1);
+      q[r][h] = p.q + row * (p.K / 2) + warp * 64 + t * 16;
+      s[r][h] = p.sf + blk::atom_word(row, NV ? 2 * warp : warp, p.words) + (NV ? (t >> 1) * 512 + (t & 1) * 2 : t & 2);
+    }
   }
-  const uint8_t* mine = sx + min(g, p.rows - 1) * stride + t * 16;
-  const float factor = (p.factor ? ld_dep(p.factor) : 1.0f) * (NV ? 512.0f : 4.0f);
-  int parity = 0;
-  // the group's last chunk of this warp is done: its warps' sums, added in warp order
-  auto finish = [&] {
+  const uint16_t* x = p.x + static_cast<int64_t>(min(g, p.rows - 1)) * p.K + warp * 128 + t * 32;
+  const int q_step = 64 * warps;
+  const int64_t s_step = (NV ? 1024 : 512) * static_cast<int64_t>(warps);
+  float acc[R][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      part[parity][warp][j][lane] = acc[j];
-      acc[j] = 0.0f;
-    }
-    __syncwarp();
-    if (ways > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(32 * ways) : "memory");
-    // accumulator j of lane 4g + t: row g (j < 2) or its second row, token 2t + (j & 1)
-    for (int i = first * 32 + lane; i < per * p.rows; i += 32 * ways) {
-      const int token = p.act ? i >> 3 : i >> 4, row = i & (per - 1), n = group * per + row;
-      if (n >= p.N) continue;
-      const int l = (row & 7) * 4 + (token >> 1), j = (token & 1) + (row >> 3) * 2;
-      float v = 0.0f, w = 0.0f;
-      for (int s = slot * ways; s < (slot + 1) * ways; ++s) {
-        v += part[parity][s][j][l];
-        if (p.act) w += part[parity][s][j + 2][l];
-      }
-      v *= factor;
-      if (p.act) v = v * (p.act == gated::kSilu ? gated::gate<gated::kSilu>(v) : gated::gate<gated::kGelu>(v)) * (w * factor);
-      uint16_t h;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
-      p.y[static_cast<int64_t>(token) * p.N + n] = h;
-    }
-    parity ^= 1;                                           // the other half is free: all have passed this group's barrier
-    group += step;
-    c = first;
-  };
-  while (group < groups) {
+  for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
+  pdl_enter();
+  Piece w[R][2];
+  uint4 xv[4];
+  auto load = [&](int c) {                                 // the next chunk, c; a warp's pointers move on
+    if (c * 128 + t * 32 < p.K) {                          // K is a multiple of 32
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (group >= groups) break;
-      if (c < chunks) {
-        uint4 xv[4];
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (XS) xv[i] = *reinterpret_cast<const uint4*>(mine + c * 256 + i * 64);
-          else xv[i] = c * 128 + t * 32 < p.K ? in_pairs(ld_dep(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(c) * 128) + i))
-                                              : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+          w[r][h].q = ld_dep(reinterpret_cast<const uint4*>(q[r][h]));
+          w[r][h].s = ld_dep(reinterpret_cast<const uint16_t*>(s[r][h]));
         }
-        __syncwarp();                                      // the MMA's and the vote's lanes together
-        chunk_mma<NV>(acc, a[u], b[u], xv, t);
-        load(a[u], b[u]);
-        c += ways;
-      }
-      if (c >= chunks) finish();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xv[i] = ld_dep(reinterpret_cast<const uint4*>(x) + i);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r][0] = w[r][1] = {make_uint4(0, 0, 0, 0), 0u};
+      xv[0] = xv[1] = xv[2] = xv[3] = make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        q[r][h] += q_step;
+        s[r][h] += s_step;
+      }
+    x += 128 * warps;
+  };
+  if (AHEAD && warp < chunks) load(warp);
+  for (int c = warp; c < chunks; c += warps) {
+    if (!AHEAD) load(c);
+    Piece now[R][2];
+    uint4 xn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xn[i] = in_pairs(xv[i]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) now[r][0] = w[r][0], now[r][1] = w[r][1];
+    if (AHEAD && c + warps < chunks) load(c + warps);
+    __syncwarp();                                          // the MMA's and the vote's lanes together
+#pragma unroll
+    for (int r = 0; r < R; ++r) chunk_mma<NV>(acc[r], now[r][0], now[r][1], xn, t);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][r][j][lane] = acc[r][j];
+  __syncthreads();
+  // accumulator j of lane 4g + t: row g (j < 2) or its second row, token 2t + (j & 1)
+  const float factor = (p.factor ? ld_dep(p.factor) : 1.0f) * (NV ? 512.0f : 4.0f);
+  for (int i = threadIdx.x; i < R * per * p.rows; i += blockDim.x) {
+    const int token = i / (R * per), o = i - token * R * per, r = o / per, row = o - r * per, n = n0 + o;
+    if (n >= p.N) continue;
+    const int l = (row & 7) * 4 + (token >> 1), j = (token & 1) + (row >> 3) * 2;
+    float v = 0.0f, w = 0.0f;
+    for (int k = 0; k < warps; ++k) {
+      v += part[k][r][j][l];
+      if (p.act) w += part[k][r][j + 2][l];
+    }
+    v *= factor;
+    if (p.act) v = v * (p.act == gated::kSilu ? gated::gate<gated::kSilu>(v) : gated::gate<gated::kGelu>(v)) * (w * factor);
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+    p.y[static_cast<int64_t>(token) * p.N + n] = h;
   }
 }
 

@@ -27,6 +27,7 @@
 #include "gemm_fp4.cuh"
 #include "fp4_matvec.cuh"
 #include "gated.cuh"
+#include "gated_rows.cuh"
 #include "muon.cuh"
 #include "mx_cast.cuh"
 #include "rmsnorm.cuh"
@@ -65,7 +66,7 @@ struct DeviceInfo {
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
   // set up by their own first calls, so that no other call loads these kernels or fails with them
-  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false}, matvec_ready{false};
+  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false};
   int fp4_cast_blocks_per_sm = 0;
   int fp4_cast_rows_blocks_per_sm = 0;
   int pair_clusters = 0;             // co-resident clusters of the pair-tile products (one CTA per SM)
@@ -1811,34 +1812,68 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int tile_n) {
   p.has_q = c.q != nullptr;
   return st;
 }
+const int64_t kGatedFewRows = getenv("GR") ? atoi(getenv("GR")) : 16;
+template <int WF, int AF>
+void launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, cudaStream_t stream) {
+  using namespace fp8t::gated;
+  const int per = mn ? 64 : 32, chunks = mn ? (p.K + 31) / 32 : (p.K + 63) / 64;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N + per - 1) / per), static_cast<unsigned>((p.M + kRowTokens - 1) / kRowTokens), 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * std::min(kRowWarps, chunks)), 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  (void)cudaLaunchKernelEx(&cfg, mn ? k_gated_rows_mn<WF, AF> : k_gated_rows<WF, AF>, p);
+}
+fp8t_status launch_gated_rows(const fp8t_gated& d, cudaStream_t stream) {
+  fp8t::gated::RowParams p = {};
+  p.a = static_cast<const uint8_t*>(d.A);
+  p.w = static_cast<const uint8_t*>(d.B);
+  p.gu = static_cast<uint16_t*>(d.gu_bf16);
+  p.h = static_cast<uint16_t*>(d.h_bf16);
+  p.q = static_cast<uint8_t*>(d.q);
+  p.sa = d.d_a_scale_inv;
+  p.sb = d.d_b_scale_inv;
+  p.scale = d.d_scale;
+  p.amax_bits = reinterpret_cast<unsigned int*>(d.d_amax_inout);
+  p.scale_inv = d.d_scale_inv_out;
+  p.M = static_cast<int32_t>(d.M);
+  p.N = static_cast<int32_t>(d.N);
+  p.K = static_cast<int32_t>(d.K);
+  p.act = d.act;
+  p.fmt = d.q_fmt;
+  const bool mn = d.b_layout == FP8T_MN_MAJOR;
+  if (d.b_fmt == FP8T_E4M3) d.a_fmt == FP8T_E4M3 ? launch_gated_rows_as<0, 0>(p, mn, stream) : launch_gated_rows_as<0, 1>(p, mn, stream);
+  else d.a_fmt == FP8T_E4M3 ? launch_gated_rows_as<1, 0>(p, mn, stream) : launch_gated_rows_as<1, 1>(p, mn, stream);
+  return after_launch("fp8_gated_gemm launch");
+}
+
 template <class Op, class P>
 fp8t_status launch_pair(const P& p, const DeviceInfo* dev, const char* what, cudaStream_t stream) {
   const int64_t grid = 2 * std::min<int64_t>(p.total_tiles, dev->pair_clusters);
   (void)launch_pdl(fp8t::pair::k_pair_gemm<Op>, grid, fp8t::pair::kPairThreads, fp8t::pair::kPairSmemBytes<Op>, stream, 0, p);
   return after_launch(what);
 }
-fp8t_status ready_matvec(DeviceInfo* d) {
-  return once_per_device(d->matvec_ready, "fp4_matvec", [] {
-    const cudaError_t e = cudaFuncSetAttribute(fp8t::mv::k_fp4_matvec<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(fp8t::mv::kMaxXBytes));
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(fp8t::mv::k_fp4_matvec<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(fp8t::mv::kMaxXBytes));
-  });
+// Most warps, CTAs per SM and loads ahead of a matrix-vector launch.
+template <bool NV, int W, int B, bool AHEAD>
+void launch_matvec_as(const fp8t::mv::Params& p, int64_t ctas, cudaStream_t stream) {
+  const int warps = std::min(W, (p.K + 127) / 128);
+  (void)launch_pdl(fp8t::mv::k_fp4_matvec<NV, W, B, AHEAD>, ctas, 32 * warps, 0, stream, 0, p);
 }
-void launch_matvec(fp8t::mv::Params& p, bool nv, int sms, cudaStream_t stream) {
-  using namespace fp8t::mv;
-  const int64_t per = p.act ? 8 : 16, groups = (p.N + per - 1) / per;
-  static const int forced = getenv("MV") ? atoi(getenv("MV")) : 0;
-  p.ways = kWarps;
-  while (p.ways > 1 && groups * p.ways >= 4 * kWarps * static_cast<int64_t>(sms)) p.ways /= 2;
-  if (forced) p.ways = forced;
-  const int64_t grid = std::min<int64_t>((groups * p.ways + kWarps - 1) / kWarps, sms);
-  const int64_t x = p.rows * x_stride(p.K);
-  const bool fits = x <= kMaxXBytes;
-  auto* kernel = nv ? (fits ? k_fp4_matvec<true, true> : k_fp4_matvec<true, false>)
-                    : (fits ? k_fp4_matvec<false, true> : k_fp4_matvec<false, false>);
-  (void)launch_pdl(kernel, grid, 32 * kWarps, fits ? static_cast<size_t>(x) : 0, stream, 0, p);
+// As many CTAs as SMs or fewer: 16 warps each, the next chunk on its way during a chunk's arithmetic. More: 8 warps, three CTAs on
+// an SM in each other's shadow. First / second, graph replays with cold weights: 1 x 4096 x 4096 4.6 / 8.4 us, 8 x 11008 x 4096
+// 9.9 / 21.8, 4 x 4096 x 2 x 11008 25.8 / 18.3.
+template <bool NV>
+void launch_matvec_of(const fp8t::mv::Params& p, int sms, cudaStream_t stream) {
+  const int64_t per = fp8t::mv::kGroups * (p.act ? 8 : 16), ctas = (p.N + per - 1) / per;
+  if (ctas <= sms) launch_matvec_as<NV, 16, 1, true>(p, ctas, stream);
+  else launch_matvec_as<NV, 8, 3, false>(p, ctas, stream);
+}
+void launch_matvec(const fp8t::mv::Params& p, bool nv, int sms, cudaStream_t stream) {
+  nv ? launch_matvec_of<true>(p, sms, stream) : launch_matvec_of<false>(p, sms, stream);
 }
 
 constexpr CUtensorMapSwizzle kSwizzle16 = CU_TENSOR_MAP_SWIZZLE_64B, kSwizzle8 = CU_TENSOR_MAP_SWIZZLE_32B;
@@ -1857,7 +1892,9 @@ fp8t_status fp8_gated_gemm(const fp8t_gated* desc, void* stream) {
   if (st != FP8T_OK) return st;
   if (!d.gu_bf16 && !d.h_bf16 && !d.q) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm: no output asked for");
   DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != FP8T_OK || (st = ready_pair(dev)) != FP8T_OK) return st;
+  if ((st = current_device(&dev)) != FP8T_OK) return st;
+  if (d.M <= kGatedFewRows) return launch_gated_rows(d, as_stream(stream));
+  if ((st = ready_pair(dev)) != FP8T_OK) return st;
   fp8t::gated::Params p = {};
   if ((st = fill_gated(p, c, 128)) != FP8T_OK) return st;
   p.keep = d.gu_bf16 != nullptr;
@@ -1919,7 +1956,7 @@ fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream) {
     return fail(FP8T_ERR_MISALIGNED, "fp4_matvec: misaligned pointer");
   DeviceInfo* dev = nullptr;
   fp8t_status st = current_device(&dev);
-  if (st != FP8T_OK || (st = ready_matvec(dev)) != FP8T_OK) return st;
+  if (st != FP8T_OK) return st;
   fp8t::mv::Params p = {};
   p.x = static_cast<const uint16_t*>(d.x_bf16);
   p.q = static_cast<const uint8_t*>(d.q);

@@ -1,0 +1,227 @@
+// gated_rows.cuh — the gated feed-forward product of gated.cuh for few rows (tokens): h = act(G) * U, [G | U] = (A . W) * sa * sb.
+//
+// The weights' bytes bound it, once each, and a pair tile (256 rows for one token) leaves a third of the SMs with a tile more than
+// the others and streams each tile through one SM pair: 1 x 4096 -> 2 x 11008 30 us, 13.8 of them the bytes. Here the tensor
+// cores are used as mma.sync m16n8k32 on FP8: 16 rows of W, 8 gate and the 8 up rows of the same outputs, so that a lane has both;
+// 8 tokens; FP32 accumulators. A warp's lanes load the weights straight into the operand's registers; which of a lane's own k
+// goes into which place of the MMA is free as long as A is taken in the same order:
+//   W as [2N][K]  a lane holds 16 consecutive k of a row, lanes 4g .. 4g + 3 a chunk of 64: two MMAs of two words each
+//   W as [K][2N]  a lane holds 8 consecutive outputs of four rows of k: a 4 x 4 byte transpose (8 byte permutations for 16
+//                 weights) makes the words of four k, and the MMA's row g is output 8g + j of the j-th MMA
+// The warps of a CTA take the chunks of K in turn, the next one's loads on their way during a chunk's arithmetic, and add up in shared
+// memory in warp order. More than eight tokens: a CTA for each eight, which finds the weights in L2.
+#pragma once
+
+#include "gated.cuh"
+
+namespace fp8t {
+namespace gated {
+
+struct RowParams {
+  const uint8_t* a;                // [M][K]
+  const uint8_t* w;                // [2N][K], or [K][2N]
+  uint16_t* gu;                    // [M][2N], or NULL
+  uint16_t* h;                     // [M][N], or NULL
+  uint8_t* q;                      // [M][N], or NULL
+  const float* sa;
+  const float* sb;
+  const float* scale;
+  unsigned int* amax_bits;
+  float* scale_inv;
+  int32_t M, N, K, act, fmt;
+};
+constexpr int kRowWarps = 8, kRowTokens = 8;
+
+template <int WF, int AF>
+__device__ __forceinline__ void mma_fp8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+#define FP8T_MMA(W, A)                                                                                                         \
+  asm("mma.sync.aligned.m16n8k32.row.col.f32." W "." A ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};" \
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                                        \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (WF == 0 && AF == 0) FP8T_MMA("e4m3", "e4m3");
+  else if constexpr (WF == 0) FP8T_MMA("e4m3", "e5m2");
+  else if constexpr (AF == 0) FP8T_MMA("e5m2", "e4m3");
+  else FP8T_MMA("e5m2", "e5m2");
+#undef FP8T_MMA
+}
+
+// The sums of a CTA's warps for output o (of `outs`) and token, and what becomes of them. part: [warp][outs / 8][4][32 + 1] floats, of
+// accumulator j of lane 4g + t: gate (j < 2) or up of the output in place g of group `o / 8`, token 2t + (j & 1); place and group as
+// `at` gives them.
+template <class At>
+__device__ __forceinline__ void finish_rows(const RowParams& p, const float* part, int warps, int outs, int n0, int token0, At&& at) {
+  const float alpha = __fmul_rn(ld_dep(p.sa), ld_dep(p.sb)), scale = p.scale ? ld_dep(p.scale) : 1.0f;
+  const int tokens = min(kRowTokens, p.M - token0), per_warp = outs / 8 * 4 * 33;
+  float top = 0.0f;
+  for (int i = threadIdx.x; i < outs * tokens; i += blockDim.x) {
+    const int token = i / outs, o = i - token * outs, n = n0 + o;
+    if (n >= p.N) continue;
+    int place, group;
+    at(o, place, group);
+    const float* s = part + (group * 4 + (token & 1)) * 33 + place * 4 + (token >> 1);
+    float g = 0.0f, u = 0.0f;
+    for (int w = 0; w < warps; ++w, s += per_warp) {
+      g += s[0];
+      u += s[2 * 33];
+    }
+    g = __fmul_rn(g, alpha);
+    u = __fmul_rn(u, alpha);
+    const int64_t row = token0 + token;
+    if (p.gu) {
+      const uint32_t both = pack_bf16x2(g, u);
+      p.gu[row * 2 * p.N + n] = static_cast<uint16_t>(both);
+      p.gu[row * 2 * p.N + p.N + n] = static_cast<uint16_t>(both >> 16);
+    }
+    const float h = g * (p.act == kSilu ? gate<kSilu>(g) : gate<kGelu>(g)) * u;
+    top = max_abs(top, h, h);
+    if (p.h) p.h[row * p.N + n] = static_cast<uint16_t>(pack_bf16x2(h, h));
+    if (p.q) {
+      const float v = __fmul_rn(h, scale);
+      p.q[row * p.N + n] = static_cast<uint8_t>(p.fmt == 0 ? cvt_fp8x2<0>(v, v) : cvt_fp8x2<1>(v, v));
+    }
+  }
+  if (p.amax_bits) {
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7FFFFFFFu);
+    if ((threadIdx.x & 31) == 0 && most) atomicMax(p.amax_bits, most > 0x7F800000u ? 0x7FC00000u : most);
+  }
+  if (p.scale_inv && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scale_inv = __fdiv_rn(1.0f, scale);
+}
+
+// W [2N][K]: a CTA takes 32 outputs, a warp all of them for its chunks of 64 k.
+template <int WF, int AF>
+__global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows(const __grid_constant__ RowParams p) {
+  constexpr int R = 4;
+  __shared__ float part[kRowWarps][R][4][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 8 * R, token0 = blockIdx.y * kRowTokens;
+  const int chunks = (p.K + 63) / 64;
+  // outputs past N and tokens past M are loaded as the last one: what they give is not stored
+  const uint8_t* w[R][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t n = min(n0 + 8 * r + g, p.N - 1);
+    w[r][0] = p.w + n * p.K + warp * 64 + t * 16;
+    w[r][1] = w[r][0] + static_cast<int64_t>(p.N) * p.K;
+  }
+  const uint8_t* a = p.a + static_cast<int64_t>(min(token0 + g, p.M - 1)) * p.K + warp * 64 + t * 16;
+  float acc[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
+  pdl_enter();
+  uint4 wv[R][2], av;
+  auto load = [&](int c) {
+    const bool in = c * 64 + t * 16 < p.K;                 // K is a multiple of 16
+    av = in ? ld_dep(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wv[r][h] = in ? ld_dep(reinterpret_cast<const uint4*>(w[r][h])) : make_uint4(0, 0, 0, 0);
+        w[r][h] += 64 * warps;
+      }
+    a += 64 * warps;
+  };
+  if (warp < chunks) load(warp);
+  for (int c = warp; c < chunks; c += warps) {
+    uint4 now[R][2];
+    const uint4 x = av;
+#pragma unroll
+    for (int r = 0; r < R; ++r) now[r][0] = wv[r][0], now[r][1] = wv[r][1];
+    if (c + warps < chunks) load(c + warps);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mma_fp8<WF, AF>(acc[r], now[r][0].x, now[r][1].x, now[r][0].y, now[r][1].y, x.x, x.y);
+      mma_fp8<WF, AF>(acc[r], now[r][0].z, now[r][1].z, now[r][0].w, now[r][1].w, x.z, x.w);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][r][j][lane] = acc[r][j];
+  __syncthreads();
+  finish_rows(p, &part[0][0][0][0], warps, 8 * R, n0, token0, [](int o, int& place, int& group) {
+    place = o & 7;
+    group = o >> 3;
+  });
+}
+
+// Four words whose bytes are four outputs of a k each -> four words whose bytes are the four k of an output each.
+__device__ __forceinline__ void transpose4(const uint32_t (&v)[4], uint32_t (&o)[4]) {
+  const uint32_t a = __byte_perm(v[0], v[1], 0x5140), b = __byte_perm(v[2], v[3], 0x5140);   // outputs 0 and 1
+  const uint32_t c = __byte_perm(v[0], v[1], 0x7362), d = __byte_perm(v[2], v[3], 0x7362);   // 2 and 3
+  o[0] = __byte_perm(a, b, 0x5410);
+  o[1] = __byte_perm(a, b, 0x7632);
+  o[2] = __byte_perm(c, d, 0x5410);
+  o[3] = __byte_perm(c, d, 0x7632);
+}
+
+// W [K][2N]: a CTA takes 64 outputs, a warp all of them for its chunks of 32 k.
+template <int WF, int AF>
+__global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows_mn(const __grid_constant__ RowParams p) {
+  __shared__ float part[kRowWarps][8][4][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 64, token0 = blockIdx.y * kRowTokens;
+  const int chunks = (p.K + 31) / 32;
+  const int64_t pitch = 2 * static_cast<int64_t>(p.N);
+  // outputs past N (a multiple of 16, a lane's eight are all past it or none) and tokens past M are loaded as the last ones
+  const uint8_t* w = p.w + (warp * 32 + 4 * t) * pitch + min(n0 + 8 * g, p.N - 8);
+  const uint8_t* a = p.a + static_cast<int64_t>(min(token0 + g, p.M - 1)) * p.K + warp * 32 + 4 * t;
+  float acc[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+  pdl_enter();
+  uint2 wv[2][2][4];                                       // [half of the chunk][gate, up][k]
+  uint32_t av[2];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = c * 32 + 16 * h < p.K;               // K is a multiple of 16
+      av[h] = in ? ld_dep(reinterpret_cast<const uint32_t*>(a + 16 * h)) : 0u;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          wv[h][u][i] = in ? ld_dep(reinterpret_cast<const uint2*>(w + (16 * h + i) * pitch + u * p.N)) : make_uint2(0, 0);
+    }
+    w += 32 * warps * pitch;
+    a += 32 * warps;
+  };
+  if (warp < chunks) load(warp);
+  for (int c = warp; c < chunks; c += warps) {
+    uint32_t m[2][2][8];                                   // [half][gate, up][output]: four k
+    const uint32_t x0 = av[0], x1 = av[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t v[4], o[4];
+#pragma unroll
+        for (int part8 = 0; part8 < 2; ++part8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = part8 ? wv[h][u][i].y : wv[h][u][i].x;
+          transpose4(v, o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m[h][u][4 * part8 + i] = o[i];
+        }
+      }
+    if (c + warps < chunks) load(c + warps);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mma_fp8<WF, AF>(acc[j], m[0][0][j], m[0][1][j], m[1][0][j], m[1][1][j], x0, x1);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) part[warp][j][k][lane] = acc[j][k];
+  __syncthreads();
+  finish_rows(p, &part[0][0][0][0], warps, 64, n0, token0, [](int o, int& place, int& group) {
+    place = o >> 3;
+    group = o & 7;
+  });
+}
+
+}  // namespace gated
+}  // namespace fp8t

@@ -339,6 +339,11 @@ __device__ __forceinline__ uint4 ld_dep(const uint4* p) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t ld_dep(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint2 ld_dep(const uint2* p) {
   uint2 v;
   asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));

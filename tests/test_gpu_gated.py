@@ -70,6 +70,36 @@ def test_forward(cuda_lib, M, K, N, act, b_mn):
     check_forward(*forward(cuda_lib, M, K, N, act, b_mn))
 
 
+@pytest.mark.parametrize("b_mn", [False, True])
+@pytest.mark.parametrize("kinds", [(E4, E4), (E4, E5), (E5, E4), (E5, E5)])
+@pytest.mark.parametrize("M,K,N", [(1, 16, 16), (2, 48, 48), (7, 80, 64), (8, 512, 80), (9, 96, 112), (15, 1040, 144), (16, 4096, 176),
+                                   (17, 112, 96), (3, 2064, 1008)])
+def test_few_rows(cuda_lib, M, K, N, kinds, b_mn):
+    """Up to 16 rows: another kernel, with and without a transpose of W's bytes; K that ends inside a chunk, idle warps."""
+    check_forward(*forward(cuda_lib, M, K, N, "silu" if N % 32 else "gelu", b_mn, kinds=kinds))
+
+
+@pytest.mark.parametrize("outs", ["g", "h", "q", "gq", "gh"])
+def test_few_rows_outputs_alone(cuda_lib, outs):
+    for b_mn in (False, True):
+        check_forward(*forward(cuda_lib, 6, 272, 144, "silu", b_mn, outs=outs))
+
+
+def test_few_rows_nan_and_infinite_operands(cuda_lib):
+    for b_mn in (False, True):
+        M, K, N = 11, 272, 80
+        a, w = codes((M, K), E4, 5), codes((2 * N, K), E5, 6)
+        a[a.view(E4).float() == 0] = 0x38
+        w[3, 7] = 0x7C                                         # an infinite gate weight: column 3, or 0 where the gate is -inf
+        a[9, 5] = 0x7F
+        o, _ = forward(cuda_lib, M, K, N, "silu", b_mn, kinds=(E4, E5), a=a, w=w)
+        good = torch.ones(M, dtype=torch.bool, device="cuda")
+        good[9] = False
+        assert bool(o["h"][9].isnan().all()) and bool((o["q"][9] == 0x7F).all()) and o["amax"].isnan().item()
+        assert bool(o["h"][good][:, :3].isfinite().all()) and bool(o["h"][good][:, 4:].isfinite().all())
+        assert not bool(o["h"][good][:, 3].isfinite().any())
+
+
 @pytest.mark.parametrize("outs", ["g", "h", "q", "gq", "gh"])
 def test_forward_outputs_alone(cuda_lib, outs):
     check_forward(*forward(cuda_lib, 140, 256, 144, "silu", True, outs=outs))
