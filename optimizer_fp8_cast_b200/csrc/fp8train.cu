@@ -66,7 +66,7 @@ struct DeviceInfo {
   int cast_rowmajor_blocks_per_sm = 0;
   void* noalloc_scratch = nullptr;   // device address of g_adamw_noalloc_scratch
   // set up by their own first calls, so that no other call loads these kernels or fails with them
-  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false};
+  std::atomic<bool> fp4_cast_ready{false}, fp4_gemm_ready{false}, norm_backward_ready{false}, pair_ready{false}, gated_rows_ready{false};
   int fp4_cast_blocks_per_sm = 0;
   int fp4_cast_rows_blocks_per_sm = 0;
   int pair_clusters = 0;             // co-resident clusters of the pair-tile products (one CTA per SM)
@@ -1814,19 +1814,42 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int tile_n) {
 }
 const int64_t kGatedFewRows = getenv("GR") ? atoi(getenv("GR")) : 16;
 template <int WF, int AF>
-void launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, cudaStream_t stream) {
+fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, cudaStream_t stream) {
   using namespace fp8t::gated;
   const int per = mn ? 64 : 32, chunks = mn ? (p.K + 31) / 32 : (p.K + 63) / 64;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.N + per - 1) / per), static_cast<unsigned>((p.M + kRowTokens - 1) / kRowTokens), 1);
   cfg.blockDim = dim3(static_cast<unsigned>(32 * std::min(kRowWarps, chunks)), 1, 1);
+  cfg.dynamicSmemBytes = mn ? kRowSmemBytes : 0;
   cfg.stream = stream;
   cudaLaunchAttribute early[1];
   early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = early;
   cfg.numAttrs = 1;
-  (void)cudaLaunchKernelEx(&cfg, mn ? k_gated_rows_mn<WF, AF> : k_gated_rows<WF, AF>, p);
+  if (!mn) {
+    (void)cudaLaunchKernelEx(&cfg, k_gated_rows<WF, AF>, p);
+    return FP8T_OK;
+  }
+  RowMnParams P = {};
+  P.p = p;
+  const fp8t_status st = encode_2d(&P.w, p.w, p.K, 2 * static_cast<int64_t>(p.N), 2 * static_cast<int64_t>(p.N), 1, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st == FP8T_OK) (void)cudaLaunchKernelEx(&cfg, k_gated_rows_mn<WF, AF>, P);
+  return st;
+}
+template <int WF, int AF>
+cudaError_t allow_gated_rows_smem() {
+  return cudaFuncSetAttribute(fp8t::gated::k_gated_rows_mn<WF, AF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fp8t::gated::kRowSmemBytes);
+}
+fp8t_status ready_gated_rows(DeviceInfo* d) {
+  return once_per_device(d->gated_rows_ready, "fp8_gated_gemm", [] {
+    cudaError_t e;
+    if ((e = allow_gated_rows_smem<0, 0>()) != cudaSuccess || (e = allow_gated_rows_smem<0, 1>()) != cudaSuccess ||
+        (e = allow_gated_rows_smem<1, 0>()) != cudaSuccess)
+      return e;
+    return allow_gated_rows_smem<1, 1>();
+  });
 }
 fp8t_status launch_gated_rows(const fp8t_gated& d, cudaStream_t stream) {
   fp8t::gated::RowParams p = {};
@@ -1845,10 +1868,10 @@ fp8t_status launch_gated_rows(const fp8t_gated& d, cudaStream_t stream) {
   p.K = static_cast<int32_t>(d.K);
   p.act = d.act;
   p.fmt = d.q_fmt;
-  const bool mn = d.b_layout == FP8T_MN_MAJOR;
-  if (d.b_fmt == FP8T_E4M3) d.a_fmt == FP8T_E4M3 ? launch_gated_rows_as<0, 0>(p, mn, stream) : launch_gated_rows_as<0, 1>(p, mn, stream);
-  else d.a_fmt == FP8T_E4M3 ? launch_gated_rows_as<1, 0>(p, mn, stream) : launch_gated_rows_as<1, 1>(p, mn, stream);
-  return after_launch("fp8_gated_gemm launch");
+  const bool mn = d.b_layout == FP8T_MN_MAJOR, w5 = d.b_fmt == FP8T_E5M2, a5 = d.a_fmt == FP8T_E5M2;
+  const fp8t_status st = w5 ? (a5 ? launch_gated_rows_as<1, 1>(p, mn, stream) : launch_gated_rows_as<1, 0>(p, mn, stream))
+                            : (a5 ? launch_gated_rows_as<0, 1>(p, mn, stream) : launch_gated_rows_as<0, 0>(p, mn, stream));
+  return st != FP8T_OK ? st : after_launch("fp8_gated_gemm launch");
 }
 
 template <class Op, class P>
@@ -1893,7 +1916,7 @@ fp8t_status fp8_gated_gemm(const fp8t_gated* desc, void* stream) {
   if (!d.gu_bf16 && !d.h_bf16 && !d.q) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm: no output asked for");
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != FP8T_OK) return st;
-  if (d.M <= kGatedFewRows) return launch_gated_rows(d, as_stream(stream));
+  if (d.M <= kGatedFewRows) return (st = ready_gated_rows(dev)) != FP8T_OK ? st : launch_gated_rows(d, as_stream(stream));
   if ((st = ready_pair(dev)) != FP8T_OK) return st;
   fp8t::gated::Params p = {};
   if ((st = fill_gated(p, c, 128)) != FP8T_OK) return st;

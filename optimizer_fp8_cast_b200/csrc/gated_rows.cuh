@@ -157,67 +157,112 @@ __device__ __forceinline__ void transpose4(const uint32_t (&v)[4], uint32_t (&o)
   o[3] = __byte_perm(c, d, 0x7632);
 }
 
-// W [K][2N]: a CTA takes 64 outputs, a warp all of them for its chunks of 32 k.
+// W [K][2N]: a CTA takes 64 outputs, a warp all of them for its chunks of 32 k. Each warp keeps kRing chunks on their way into
+// shared memory (two boxes of 32 k x 64 outputs, 64-byte swizzle) and waits for them alone; 96 KB of a CTA are in flight where
+// loads into registers held 32 (25.6 us for 1 x 4096 -> 2 x 11008).
+constexpr int kRing = 3, kRowChunkBytes = 2 * 32 * 64;
+constexpr int kRowRingBytes = kRowWarps * kRing * kRowChunkBytes;
+constexpr int kRowSmemBytes = kRowRingBytes + 1024;
+static_assert(kRowRingBytes >= kRowWarps * 8 * 4 * 33 * 4, "the warps' sums lie in the ring");
+struct alignas(64) RowMnParams {
+  CUtensorMap w;
+  RowParams p;
+};
 template <int WF, int AF>
-__global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows_mn(const __grid_constant__ RowParams p) {
-  __shared__ float part[kRowWarps][8][4][33];
+__global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows_mn(const __grid_constant__ RowMnParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t landed[kRowWarps][kRing];
+  __shared__ int given_up;
+  const RowParams& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * 64, token0 = blockIdx.y * kRowTokens;
   const int chunks = (p.K + 31) / 32;
-  const int64_t pitch = 2 * static_cast<int64_t>(p.N);
-  // outputs past N (a multiple of 16, a lane's eight are all past it or none) and tokens past M are loaded as the last ones
-  const uint8_t* w = p.w + (warp * 32 + 4 * t) * pitch + min(n0 + 8 * g, p.N - 8);
-  const uint8_t* a = p.a + static_cast<int64_t>(min(token0 + g, p.M - 1)) * p.K + warp * 32 + 4 * t;
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < warps; ++w)
+      for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&landed[w][s]), 1);
+    given_up = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const uint64_t limit = wait_limit_ns();
+  const bool expire = expire_mode() == kExpireAll;
+  pdl_enter();
+  uint8_t* mine = ring + warp * kRing * kRowChunkBytes;
+  // boxes past K or 2N read zeros there; gate columns past N are the up projection's: what they give is not stored
+  auto fetch = [&](int c, int s) {
+    if (lane == 0 && c < chunks) {
+      const uint32_t bar = smem_u32(&landed[warp][s]), dst = smem_u32(mine + s * kRowChunkBytes);
+      mbar_arrive_expect_tx(bar, kRowChunkBytes);
+      tma_load_2d(dst, &P.w, n0, c * 32, bar);
+      tma_load_2d(dst + kRowChunkBytes / 2, &P.w, p.N + n0, c * 32, bar);
+    }
+  };
+  for (int s = 0; s < kRing; ++s) fetch(warp + s * warps, s);
+  // tokens past M are loaded as the last one; K is a multiple of 16
+  const uint8_t* a = p.a + static_cast<int64_t>(min(token0 + g, p.M - 1)) * p.K + 4 * t;
+  auto x_of = [&](int c, int h) {
+    const int k = c * 32 + 16 * h;
+    return k < p.K ? ld_dep(reinterpret_cast<const uint32_t*>(a + k)) : 0u;
+  };
   float acc[8][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-  pdl_enter();
-  uint2 wv[2][2][4];                                       // [half of the chunk][gate, up][k]
-  uint32_t av[2];
-  auto load = [&](int c) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = c * 32 + 16 * h < p.K;               // K is a multiple of 16
-      av[h] = in ? ld_dep(reinterpret_cast<const uint32_t*>(a + 16 * h)) : 0u;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          wv[h][u][i] = in ? ld_dep(reinterpret_cast<const uint2*>(w + (16 * h + i) * pitch + u * p.N)) : make_uint2(0, 0);
-    }
-    w += 32 * warps * pitch;
-    a += 32 * warps;
-  };
-  if (warp < chunks) load(warp);
+  uint32_t x0 = x_of(warp, 0), x1 = x_of(warp, 1);
+  int s = 0, parity = 0;
   for (int c = warp; c < chunks; c += warps) {
-    uint32_t m[2][2][8];                                   // [half][gate, up][output]: four k
-    const uint32_t x0 = av[0], x1 = av[1];
+    const uint32_t b0 = x0, b1 = x1;
+    if (c + warps < chunks) x0 = x_of(c + warps, 0), x1 = x_of(c + warps, 1);
+    if (!warp_wait(smem_u32(&landed[warp][s]), parity, limit, expire)) {
+      if (lane == 0) record_error(kErrTimeout);
+      given_up = 1;
+      break;
+    }
+    uint2 v[2][2][4];                                      // [half of the chunk][gate, up][k]
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t v[4], o[4];
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int part8 = 0; part8 < 2; ++part8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = part8 ? wv[h][u][i].y : wv[h][u][i].x;
-          transpose4(v, o);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m[h][u][4 * part8 + i] = o[i];
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * h + 4 * t + i;
+          v[h][u][i] = *reinterpret_cast<const uint2*>(mine + s * kRowChunkBytes + u * (kRowChunkBytes / 2) + row * 64 +
+                                                       (((g >> 1) ^ ((row >> 1) & 3)) * 16) + (g & 1) * 8);
         }
-      }
-    if (c + warps < chunks) load(c + warps);
-    __syncwarp();
+    __syncwarp();                                          // all have read the slot, and the MMA's lanes come together
+    fetch(c + kRing * warps, s);
+    if (++s == kRing) s = 0, parity ^= 1;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mma_fp8<WF, AF>(acc[j], m[0][0][j], m[0][1][j], m[1][0][j], m[1][1][j], x0, x1);
+    for (int q = 0; q < 2; ++q) {                          // four outputs at a time
+      uint32_t m[2][2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t in[4] = {q ? v[h][u][0].y : v[h][u][0].x, q ? v[h][u][1].y : v[h][u][1].x,
+                                  q ? v[h][u][2].y : v[h][u][2].x, q ? v[h][u][3].y : v[h][u][3].x};
+          transpose4(in, m[h][u]);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma_fp8<WF, AF>(acc[4 * q + j], m[0][0][j], m[0][1][j], m[1][0][j], m[1][1][j], b0, b1);
+    }
   }
+  __syncthreads();
+  if (given_up) {                                          // loads may still be in flight
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kSettleNs) {
+    }
+    if (threadIdx.x == 0 && p.amax_bits) atomicMax(p.amax_bits, 0x7FC00000u);
+    return;
+  }
+  float* part = reinterpret_cast<float*>(ring);            // [warp][8][4][33]
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) part[warp][j][k][lane] = acc[j][k];
+    for (int k = 0; k < 4; ++k) part[((warp * 8 + j) * 4 + k) * 33 + lane] = acc[j][k];
   __syncthreads();
-  finish_rows(p, &part[0][0][0][0], warps, 64, n0, token0, [](int o, int& place, int& group) {
+  finish_rows(p, part, warps, 64, n0, token0, [](int o, int& place, int& group) {
     place = o >> 3;
     group = o & 7;
   });
