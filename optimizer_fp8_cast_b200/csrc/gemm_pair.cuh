@@ -396,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ok = Op::epilogue(g, w, ph, k, o, row0, half, t_base, [&] {   // called once, behind the last TMEM load
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->acc_empty[acc]), 0));
+          if (lane == 0) mbar_arrive_cluster_tmem(mapa_shared(smem_u32(&S->acc_empty[acc]), 0));
         }, [&] { ahead(tile + n_clusters); });             // called once, when the last chunk has been read
         if (!ok) {
           *abort_flag = 1;
