@@ -1722,7 +1722,8 @@ fp8t_status ready_pair(DeviceInfo* d) {
     if ((e = allow_pair_smem<gated::Forward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Forward<kGelu>>()) != cudaSuccess ||
         (e = allow_pair_smem<gated::Backward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Backward<kGelu>>()) != cudaSuccess ||
         (e = allow_pair_smem<muon::Steps<4>>()) != cudaSuccess ||
-        (e = allow_pair_smem<muon::Steps<muon::kMaxMatrices>>()) != cudaSuccess)
+        (e = allow_pair_smem<muon::Steps<muon::kMaxMatrices>>()) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(muon::k_muon_small, cudaFuncAttributeMaxDynamicSharedMemorySize, muon::kSmallSmemBytes)) != cudaSuccess)
       return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (d->sms / 2), 1, 1);
@@ -2062,25 +2063,18 @@ fp8t_status fill_muon_matrix(fp8t::muon::Matrix& m, const MuonSizes& z, char* at
   x_tiles += static_cast<int32_t>((z.rows + 255) / 256 * ((z.cols + 255) / 256));
   return st;
 }
+// The steps of the table's matrices `which`, grid-wide.
 template <int NP>
-fp8t_status newton_schulz(const std::vector<MuonSizes>& z, char* copies, int32_t steps, const fp8t::pair::Grid& grid,
-                          const DeviceInfo* dev, cudaStream_t stream) {
+fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<char*>& at, const std::vector<int32_t>& which, int32_t steps,
+                          const fp8t::pair::Grid& grid, const DeviceInfo* dev, cudaStream_t stream) {
   using Op = fp8t::muon::Steps<NP>;
   static thread_local fp8t::muon::Group<NP> g;
-  g.n = static_cast<int32_t>(z.size());
+  g.n = static_cast<int32_t>(which.size());
   g.steps = steps;
   g.sym_tiles = g.x_tiles = 0;
   g.grid = grid;
-  // the longest first: a cluster takes every n-th tile, and the phase of A ends with the shortest (its K is the longer side)
-  std::vector<int32_t> order(z.size());
-  std::vector<char*> at(z.size());
-  for (int32_t k = 0; k < g.n; copies += z[k].bytes(), ++k) {
-    order[k] = k;
-    at[k] = copies;
-  }
-  std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return std::max(z[a].rows, z[a].cols) > std::max(z[b].rows, z[b].cols); });
   for (int32_t k = 0; k < g.n; ++k) {
-    const fp8t_status st = fill_muon_matrix(g.m[k], z[order[k]], at[order[k]], g.sym_tiles, g.x_tiles);
+    const fp8t_status st = fill_muon_matrix(g.m[k], z[which[k]], at[which[k]], g.sym_tiles, g.x_tiles);
     if (st != FP8T_OK) return st;
   }
   // its CTAs wait for one another: a cooperative launch has them all resident or fails
@@ -2096,6 +2090,45 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, char* copies, int32_t
   cfg.numAttrs = 1;
   (void)cudaLaunchKernelEx(&cfg, fp8t::pair::k_pair_gemm<Op>, g);
   return after_launch("Newton-Schulz products launch");
+}
+// The same for matrices of at most 256 x 256, a CTA pair each.
+fp8t_status newton_schulz_small(const std::vector<MuonSizes>& z, const std::vector<char*>& at, const std::vector<int32_t>& which,
+                                int32_t steps, int32_t* expired, cudaStream_t stream) {
+  using namespace fp8t::muon;
+  static thread_local SmallGroup g;
+  g.steps = steps;
+  g.expired = expired;
+  for (size_t k = 0; k < which.size(); ++k) {
+    const MuonSizes& s = z[which[k]];
+    SmallMatrix& m = g.m[k];
+    char* x = at[which[k]];
+    const fp8t_status st = encode_2d(&m.x, x, s.rows, s.cols, s.pitch_x, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != FP8T_OK) return st;
+    m.out = reinterpret_cast<uint16_t*>(x + (steps & 1 ? s.x : 0));
+    m.rows = static_cast<int32_t>(s.rows);
+    m.cols = static_cast<int32_t>(s.cols);
+    m.pitch = static_cast<int32_t>(s.pitch_x);
+  }
+  (void)launch_pdl(k_muon_small, 2 * static_cast<int64_t>(which.size()), kSmallThreads, kSmallSmemBytes, stream, 0, g);
+  return after_launch("Newton-Schulz products launch");
+}
+// A table's steps: the longest matrices first, for a cluster takes every n-th tile and the phase of A should end with the
+// shortest (its K is the longer side).
+fp8t_status newton_schulz_table(const std::vector<MuonSizes>& z, char* copies, int32_t steps, const fp8t::pair::Grid& grid,
+                                const DeviceInfo* dev, cudaStream_t stream) {
+  std::vector<char*> at(z.size());
+  std::vector<int32_t> large, small;
+  for (size_t k = 0; k < z.size(); copies += z[k].bytes(), ++k) {
+    at[k] = copies;
+    (std::max(z[k].rows, z[k].cols) <= fp8t::muon::kSmallSide ? small : large).push_back(static_cast<int32_t>(k));
+  }
+  std::stable_sort(large.begin(), large.end(), [&](int32_t a, int32_t b) { return std::max(z[a].rows, z[a].cols) > std::max(z[b].rows, z[b].cols); });
+  fp8t_status st = FP8T_OK;
+  if (!large.empty())
+    st = large.size() <= 4 ? newton_schulz<4>(z, at, large, steps, grid, dev, stream)
+                           : newton_schulz<fp8t::muon::kMaxMatrices>(z, at, large, steps, grid, dev, stream);
+  if (st == FP8T_OK && !small.empty()) st = newton_schulz_small(z, at, small, steps, grid.expired, stream);
+  return st;
 }
 
 // Both calls; `get(i)` gives the kernels' view of matrix i (x, chunk_start and pitch are filled here).
@@ -2158,8 +2191,7 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
     if (n > kMaxMatrices) table(b0);
     (void)launch_pdl(k_muon_scale<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
     if ((st = after_launch(name)) != FP8T_OK) return st;
-    st = t.n <= 4 ? newton_schulz<4>(sizes, copies, steps, t.grid, dev, stream)
-                  : newton_schulz<kMaxMatrices>(sizes, copies, steps, t.grid, dev, stream);
+    st = newton_schulz_table(sizes, copies, steps, t.grid, dev, stream);
     if (st != FP8T_OK) return st;
     if (steps & 1)                 // the result is in the second copy
       for (int32_t i = 0; i < t.n; ++i) t.t[i].x += sizes[i].x / 2;

@@ -173,6 +173,203 @@ struct Steps {
   }
 };
 
+// ------------------------------------------------------------------ small matrices
+// Up to 256 x 256: one CTA pair keeps a matrix in shared memory over all steps. The phases of the grid-wide form have little to do
+// there (6.4 us each, of which the MMAs are one: barrier, first loads, stores); here the epilogue writes the next phase's
+// operand where the tensor cores read it, and a phase ends with the pair's own barrier (256 x 256 97 -> 48 us a call).
+// CTA r holds (FP16, 128-byte swizzle, zeros past the matrix):
+//   xk   rows 128r .. of X, K-major: four blocks of 64 columns
+//   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns
+//   s    rows 128r .. of A, then of B, K-major
+// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, the other CTA's columns of xm through
+// distributed shared memory.
+constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
+constexpr int kSmallThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 256;
+struct alignas(64) SmallMatrix {
+  CUtensorMap x;                   // boxes of 64 rows x 64 values
+  uint16_t* out;
+  int32_t rows, cols, pitch, pad;
+};
+struct alignas(64) SmallGroup {
+  SmallMatrix m[kMaxMatrices];     // a CTA pair each
+  int32_t steps;
+  int32_t* expired;
+};
+struct SmallSmem {
+  uint64_t loaded;                 // X has landed
+  uint64_t acc_full;               // both CTAs: a phase's MMAs have completed
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int given_up;                    // 2 + the phase in which a wait expired (1: X did not land), 0: none
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_muon_small(const __grid_constant__ SmallGroup g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* xk = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *xm = xk + kSmallOperand, *sq = xm + kSmallOperand;
+  SmallSmem* S = reinterpret_cast<SmallSmem*>(sq + kSmallOperand);
+  volatile int* given_up = &S->given_up;
+  const SmallMatrix& M = g.m[blockIdx.x >> 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool wide = M.cols >= M.rows;
+  const int side = wide ? M.rows : M.cols, lengthwise = wide ? M.cols : M.rows;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&S->loaded), 1);
+    mbar_init(smem_u32(&S->acc_full), 1);
+    mbar_init(smem_u32(&S->mma_done), 1);
+    *given_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&S->tmem_base), kAccCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  const uint64_t limit = wait_limit_ns();
+  const int expire = expire_mode();
+  const bool expire_main = expire == kExpireAll, expire_epi = expire == kExpireAll || expire == kExpireGemmEpilogue;
+  pdl_enter();
+  // Both CTAs give up together: the word is written in both before a barrier that all threads of both pass, and names the
+  // phase, so that every thread leaves behind the same barrier however late it reads the word.
+  auto give_up = [&](int when) {
+    if (lane == 0) {
+      record_error(kErrTimeout);
+      for (uint32_t r = 0; r < 2; ++r)
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S->given_up), r)), "r"(when) : "memory");
+    }
+    __syncwarp();
+  };
+  auto going_on = [&](int when) {
+    const int v = *given_up;
+    return v == 0 || v > when;
+  };
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_arrive_expect_tx(smem_u32(&S->loaded), 2 * kSmallOperand);
+      const int at = static_cast<int>(rank) * kHalf;
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t to = smem_u32(xk + b * kSmallBlock + i * 8192);
+          tma_load_2d(to, &M.x, b * 64, at + i * 64, smem_u32(&S->loaded));
+          tma_load_2d(to + kSmallOperand, &M.x, at + i * 64, b * 64, smem_u32(&S->loaded));
+        }
+    }
+    __syncwarp();
+    if (!warp_wait(smem_u32(&S->loaded), 0, limit, expire_main)) give_up(1);
+  }
+  cluster_sync();                                          // X is there in both CTAs
+  bool alive = going_on(1);
+  for (int ph = 0; ph < 3 * g.steps && alive; ++ph) {
+    const int phase = ph % 3;
+    if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer
+      const uint32_t k0 = smem_u32(xk), m0 = smem_u32(xm), s0 = smem_u32(sq);
+      const bool a_mn = phase == 0 && !wide, b_mn = phase == 0 ? !wide : phase == 2 && wide;
+      const uint32_t a0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || wide ? s0 : k0;
+      const uint32_t b0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || !wide ? s0 : m0;
+      const uint32_t idesc = make_idesc_f16(a_mn, b_mn);
+      const int blocks = ((phase == 0 ? lengthwise : side) + 63) / 64;
+      tc_fence_after();
+      if (elect_one()) {
+        for (int b = 0; b < blocks; ++b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock;
+            tc_mma_f16_pair(tmem, a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
+                            b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc, (b | k) != 0 ? 1u : 0u);
+          }
+        tc_commit_pair_mc(smem_u32(&S->acc_full), 0x3);
+      }
+      __syncwarp();
+    } else if (warp >= 2) {
+      // ---------------- epilogue: what becomes the next phase's operand
+      using namespace blk;
+      const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
+      const int all = static_cast<int>(rank) * kHalf + row;                            // of the matrix
+      if (!warp_wait(smem_u32(&S->acc_full), ph & 1, limit, expire_epi)) {
+        give_up(2 + ph);
+      } else {
+        tc_fence_after();
+        const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
+        const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
+        const bool last = ph + 1 == 3 * g.steps;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          const int n = half * 128 + s * 32;
+          uint8_t* line = (phase == 2 ? xk : sq) + (n >> 6) * kSmallBlock + row * 128;  // K-major place of (row, n ..)
+          const int piece = (n >> 3) & 7;
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
+          tmem_ld_wait();
+          tmem_reg_fence(r);
+          uint4 q[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint4 was = make_uint4(0, 0, 0, 0);
+            uint4* place = reinterpret_cast<uint4*>(line + ((piece + p) ^ (row & 7)) * 16);
+            if (phase == 1) was = *place;                  // A, which B takes the place of
+            const uint32_t h[4] = {was.x, was.y, was.z, was.w};
+            uint32_t out[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = 8 * p + 2 * j;
+              f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
+              if (phase == 1) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+                v = fma2(be, blk::pair(f.x, f.y), v);
+                v = add2(v, blk::pair(all == n + c ? kA * kFactor : 0.0f, all == n + c + 1 ? kA * kFactor : 0.0f));
+              }
+              out[j] = pack_f16x2(lo(v), hi(v));
+            }
+            q[p] = make_uint4(out[0], out[1], out[2], out[3]);
+            *place = q[p];
+          }
+          if (phase == 2 && !last) {                       // and X's columns: those of the CTA that holds them
+            const int k = all & 63;
+            const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128);
+            const uint32_t there = mapa_shared(to, half);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              st_cluster_v4(there + ((piece + p) ^ (k & 7)) * 16, q[p].x, q[p].y, q[p].z, q[p].w);
+          }
+          if (last && all < M.rows) {
+            uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_all();                           // for the tensor cores of both CTAs
+      }
+    }
+    cluster_sync();
+    alive = going_on(2 + ph);
+  }
+  if (warp == 1 && rank == 0) {                            // MMAs may be in flight when a wait expired
+    if (elect_one()) tc_commit_pair(smem_u32(&S->mma_done));
+    __syncwarp();
+    mbar_wait(smem_u32(&S->mma_done), 0, kDrainLimitNs);
+  }
+  if (!alive && threadIdx.x == 0) {
+    atomicExch(g.expired, 1);
+    const uint64_t t0 = globaltimer_ns();                  // loads too
+    while (globaltimer_ns() - t0 < kSettleNs) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();                 // neither CTA leaves while the other may still write to it or the MMAs read it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kAccCols);
+}
+
 // ------------------------------------------------------------------ the passes over the elements
 enum : int { kMuon = 0, kOrthBf16 = 1, kOrthF32 = 2 };
 struct Tensor {

@@ -209,10 +209,24 @@ def test_another_stream_allocates_there(cuda_lib):
     assert torch.equal(s["p"][0], t["p"][0])
 
 
+@pytest.mark.parametrize("rows,cols", [(2, 256), (256, 2), (64, 64), (65, 129), (129, 65), (128, 256), (256, 128), (255, 255), (256, 256),
+                                       (200, 256), (256, 257), (257, 3)])
+def test_one_pair_holds_up_to_256(cuda_lib, rows, cols):
+    """The form that keeps a matrix in shared memory, at the edges of its blocks, and its neighbours past them."""
+    for steps in (1, 2, 5):
+        x = matrix(rows, cols, 3 * rows + cols + steps)
+        out, check = guarded(torch.zeros_like(x, dtype=torch.bfloat16))
+        cuda_lib.muon_orthogonalize([x], [out], steps=steps)
+        cuda_lib.fp8t_check_device_error()
+        check()
+        check_orth(out, x, steps)
+
+
+@pytest.mark.parametrize("rows,cols", [(600, 700), (200, 130)])
 @pytest.mark.parametrize("mode", [1, 2])
-def test_waits_expire_and_context_survives(cuda_lib, mode):
+def test_waits_expire_and_context_survives(cuda_lib, mode, rows, cols):
     """A product that gave up leaves p and w alone; the next step is right."""
-    s, _ = state([(600, 700)])
+    s, _ = state([(rows, cols)])
     old = {k: [t.clone() for t in v] for k, v in s.items()}
     skipped = torch.zeros(1, dtype=torch.int32, device="cuda")
     _run_expired(cuda_lib, mode, lambda: step(cuda_lib, s, skipped=skipped))
