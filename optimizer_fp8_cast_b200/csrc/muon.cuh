@@ -184,7 +184,7 @@ struct Steps {
 // wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, the other CTA's columns of xm through
 // distributed shared memory.
 constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
-constexpr int kSmallThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kSmallThreads = 64 + 32 * 16;               // 16 epilogue warps: a TMEM lane quarter and 64 columns each
 constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 256;
 struct alignas(64) SmallMatrix {
   CUtensorMap x;                   // boxes of 64 rows x 64 values
@@ -289,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     } else if (warp >= 2) {
       // ---------------- epilogue: what becomes the next phase's operand
       using namespace blk;
-      const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
+      const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
       const int all = static_cast<int>(rank) * kHalf + row;                            // of the matrix
       if (!warp_wait(smem_u32(&S->acc_full), ph & 1, limit, expire_epi)) {
         give_up(2 + ph);
@@ -298,11 +298,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
         const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
         const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
         const bool last = ph + 1 == 3 * g.steps;
-#pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
-          const int n = half * 128 + s * 32;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int n = part * 64 + s * 32;
           uint8_t* line = (phase == 2 ? xk : sq) + (n >> 6) * kSmallBlock + row * 128;  // K-major place of (row, n ..)
           const int piece = (n >> 3) & 7;
+          const bool diagonal = all - lane == n;           // it runs through these 32 columns
           uint32_t r[32];
           __syncwarp();
           tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
@@ -323,7 +324,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
               if (phase == 1) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
                 v = fma2(be, blk::pair(f.x, f.y), v);
-                v = add2(v, blk::pair(all == n + c ? kA * kFactor : 0.0f, all == n + c + 1 ? kA * kFactor : 0.0f));
+                if (diagonal)
+                  v = add2(v, blk::pair(lane == c ? kA * kFactor : 0.0f, lane == c + 1 ? kA * kFactor : 0.0f));
               }
               out[j] = pack_f16x2(lo(v), hi(v));
             }
@@ -333,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
           if (phase == 2 && !last) {                       // and X's columns: those of the CTA that holds them
             const int k = all & 63;
             const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128);
-            const uint32_t there = mapa_shared(to, half);
+            const uint32_t there = mapa_shared(to, n >> 7);
 #pragma unroll
             for (int p = 0; p < 4; ++p)
               st_cluster_v4(there + ((piece + p) ^ (k & 7)) * 16, q[p].x, q[p].y, q[p].z, q[p].w);
