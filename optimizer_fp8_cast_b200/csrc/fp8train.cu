@@ -2043,8 +2043,15 @@ struct MuonPlan {
   size_t bytes() const { return norms + partials + copies; }
 };
 
-// A matrix's tensor maps and tiles. Only the tiles of A and B on and above the diagonal count.
-fp8t_status fill_muon_matrix(fp8t::muon::Matrix& m, const MuonSizes& z, char* at, int32_t& sym_tiles, int32_t& x_tiles) {
+// Tiles of A and of X in columns of tile_n; half: only those of A on and above the diagonal.
+int64_t muon_sym_tiles(const MuonSizes& z, int tile_n, bool half) {
+  const int64_t m = (z.side + 255) / 256;
+  return half ? m * (m + 1) / 2 : m * ((z.side + tile_n - 1) / tile_n);
+}
+int64_t muon_x_tiles(const MuonSizes& z, int tile_n) { return (z.rows + 255) / 256 * ((z.cols + tile_n - 1) / tile_n); }
+// A matrix's tensor maps and tiles.
+fp8t_status fill_muon_matrix(fp8t::muon::Matrix& m, const MuonSizes& z, char* at, int tile_n, bool half, int32_t& sym_tiles,
+                             int32_t& x_tiles) {
   fp8t_status st = FP8T_OK;
   for (int i = 0; i < 2; ++i) {
     char *x = at + i * z.x, *s = at + 2 * z.x + i * z.s;
@@ -2058,9 +2065,8 @@ fp8t_status fill_muon_matrix(fp8t::muon::Matrix& m, const MuonSizes& z, char* at
   m.cols = static_cast<int32_t>(z.cols);
   m.sym_start = sym_tiles;
   m.x_start = x_tiles;
-  const int32_t side = static_cast<int32_t>((z.side + 255) / 256);
-  sym_tiles += side * (side + 1) / 2;
-  x_tiles += static_cast<int32_t>((z.rows + 255) / 256 * ((z.cols + 255) / 256));
+  sym_tiles += static_cast<int32_t>(muon_sym_tiles(z, tile_n, half));
+  x_tiles += static_cast<int32_t>(muon_x_tiles(z, tile_n));
   return st;
 }
 // The steps of the table's matrices `which`, grid-wide.
@@ -2073,8 +2079,17 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<cha
   g.steps = steps;
   g.sym_tiles = g.x_tiles = 0;
   g.grid = grid;
+  // Where all tiles of A fit the clusters at once, computing both halves spares the transposed stores; where tiles half as wide
+  // do, a phase has half the columns to compute and to store (1237 x 611 190 / 141 us).
+  int64_t whole = 0, narrow = 0;
+  for (int32_t k : which) {
+    whole += muon_sym_tiles(z[k], 256, false);
+    narrow += std::max(muon_sym_tiles(z[k], 128, false), muon_x_tiles(z[k], 128));
+  }
+  g.tile_n = narrow <= dev->pair_clusters ? 128 : 256;
+  g.whole = whole <= dev->pair_clusters ? 1 : 0;
   for (int32_t k = 0; k < g.n; ++k) {
-    const fp8t_status st = fill_muon_matrix(g.m[k], z[which[k]], at[which[k]], g.sym_tiles, g.x_tiles);
+    const fp8t_status st = fill_muon_matrix(g.m[k], z[which[k]], at[which[k]], g.tile_n, !g.whole, g.sym_tiles, g.x_tiles);
     if (st != FP8T_OK) return st;
   }
   // its CTAs wait for one another: a cooperative launch has them all resident or fails

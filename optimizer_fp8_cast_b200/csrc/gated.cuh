@@ -146,6 +146,7 @@ struct Base {
     w.b = &g.b;
     w.a_row = w.mt * kBM + rank * kHalf;
     w.b_row = w.nt * b_step + rank * b_other;
+    w.half_n = kHalf;
     w.num_kb = g.num_kb;
     w.a_mn = 0;
     w.b_mn = g.b_mn;

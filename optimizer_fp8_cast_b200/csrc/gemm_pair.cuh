@@ -66,8 +66,10 @@ __device__ __forceinline__ uint64_t make_sw128_desc_mn16(uint32_t saddr) {
   d |= static_cast<uint64_t>(2) << 61;                       // 128-byte swizzle
   return d;
 }
-// FP32 accumulator, FP16 operands, M = 256 (pair), N = 256.
-__host__ __device__ constexpr uint32_t make_idesc_f16(int a_mn, int b_mn) { return make_idesc(0, 0, a_mn, b_mn); }
+// FP32 accumulator, FP16 operands, M = 256 (pair), N = 256 or n.
+__host__ __device__ constexpr uint32_t make_idesc_f16(int a_mn, int b_mn, int n = kBN) {
+  return make_idesc(0, 0, a_mn, b_mn) - (static_cast<uint32_t>((kBN - n) >> 3) << 17);
+}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -157,6 +159,7 @@ struct Work {
   const CUtensorMap *a, *b;
   int a_row, b_row;                // first row of A and of B that this CTA holds
   int mt, nt;                      // row and column tile
+  int half_n;                      // rows of B that each CTA holds: 128, or 64 (FP16) for tiles of 128 columns
   int num_kb;
   int a_mn, b_mn;                  // 1: operand stored MN-major
   uint32_t idesc;
@@ -276,14 +279,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           if (one) {
             const uint32_t full_leader = mapa_shared(smem_u32(&S->full[s]), 0);
-            if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), kPairTxBytes);
+            const bool second = Op::kF16 && w.half_n > 64;   // B's second box of 64
+            if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), !Op::kF16 || second ? kPairTxBytes : kPairTxBytes - 2 * 8192);
             const uint32_t a_dst = smem_u32(smem + s * kStageBytes), b_dst = a_dst + kABytes;
             const int k0 = kb * kElems;
             tma_load_2d_pair(a_dst, w.a, w.a_mn ? w.a_row : k0, w.a_mn ? k0 : w.a_row, full_leader);
             if (Op::kF16)
               tma_load_2d_pair(a_dst + 8192, w.a, w.a_mn ? w.a_row + 64 : k0, w.a_mn ? k0 : w.a_row + 64, full_leader);
             tma_load_2d_pair(b_dst, w.b, w.b_mn ? w.b_row : k0, w.b_mn ? k0 : w.b_row, full_leader);
-            if (Op::kF16)
+            if (second)
               tma_load_2d_pair(b_dst + 8192, w.b, w.b_mn ? w.b_row + 64 : k0, w.b_mn ? k0 : w.b_row + 64, full_leader);
           }
           ++issued;

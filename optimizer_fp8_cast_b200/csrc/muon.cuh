@@ -47,6 +47,8 @@ struct alignas(64) Group {
   Matrix m[NP];
   int32_t n, steps;
   int32_t sym_tiles, x_tiles;      // of the phases
+  int32_t tile_n;                  // columns of a tile: 256, or 128
+  int32_t whole;                   // 1: every tile of A and B is computed, none mirrored
   Grid grid;
 };
 
@@ -82,17 +84,22 @@ struct Steps {
     w.a_mn = w.b_mn = 0;
     int inner = side;
     if (phase == 2) {                                      // wide: B X; tall: X B
-      const int tiles_n = (m.cols + kBN - 1) / kBN, local = tile - m.x_start;
+      const int tiles_n = (m.cols + g.tile_n - 1) / g.tile_n, local = tile - m.x_start;
       w.mt = local / tiles_n;
       w.nt = local - w.mt * tiles_n;
       w.a = wide ? &m.s[1] : &m.x[cur];
       w.b = wide ? &m.x[cur] : &m.s[1];
       w.b_mn = wide ? 1 : 0;
-    } else {                                               // the tiles on and above the diagonal: rows of n, n - 1, ...
-      int local = tile - m.sym_start, n = (side + kBN - 1) / kBN;
+    } else {
+      int local = tile - m.sym_start, n = (side + g.tile_n - 1) / g.tile_n;
       w.mt = 0;
-      while (local >= n) local -= n--, ++w.mt;
-      w.nt = w.mt + local;
+      if (g.whole) {
+        w.mt = local / n;
+        w.nt = local - w.mt * n;
+      } else {                                             // the tiles on and above the diagonal: rows of n, n - 1, ...
+        while (local >= n) local -= n--, ++w.mt;
+        w.nt = w.mt + local;
+      }
       w.a = w.b = phase == 0 ? &m.x[cur] : &m.s[0];
       if (phase == 0) {                                    // wide: rows of X; tall: its columns
         inner = lengthwise;
@@ -100,9 +107,10 @@ struct Steps {
       }
     }
     w.a_row = w.mt * kBM + rank * kHalf;
-    w.b_row = w.nt * kBN + rank * kHalf;
+    w.half_n = g.tile_n / 2;
+    w.b_row = w.nt * g.tile_n + rank * w.half_n;
     w.num_kb = (inner + 63) / 64;
-    w.idesc = make_idesc_f16(w.a_mn, w.b_mn);
+    w.idesc = make_idesc_f16(w.a_mn, w.b_mn, g.tile_n);
     return w;
   }
   static __device__ __forceinline__ void fetch_at(const Params& g, const Work& w, Out& o, int row0, int n) {
@@ -111,7 +119,7 @@ struct Steps {
     fetch(o, maps, x, row0);
   }
   static __device__ __forceinline__ void prefetch(const Params& g, const Work& w, int ph, Out& o, int row0, int half) {
-    if (reads(ph)) fetch_at(g, w, o, row0, w.nt * kBN + half * 128);
+    if (reads(ph)) fetch_at(g, w, o, row0, 2 * w.half_n * w.nt + half * w.half_n);
   }
   // 32 columns of the accumulator, times alpha: with READ also kB times A's values and a I.
   template <bool READ, class Release, class Ahead>
@@ -119,14 +127,15 @@ struct Steps {
                                                 int M, int N, bool mirrored, float alpha, uint32_t t_base, Release&& release,
                                                 Ahead&& ahead) {
     using namespace blk;
+    const int steps = w.half_n / 32;
 #pragma unroll 1
-    for (int s = 0; s < 4; ++s) {
-      const int c = half * 128 + s * 32, n = w.nt * kBN + c;
+    for (int s = 0; s < steps; ++s) {
+      const int c = half * w.half_n + s * 32, n = 2 * w.half_n * w.nt + c;
       uint4 av[4];
       if constexpr (READ) {
         if (!fetched(o)) return false;
         chunk_row(o, 0, av);
-        if (s < 3) fetch_at(g, w, o, row0, n + 32);
+        if (s + 1 < steps) fetch_at(g, w, o, row0, n + 32);
         else ahead();
       }
       uint32_t r[32];
@@ -134,7 +143,7 @@ struct Steps {
       tmem_ld_32x32b_x32(t_base + c, r);
       tmem_ld_wait();
       tmem_reg_fence(r);
-      if (s == 3) release();
+      if (s + 1 == steps) release();
       if (n >= N || row0 >= M) continue;
       const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
       f32x2 v[16];
@@ -166,10 +175,11 @@ struct Steps {
                                                   uint32_t t_base, Release&& release, Ahead&& ahead) {
     const Matrix& m = g.m[w.which];
     const int phase = ph % 3, side = min(m.rows, m.cols);
-    if (phase == 1) return chunks<true>(g, w, &m.sd[1], o, row0, half, side, side, w.mt != w.nt, kC / kFactor, t_base, release, ahead);
+    const bool mirrored = phase < 2 && !g.whole && w.mt != w.nt;
+    if (phase == 1) return chunks<true>(g, w, &m.sd[1], o, row0, half, side, side, mirrored, kC / kFactor, t_base, release, ahead);
     const bool sym = phase == 0;
     return chunks<false>(g, w, sym ? &m.sd[0] : &m.xd[((ph / 3) & 1) ^ 1], o, row0, half, sym ? side : m.rows, sym ? side : m.cols,
-                         sym && w.mt != w.nt, 1.0f / kFactor, t_base, release, ahead);
+                         mirrored, 1.0f / kFactor, t_base, release, ahead);
   }
 };
 
