@@ -80,16 +80,6 @@ __device__ __forceinline__ float gate(float g) {
   return blk::lo(gate<ACT>(both(g), dw));
 }
 
-// Runs of `kRun` row tiles share their column tiles, so that the weights a wave of tiles reads are read by several rows
-// of A while they are in L2.
-constexpr int kRun = 8;
-__device__ __forceinline__ void place_in_runs(int tiles_m, int tiles_n, int local, int& mt, int& nt) {
-  const int run = local / (kRun * tiles_n), in = local - run * kRun * tiles_n;
-  const int rows = min(kRun, tiles_m - run * kRun);
-  nt = in / rows;
-  mt = run * kRun + in - nt * rows;
-}
-
 // max(|a|, |b|, |c|), NaN if one is.
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
   float r;

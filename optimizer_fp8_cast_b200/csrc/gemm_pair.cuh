@@ -166,6 +166,16 @@ struct Work {
   int which;                       // the operator's own
 };
 
+// Tiles in runs of kRun row tiles, column by column: the 74 tiles that run at a time then read 8 row panels of A and 9 column
+// panels of B where row by row they read 2 and all of B's (X = B X of 4096 x 11008: a third of the bytes from memory).
+constexpr int kRun = 8;
+__device__ __forceinline__ void place_in_runs(int tiles_m, int tiles_n, int local, int& mt, int& nt) {
+  const int run = local / (kRun * tiles_n), in = local - run * kRun * tiles_n;
+  const int rows = min(kRun, tiles_m - run * kRun);
+  nt = in / rows;
+  mt = run * kRun + in - nt * rows;
+}
+
 // ------------------------------------------------------------------ a barrier of the whole grid
 // counter counts the CTAs that have ended a phase, expired is set by one that gave up; both zero at the launch.
 struct Grid {

@@ -84,9 +84,7 @@ struct Steps {
     w.a_mn = w.b_mn = 0;
     int inner = side;
     if (phase == 2) {                                      // wide: B X; tall: X B
-      const int tiles_n = (m.cols + g.tile_n - 1) / g.tile_n, local = tile - m.x_start;
-      w.mt = local / tiles_n;
-      w.nt = local - w.mt * tiles_n;
+      place_in_runs((m.rows + kBM - 1) / kBM, (m.cols + g.tile_n - 1) / g.tile_n, tile - m.x_start, w.mt, w.nt);
       w.a = wide ? &m.s[1] : &m.x[cur];
       w.b = wide ? &m.x[cur] : &m.s[1];
       w.b_mn = wide ? 1 : 0;
