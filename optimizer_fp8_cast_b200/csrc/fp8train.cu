@@ -1813,11 +1813,17 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int tile_n) {
   p.has_q = c.q != nullptr;
   return st;
 }
-const int64_t kGatedFewRows = getenv("GR") ? atoi(getenv("GR")) : 16;
+// Few rows: always up to eight, and while the weights, read once for every eight rows, are small. Few-rows kernel / pair tiles,
+// graph replays: 8 x 4096 -> 2 x 11008 24.5 / 28.8 us (W in x out), 21.3 / 29.4 (out x in); 16 rows 36.5 / 28.2 and 33.7 / 28.4;
+// 16 x 1024 -> 2 x 2752 (11 MB) 8.2 / 7.8 and 3.8 / 7.8; 32 x 256 -> 2 x 688 4.1 / 6.1 and 2.3 / 5.8.
+bool gated_few_rows(const fp8t_gated& d) {
+  const int64_t groups = (d.M + 7) / 8, most = d.b_layout == FP8T_MN_MAJOR ? int64_t(8) << 20 : int64_t(16) << 20;
+  return groups == 1 || (d.M <= 32 && groups * 2 * d.N * d.K <= most);
+}
 template <int WF, int AF>
 fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, cudaStream_t stream) {
   using namespace fp8t::gated;
-  const int per = mn ? 64 : 32, chunks = mn ? (p.K + 31) / 32 : (p.K + 63) / 64;
+  const int per = mn ? 64 : 16, chunks = mn ? (p.K + 31) / 32 : (p.K + 63) / 64;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.N + per - 1) / per), static_cast<unsigned>((p.M + kRowTokens - 1) / kRowTokens), 1);
   cfg.blockDim = dim3(static_cast<unsigned>(32 * std::min(kRowWarps, chunks)), 1, 1);
@@ -1917,7 +1923,7 @@ fp8t_status fp8_gated_gemm(const fp8t_gated* desc, void* stream) {
   if (!d.gu_bf16 && !d.h_bf16 && !d.q) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm: no output asked for");
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != FP8T_OK) return st;
-  if (d.M <= kGatedFewRows) return (st = ready_gated_rows(dev)) != FP8T_OK ? st : launch_gated_rows(d, as_stream(stream));
+  if (gated_few_rows(d)) return (st = ready_gated_rows(dev)) != FP8T_OK ? st : launch_gated_rows(d, as_stream(stream));
   if ((st = ready_pair(dev)) != FP8T_OK) return st;
   fp8t::gated::Params p = {};
   if ((st = fill_gated(p, c, 128)) != FP8T_OK) return st;

@@ -9,7 +9,7 @@
 //   W as [K][2N]  a lane holds 8 consecutive outputs of four rows of k: a 4 x 4 byte transpose (8 byte permutations for 16
 //                 weights) makes the words of four k, and the MMA's row g is output 8g + j of the j-th MMA
 // The warps of a CTA take the chunks of K in turn, the next one's loads on their way during a chunk's arithmetic, and add up in shared
-// memory in warp order. More than eight tokens: a CTA for each eight, which finds the weights in L2.
+// memory in warp order. More than eight tokens: a CTA for each eight, which finds the weights in L2; that pays while they are few.
 #pragma once
 
 #include "gated.cuh"
@@ -87,10 +87,11 @@ __device__ __forceinline__ void finish_rows(const RowParams& p, const float* par
   if (p.scale_inv && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scale_inv = __fdiv_rn(1.0f, scale);
 }
 
-// W [2N][K]: a CTA takes 32 outputs, a warp all of them for its chunks of 64 k.
+// W [2N][K]: a CTA takes 16 outputs, a warp all of them for its chunks of 64 k; three CTAs on an SM (1 x 4096 -> 2 x 11008 20.7 us;
+// 32 outputs and two CTAs, whose 344 do not all fit at once, 23.2).
 template <int WF, int AF>
-__global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows(const __grid_constant__ RowParams p) {
-  constexpr int R = 4;
+__global__ void __launch_bounds__(32 * kRowWarps, 3) k_gated_rows(const __grid_constant__ RowParams p) {
+  constexpr int R = 2;
   __shared__ float part[kRowWarps][R][4][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
