@@ -4,8 +4,8 @@
 // Forward. W holds the gate's and the up projection's weights side by side (N columns each):
 //   [G | U] = (A . W) * sa * sb,  h = act(G) * U,  act(g) = g * sigmoid(w(g))
 //   w = g (SiLU) or 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU in its tanh form: (1 + tanh(z)) / 2 = sigmoid(2z))
-// One accumulator of a pair tile holds 128 columns of G and the same 128 of U: the even CTA's half of B is 128 gate rows, the
-// odd CTA's the up rows of the same columns, so every lane has g and u of an element at the same time and h never
+// One accumulator of a pair tile holds 128 columns of G and the same 128 of U (64 in small products): the even CTA's half of B is
+// gate rows, the odd CTA's the up rows of the same columns, so every lane has g and u of an element at the same time and h never
 // leaves the registers before it is rounded. h is formed from the f32 accumulators; G and U are rounded to BF16 only
 // where they are kept for the gradient.
 // Backward. dH = (dY . Wd^T) * sa * sb stays in the accumulator (256 columns); with s = sigmoid(w(g))
@@ -37,6 +37,7 @@ struct alignas(64) Params {
   float* scale_inv;
   int32_t M, N;
   int32_t tiles_m, tiles_n, total_tiles, num_kb;
+  int32_t half_n;                  // rows of B of a CTA: a tile has as many outputs (forward) or twice as many (backward)
   int32_t a_mn, b_mn;
   uint32_t idesc;
   int32_t act, fmt;                // fmt of the codes
@@ -136,7 +137,7 @@ struct Base {
     w.b = &g.b;
     w.a_row = w.mt * kBM + rank * kHalf;
     w.b_row = w.nt * b_step + rank * b_other;
-    w.half_n = kHalf;
+    w.half_n = g.half_n;
     w.num_kb = g.num_kb;
     w.a_mn = 0;
     w.b_mn = g.b_mn;
@@ -159,21 +160,22 @@ template <int ACT>
 struct Forward : Base {
   static constexpr int kLoads = 0;
   static __device__ __forceinline__ void prefetch(const Params&, const Work&, int, Out&, int, int) {}
-  static __device__ __forceinline__ Work work(const Params& g, int, int tile, int rank) { return work_of(g, tile, rank, 128, g.N); }
+  static __device__ __forceinline__ Work work(const Params& g, int, int tile, int rank) { return work_of(g, tile, rank, g.half_n, g.N); }
   template <class Release, class Ahead>
   static __device__ __forceinline__ bool epilogue(const Params& g, const Work& w, int, const Scalars& k, Out& o, int row0, int half,
                                                   uint32_t t_base, Release&& release, Ahead&&) {
+    const int steps = w.half_n / 64;
 #pragma unroll 1
-    for (int s = 0; s < 2; ++s) {
-      const int c = half * 64 + s * 32, n = w.nt * 128 + c;
+    for (int s = 0; s < steps; ++s) {
+      const int c = (half * steps + s) * 32, n = w.nt * w.half_n + c;
       uint32_t rg[32], ru[32];
       __syncwarp();                                        // one lane stored the chunk before
       tmem_ld_32x32b_x32(t_base + c, rg);
-      tmem_ld_32x32b_x32(t_base + 128 + c, ru);
+      tmem_ld_32x32b_x32(t_base + w.half_n + c, ru);
       tmem_ld_wait();
       tmem_reg_fence(rg);
       tmem_reg_fence(ru);
-      if (s == 1) release();
+      if (s + 1 == steps) release();
       if (n >= g.N || row0 >= g.M) continue;               // chunk entirely outside the matrix
       f32x2 gv[16], uv[16];
       scaled(rg, k.alpha, gv);
@@ -217,28 +219,29 @@ struct Backward : Base {
     fetch(o, maps, x, row0);
   }
   static __device__ __forceinline__ void prefetch(const Params& g, const Work& w, int, Out& o, int row0, int half) {
-    fetch_at(g, o, row0, w.nt * kBN + half * 128);
+    fetch_at(g, o, row0, (2 * w.nt + half) * w.half_n);
   }
-  static __device__ __forceinline__ Work work(const Params& g, int, int tile, int rank) { return work_of(g, tile, rank, kBN, kHalf); }
+  static __device__ __forceinline__ Work work(const Params& g, int, int tile, int rank) { return work_of(g, tile, rank, 2 * g.half_n, g.half_n); }
   template <class Release, class Ahead>
   static __device__ __forceinline__ bool epilogue(const Params& g, const Work& w, int, const Scalars& k, Out& o, int row0, int half,
                                                   uint32_t t_base, Release&& release, Ahead&& ahead) {
     const bool in = row0 + o.lane < g.M;
+    const int steps = w.half_n / 32;
 #pragma unroll 1
-    for (int s = 0; s < 4; ++s) {
-      const int c = half * 128 + s * 32, n = w.nt * kBN + c;
+    for (int s = 0; s < steps; ++s) {
+      const int c = half * w.half_n + s * 32, n = 2 * w.half_n * w.nt + c;
       uint4 gw[4], uw[4];
       if (!fetched(o)) return false;
       chunk_row(o, 0, gw);
       chunk_row(o, 1, uw);
-      if (s < 3) fetch_at(g, o, row0, n + 32);
+      if (s + 1 < steps) fetch_at(g, o, row0, n + 32);
       else ahead();
       uint32_t r[32];
       __syncwarp();
       tmem_ld_32x32b_x32(t_base + c, r);
       tmem_ld_wait();
       tmem_reg_fence(r);
-      if (s == 3) release();
+      if (s + 1 == steps) release();
       if (n >= g.N || row0 >= g.M) continue;
       f32x2 gv[16], uv[16], dh[16];
       scaled(r, k.alpha, dh);

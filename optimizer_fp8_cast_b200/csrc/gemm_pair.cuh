@@ -154,12 +154,12 @@ __device__ __forceinline__ void store8(Out& o, const CUtensorMap* map, const uin
   send(o, map, b, x, y);
 }
 
-// A tile of a product. Boxes are 128 rows (FP8) or 64 (FP16, two of them) of 128 bytes.
+// A tile of a product. FP8 boxes are as many rows as a CTA holds, FP16 boxes 64 (one or two of them), of 128 bytes.
 struct Work {
   const CUtensorMap *a, *b;
   int a_row, b_row;                // first row of A and of B that this CTA holds
   int mt, nt;                      // row and column tile
-  int half_n;                      // rows of B that each CTA holds: 128, or 64 (FP16) for tiles of 128 columns
+  int half_n;                      // rows of B that each CTA holds: 128, or 64 for tiles of 128 columns (not of MN-major FP8)
   int num_kb;
   int a_mn, b_mn;                  // 1: operand stored MN-major
   uint32_t idesc;
@@ -290,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (one) {
             const uint32_t full_leader = mapa_shared(smem_u32(&S->full[s]), 0);
             const bool second = Op::kF16 && w.half_n > 64;   // B's second box of 64
-            if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), !Op::kF16 || second ? kPairTxBytes : kPairTxBytes - 2 * 8192);
+            if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), 2 * (kABytes + w.half_n * kBK));
             const uint32_t a_dst = smem_u32(smem + s * kStageBytes), b_dst = a_dst + kABytes;
             const int k0 = kb * kElems;
             tma_load_2d_pair(a_dst, w.a, w.a_mn ? w.a_row : k0, w.a_mn ? k0 : w.a_row, full_leader);
