@@ -597,8 +597,8 @@ fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream);
  *   steps          1 .. 16
  *   d_workspace    muon_workspace_bytes of the sizes, 256-byte aligned, contents on entry ignored. Calls that may run
  *                  at the same time need their own.
- * out may be a BF16 X0 itself. Errors: INVALID_ARG (also two outputs at one address), UNSUPPORTED_SHAPE,
- * MISALIGNED (16 bytes), CUDA.
+ * out may be the matrix's own BF16 X0. Errors: INVALID_ARG (also an output given twice or another matrix's X0),
+ * UNSUPPORTED_SHAPE, MISALIGNED (16 bytes), CUDA.
  */
 typedef struct fp8t_orth_matrix {
     const void* x;                 /* rows x cols                                                   */
@@ -617,7 +617,9 @@ fp8t_status muon_orthogonalize(const fp8t_orth_matrix* matrices, int32_t n_matri
  * (O's entries have a root mean square of about 1 / sqrt(max(rows, cols)), so the update's is lr * update_rms;
  * 0.2 is about AdamW's). If any u has a non-finite norm nothing is changed and *d_skipped_out (int32, or
  * NULL) is 1, else 0. There is no clipping: O does not depend on the gradient's size.
- * Tensors must not overlap. Errors and workspace as muon_orthogonalize; hyperparameters finite, loss_scale > 0.
+ * Tensors must not overlap, but weight may be the tensor's own grad. Where a wait inside the products expired
+ * (FP8T_ERR_TIMEOUT) master and weight of its table stay as they are, momentum is new, and *d_skipped_out is 1.
+ * Errors and workspace as muon_orthogonalize; hyperparameters finite, loss_scale > 0.
  */
 typedef struct fp8t_muon_tensor {
     float* master;                 /* rows x cols                                                   */

@@ -1734,6 +1734,12 @@ fp8t_status ready_pair(DeviceInfo* d) {
       (void)cudaGetLastError();
       clusters = d->sms / 2;
     }
+    // and of the grid-wide steps, whose CTAs all have to be resident
+    int together = 0;
+    if (cudaOccupancyMaxActiveClusters(&together, pair::k_pair_gemm<muon::Steps<muon::kMaxMatrices>>, &cfg) == cudaSuccess && together > 0)
+      clusters = std::min(clusters, together);
+    else
+      (void)cudaGetLastError();
     d->pair_clusters = clusters;
     return cudaSuccess;
   });
@@ -2228,10 +2234,33 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
   return FP8T_OK;
 }
 
-// Whether two of the addresses are the same.
-bool any_twice(std::vector<const void*>& v) {
-  std::sort(v.begin(), v.end());
-  return std::adjacent_find(v.begin(), v.end()) != v.end();
+// What a call reads and writes, by address and matrix; `own`: a matrix's output may be its own input.
+struct MuonBuffer {
+  const void* p;
+  int32_t matrix;
+  bool own;
+};
+bool by_address(const MuonBuffer& a, const MuonBuffer& b) { return std::less<const void*>()(a.p, b.p); }
+// Whether an address is written twice, or written for one matrix and read for another (the tables of a long list run one after
+// the other).
+bool muon_conflict(std::vector<MuonBuffer>& outs, std::vector<MuonBuffer>& ins) {
+  std::sort(outs.begin(), outs.end(), by_address);
+  std::sort(ins.begin(), ins.end(), by_address);
+  for (size_t i = 0; i + 1 < outs.size(); ++i)
+    if (outs[i].p == outs[i + 1].p) return true;
+  for (const MuonBuffer& o : outs)
+    for (auto it = std::lower_bound(ins.begin(), ins.end(), o, by_address); it != ins.end() && it->p == o.p; ++it)
+      if (!o.own || it->matrix != o.matrix) return true;
+  return false;
+}
+// No exception leaves a C entry: the lists above are the only ones that allocate.
+template <class F>
+fp8t_status without_exceptions(const char* name, F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(FP8T_ERR_CUDA, "%s: %s", name, e.what());
+  }
 }
 
 }  // namespace
@@ -2250,26 +2279,29 @@ fp8t_status muon_orthogonalize(const fp8t_orth_matrix* matrices, int32_t n_matri
   if (!matrices || n_matrices < 1 || n_matrices > 4096)
     return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrices NULL or n_matrices out of range");
   if (steps < 1 || steps > 16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: steps in 1..16");
-  std::vector<const void*> outs;
-  for (int32_t i = 0; i < n_matrices; ++i) {
-    const fp8t_orth_matrix& m = matrices[i];
-    if (!m.x || !m.out_bf16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrix %d: NULL pointer", i);
-    if (x_f32 && m.x == m.out_bf16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrix %d: out is the f32 input", i);
-    if (!aligned(m.x, 16) || !aligned(m.out_bf16, 16))
-      return fail(FP8T_ERR_MISALIGNED, "muon_orthogonalize: matrix %d: misaligned pointer", i);
-    outs.push_back(m.out_bf16);
-  }
-  if (any_twice(outs)) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: two results at one address");
-  fp8t::muon::Table t = {};
-  auto get = [&](int32_t i, fp8t::muon::Tensor& T, int64_t& r, int64_t& c) {
-    T = {};
-    T.g = matrices[i].x;
-    T.w = static_cast<uint16_t*>(matrices[i].out_bf16);
-    r = matrices[i].rows;
-    c = matrices[i].cols;
-  };
-  return x_f32 ? muon_call<fp8t::muon::kOrthF32>("muon_orthogonalize", n_matrices, steps, t, d_workspace, workspace_bytes, as_stream(stream), get)
-               : muon_call<fp8t::muon::kOrthBf16>("muon_orthogonalize", n_matrices, steps, t, d_workspace, workspace_bytes, as_stream(stream), get);
+  return without_exceptions("muon_orthogonalize", [&]() -> fp8t_status {
+    std::vector<MuonBuffer> outs, ins;
+    for (int32_t i = 0; i < n_matrices; ++i) {
+      const fp8t_orth_matrix& m = matrices[i];
+      if (!m.x || !m.out_bf16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrix %d: NULL pointer", i);
+      if (x_f32 && m.x == m.out_bf16) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: matrix %d: out is the f32 input", i);
+      if (!aligned(m.x, 16) || !aligned(m.out_bf16, 16))
+        return fail(FP8T_ERR_MISALIGNED, "muon_orthogonalize: matrix %d: misaligned pointer", i);
+      outs.push_back({m.out_bf16, i, true});
+      ins.push_back({m.x, i, true});
+    }
+    if (muon_conflict(outs, ins)) return fail(FP8T_ERR_INVALID_ARG, "muon_orthogonalize: a result twice, or in another matrix");
+    fp8t::muon::Table t = {};
+    auto get = [&](int32_t i, fp8t::muon::Tensor& T, int64_t& r, int64_t& c) {
+      T = {};
+      T.g = matrices[i].x;
+      T.w = static_cast<uint16_t*>(matrices[i].out_bf16);
+      r = matrices[i].rows;
+      c = matrices[i].cols;
+    };
+    return x_f32 ? muon_call<fp8t::muon::kOrthF32>("muon_orthogonalize", n_matrices, steps, t, d_workspace, workspace_bytes, as_stream(stream), get)
+                 : muon_call<fp8t::muon::kOrthBf16>("muon_orthogonalize", n_matrices, steps, t, d_workspace, workspace_bytes, as_stream(stream), get);
+  });
 }
 
 fp8t_status fused_muon_multi_tensor(const fp8t_muon_tensor* tensors, int32_t n_tensors, float lr, float beta,
@@ -2283,38 +2315,41 @@ fp8t_status fused_muon_multi_tensor(const fp8t_muon_tensor* tensors, int32_t n_t
   if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale) || !std::isfinite(lr) || !std::isfinite(beta) ||
       !std::isfinite(weight_decay) || !std::isfinite(update_rms))
     return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: non-finite hyperparameter or loss_scale <= 0");
-  std::vector<const void*> outs;
-  for (int32_t i = 0; i < n_tensors; ++i) {
-    const fp8t_muon_tensor& m = tensors[i];
-    if (!m.master || !m.momentum || !m.grad_bf16 || !m.weight_bf16)
-      return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: tensor %d: NULL pointer", i);
-    if (!aligned(m.master, 16) || !aligned(m.momentum, 16) || !aligned(m.grad_bf16, 16) || !aligned(m.weight_bf16, 16))
-      return fail(FP8T_ERR_MISALIGNED, "fused_muon_multi_tensor: tensor %d: misaligned pointer", i);
-    outs.push_back(m.master);
-    outs.push_back(m.momentum);
-    outs.push_back(m.weight_bf16);
-  }
-  if (any_twice(outs)) return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: a tensor is given twice");
-  if (!aligned(d_skipped_out, 4)) return fail(FP8T_ERR_MISALIGNED, "fused_muon_multi_tensor: misaligned skipped");
-  fp8t::muon::Table t = {};
-  t.beta = beta;
-  t.inv_scale = static_cast<float>(1.0 / static_cast<double>(loss_scale));
-  t.keep = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
-  t.nesterov = nesterov ? 1 : 0;
-  t.skipped = d_skipped_out;
-  auto get = [&](int32_t i, fp8t::muon::Tensor& T, int64_t& r, int64_t& c) {
-    const fp8t_muon_tensor& m = tensors[i];
-    T = {};
-    T.p = m.master;
-    T.m = m.momentum;
-    T.g = m.grad_bf16;
-    T.w = static_cast<uint16_t*>(m.weight_bf16);
-    r = m.rows;
-    c = m.cols;
-    T.rate = static_cast<float>(static_cast<double>(lr) * static_cast<double>(update_rms) *
-                                std::sqrt(static_cast<double>(std::max(r, c))));
-  };
-  return muon_call<fp8t::muon::kMuon>("fused_muon_multi_tensor", n_tensors, steps, t, d_workspace, workspace_bytes, as_stream(stream), get);
+  return without_exceptions("fused_muon_multi_tensor", [&]() -> fp8t_status {
+    std::vector<MuonBuffer> outs, ins;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+      const fp8t_muon_tensor& m = tensors[i];
+      if (!m.master || !m.momentum || !m.grad_bf16 || !m.weight_bf16)
+        return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: tensor %d: NULL pointer", i);
+      if (!aligned(m.master, 16) || !aligned(m.momentum, 16) || !aligned(m.grad_bf16, 16) || !aligned(m.weight_bf16, 16))
+        return fail(FP8T_ERR_MISALIGNED, "fused_muon_multi_tensor: tensor %d: misaligned pointer", i);
+      outs.push_back({m.master, i, false});
+      outs.push_back({m.momentum, i, false});
+      outs.push_back({m.weight_bf16, i, true});
+      ins.push_back({m.grad_bf16, i, true});
+    }
+    if (muon_conflict(outs, ins)) return fail(FP8T_ERR_INVALID_ARG, "fused_muon_multi_tensor: a tensor is written twice or read elsewhere");
+    if (!aligned(d_skipped_out, 4)) return fail(FP8T_ERR_MISALIGNED, "fused_muon_multi_tensor: misaligned skipped");
+    fp8t::muon::Table t = {};
+    t.beta = beta;
+    t.inv_scale = static_cast<float>(1.0 / static_cast<double>(loss_scale));
+    t.keep = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
+    t.nesterov = nesterov ? 1 : 0;
+    t.skipped = d_skipped_out;
+    auto get = [&](int32_t i, fp8t::muon::Tensor& T, int64_t& r, int64_t& c) {
+      const fp8t_muon_tensor& m = tensors[i];
+      T = {};
+      T.p = m.master;
+      T.m = m.momentum;
+      T.g = m.grad_bf16;
+      T.w = static_cast<uint16_t*>(m.weight_bf16);
+      r = m.rows;
+      c = m.cols;
+      T.rate = static_cast<float>(static_cast<double>(lr) * static_cast<double>(update_rms) *
+                                  std::sqrt(static_cast<double>(std::max(r, c))));
+    };
+    return muon_call<fp8t::muon::kMuon>("fused_muon_multi_tensor", n_tensors, steps, t, d_workspace, workspace_bytes, as_stream(stream), get);
+  });
 }
 
 // ------------------------------------------------------------------ scale update

@@ -550,7 +550,8 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_scale(const __grid_consta
   if (blockIdx.x == 0 && threadIdx.x == 0) *t.grid.counter = 0, *t.grid.expired = 0;
   if (MODE == kMuon) {
     const bool go = all_finite(t);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && t.skipped) *t.skipped = go ? 0 : 1;
+    // a later table's 0 would hide that an earlier one's products gave up
+    if (blockIdx.x == 0 && threadIdx.x == 0 && t.skipped && (!go || t.first == 0)) *t.skipped = go ? 0 : 1;
     if (!go) return;
   }
   const int chunk = blockIdx.x, k = find_tensor(t, chunk);

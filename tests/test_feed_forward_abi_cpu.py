@@ -99,6 +99,8 @@ def test_muon_refusals(lib):
     assert step(w=None) == 1 and step(size=100) == 1 and step(w=P + 16) == 3 and step(skipped=O) == 3
     assert step(n=2, master=5 * P) == 1 and b"twice" in lib.fp8t_last_error_message()
     assert step(momentum=P) == 1
+    assert step(n=2, grad_bf16=8 * P) == 1                           # another tensor's weight, or this one's master
+    assert step(grad_bf16=P) == 1
 
     def orth(n=1, f32=0, steps=5, w=P, size=ws, **kw):
         a = dict(x=P, out_bf16=2 * P, rows=4, cols=4)
@@ -110,6 +112,7 @@ def test_muon_refusals(lib):
     assert orth(x=U) == 3 and orth(out_bf16=U) == 3 and orth(rows=0) == 2 and orth(size=10) == 1
     assert orth(f32=1, out_bf16=P) == 1                              # an f32 matrix has no room for itself in BF16
     assert orth(n=2, out_bf16=4 * P) == 1
+    assert orth(n=2, out_bf16=3 * P) == 1 and b"another matrix" in lib.fp8t_last_error_message()
 
 
 def test_muon_workspace_bytes(lib):
