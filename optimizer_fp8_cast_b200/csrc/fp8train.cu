@@ -1808,7 +1808,7 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int outputs, 
   p.M = static_cast<int32_t>(c.M);
   p.N = static_cast<int32_t>(c.N);
   p.tiles_m = static_cast<int32_t>((c.M + kBM - 1) / kBM);
-  // tiles of half the columns where all of them run at once: half an epilogue at the end (back 512 x 256 x 688 10.2 / 8.6 us)
+  // tiles of half the columns where all of them run at once: half an epilogue at the end (back 512 x 256 x 688 10.1 / 7.1 us)
   const int64_t half = (c.N + outputs / 2 - 1) / (outputs / 2);
   const bool narrow = !mn && half * p.tiles_m <= dev->pair_clusters;
   p.half_n = narrow ? 64 : 128;
@@ -2098,7 +2098,7 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<cha
   g.sym_tiles = g.x_tiles = 0;
   g.grid = grid;
   // Where all tiles of A fit the clusters at once, computing both halves spares the transposed stores; where tiles half as wide
-  // do, a phase has half the columns to compute and to store (1237 x 611 190 / 141 us).
+  // do, a phase has half the columns to compute and to store (1237 x 611 190 / 151 us).
   int64_t whole = 0, narrow = 0;
   for (int32_t k : which) {
     whole += muon_sym_tiles(z[k], 256, false);

@@ -184,7 +184,7 @@ struct Steps {
 // ------------------------------------------------------------------ small matrices
 // Up to 256 x 256: one CTA pair keeps a matrix in shared memory over all steps. The phases of the grid-wide form have little to do
 // there (6.4 us each, of which the MMAs are one: barrier, first loads, stores); here the epilogue writes the next phase's
-// operand where the tensor cores read it, and a phase ends with the pair's own barrier (256 x 256 97 -> 48 us a call).
+// operand where the tensor cores read it, and a phase ends with the pair's own barrier (256 x 256 97 -> 60 us a call).
 // CTA r holds (FP16, 128-byte swizzle, zeros past the matrix):
 //   xk   rows 128r .. of X, K-major: four blocks of 64 columns
 //   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns

@@ -30,8 +30,8 @@ def slope_of(g, act):
 
 
 def sigmoid_error(g, act):
-    """Relative error of the kernel's sigmoid s = 1 / (1 + exp(-w)): CUDA's bound for __expf is 2 + 1.173 |w| ulp, w's own
-    four roundings move it by 4 |w| * 2^-24, and of both 1 - s arrives in s; the sum and __fdividef add 3 ulp."""
+    """Relative error of the kernel's sigmoid s = 1 / (1 + 2^(-w log2 e)): the power is good to 2 ulp, its argument's roundings
+    and w's own four move it by less than 5.2 |w| ulp, and of both 1 - s arrives in s; the sum and the reciprocal add 3 ulp."""
     w = gate(g, act)[0]
     return ((2 + 5.2 * w.abs()) * torch.sigmoid(-w) + 6) * 2.0 ** -23
 
