@@ -1715,6 +1715,10 @@ cudaError_t allow_pair_smem() {
 }
 using fp8t::gated::kGelu;
 using fp8t::gated::kSilu;
+template <int MODE>
+cudaError_t muon_small_smem() {
+  return cudaFuncSetAttribute(fp8t::muon::k_muon_small<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8t::muon::kSmallSmemBytes);
+}
 fp8t_status ready_pair(DeviceInfo* d) {
   using namespace fp8t;
   return once_per_device(d->pair_ready, "pair products", [&] {
@@ -1723,7 +1727,8 @@ fp8t_status ready_pair(DeviceInfo* d) {
         (e = allow_pair_smem<gated::Backward<kSilu>>()) != cudaSuccess || (e = allow_pair_smem<gated::Backward<kGelu>>()) != cudaSuccess ||
         (e = allow_pair_smem<muon::Steps<4>>()) != cudaSuccess ||
         (e = allow_pair_smem<muon::Steps<muon::kMaxMatrices>>()) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(muon::k_muon_small, cudaFuncAttributeMaxDynamicSharedMemorySize, muon::kSmallSmemBytes)) != cudaSuccess)
+        (e = muon_small_smem<muon::kMuon>()) != cudaSuccess || (e = muon_small_smem<muon::kOrthBf16>()) != cudaSuccess ||
+        (e = muon_small_smem<muon::kOrthF32>()) != cudaSuccess)
       return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (d->sms / 2), 1, 1);
@@ -2124,6 +2129,7 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<cha
   (void)cudaLaunchKernelEx(&cfg, fp8t::pair::k_pair_gemm<Op>, g);
   return after_launch("Newton-Schulz products launch");
 }
+bool muon_small(const MuonSizes& z) { return std::max(z.rows, z.cols) <= fp8t::muon::kSmallSide; }
 // The same for matrices of at most 256 x 256, a CTA pair each.
 fp8t_status newton_schulz_small(const std::vector<MuonSizes>& z, const std::vector<char*>& at, const std::vector<int32_t>& which,
                                 int32_t steps, int32_t* expired, cudaStream_t stream) {
@@ -2142,7 +2148,7 @@ fp8t_status newton_schulz_small(const std::vector<MuonSizes>& z, const std::vect
     m.cols = static_cast<int32_t>(s.cols);
     m.pitch = static_cast<int32_t>(s.pitch_x);
   }
-  (void)launch_pdl(k_muon_small, 2 * static_cast<int64_t>(which.size()), kSmallThreads, kSmallSmemBytes, stream, 0, g);
+  (void)launch_pdl(k_muon_small<kMuon>, 2 * static_cast<int64_t>(which.size()), kSmallThreads, kSmallSmemBytes, stream, 0, g);
   return after_launch("Newton-Schulz products launch");
 }
 // A table's steps: the longest matrices first, for a cluster takes every n-th tile and the phase of A should end with the
@@ -2153,7 +2159,7 @@ fp8t_status newton_schulz_table(const std::vector<MuonSizes>& z, char* copies, i
   std::vector<int32_t> large, small;
   for (size_t k = 0; k < z.size(); copies += z[k].bytes(), ++k) {
     at[k] = copies;
-    (std::max(z[k].rows, z[k].cols) <= fp8t::muon::kSmallSide ? small : large).push_back(static_cast<int32_t>(k));
+    (muon_small(z[k]) ? small : large).push_back(static_cast<int32_t>(k));
   }
   std::stable_sort(large.begin(), large.end(), [&](int32_t a, int32_t b) { return std::max(z[a].rows, z[a].cols) > std::max(z[b].rows, z[b].cols); });
   fp8t_status st = FP8T_OK;
@@ -2162,6 +2168,30 @@ fp8t_status newton_schulz_table(const std::vector<MuonSizes>& z, char* copies, i
                            : newton_schulz<fp8t::muon::kMaxMatrices>(z, at, large, steps, grid, dev, stream);
   if (st == FP8T_OK && !small.empty()) st = newton_schulz_small(z, at, small, steps, grid.expired, stream);
   return st;
+}
+
+// Of the batch's matrices [b0, b1), those of at most 256 x 256, orthogonalised by one kernel.
+template <int MODE, class Get>
+fp8t_status orthogonalize_small(const char* name, int32_t b0, int32_t b1, int32_t steps, cudaStream_t stream, Get&& get) {
+  using namespace fp8t::muon;
+  static thread_local SmallGroup g;
+  g.steps = steps;
+  g.expired = nullptr;
+  int32_t k = 0;
+  for (int32_t i = b0; i < b1; ++i) {
+    int64_t r, c;
+    Tensor T;
+    get(i, T, r, c);
+    if (!muon_small(MuonSizes(r, c))) continue;
+    SmallMatrix& m = g.m[k++];
+    m.g = T.g;
+    m.out = T.w;
+    m.rows = static_cast<int32_t>(r);
+    m.cols = static_cast<int32_t>(c);
+  }
+  if (k == 0) return FP8T_OK;
+  (void)launch_pdl(k_muon_small<MODE>, 2 * static_cast<int64_t>(k), kSmallThreads, kSmallSmemBytes, stream, 0, g);
+  return after_launch(name);
 }
 
 // Both calls; `get(i)` gives the kernels' view of matrix i (x, chunk_start and pitch are filled here).
@@ -2194,14 +2224,16 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
   auto table = [&](int32_t b0) {
     const int32_t b1 = std::min<int32_t>(n, b0 + kMaxMatrices);
     sizes.clear();
-    t.n = b1 - b0;
+    t.n = 0;
     t.first = b0;
     t.chunks = 0;
     char* at = copies;
     for (int32_t i = b0; i < b1; ++i) {
-      Tensor& T = t.t[i - b0];
+      Tensor& T = t.t[t.n];
       int64_t r, c;
       get(i, T, r, c);
+      if (MODE != kMuon && muon_small(MuonSizes(r, c))) continue;
+      ++t.n;
       sizes.emplace_back(r, c);
       T.x = reinterpret_cast<uint16_t*>(at);
       T.numel = r * c;
@@ -2215,13 +2247,17 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
   // every norm before the first write: a non-finite one anywhere leaves all matrices as they are
   for (int32_t b0 = 0; b0 < n; b0 += kMaxMatrices) {
     table(b0);
+    if (t.n == 0) continue;
     (void)launch_pdl(k_muon_sumsq<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
     if ((st = after_launch(name)) != FP8T_OK) return st;
     (void)launch_pdl(k_muon_norms, t.n, kPassThreads, 0, stream, 0, t);
     if ((st = after_launch(name)) != FP8T_OK) return st;
   }
   for (int32_t b0 = 0; b0 < n; b0 += kMaxMatrices) {
+    if (MODE != kMuon && (st = orthogonalize_small<MODE>(name, b0, std::min<int32_t>(n, b0 + kMaxMatrices), steps, stream, get)) != FP8T_OK)
+      return st;
     if (n > kMaxMatrices) table(b0);
+    if (t.n == 0) continue;
     (void)launch_pdl(k_muon_scale<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
     if ((st = after_launch(name)) != FP8T_OK) return st;
     st = newton_schulz_table(sizes, copies, steps, t.grid, dev, stream);

@@ -181,205 +181,6 @@ struct Steps {
   }
 };
 
-// ------------------------------------------------------------------ small matrices
-// Up to 256 x 256: one CTA pair keeps a matrix in shared memory over all steps. The phases of the grid-wide form have little to do
-// there (6.4 us each, of which the MMAs are one: barrier, first loads, stores); here the epilogue writes the next phase's
-// operand where the tensor cores read it, and a phase ends with the pair's own barrier (256 x 256 97 -> 60 us a call).
-// CTA r holds (FP16, 128-byte swizzle, zeros past the matrix):
-//   xk   rows 128r .. of X, K-major: four blocks of 64 columns
-//   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns
-//   s    rows 128r .. of A, then of B, K-major
-// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, the other CTA's columns of xm through
-// distributed shared memory.
-constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
-constexpr int kSmallThreads = 64 + 32 * 16;               // 16 epilogue warps: a TMEM lane quarter and 64 columns each
-constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 256;
-struct alignas(64) SmallMatrix {
-  CUtensorMap x;                   // boxes of 64 rows x 64 values
-  uint16_t* out;
-  int32_t rows, cols, pitch, pad;
-};
-struct alignas(64) SmallGroup {
-  SmallMatrix m[kMaxMatrices];     // a CTA pair each
-  int32_t steps;
-  int32_t* expired;
-};
-struct SmallSmem {
-  uint64_t loaded;                 // X has landed
-  uint64_t acc_full;               // both CTAs: a phase's MMAs have completed
-  uint64_t mma_done;
-  uint32_t tmem_base;
-  int given_up;                    // 2 + the phase in which a wait expired (1: X did not land), 0: none
-};
-
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_muon_small(const __grid_constant__ SmallGroup g) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* xk = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *xm = xk + kSmallOperand, *sq = xm + kSmallOperand;
-  SmallSmem* S = reinterpret_cast<SmallSmem*>(sq + kSmallOperand);
-  volatile int* given_up = &S->given_up;
-  const SmallMatrix& M = g.m[blockIdx.x >> 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const bool wide = M.cols >= M.rows;
-  const int side = wide ? M.rows : M.cols, lengthwise = wide ? M.cols : M.rows;
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&S->loaded), 1);
-    mbar_init(smem_u32(&S->acc_full), 1);
-    mbar_init(smem_u32(&S->mma_done), 1);
-    *given_up = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&S->tmem_base), kAccCols);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = S->tmem_base;
-  const uint64_t limit = wait_limit_ns();
-  const int expire = expire_mode();
-  const bool expire_main = expire == kExpireAll, expire_epi = expire == kExpireAll || expire == kExpireGemmEpilogue;
-  pdl_enter();
-  // Both CTAs give up together: the word is written in both before a barrier that all threads of both pass, and names the
-  // phase, so that every thread leaves behind the same barrier however late it reads the word.
-  auto give_up = [&](int when) {
-    if (lane == 0) {
-      record_error(kErrTimeout);
-      for (uint32_t r = 0; r < 2; ++r)
-        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S->given_up), r)), "r"(when) : "memory");
-    }
-    __syncwarp();
-  };
-  auto going_on = [&](int when) {
-    const int v = *given_up;
-    return v == 0 || v > when;
-  };
-  if (warp == 0) {
-    if (elect_one()) {
-      mbar_arrive_expect_tx(smem_u32(&S->loaded), 2 * kSmallOperand);
-      const int at = static_cast<int>(rank) * kHalf;
-      for (int b = 0; b < 4; ++b)
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t to = smem_u32(xk + b * kSmallBlock + i * 8192);
-          tma_load_2d(to, &M.x, b * 64, at + i * 64, smem_u32(&S->loaded));
-          tma_load_2d(to + kSmallOperand, &M.x, at + i * 64, b * 64, smem_u32(&S->loaded));
-        }
-    }
-    __syncwarp();
-    if (!warp_wait(smem_u32(&S->loaded), 0, limit, expire_main)) give_up(1);
-  }
-  cluster_sync();                                          // X is there in both CTAs
-  bool alive = going_on(1);
-  for (int ph = 0; ph < 3 * g.steps && alive; ++ph) {
-    const int phase = ph % 3;
-    if (warp == 1 && rank == 0) {
-      // ---------------- MMA issuer
-      const uint32_t k0 = smem_u32(xk), m0 = smem_u32(xm), s0 = smem_u32(sq);
-      const bool a_mn = phase == 0 && !wide, b_mn = phase == 0 ? !wide : phase == 2 && wide;
-      const uint32_t a0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || wide ? s0 : k0;
-      const uint32_t b0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || !wide ? s0 : m0;
-      const uint32_t idesc = make_idesc_f16(a_mn, b_mn);
-      const int blocks = ((phase == 0 ? lengthwise : side) + 63) / 64;
-      tc_fence_after();
-      if (elect_one()) {
-        for (int b = 0; b < blocks; ++b)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock;
-            tc_mma_f16_pair(tmem, a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
-                            b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc, (b | k) != 0 ? 1u : 0u);
-          }
-        tc_commit_pair_mc(smem_u32(&S->acc_full), 0x3);
-      }
-      __syncwarp();
-    } else if (warp >= 2) {
-      // ---------------- epilogue: what becomes the next phase's operand
-      using namespace blk;
-      const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
-      const int all = static_cast<int>(rank) * kHalf + row;                            // of the matrix
-      if (!warp_wait(smem_u32(&S->acc_full), ph & 1, limit, expire_epi)) {
-        give_up(2 + ph);
-      } else {
-        tc_fence_after();
-        const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
-        const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
-        const bool last = ph + 1 == 3 * g.steps;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int n = part * 64 + s * 32;
-          uint8_t* line = (phase == 2 ? xk : sq) + (n >> 6) * kSmallBlock + row * 128;  // K-major place of (row, n ..)
-          const int piece = (n >> 3) & 7;
-          const bool diagonal = all - lane == n;           // it runs through these 32 columns
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
-          tmem_ld_wait();
-          tmem_reg_fence(r);
-          uint4 q[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint4 was = make_uint4(0, 0, 0, 0);
-            uint4* place = reinterpret_cast<uint4*>(line + ((piece + p) ^ (row & 7)) * 16);
-            if (phase == 1) was = *place;                  // A, which B takes the place of
-            const uint32_t h[4] = {was.x, was.y, was.z, was.w};
-            uint32_t out[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int c = 8 * p + 2 * j;
-              f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
-              if (phase == 1) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-                v = fma2(be, blk::pair(f.x, f.y), v);
-                if (diagonal)
-                  v = add2(v, blk::pair(lane == c ? kA * kFactor : 0.0f, lane == c + 1 ? kA * kFactor : 0.0f));
-              }
-              out[j] = pack_f16x2(lo(v), hi(v));
-            }
-            q[p] = make_uint4(out[0], out[1], out[2], out[3]);
-            *place = q[p];
-          }
-          if (phase == 2 && !last) {                       // and X's columns: those of the CTA that holds them
-            const int k = all & 63;
-            const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128);
-            const uint32_t there = mapa_shared(to, n >> 7);
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-              st_cluster_v4(there + ((piece + p) ^ (k & 7)) * 16, q[p].x, q[p].y, q[p].z, q[p].w);
-          }
-          if (last && all < M.rows) {
-            uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-              if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
-          }
-        }
-        tc_fence_before();
-        fence_proxy_async_all();                           // for the tensor cores of both CTAs
-      }
-    }
-    cluster_sync();
-    alive = going_on(2 + ph);
-  }
-  if (warp == 1 && rank == 0) {                            // MMAs may be in flight when a wait expired
-    if (elect_one()) tc_commit_pair(smem_u32(&S->mma_done));
-    __syncwarp();
-    mbar_wait(smem_u32(&S->mma_done), 0, kDrainLimitNs);
-  }
-  if (!alive && threadIdx.x == 0) {
-    atomicExch(g.expired, 1);
-    const uint64_t t0 = globaltimer_ns();                  // loads too
-    while (globaltimer_ns() - t0 < kSettleNs) {
-    }
-  }
-  __syncwarp();
-  tc_fence_before();
-  cluster_sync();                 // neither CTA leaves while the other may still write to it or the MMAs read it
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, kAccCols);
-}
-
 // ------------------------------------------------------------------ the passes over the elements
 enum : int { kMuon = 0, kOrthBf16 = 1, kOrthF32 = 2 };
 struct Tensor {
@@ -453,6 +254,25 @@ __device__ __forceinline__ void load_g(const Tensor& T, int64_t e, int n, float 
     }
   }
 }
+// Up to eight elements of a row from e on (`left` of them), 16 bytes aligned or not.
+template <int MODE>
+__device__ __forceinline__ void load_row(const void* g, int64_t e, int left, bool aligned, float (&v)[8]) {
+  const float* f = static_cast<const float*>(g) + e;
+  const uint16_t* b = static_cast<const uint16_t*>(g) + e;
+  if (aligned && left > 0) {
+    if constexpr (MODE == kOrthF32) f32x8(f, v);
+    else bf16x8(ld_dep(reinterpret_cast<const uint4*>(b)), v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.0f;
+    if (j < left) {
+      if constexpr (MODE == kOrthF32) v[j] = ld_dep(f + j);
+      else v[j] = __uint_as_float(static_cast<uint32_t>(ld_dep(b + j)) << 16);
+    }
+  }
+}
 __device__ __forceinline__ void load_f32(const float* p, int64_t e, int n, float (&v)[8]) {
   if (n == 8) return f32x8(p + e, v);
 #pragma unroll
@@ -471,6 +291,21 @@ __device__ __forceinline__ void update(const Table& t, const Tensor& T, int64_t 
       u[j] = t.nesterov ? __fadd_rn(__fmul_rn(m[j], t.beta), g) : m[j];
     }
   }
+}
+
+// The factors from the sum of u^2.
+__device__ __forceinline__ Norm norm_of(double sum) {
+  Norm r = {0.0f, 0.0f, 1, 0};
+  if (!isfinite(sum)) {
+    r.ok = 0;
+    r.s1 = r.s2 = __int_as_float(0x7FC00000);
+  } else if (sum > 0.0) {                                  // |u| = f 2^e, f in [0.5, 1); a zero matrix stays zero
+    int e;
+    const double f = frexp(sqrt(sum), &e);
+    r.s1 = ldexpf(1.0f, -(e / 2));
+    r.s2 = static_cast<float>(ldexp(static_cast<double>(kFactor) / f, -(e - e / 2)));
+  }
+  return r;
 }
 
 // One partial sum of u^2 a chunk, in a fixed order.
@@ -517,20 +352,7 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_norms(const __grid_consta
     if (threadIdx.x < o) part[threadIdx.x] = __dadd_rn(part[threadIdx.x], part[threadIdx.x + o]);
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    sum = part[0];
-    Norm r = {0.0f, 0.0f, 1, 0};
-    if (!isfinite(sum)) {
-      r.ok = 0;
-      r.s1 = r.s2 = __int_as_float(0x7FC00000);
-    } else if (sum > 0.0) {                                // |u| = f 2^e, f in [0.5, 1); a zero matrix stays zero
-      int e;
-      const double f = frexp(sqrt(sum), &e);
-      r.s1 = ldexpf(1.0f, -(e / 2));
-      r.s2 = static_cast<float>(ldexp(static_cast<double>(kFactor) / f, -(e - e / 2)));
-    }
-    t.norms[t.first + k] = r;
-  }
+  if (threadIdx.x == 0) t.norms[t.first + k] = norm_of(part[0]);
 }
 
 // Whether every tensor of the call has a finite norm; all threads call.
@@ -653,6 +475,276 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_consta
         if (j < n) T.w[e + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
     }
   }
+}
+
+// ------------------------------------------------------------------ small matrices
+// Up to 256 x 256: one CTA pair keeps a matrix in shared memory over all steps. The phases of the grid-wide form have little to do
+// there (6.4 us each, of which the MMAs are one: barrier, first loads, stores); here the epilogue writes the next phase's
+// operand where the tensor cores read it, and a phase ends with the pair's own barrier (256 x 256 97 -> 60 us a call).
+// CTA r holds (FP16, 128-byte swizzle, zeros past the matrix):
+//   xk   rows 128r .. of X, K-major: four blocks of 64 columns
+//   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns
+//   s    rows 128r .. of A, then of B, K-major
+// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, the other CTA's columns of xm through
+// distributed shared memory.
+constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
+constexpr int kSmallThreads = 64 + 32 * 16;               // 16 epilogue warps: a TMEM lane quarter and 64 columns each
+constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 256;
+struct alignas(64) SmallMatrix {
+  CUtensorMap x;                   // kMuon: boxes of 64 rows x 64 values of X0
+  const void* g;                   // otherwise: the matrix, rows of cols
+  uint16_t* out;                   // kMuon: X in FP16, rows of pitch; otherwise the result
+  int32_t rows, cols, pitch, pad;
+};
+struct alignas(64) SmallGroup {
+  SmallMatrix m[kMaxMatrices];     // a CTA pair each
+  int32_t steps;
+  int32_t* expired;
+};
+struct SmallSmem {
+  double sums[32];                 // of u^2: the cluster's warps
+  uint64_t loaded;                 // X has landed
+  uint64_t acc_full;               // both CTAs: a phase's MMAs have completed
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int given_up;                    // 2 + the phase in which a wait expired (1: X did not land), 0: none
+};
+
+// kMuon: X0 comes from the workspace and X goes back there. Otherwise the kernel is the whole call: norm, X0, steps and result (256 x
+// 256 in BF16 60.4 -> 55.7 us).
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_muon_small(const __grid_constant__ SmallGroup g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* xk = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *xm = xk + kSmallOperand, *sq = xm + kSmallOperand;
+  SmallSmem* S = reinterpret_cast<SmallSmem*>(sq + kSmallOperand);
+  volatile int* given_up = &S->given_up;
+  const SmallMatrix& M = g.m[blockIdx.x >> 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool wide = M.cols >= M.rows;
+  const int side = wide ? M.rows : M.cols, lengthwise = wide ? M.cols : M.rows;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&S->loaded), 1);
+    mbar_init(smem_u32(&S->acc_full), 1);
+    mbar_init(smem_u32(&S->mma_done), 1);
+    *given_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&S->tmem_base), kAccCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  const uint64_t limit = wait_limit_ns();
+  const int expire = expire_mode();
+  const bool expire_main = expire == kExpireAll, expire_epi = expire == kExpireAll || expire == kExpireGemmEpilogue;
+  pdl_enter();
+  // Both CTAs give up together: the word is written in both before a barrier that all threads of both pass, and names the
+  // phase, so that every thread leaves behind the same barrier however late it reads the word.
+  auto give_up = [&](int when) {
+    if (lane == 0) {
+      record_error(kErrTimeout);
+      for (uint32_t r = 0; r < 2; ++r)
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S->given_up), r)), "r"(when) : "memory");
+    }
+    __syncwarp();
+  };
+  auto going_on = [&](int when) {
+    const int v = *given_up;
+    return v == 0 || v > when;
+  };
+  if constexpr (MODE != kMuon) {
+    // a warp takes every 16th of the CTA's rows, a lane eight columns; X's rows are xk's lines, and its columns those of xm
+    const int part = warp - 2, n = lane * 8;
+    float v[8][8];
+    if (warp >= 2) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int all = static_cast<int>(rank) * kHalf + i * 16 + part;
+        load_row<MODE>(M.g, static_cast<int64_t>(all) * M.cols + n, all < M.rows ? M.cols - n : 0, M.cols % 8 == 0, v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __fma_rn(static_cast<double>(v[i][j]), static_cast<double>(v[i][j]), sum);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum = __dadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+      if (lane < 2)
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S->sums[rank * 16 + part]), lane)), "d"(sum) : "memory");
+      __syncwarp();
+    }
+    cluster_sync();
+    if (warp >= 2) {
+      double sum = S->sums[lane];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum = __dadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+      const Norm norm = norm_of(sum);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 16 + part, all = static_cast<int>(rank) * kHalf + row, k = all & 63;
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = __fmul_rn(__fmul_rn(v[i][2 * j], norm.s1), norm.s2), x1 = __fmul_rn(__fmul_rn(v[i][2 * j + 1], norm.s1), norm.s2);
+          h[j] = pack_f16x2(all < M.rows && n + 2 * j < M.cols ? x0 : 0.0f, all < M.rows && n + 2 * j + 1 < M.cols ? x1 : 0.0f);
+        }
+        const int at = ((lane & 7) ^ (row & 7)) * 16;
+        *reinterpret_cast<uint4*>(xk + (n >> 6) * kSmallBlock + row * 128 + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128 + at);
+        st_cluster_v4(mapa_shared(to, n >> 7), h[0], h[1], h[2], h[3]);
+      }
+      fence_proxy_async_all();
+    }
+  } else if (warp == 0) {
+    if (elect_one()) {
+      mbar_arrive_expect_tx(smem_u32(&S->loaded), 2 * kSmallOperand);
+      const int at = static_cast<int>(rank) * kHalf;
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t to = smem_u32(xk + b * kSmallBlock + i * 8192);
+          tma_load_2d(to, &M.x, b * 64, at + i * 64, smem_u32(&S->loaded));
+          tma_load_2d(to + kSmallOperand, &M.x, at + i * 64, b * 64, smem_u32(&S->loaded));
+        }
+    }
+    __syncwarp();
+    if (!warp_wait(smem_u32(&S->loaded), 0, limit, expire_main)) give_up(1);
+  }
+  cluster_sync();                                          // X is there in both CTAs
+  bool alive = going_on(1);
+  for (int ph = 0; ph < 3 * g.steps && alive; ++ph) {
+    const int phase = ph % 3;
+    if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer
+      const uint32_t k0 = smem_u32(xk), m0 = smem_u32(xm), s0 = smem_u32(sq);
+      const bool a_mn = phase == 0 && !wide, b_mn = phase == 0 ? !wide : phase == 2 && wide;
+      const uint32_t a0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || wide ? s0 : k0;
+      const uint32_t b0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || !wide ? s0 : m0;
+      const uint32_t idesc = make_idesc_f16(a_mn, b_mn);
+      const int blocks = ((phase == 0 ? lengthwise : side) + 63) / 64;
+      tc_fence_after();
+      if (elect_one()) {
+        for (int b = 0; b < blocks; ++b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock;
+            tc_mma_f16_pair(tmem, a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
+                            b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc, (b | k) != 0 ? 1u : 0u);
+          }
+        tc_commit_pair_mc(smem_u32(&S->acc_full), 0x3);
+      }
+      __syncwarp();
+    } else if (warp >= 2) {
+      // ---------------- epilogue: what becomes the next phase's operand
+      using namespace blk;
+      const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
+      const int all = static_cast<int>(rank) * kHalf + row;                            // of the matrix
+      if (!warp_wait(smem_u32(&S->acc_full), ph & 1, limit, expire_epi)) {
+        give_up(2 + ph);
+      } else {
+        tc_fence_after();
+        const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
+        const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
+        const bool last = ph + 1 == 3 * g.steps;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int n = part * 64 + s * 32;
+          uint8_t* line = (phase == 2 ? xk : sq) + (n >> 6) * kSmallBlock + row * 128;  // K-major place of (row, n ..)
+          const int piece = (n >> 3) & 7;
+          const bool diagonal = all - lane == n;           // it runs through these 32 columns
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
+          tmem_ld_wait();
+          tmem_reg_fence(r);
+          uint4 q[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint4 was = make_uint4(0, 0, 0, 0);
+            uint4* place = reinterpret_cast<uint4*>(line + ((piece + p) ^ (row & 7)) * 16);
+            if (phase == 1) was = *place;                  // A, which B takes the place of
+            const uint32_t h[4] = {was.x, was.y, was.z, was.w};
+            uint32_t out[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = 8 * p + 2 * j;
+              f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
+              if (phase == 1) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+                v = fma2(be, blk::pair(f.x, f.y), v);
+                if (diagonal)
+                  v = add2(v, blk::pair(lane == c ? kA * kFactor : 0.0f, lane == c + 1 ? kA * kFactor : 0.0f));
+              }
+              out[j] = pack_f16x2(lo(v), hi(v));
+            }
+            q[p] = make_uint4(out[0], out[1], out[2], out[3]);
+            *place = q[p];
+          }
+          if (phase == 2 && !last) {                       // and X's columns: those of the CTA that holds them
+            const int k = all & 63;
+            const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128);
+            const uint32_t there = mapa_shared(to, n >> 7);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              st_cluster_v4(there + ((piece + p) ^ (k & 7)) * 16, q[p].x, q[p].y, q[p].z, q[p].w);
+          }
+          if (MODE == kMuon && last && all < M.rows) {
+            uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_all();                           // for the tensor cores of both CTAs
+      }
+    }
+    cluster_sync();
+    alive = going_on(2 + ph);
+  }
+  if constexpr (MODE != kMuon) {                           // X is in xk
+    if (warp >= 2) {
+      const int part = warp - 2, n = lane * 8;
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 16 + part, all = static_cast<int>(rank) * kHalf + row;
+        if (all >= M.rows || n >= M.cols) continue;
+        const uint4 q = *reinterpret_cast<const uint4*>(xk + (n >> 6) * kSmallBlock + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
+        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+          w[j] = alive ? pack_bf16x2(f.x * (1.0f / kFactor), f.y * (1.0f / kFactor)) : 0x7FC07FC0u;
+        }
+        uint16_t* o = M.out + static_cast<int64_t>(all) * M.cols + n;
+        if (M.cols % 8 == 0) {
+          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (n + j < M.cols) o[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+        }
+      }
+    }
+  }
+  if (warp == 1 && rank == 0) {                            // MMAs may be in flight when a wait expired
+    if (elect_one()) tc_commit_pair(smem_u32(&S->mma_done));
+    __syncwarp();
+    mbar_wait(smem_u32(&S->mma_done), 0, kDrainLimitNs);
+  }
+  if (!alive && threadIdx.x == 0) {
+    if (MODE == kMuon) atomicExch(g.expired, 1);
+    const uint64_t t0 = globaltimer_ns();                  // loads too
+    while (globaltimer_ns() - t0 < kSettleNs) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();                 // neither CTA leaves while the other may still write to it or the MMAs read it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kAccCols);
 }
 
 }  // namespace muon
