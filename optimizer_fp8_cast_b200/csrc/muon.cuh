@@ -485,9 +485,12 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_consta
 //   xk   rows 128r .. of X, K-major: four blocks of 64 columns
 //   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns
 //   s    rows 128r .. of A, then of B, K-major
+// A's epilogue leaves (b A + a I) / c in a second accumulator, to which A^2 is added: B's epilogue only scales (read back from s
+// 1.2 us, now 0.5).
 // wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, the other CTA's columns of xm through
 // distributed shared memory.
 constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
+constexpr int kSmallTmem = 512;                           // two accumulators
 constexpr int kSmallThreads = 64 + 32 * 16;               // 16 epilogue warps: a TMEM lane quarter and 64 columns each
 constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 256;
 struct alignas(64) SmallMatrix {
@@ -532,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&S->tmem_base), kAccCols);
+    tmem_alloc_pair(smem_u32(&S->tmem_base), kSmallTmem);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -630,8 +633,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock;
-            tc_mma_f16_pair(tmem, a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
-                            b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc, (b | k) != 0 ? 1u : 0u);
+            tc_mma_f16_pair(tmem + (phase == 1 ? kSmallSide : 0), a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
+                            b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc,
+                            (b | k) != 0 || phase == 1 ? 1u : 0u);
           }
         tc_commit_pair_mc(smem_u32(&S->acc_full), 0x3);
       }
@@ -646,55 +650,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
       } else {
         tc_fence_after();
         const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
-        const f32x2 al = blk::pair(alpha, alpha), be = blk::pair(kB, kB);
+        const f32x2 al = blk::pair(alpha, alpha);
         const bool last = ph + 1 == 3 * g.steps;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int n = part * 64 + s * 32;
           uint8_t* line = (phase == 2 ? xk : sq) + (n >> 6) * kSmallBlock + row * 128;  // K-major place of (row, n ..)
           const int piece = (n >> 3) & 7;
-          const bool diagonal = all - lane == n;           // it runs through these 32 columns
           uint32_t r[32];
           __syncwarp();
-          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
+          tmem_ld_32x32b_x32(tmem + (phase == 1 ? kSmallSide : 0) + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
           tmem_ld_wait();
           tmem_reg_fence(r);
           uint4 q[4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            uint4 was = make_uint4(0, 0, 0, 0);
             uint4* place = reinterpret_cast<uint4*>(line + ((piece + p) ^ (row & 7)) * 16);
-            if (phase == 1) was = *place;                  // A, which B takes the place of
-            const uint32_t h[4] = {was.x, was.y, was.z, was.w};
             uint32_t out[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int c = 8 * p + 2 * j;
-              f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
-              if (phase == 1) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-                v = fma2(be, blk::pair(f.x, f.y), v);
-                if (diagonal)
-                  v = add2(v, blk::pair(lane == c ? kA * kFactor : 0.0f, lane == c + 1 ? kA * kFactor : 0.0f));
-              }
+              const f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
               out[j] = pack_f16x2(lo(v), hi(v));
             }
             q[p] = make_uint4(out[0], out[1], out[2], out[3]);
             *place = q[p];
           }
-          if (phase == 2 && !last) {                       // and X's columns: those of the CTA that holds them
-            const int k = all & 63;
-            const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128);
-            const uint32_t there = mapa_shared(to, n >> 7);
+          if (phase == 0) {                                // where c A^2 is to be added up: b A + a I
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-              st_cluster_v4(there + ((piece + p) ^ (k & 7)) * 16, q[p].x, q[p].y, q[p].z, q[p].w);
+            for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * (kB / kC));
+            if (static_cast<int>(rank) * kHalf + quad * 32 == n) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c == lane) r[c] = __float_as_uint(__uint_as_float(r[c]) + kA / kC * (kFactor * kFactor));
+            }
+            tmem_st_32x32b_x32(tmem + kSmallSide + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
+            tmem_st_wait();
           }
           if (MODE == kMuon && last && all < M.rows) {
             uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
 #pragma unroll
             for (int p = 0; p < 4; ++p)
               if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
+          }
+        }
+        if (phase == 2 && !last) {
+          // and X's columns: a warp's 32 rows x 64 columns lie in xm of the CTA that has them as they do here, and eight lanes
+          // take a line (lines a lane: 1.3 us a step more)
+          const int from = static_cast<int>(rank) * kHalf + quad * 32;
+          const uint8_t* lines = xk + part * kSmallBlock + quad * 4096 + lane * 16;
+          const uint32_t to = mapa_shared(smem_u32(xm + (from >> 6) * kSmallBlock + (part & 1) * 8192 + (from & 63) * 128 + lane * 16), part >> 1);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 q = *reinterpret_cast<const uint4*>(lines + i * 512);
+            st_cluster_v4(to + i * 512, q.x, q.y, q.z, q.w);
           }
         }
         tc_fence_before();
@@ -744,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
   tc_fence_before();
   cluster_sync();                 // neither CTA leaves while the other may still write to it or the MMAs read it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, kAccCols);
+  if (warp == 1) tmem_dealloc_pair(tmem, kSmallTmem);
 }
 
 }  // namespace muon
