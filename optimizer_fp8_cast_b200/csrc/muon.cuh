@@ -485,14 +485,18 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_consta
 //   xk   rows 128r .. of X, K-major: four blocks of 64 columns
 //   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns
 //   s    rows 128r .. of A, then of B, K-major
+// A phase computes the columns 64h .. and 128 + 64h .. (64 each) for h = 0, then h = 1: a CTA's own rows or columns hold the 64 that
+// it brings as the second operand, and the first half's epilogue runs beside the second's MMAs. That needs results elsewhere than
+// the operands: a wide matrix's B takes xk's place and its next X that of s, and they change names every step.
 // A's epilogue leaves (b A + a I) / c in a second accumulator, to which A^2 is added: B's epilogue only scales (read back from s
 // 1.2 us, now 0.5).
-// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, the other CTA's columns of xm through
+// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, xm where its columns are, through
 // distributed shared memory.
 constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
+constexpr int kSmallN = 128;                              // columns of half a phase
 constexpr int kSmallTmem = 512;                           // two accumulators
-constexpr int kSmallThreads = 64 + 32 * 16;               // 16 epilogue warps: a TMEM lane quarter and 64 columns each
-constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 256;
+constexpr int kSmallThreads = 64 + 32 * 16;               // 16 epilogue warps: a TMEM lane quarter and 32 columns of a half each
+constexpr int kSmallSmemBytes = 3 * kSmallOperand + 1024 + 512;
 struct alignas(64) SmallMatrix {
   CUtensorMap x;                   // kMuon: boxes of 64 rows x 64 values of X0
   const void* g;                   // otherwise: the matrix, rows of cols
@@ -507,11 +511,12 @@ struct alignas(64) SmallGroup {
 struct SmallSmem {
   double sums[32];                 // of u^2: the cluster's warps
   uint64_t loaded;                 // X has landed
-  uint64_t acc_full;               // both CTAs: a phase's MMAs have completed
+  uint64_t acc_full[2];            // both CTAs: the MMAs of half a phase's columns have completed
   uint64_t mma_done;
   uint32_t tmem_base;
   int given_up;                    // 2 + the phase in which a wait expired (1: X did not land), 0: none
 };
+static_assert(sizeof(SmallSmem) <= 512, "");
 
 // kMuon: X0 comes from the workspace and X goes back there. Otherwise the kernel is the whole call: norm, X0, steps and result (256 x
 // 256 in BF16 60.4 -> 55.7 us).
@@ -529,7 +534,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
   const int side = wide ? M.rows : M.cols, lengthwise = wide ? M.cols : M.rows;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&S->loaded), 1);
-    mbar_init(smem_u32(&S->acc_full), 1);
+    mbar_init(smem_u32(&S->acc_full[0]), 1);
+    mbar_init(smem_u32(&S->acc_full[1]), 1);
     mbar_init(smem_u32(&S->mma_done), 1);
     *given_up = 0;
     fence_mbar_init();
@@ -619,25 +625,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
   bool alive = going_on(1);
   for (int ph = 0; ph < 3 * g.steps && alive; ++ph) {
     const int phase = ph % 3;
+    const bool swapped = wide && ((ph / 3) & 1);
+    uint8_t *kx = swapped ? sq : xk, *ks = swapped ? xk : sq;
     if (warp == 1 && rank == 0) {
       // ---------------- MMA issuer
-      const uint32_t k0 = smem_u32(xk), m0 = smem_u32(xm), s0 = smem_u32(sq);
+      const uint32_t k0 = smem_u32(kx), m0 = smem_u32(xm), s0 = smem_u32(ks);
       const bool a_mn = phase == 0 && !wide, b_mn = phase == 0 ? !wide : phase == 2 && wide;
-      const uint32_t a0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || wide ? s0 : k0;
+      const uint32_t a0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 ? s0 : k0;
       const uint32_t b0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || !wide ? s0 : m0;
-      const uint32_t idesc = make_idesc_f16(a_mn, b_mn);
+      const uint32_t idesc = make_idesc_f16(a_mn, b_mn, kSmallN);
       const int blocks = ((phase == 0 ? lengthwise : side) + 63) / 64;
       tc_fence_after();
       if (elect_one()) {
-        for (int b = 0; b < blocks; ++b)
+        for (int h = 0; h < 2; ++h) {
+          for (int b = 0; b < blocks; ++b)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock;
-            tc_mma_f16_pair(tmem + (phase == 1 ? kSmallSide : 0), a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
-                            b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc,
-                            (b | k) != 0 || phase == 1 ? 1u : 0u);
-          }
-        tc_commit_pair_mc(smem_u32(&S->acc_full), 0x3);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock + h * 8192;
+              tc_mma_f16_pair(tmem + (phase == 1 ? kSmallSide : 0) + h * kSmallN,
+                              a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
+                              b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc,
+                              (b | k) != 0 || phase == 1 ? 1u : 0u);
+            }
+          tc_commit_pair_mc(smem_u32(&S->acc_full[h]), 0x3);
+        }
       }
       __syncwarp();
     } else if (warp >= 2) {
@@ -645,21 +656,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
       using namespace blk;
       const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
       const int all = static_cast<int>(rank) * kHalf + row;                            // of the matrix
-      if (!warp_wait(smem_u32(&S->acc_full), ph & 1, limit, expire_epi)) {
-        give_up(2 + ph);
-      } else {
-        tc_fence_after();
-        const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
-        const f32x2 al = blk::pair(alpha, alpha);
-        const bool last = ph + 1 == 3 * g.steps;
+      const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
+      const f32x2 al = blk::pair(alpha, alpha);
+      const bool last = ph + 1 == 3 * g.steps;
+      uint8_t* to = phase == 0 || (wide && phase == 2) ? ks : wide || phase == 2 ? kx : ks;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int n = part * 64 + s * 32;
-          uint8_t* line = (phase == 2 ? xk : sq) + (n >> 6) * kSmallBlock + row * 128;  // K-major place of (row, n ..)
+      for (int h = 0; h < 2; ++h) {
+        // a tall matrix's phases 1 and 2 write where the second half's MMAs read
+        bool there = h == 1 && !(wide || phase == 0);
+        if (!there) there = warp_wait(smem_u32(&S->acc_full[h]), ph & 1, limit, expire_epi);
+        if (there && h == 0 && !(wide || phase == 0)) there = warp_wait(smem_u32(&S->acc_full[1]), ph & 1, limit, expire_epi);
+        if (!there) {
+          give_up(2 + ph);
+          break;
+        }
+        tc_fence_after();
+        {
+          const int n = (part >> 1) * 128 + h * 64 + (part & 1) * 32;                  // the columns' place in the matrix
+          const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * kSmallN + part * 32;
+          uint8_t* line = to + (n >> 6) * kSmallBlock + row * 128;                     // K-major place of (row, n ..)
           const int piece = (n >> 3) & 7;
           uint32_t r[32];
           __syncwarp();
-          tmem_ld_32x32b_x32(tmem + (phase == 1 ? kSmallSide : 0) + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
+          tmem_ld_32x32b_x32(acc + (phase == 1 ? kSmallSide : 0), r);
           tmem_ld_wait();
           tmem_reg_fence(r);
           uint4 q[4];
@@ -684,7 +703,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
               for (int c = 0; c < 32; ++c)
                 if (c == lane) r[c] = __float_as_uint(__uint_as_float(r[c]) + kA / kC * (kFactor * kFactor));
             }
-            tmem_st_32x32b_x32(tmem + kSmallSide + (static_cast<uint32_t>(quad * 32) << 16) + n, r);
+            tmem_st_32x32b_x32(acc + kSmallSide, r);
             tmem_st_wait();
           }
           if (MODE == kMuon && last && all < M.rows) {
@@ -693,34 +712,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
             for (int p = 0; p < 4; ++p)
               if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
           }
-        }
-        if (phase == 2 && !last) {
-          // and X's columns: a warp's 32 rows x 64 columns lie in xm of the CTA that has them as they do here, and eight lanes
-          // take a line (lines a lane: 1.3 us a step more)
-          const int from = static_cast<int>(rank) * kHalf + quad * 32;
-          const uint8_t* lines = xk + part * kSmallBlock + quad * 4096 + lane * 16;
-          const uint32_t to = mapa_shared(smem_u32(xm + (from >> 6) * kSmallBlock + (part & 1) * 8192 + (from & 63) * 128 + lane * 16), part >> 1);
-          __syncwarp();
+          if (phase == 2 && !last) {
+            // and X's columns: a warp's 32 rows x 64 bytes lie in xm of the CTA that has them as they do here, and four lanes take
+            // those of a row (a row a lane: 1.3 us a step more)
+            const int from = static_cast<int>(rank) * kHalf + quad * 32, r0 = lane >> 2;
+            const int at = r0 * 128 + ((piece + (lane & 3)) ^ r0) * 16;
+            const uint8_t* lines = to + (n >> 6) * kSmallBlock + quad * 4096 + at;
+            const uint32_t column = mapa_shared(smem_u32(xm + (from >> 6) * kSmallBlock + h * 8192 + (from & 63) * 128 + at), part >> 1);
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 q = *reinterpret_cast<const uint4*>(lines + i * 512);
-            st_cluster_v4(to + i * 512, q.x, q.y, q.z, q.w);
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(lines + i * 1024);
+              st_cluster_v4(column + i * 1024, v.x, v.y, v.z, v.w);
+            }
           }
         }
-        tc_fence_before();
-        fence_proxy_async_all();                           // for the tensor cores of both CTAs
       }
+      tc_fence_before();
+      fence_proxy_async_all();                             // for the tensor cores of both CTAs
     }
     cluster_sync();
     alive = going_on(2 + ph);
   }
-  if constexpr (MODE != kMuon) {                           // X is in xk
+  if constexpr (MODE != kMuon) {
     if (warp >= 2) {
+      const uint8_t* x = wide && (g.steps & 1) ? sq : xk;
       const int part = warp - 2, n = lane * 8;
       for (int i = 0; i < 8; ++i) {
         const int row = i * 16 + part, all = static_cast<int>(rank) * kHalf + row;
         if (all >= M.rows || n >= M.cols) continue;
-        const uint4 q = *reinterpret_cast<const uint4*>(xk + (n >> 6) * kSmallBlock + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
+        const uint4 q = *reinterpret_cast<const uint4*>(x + (n >> 6) * kSmallBlock + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
         const uint32_t h[4] = {q.x, q.y, q.z, q.w};
         uint32_t w[4];
 #pragma unroll
