@@ -512,9 +512,10 @@ struct SmallSmem {
   double sums[32];                 // of u^2: the cluster's warps
   uint64_t loaded;                 // X has landed
   uint64_t acc_full[2];            // both CTAs: the MMAs of half a phase's columns have completed
+  uint64_t ready[2];               // even CTA: the epilogue warps of both have stored that half's results
   uint64_t mma_done;
   uint32_t tmem_base;
-  int given_up;                    // 2 + the phase in which a wait expired (1: X did not land), 0: none
+  int given_up;                    // a wait expired
 };
 static_assert(sizeof(SmallSmem) <= 512, "");
 
@@ -536,6 +537,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     mbar_init(smem_u32(&S->loaded), 1);
     mbar_init(smem_u32(&S->acc_full[0]), 1);
     mbar_init(smem_u32(&S->acc_full[1]), 1);
+    mbar_init(smem_u32(&S->ready[0]), 32);
+    mbar_init(smem_u32(&S->ready[1]), 32);
     mbar_init(smem_u32(&S->mma_done), 1);
     *given_up = 0;
     fence_mbar_init();
@@ -552,19 +555,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
   const int expire = expire_mode();
   const bool expire_main = expire == kExpireAll, expire_epi = expire == kExpireAll || expire == kExpireGemmEpilogue;
   pdl_enter();
-  // Both CTAs give up together: the word is written in both before a barrier that all threads of both pass, and names the
-  // phase, so that every thread leaves behind the same barrier however late it reads the word.
-  auto give_up = [&](int when) {
+  // Both CTAs give up: who waits for one that has done so waits in vain, and all meet behind the steps.
+  auto give_up = [&] {
     if (lane == 0) {
       record_error(kErrTimeout);
       for (uint32_t r = 0; r < 2; ++r)
-        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S->given_up), r)), "r"(when) : "memory");
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S->given_up), r)), "r"(1) : "memory");
     }
     __syncwarp();
-  };
-  auto going_on = [&](int when) {
-    const int v = *given_up;
-    return v == 0 || v > when;
   };
   if constexpr (MODE != kMuon) {
     // a warp takes every 16th of the CTA's rows, a lane eight columns; X's rows are xk's lines, and its columns those of xm
@@ -619,43 +617,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
         }
     }
     __syncwarp();
-    if (!warp_wait(smem_u32(&S->loaded), 0, limit, expire_main)) give_up(1);
+    if (!warp_wait(smem_u32(&S->loaded), 0, limit, expire_main)) give_up();
   }
   cluster_sync();                                          // X is there in both CTAs
-  bool alive = going_on(1);
-  for (int ph = 0; ph < 3 * g.steps && alive; ++ph) {
-    const int phase = ph % 3;
-    const bool swapped = wide && ((ph / 3) & 1);
-    uint8_t *kx = swapped ? sq : xk, *ks = swapped ? xk : sq;
-    if (warp == 1 && rank == 0) {
-      // ---------------- MMA issuer
-      const uint32_t k0 = smem_u32(kx), m0 = smem_u32(xm), s0 = smem_u32(ks);
+  const int phases = *given_up ? 0 : 3 * g.steps;
+  if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer
+    for (int ph = 0; ph < phases; ++ph) {
+      const int phase = ph % 3;
+      const bool swapped = wide && ((ph / 3) & 1);
+      const uint32_t k0 = smem_u32(swapped ? sq : xk), m0 = smem_u32(xm), s0 = smem_u32(swapped ? xk : sq);
       const bool a_mn = phase == 0 && !wide, b_mn = phase == 0 ? !wide : phase == 2 && wide;
       const uint32_t a0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 ? s0 : k0;
       const uint32_t b0 = phase == 0 ? (wide ? k0 : m0) : phase == 1 || !wide ? s0 : m0;
       const uint32_t idesc = make_idesc_f16(a_mn, b_mn, kSmallN);
       const int blocks = ((phase == 0 ? lengthwise : side) + 63) / 64;
-      tc_fence_after();
-      if (elect_one()) {
-        for (int h = 0; h < 2; ++h) {
-          for (int b = 0; b < blocks; ++b)
+      auto multiply = [&](int h, int b) {
+        if (b >= blocks) return;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock + h * 8192;
-              tc_mma_f16_pair(tmem + (phase == 1 ? kSmallSide : 0) + h * kSmallN,
-                              a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
-                              b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc,
-                              (b | k) != 0 || phase == 1 ? 1u : 0u);
-            }
-          tc_commit_pair_mc(smem_u32(&S->acc_full[h]), 0x3);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t a = a0 + b * kSmallBlock, c = b0 + b * kSmallBlock + h * 8192;
+          tc_mma_f16_pair(tmem + (phase == 1 ? kSmallSide : 0) + h * kSmallN,
+                          a_mn ? make_sw128_desc_mn16(a + k * 2048) : make_sw128_desc(a + k * 32),
+                          b_mn ? make_sw128_desc_mn16(c + k * 2048) : make_sw128_desc(c + k * 32), idesc,
+                          (b | k) != 0 || phase == 1 ? 1u : 0u);
         }
+      };
+      bool there = ph == 0 || warp_wait(smem_u32(&S->ready[0]), (ph - 1) & 1, limit, expire_main);
+      if (there && ph > 0 && !wide) there = warp_wait(smem_u32(&S->ready[1]), (ph - 1) & 1, limit, expire_main);
+      tc_fence_after();
+      if (there && elect_one()) {
+        multiply(0, 0);
+        multiply(0, 2);
       }
       __syncwarp();
-    } else if (warp >= 2) {
-      // ---------------- epilogue: what becomes the next phase's operand
-      using namespace blk;
-      const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;       // of this CTA's 128
-      const int all = static_cast<int>(rank) * kHalf + row;                            // of the matrix
+      if (there && ph > 0 && wide) there = warp_wait(smem_u32(&S->ready[1]), (ph - 1) & 1, limit, expire_main);
+      if (!there) {
+        give_up();
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        multiply(0, 1);
+        multiply(0, 3);
+        tc_commit_pair_mc(smem_u32(&S->acc_full[0]), 0x3);
+        for (int b = 0; b < 4; ++b) multiply(1, b);
+        tc_commit_pair_mc(smem_u32(&S->acc_full[1]), 0x3);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 2) {
+    // ---------------- epilogue: what becomes the next phase's operand
+    using namespace blk;
+    const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;         // of this CTA's 128
+    const int all = static_cast<int>(rank) * kHalf + row;                              // of the matrix
+    bool there = true;
+    for (int ph = 0; ph < phases && there; ++ph) {
+      const int phase = ph % 3;
+      const bool swapped = wide && ((ph / 3) & 1);
+      uint8_t *kx = swapped ? sq : xk, *ks = swapped ? xk : sq;
       const float alpha = (phase == 1 ? kC : 1.0f) / kFactor;
       const f32x2 al = blk::pair(alpha, alpha);
       const bool last = ph + 1 == 3 * g.steps;
@@ -663,77 +683,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // a tall matrix's phases 1 and 2 write where the second half's MMAs read
-        bool there = h == 1 && !(wide || phase == 0);
-        if (!there) there = warp_wait(smem_u32(&S->acc_full[h]), ph & 1, limit, expire_epi);
-        if (there && h == 0 && !(wide || phase == 0)) there = warp_wait(smem_u32(&S->acc_full[1]), ph & 1, limit, expire_epi);
+        if (there) there = warp_wait(smem_u32(&S->acc_full[h]), ph & 1, limit, expire_epi);
+        if (there && h == 0 && !wide && phase > 0) there = warp_wait(smem_u32(&S->acc_full[1]), ph & 1, limit, expire_epi);
         if (!there) {
-          give_up(2 + ph);
+          give_up();
           break;
         }
         tc_fence_after();
-        {
-          const int n = (part >> 1) * 128 + h * 64 + (part & 1) * 32;                  // the columns' place in the matrix
-          const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * kSmallN + part * 32;
-          uint8_t* line = to + (n >> 6) * kSmallBlock + row * 128;                     // K-major place of (row, n ..)
-          const int piece = (n >> 3) & 7;
-          uint32_t r[32];
+        const int n = (part >> 1) * 128 + h * 64 + (part & 1) * 32;                  // the columns' place in the matrix
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * kSmallN + part * 32;
+        uint8_t* line = to + (n >> 6) * kSmallBlock + row * 128;                     // K-major place of (row, n ..)
+        const int piece = (n >> 3) & 7;
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(acc + (phase == 1 ? kSmallSide : 0), r);
+        tmem_ld_wait();
+        tmem_reg_fence(r);
+        uint4 q[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint4* place = reinterpret_cast<uint4*>(line + ((piece + p) ^ (row & 7)) * 16);
+          uint32_t out[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = 8 * p + 2 * j;
+            const f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
+            out[j] = pack_f16x2(lo(v), hi(v));
+          }
+          q[p] = make_uint4(out[0], out[1], out[2], out[3]);
+          *place = q[p];
+        }
+        if (phase == 0) {                                // where c A^2 is to be added up: b A + a I
+#pragma unroll
+          for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * (kB / kC));
+          if (static_cast<int>(rank) * kHalf + quad * 32 == n) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c == lane) r[c] = __float_as_uint(__uint_as_float(r[c]) + kA / kC * (kFactor * kFactor));
+          }
+          tmem_st_32x32b_x32(acc + kSmallSide, r);
+          tmem_st_wait();
+        }
+        if (MODE == kMuon && last && all < M.rows) {
+          uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
+        }
+        if (phase == 2 && !last) {
+          // and X's columns: a warp's 32 rows x 64 bytes lie in xm of the CTA that has them as they do here, and four lanes take
+          // those of a row (a row a lane: 1.3 us a step more)
+          const int from = static_cast<int>(rank) * kHalf + quad * 32, r0 = lane >> 2;
+          const int at = r0 * 128 + ((piece + (lane & 3)) ^ r0) * 16;
+          const uint8_t* lines = to + (n >> 6) * kSmallBlock + quad * 4096 + at;
+          const uint32_t column = mapa_shared(smem_u32(xm + (from >> 6) * kSmallBlock + h * 8192 + (from & 63) * 128 + at), part >> 1);
           __syncwarp();
-          tmem_ld_32x32b_x32(acc + (phase == 1 ? kSmallSide : 0), r);
-          tmem_ld_wait();
-          tmem_reg_fence(r);
-          uint4 q[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint4* place = reinterpret_cast<uint4*>(line + ((piece + p) ^ (row & 7)) * 16);
-            uint32_t out[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int c = 8 * p + 2 * j;
-              const f32x2 v = mul2(blk::pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), al);
-              out[j] = pack_f16x2(lo(v), hi(v));
-            }
-            q[p] = make_uint4(out[0], out[1], out[2], out[3]);
-            *place = q[p];
-          }
-          if (phase == 0) {                                // where c A^2 is to be added up: b A + a I
-#pragma unroll
-            for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * (kB / kC));
-            if (static_cast<int>(rank) * kHalf + quad * 32 == n) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c == lane) r[c] = __float_as_uint(__uint_as_float(r[c]) + kA / kC * (kFactor * kFactor));
-            }
-            tmem_st_32x32b_x32(acc + kSmallSide, r);
-            tmem_st_wait();
-          }
-          if (MODE == kMuon && last && all < M.rows) {
-            uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-              if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
-          }
-          if (phase == 2 && !last) {
-            // and X's columns: a warp's 32 rows x 64 bytes lie in xm of the CTA that has them as they do here, and four lanes take
-            // those of a row (a row a lane: 1.3 us a step more)
-            const int from = static_cast<int>(rank) * kHalf + quad * 32, r0 = lane >> 2;
-            const int at = r0 * 128 + ((piece + (lane & 3)) ^ r0) * 16;
-            const uint8_t* lines = to + (n >> 6) * kSmallBlock + quad * 4096 + at;
-            const uint32_t column = mapa_shared(smem_u32(xm + (from >> 6) * kSmallBlock + h * 8192 + (from & 63) * 128 + at), part >> 1);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 v = *reinterpret_cast<const uint4*>(lines + i * 1024);
-              st_cluster_v4(column + i * 1024, v.x, v.y, v.z, v.w);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(lines + i * 1024);
+            st_cluster_v4(column + i * 1024, v.x, v.y, v.z, v.w);
           }
         }
+        tc_fence_before();
+        fence_proxy_async_all();                           // for the tensor cores of both CTAs
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->ready[h]), 0));
       }
-      tc_fence_before();
-      fence_proxy_async_all();                             // for the tensor cores of both CTAs
     }
-    cluster_sync();
-    alive = going_on(2 + ph);
   }
+  __syncwarp();
+  cluster_sync();
+  const bool alive = *given_up == 0;
   if constexpr (MODE != kMuon) {
     if (warp >= 2) {
       const uint8_t* x = wide && (g.steps & 1) ? sq : xk;
