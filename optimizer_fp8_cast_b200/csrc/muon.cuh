@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_consta
 // the operands: a wide matrix's B takes xk's place and its next X that of s, and they change names every step.
 // A's epilogue leaves (b A + a I) / c in a second accumulator, to which A^2 is added: B's epilogue only scales (read back from s
 // 1.2 us, now 0.5).
-// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes both forms, xm where its columns are, through
-// distributed shared memory.
+// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes xk, and a warp
+// beside it sends xm's lines to the CTA that has these columns, through distributed shared memory.
 constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
 constexpr int kSmallN = 128;                              // columns of half a phase
 constexpr int kSmallTmem = 512;                           // two accumulators
@@ -513,6 +513,9 @@ struct SmallSmem {
   uint64_t loaded;                 // X has landed
   uint64_t acc_full[2];            // both CTAs: the MMAs of half a phase's columns have completed
   uint64_t ready[2];               // even CTA: the epilogue warps of both have stored that half's results
+  uint64_t lines[2];               // this CTA's epilogue warps have stored that half of X
+  uint64_t sent;                   // the other CTA's lines of xm have come
+  uint64_t columns;                // even CTA: xm is there in both
   uint64_t mma_done;
   uint32_t tmem_base;
   int given_up;                    // a wait expired
@@ -537,6 +540,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     mbar_init(smem_u32(&S->loaded), 1);
     mbar_init(smem_u32(&S->acc_full[0]), 1);
     mbar_init(smem_u32(&S->acc_full[1]), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&S->lines[i]), 16);
+    mbar_init(smem_u32(&S->sent), 1);
+    mbar_init(smem_u32(&S->columns), 2);
     mbar_init(smem_u32(&S->ready[0]), 32);
     mbar_init(smem_u32(&S->ready[1]), 32);
     mbar_init(smem_u32(&S->mma_done), 1);
@@ -621,7 +627,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
   }
   cluster_sync();                                          // X is there in both CTAs
   const int phases = *given_up ? 0 : 3 * g.steps;
-  if (warp == 1 && rank == 0) {
+  if (warp == 0) {
+    // ---------------- X's columns: lines of xk lie in xm of the CTA that has them as they do here
+    bool there = true;
+    for (int step = 0; 3 * (step + 1) < phases && there; ++step) {
+      const uint8_t* x = wide && !(step & 1) ? sq : xk;    // the step's result
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&S->sent), kSmallOperand / 2);
+      for (int h = 0; h < 2 && there; ++h) {
+        there = warp_wait(smem_u32(&S->lines[h]), step & 1, limit, expire_epi);
+        if (!there) break;
+        for (int i = 0; i < 2; ++i) {                      // 64 rows x 64 columns: the other CTA's, and this one's
+          const int at = (static_cast<int>(rank) * 2 + i) * kSmallBlock + h * 8192;
+          const uint8_t* from = x + h * kSmallBlock + i * 8192;
+          if (lane == 0)
+            bulk_copy_cluster(mapa_shared(smem_u32(xm + at), rank ^ 1), smem_u32(from + (rank ^ 1) * 2 * kSmallBlock), 8192,
+                              mapa_shared(smem_u32(&S->sent), rank ^ 1));
+          const uint4* own = reinterpret_cast<const uint4*>(from + rank * 2 * kSmallBlock) + lane;
+          uint4* to = reinterpret_cast<uint4*>(xm + at) + lane;
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = own[(j + k) * 32];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[(j + k) * 32] = v[k];
+          }
+        }
+      }
+      if (there) there = warp_wait(smem_u32(&S->sent), step & 1, limit, expire_epi);
+      if (!there) {
+        give_up();
+        break;
+      }
+      fence_proxy_async_all();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->columns), 0));
+    }
+  } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer
     for (int ph = 0; ph < phases; ++ph) {
       const int phase = ph % 3;
@@ -644,6 +686,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
         }
       };
       bool there = ph == 0 || warp_wait(smem_u32(&S->ready[0]), (ph - 1) & 1, limit, expire_main);
+      // xm has come: a tall matrix's phase 0 reads it, a wide one's phase 1 lets its lines in xk be written over
+      if (there && ph >= 3 && phase == (wide ? 1 : 0)) there = warp_wait(smem_u32(&S->columns), (ph / 3 - 1) & 1, limit, expire_main);
       if (there && ph > 0 && !wide) there = warp_wait(smem_u32(&S->ready[1]), (ph - 1) & 1, limit, expire_main);
       tc_fence_after();
       if (there && elect_one()) {
@@ -719,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
           if (static_cast<int>(rank) * kHalf + quad * 32 == n) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c == lane) r[c] = __float_as_uint(__uint_as_float(r[c]) + kA / kC * (kFactor * kFactor));
+              r[c] = __float_as_uint(__uint_as_float(r[c]) + (c == lane ? kA / kC * (kFactor * kFactor) : 0.0f));
           }
           tmem_st_32x32b_x32(acc + kSmallSide, r);
           tmem_st_wait();
@@ -730,24 +774,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
           for (int p = 0; p < 4; ++p)
             if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
         }
-        if (phase == 2 && !last) {
-          // and X's columns: a warp's 32 rows x 64 bytes lie in xm of the CTA that has them as they do here, and four lanes take
-          // those of a row (a row a lane: 1.3 us a step more)
-          const int from = static_cast<int>(rank) * kHalf + quad * 32, r0 = lane >> 2;
-          const int at = r0 * 128 + ((piece + (lane & 3)) ^ r0) * 16;
-          const uint8_t* lines = to + (n >> 6) * kSmallBlock + quad * 4096 + at;
-          const uint32_t column = mapa_shared(smem_u32(xm + (from >> 6) * kSmallBlock + h * 8192 + (from & 63) * 128 + at), part >> 1);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(lines + i * 1024);
-            st_cluster_v4(column + i * 1024, v.x, v.y, v.z, v.w);
-          }
-        }
         tc_fence_before();
         fence_proxy_async_all();                           // for the tensor cores of both CTAs
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&S->ready[h]), 0));
+        if (lane == 0) {
+          mbar_arrive_cluster(mapa_shared(smem_u32(&S->ready[h]), 0));
+          if (phase == 2 && !last) mbar_arrive(smem_u32(&S->lines[h]));
+        }
       }
     }
   }
