@@ -480,18 +480,22 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_consta
 // ------------------------------------------------------------------ small matrices
 // Up to 256 x 256: one CTA pair keeps a matrix in shared memory over all steps. The phases of the grid-wide form have little to do
 // there (6.4 us each, of which the MMAs are one: barrier, first loads, stores); here the epilogue writes the next phase's
-// operand where the tensor cores read it, and a phase ends with the pair's own barrier (256 x 256 97 -> 60 us a call).
+// operand where the tensor cores read it (256 x 256: fifteen launches 142 us a call, grid-wide 97, here 39.5; 1.9 us a phase, of
+// which the tensor cores compute 1.1).
 // CTA r holds (FP16, 128-byte swizzle, zeros past the matrix):
 //   xk   rows 128r .. of X, K-major: four blocks of 64 columns
 //   xm   columns 128r .. of X, all rows, MN-major: four blocks of 64 rows, each two boxes of 64 columns
 //   s    rows 128r .. of A, then of B, K-major
+// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s.
 // A phase computes the columns 64h .. and 128 + 64h .. (64 each) for h = 0, then h = 1: a CTA's own rows or columns hold the 64 that
-// it brings as the second operand, and the first half's epilogue runs beside the second's MMAs. That needs results elsewhere than
-// the operands: a wide matrix's B takes xk's place and its next X that of s, and they change names every step.
-// A's epilogue leaves (b A + a I) / c in a second accumulator, to which A^2 is added: B's epilogue only scales (read back from s
-// 1.2 us, now 0.5).
-// wide: A = xk xk^T, X <- s xm;  tall: A = xm^T xm, X <- xk s. X's epilogue writes xk, and a warp
-// beside it sends xm's lines to the CTA that has these columns, through distributed shared memory.
+// it brings as the second operand, and the first half's epilogue runs beside the second's MMAs (50.8 -> 47.9 us). For that a wide
+// matrix's results go elsewhere than its operands: B takes xk's place and the next X that of s, and they change names every step;
+// the next phase's MMAs start with the half that is there (47.7 -> 45.8). A tall one waits for both halves.
+// A's epilogue leaves (b A + a I) / c in a second accumulator, to which A^2 is added, so that B's only scales (55.5 -> 50.6, with
+// A read back from s before).
+// X's epilogue writes xk. Its lines lie in xm of the CTA that has their columns just as they do here: an otherwise idle warp
+// brings them there, the other CTA's by asynchronous copies (46.0 -> 40.1; the epilogue's own stores of them took 0.7 us a half,
+// and all of them by that warp's stores 5 us a step).
 constexpr int kSmallSide = 256, kSmallBlock = 16384, kSmallOperand = 4 * kSmallBlock;
 constexpr int kSmallN = 128;                              // columns of half a phase
 constexpr int kSmallTmem = 512;                           // two accumulators
@@ -522,8 +526,8 @@ struct SmallSmem {
 };
 static_assert(sizeof(SmallSmem) <= 512, "");
 
-// kMuon: X0 comes from the workspace and X goes back there. Otherwise the kernel is the whole call: norm, X0, steps and result (256 x
-// 256 in BF16 60.4 -> 55.7 us).
+// kMuon: X0 comes from the workspace and X goes back there. Otherwise the kernel is the whole call: norm, X0, steps and result, 8 us of
+// it where the four passes around the steps took 13.
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_muon_small(const __grid_constant__ SmallGroup g) {
   extern __shared__ uint8_t smem_raw[];
@@ -571,18 +575,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     __syncwarp();
   };
   if constexpr (MODE != kMuon) {
-    // a warp takes every 16th of the CTA's rows, a lane eight columns; X's rows are xk's lines, and its columns those of xm
+    // a warp takes every 16th of the CTA's rows, a lane eight columns
     const int part = warp - 2, n = lane * 8;
     float v[8][8];
     if (warp >= 2) {
-      double sum = 0.0;
+      // A thread's 64 squares in f32 where they are in its range (their sum is off by at most 2^-20, of which the norm has half
+      // and X0's FP16 rounds 2^-11 away); FP64 throughout took 1 us more.
+      float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int all = static_cast<int>(rank) * kHalf + i * 16 + part;
         load_row<MODE>(M.g, static_cast<int64_t>(all) * M.cols + n, all < M.rows ? M.cols - n : 0, M.cols % 8 == 0, v[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __fma_rn(static_cast<double>(v[i][j]), static_cast<double>(v[i][j]), sum);
+        for (int j = 0; j < 8; ++j) part4[j & 3] = __fmaf_rn(v[i][j], v[i][j], part4[j & 3]);
       }
+      const float squares = __fadd_rn(__fadd_rn(part4[0], part4[1]), __fadd_rn(part4[2], part4[3]));
+      double sum = static_cast<double>(squares);
+      if (!(squares >= 0x1p-60f && squares <= 0x1p100f)) {
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum = __fma_rn(static_cast<double>(v[i][j]), static_cast<double>(v[i][j]), sum);
+      }
+      __syncwarp();
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum = __dadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
       if (lane < 2)
@@ -597,16 +613,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
       const Norm norm = norm_of(sum);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int row = i * 16 + part, all = static_cast<int>(rank) * kHalf + row, k = all & 63;
+        const int row = i * 16 + part;
         uint32_t h[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float x0 = __fmul_rn(__fmul_rn(v[i][2 * j], norm.s1), norm.s2), x1 = __fmul_rn(__fmul_rn(v[i][2 * j + 1], norm.s1), norm.s2);
-          h[j] = pack_f16x2(all < M.rows && n + 2 * j < M.cols ? x0 : 0.0f, all < M.rows && n + 2 * j + 1 < M.cols ? x1 : 0.0f);
+          h[j] = pack_f16x2(x0, x1);                       // zeros past the matrix, or all of it NaN
         }
         const int at = ((lane & 7) ^ (row & 7)) * 16;
         *reinterpret_cast<uint4*>(xk + (n >> 6) * kSmallBlock + row * 128 + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + k * 128 + at);
+        const int all = static_cast<int>(rank) * kHalf + row;
+        const uint32_t to = smem_u32(xm + (all >> 6) * kSmallBlock + ((n & 127) >> 6) * 8192 + (all & 63) * 128 + at);
         st_cluster_v4(mapa_shared(to, n >> 7), h[0], h[1], h[2], h[3]);
       }
       fence_proxy_async_all();
@@ -714,7 +731,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     // ---------------- epilogue: what becomes the next phase's operand
     using namespace blk;
     const int quad = warp & 3, part = (warp - 2) >> 2, row = quad * 32 + lane;         // of this CTA's 128
-    const int all = static_cast<int>(rank) * kHalf + row;                              // of the matrix
     bool there = true;
     for (int ph = 0; ph < phases && there; ++ph) {
       const int phase = ph % 3;
@@ -768,12 +784,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
           tmem_st_32x32b_x32(acc + kSmallSide, r);
           tmem_st_wait();
         }
-        if (MODE == kMuon && last && all < M.rows) {
-          uint16_t* o = M.out + static_cast<int64_t>(all) * M.pitch + n;
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-            if (n + 8 * p < M.cols) *reinterpret_cast<uint4*>(o + 8 * p) = q[p];      // within the pitch, a multiple of 8
-        }
         tc_fence_before();
         fence_proxy_async_all();                           // for the tensor cores of both CTAs
         __syncwarp();
@@ -787,22 +797,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
   __syncwarp();
   cluster_sync();
   const bool alive = *given_up == 0;
-  if constexpr (MODE != kMuon) {
-    if (warp >= 2) {
-      const uint8_t* x = wide && (g.steps & 1) ? sq : xk;
-      const int part = warp - 2, n = lane * 8;
-      for (int i = 0; i < 8; ++i) {
-        const int row = i * 16 + part, all = static_cast<int>(rank) * kHalf + row;
-        if (all >= M.rows || n >= M.cols) continue;
-        const uint4 q = *reinterpret_cast<const uint4*>(x + (n >> 6) * kSmallBlock + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
-        const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+  if (warp >= 2) {
+    // ---------------- the result, a warp a row
+    const uint8_t* x = wide && (g.steps & 1) ? sq : xk;
+    const int pitch = MODE == kMuon ? M.pitch : M.cols, n = lane * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = i * 16 + warp - 2, all = static_cast<int>(rank) * kHalf + row;
+      if (all >= M.rows || n >= M.cols) continue;
+      uint16_t* o = M.out + static_cast<int64_t>(all) * pitch + n;
+      const uint4 q = *reinterpret_cast<const uint4*>(x + (n >> 6) * kSmallBlock + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
+      if constexpr (MODE == kMuon) {
+        *reinterpret_cast<uint4*>(o) = q;                  // within the pitch, a multiple of 8
+      } else {
+        const uint32_t f[4] = {q.x, q.y, q.z, q.w};
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-          w[j] = alive ? pack_bf16x2(f.x * (1.0f / kFactor), f.y * (1.0f / kFactor)) : 0x7FC07FC0u;
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+          w[j] = alive ? pack_bf16x2(v.x * (1.0f / kFactor), v.y * (1.0f / kFactor)) : 0x7FC07FC0u;
         }
-        uint16_t* o = M.out + static_cast<int64_t>(all) * M.cols + n;
         if (M.cols % 8 == 0) {
           *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
@@ -813,20 +827,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
       }
     }
   }
-  if (warp == 1 && rank == 0) {                            // MMAs may be in flight when a wait expired
-    if (elect_one()) tc_commit_pair(smem_u32(&S->mma_done));
-    __syncwarp();
-    mbar_wait(smem_u32(&S->mma_done), 0, kDrainLimitNs);
-  }
-  if (!alive && threadIdx.x == 0) {
-    if (MODE == kMuon) atomicExch(g.expired, 1);
-    const uint64_t t0 = globaltimer_ns();                  // loads too
-    while (globaltimer_ns() - t0 < kSettleNs) {
+  if (!alive) {
+    if (warp == 1 && rank == 0) {                          // MMAs may be in flight
+      if (elect_one()) tc_commit_pair(smem_u32(&S->mma_done));
+      __syncwarp();
+      mbar_wait(smem_u32(&S->mma_done), 0, kDrainLimitNs);
+    }
+    if (threadIdx.x == 0) {
+      if (MODE == kMuon) atomicExch(g.expired, 1);
+      const uint64_t t0 = globaltimer_ns();                // loads and copies too
+      while (globaltimer_ns() - t0 < kSettleNs) {
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();                 // neither CTA leaves while the other may still write to it or the MMAs read it
+  cluster_arrive();               // neither CTA leaves while the other may still write to it or the MMAs read it; a release would
+  cluster_wait();                 // wait for the result's stores
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, kSmallTmem);
 }
