@@ -164,10 +164,9 @@ struct Forward : Base {
   template <class Release, class Ahead>
   static __device__ __forceinline__ bool epilogue(const Params& g, const Work& w, int, const Scalars& k, Out& o, int row0, int half,
                                                   uint32_t t_base, Release&& release, Ahead&&) {
-    const int steps = w.half_n / 64;
 #pragma unroll 1
-    for (int s = 0; s < steps; ++s) {
-      const int c = (half * steps + s) * 32, n = w.nt * w.half_n + c;
+    for (int c = half * 32; c < w.half_n; c += 64) {
+      const int n = w.nt * w.half_n + c;
       uint32_t rg[32], ru[32];
       __syncwarp();                                        // one lane stored the chunk before
       tmem_ld_32x32b_x32(t_base + c, rg);
@@ -175,7 +174,7 @@ struct Forward : Base {
       tmem_ld_wait();
       tmem_reg_fence(rg);
       tmem_reg_fence(ru);
-      if (s + 1 == steps) release();
+      if (c + 64 >= w.half_n) release();
       if (n >= g.N || row0 >= g.M) continue;               // chunk entirely outside the matrix
       f32x2 gv[16], uv[16];
       scaled(rg, k.alpha, gv);

@@ -159,7 +159,7 @@ struct Work {
   const CUtensorMap *a, *b;
   int a_row, b_row;                // first row of A and of B that this CTA holds
   int mt, nt;                      // row and column tile
-  int half_n;                      // rows of B that each CTA holds: 128, or 64 for tiles of 128 columns (not of MN-major FP8)
+  int half_n;                      // rows of B that each CTA holds: 128; 64 or, of FP8, 96 for narrower tiles (not of MN-major FP8)
   int num_kb;
   int a_mn, b_mn;                  // 1: operand stored MN-major
   uint32_t idesc;
