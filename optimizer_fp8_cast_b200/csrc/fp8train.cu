@@ -1833,20 +1833,35 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int outputs, 
   return st;
 }
 // Few rows: always up to eight, and while the weights, read once for every eight rows, are small. Few-rows kernel / pair tiles,
-// graph replays: 8 x 4096 -> 2 x 11008 24.5 / 28.8 us (W in x out), 21.3 / 29.4 (out x in); 16 rows 36.5 / 28.2 and 33.7 / 28.4;
-// 16 x 1024 -> 2 x 2752 (11 MB) 8.2 / 7.8 and 3.8 / 7.8; 32 x 256 -> 2 x 688 4.1 / 6.1 and 2.3 / 5.8.
+// graph replays: 8 x 4096 -> 2 x 11008 19.9 / 28.8 us (W in x out), 21.3 / 29.4 (out x in); 16 rows 36.5 (in 64 outputs a CTA) /
+// 28.2 and 33.7 / 28.4; 16 x 1024 -> 2 x 2752 (11 MB) 7.5 / 7.8 and 3.8 / 7.8; 32 x 256 -> 2 x 688 3.4 / 6.1 and 2.3 / 5.8.
 bool gated_few_rows(const fp8t_gated& d) {
   const int64_t groups = (d.M + 7) / 8, most = d.b_layout == FP8T_MN_MAJOR ? int64_t(8) << 20 : int64_t(16) << 20;
   return groups == 1 || (d.M <= 32 && groups * 2 * d.N * d.K <= most);
 }
-template <int WF, int AF>
-fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, cudaStream_t stream) {
+// Chunks of a warp's ring for tiles of 32 G outputs: 144 to 192 KB of a CTA.
+constexpr int gated_ring(int g) { return g == 1 ? 9 : g == 2 ? 5 : 3; }
+template <int WF, int AF, int G>
+fp8t_status launch_gated_rows_mn(const fp8t::gated::RowParams& p, cudaLaunchConfig_t& cfg) {
   using namespace fp8t::gated;
-  const int per = mn ? 64 : 16, chunks = mn ? (p.K + 31) / 32 : (p.K + 63) / 64;
+  RowMnParams P = {};
+  P.p = p;
+  P.ring = gated_ring(G);
+  const int warps = std::min(kRowWarps, (p.K + 31) / 32);
+  cfg.gridDim.x = static_cast<unsigned>((p.N + 32 * G - 1) / (32 * G));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
+  cfg.dynamicSmemBytes = row_smem_bytes(G, P.ring, warps);
+  const fp8t_status st = encode_2d(&P.w, p.w, p.K, 2 * static_cast<int64_t>(p.N), 2 * static_cast<int64_t>(p.N), 1, 32, 32 * G,
+                                   G == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (st == FP8T_OK) (void)cudaLaunchKernelEx(&cfg, k_gated_rows_mn<WF, AF, G>, P);
+  return st;
+}
+template <int WF, int AF>
+fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, int sms, cudaStream_t stream) {
+  using namespace fp8t::gated;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.N + per - 1) / per), static_cast<unsigned>((p.M + kRowTokens - 1) / kRowTokens), 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(32 * std::min(kRowWarps, chunks)), 1, 1);
-  cfg.dynamicSmemBytes = mn ? kRowSmemBytes : 0;
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N + 15) / 16), static_cast<unsigned>((p.M + kRowTokens - 1) / kRowTokens), 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * std::min(kRowWarps, (p.K + 63) / 64)), 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute early[1];
   early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1857,16 +1872,36 @@ fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, cudaS
     (void)cudaLaunchKernelEx(&cfg, k_gated_rows<WF, AF>, p);
     return FP8T_OK;
   }
-  RowMnParams P = {};
-  P.p = p;
-  const fp8t_status st = encode_2d(&P.w, p.w, p.K, 2 * static_cast<int64_t>(p.N), 2 * static_cast<int64_t>(p.N), 1, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B);
-  if (st == FP8T_OK) (void)cudaLaunchKernelEx(&cfg, k_gated_rows_mn<WF, AF>, P);
-  return st;
+  // Tiles for which the SMs' rounds take the least time, a CTA an SM: its time goes with the width, and something for its start.
+  // The ring keeps a second CTA out: it would be the next call's, and take a place that the scheduler then fills unevenly (1 x 4096
+  // -> 2 x 11008 in 172 tiles of 64, two an SM, 23.0 us; in 115 of 96 18.3).
+  const int64_t groups = cfg.gridDim.y;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int g = 1; g <= 4; ++g) {
+    const int64_t cost = ((p.N + 32 * g - 1) / (32 * g) * groups + sms - 1) / sms * (2 * g + 1);
+    if (cost < least) least = cost, best = g;
+  }
+  switch (best) {
+    case 1: return launch_gated_rows_mn<WF, AF, 1>(p, cfg);
+    case 2: return launch_gated_rows_mn<WF, AF, 2>(p, cfg);
+    case 3: return launch_gated_rows_mn<WF, AF, 3>(p, cfg);
+    default: return launch_gated_rows_mn<WF, AF, 4>(p, cfg);
+  }
+}
+template <int WF, int AF, int G>
+cudaError_t allow_gated_rows_smem_of() {
+  using namespace fp8t::gated;
+  return cudaFuncSetAttribute(k_gated_rows_mn<WF, AF, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              row_smem_bytes(G, gated_ring(G), kRowWarps));
 }
 template <int WF, int AF>
 cudaError_t allow_gated_rows_smem() {
-  return cudaFuncSetAttribute(fp8t::gated::k_gated_rows_mn<WF, AF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fp8t::gated::kRowSmemBytes);
+  cudaError_t e;
+  if ((e = allow_gated_rows_smem_of<WF, AF, 1>()) != cudaSuccess || (e = allow_gated_rows_smem_of<WF, AF, 2>()) != cudaSuccess ||
+      (e = allow_gated_rows_smem_of<WF, AF, 3>()) != cudaSuccess)
+    return e;
+  return allow_gated_rows_smem_of<WF, AF, 4>();
 }
 fp8t_status ready_gated_rows(DeviceInfo* d) {
   return once_per_device(d->gated_rows_ready, "fp8_gated_gemm", [] {
@@ -1877,7 +1912,7 @@ fp8t_status ready_gated_rows(DeviceInfo* d) {
     return allow_gated_rows_smem<1, 1>();
   });
 }
-fp8t_status launch_gated_rows(const fp8t_gated& d, cudaStream_t stream) {
+fp8t_status launch_gated_rows(const fp8t_gated& d, int sms, cudaStream_t stream) {
   fp8t::gated::RowParams p = {};
   p.a = static_cast<const uint8_t*>(d.A);
   p.w = static_cast<const uint8_t*>(d.B);
@@ -1895,8 +1930,8 @@ fp8t_status launch_gated_rows(const fp8t_gated& d, cudaStream_t stream) {
   p.act = d.act;
   p.fmt = d.q_fmt;
   const bool mn = d.b_layout == FP8T_MN_MAJOR, w5 = d.b_fmt == FP8T_E5M2, a5 = d.a_fmt == FP8T_E5M2;
-  const fp8t_status st = w5 ? (a5 ? launch_gated_rows_as<1, 1>(p, mn, stream) : launch_gated_rows_as<1, 0>(p, mn, stream))
-                            : (a5 ? launch_gated_rows_as<0, 1>(p, mn, stream) : launch_gated_rows_as<0, 0>(p, mn, stream));
+  const fp8t_status st = w5 ? (a5 ? launch_gated_rows_as<1, 1>(p, mn, sms, stream) : launch_gated_rows_as<1, 0>(p, mn, sms, stream))
+                            : (a5 ? launch_gated_rows_as<0, 1>(p, mn, sms, stream) : launch_gated_rows_as<0, 0>(p, mn, sms, stream));
   return st != FP8T_OK ? st : after_launch("fp8_gated_gemm launch");
 }
 
@@ -1942,7 +1977,7 @@ fp8t_status fp8_gated_gemm(const fp8t_gated* desc, void* stream) {
   if (!d.gu_bf16 && !d.h_bf16 && !d.q) return fail(FP8T_ERR_INVALID_ARG, "fp8_gated_gemm: no output asked for");
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != FP8T_OK) return st;
-  if (gated_few_rows(d)) return (st = ready_gated_rows(dev)) != FP8T_OK ? st : launch_gated_rows(d, as_stream(stream));
+  if (gated_few_rows(d)) return (st = ready_gated_rows(dev)) != FP8T_OK ? st : launch_gated_rows(d, dev->sms, as_stream(stream));
   if ((st = ready_pair(dev)) != FP8T_OK) return st;
   fp8t::gated::Params p = {};
   if ((st = fill_gated(p, c, 128, dev)) != FP8T_OK) return st;

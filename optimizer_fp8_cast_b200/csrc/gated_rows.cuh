@@ -6,9 +6,9 @@
 // 8 tokens; FP32 accumulators. A warp's lanes load the weights straight into the operand's registers; which of a lane's own k
 // goes into which place of the MMA is free as long as A is taken in the same order:
 //   W as [2N][K]  a lane holds 16 consecutive k of a row, lanes 4g .. 4g + 3 a chunk of 64: two MMAs of two words each
-//   W as [K][2N]  a lane holds 8 consecutive outputs of four rows of k: a 4 x 4 byte transpose (8 byte permutations for 16
-//                 weights) makes the words of four k, and the MMA's row g is output 8g + j of the j-th MMA
-// The warps of a CTA take the chunks of K in turn, the next one's loads on their way during a chunk's arithmetic, and add up in shared
+//   W as [K][2N]  a lane holds 4 consecutive outputs of four rows of k: a 4 x 4 byte transpose (8 byte permutations for 16
+//                 weights) makes the words of four k, and the MMA's row g is output 4g + j of the j-th MMA
+// The warps of a CTA take the chunks of K in turn, the next ones' loads on their way during a chunk's arithmetic, and add up in shared
 // memory in warp order. More than eight tokens: a CTA for each eight, which finds the weights in L2; that pays while they are few.
 #pragma once
 
@@ -158,95 +158,116 @@ __device__ __forceinline__ void transpose4(const uint32_t (&v)[4], uint32_t (&o)
   o[3] = __byte_perm(c, d, 0x7632);
 }
 
-// W [K][2N]: a CTA takes 64 outputs, a warp all of them for its chunks of 32 k. Each warp keeps kRing chunks on their way into
-// shared memory (two boxes of 32 k x 64 outputs, 64-byte swizzle) and waits for them alone; 96 KB of a CTA are in flight where
-// loads into registers held 32 (25.6 us for 1 x 4096 -> 2 x 11008).
-constexpr int kRing = 3, kRowChunkBytes = 2 * 32 * 64;
-constexpr int kRowRingBytes = kRowWarps * kRing * kRowChunkBytes;
-constexpr int kRowSmemBytes = kRowRingBytes + 1024;
-static_assert(kRowRingBytes >= kRowWarps * 8 * 4 * 33 * 4, "the warps' sums lie in the ring");
+// W [K][2N]: a CTA takes 32 G outputs, a warp all of them for its chunks of 32 k. Each warp keeps `ring` chunks on their way into
+// shared memory (two boxes of 32 k x 32 G outputs, with 128 of them in the 128-byte swizzle, against bank conflicts) and waits for
+// them alone; 144 to 192 KB of an SM are in flight. A's words come kAhead chunks ahead, in registers: one chunk ahead their latency
+// was the chunk's time (8 x 4096 -> 2 x 11008 21.7 -> 19.8 us, 1 x 11008 -> 2 x 4096 28.2 -> 26.2).
+constexpr int kMaxRing = 9, kAhead = 4;
+constexpr int row_smem_bytes(int groups, int ring, int warps) { return warps * ring * 2 * 32 * 32 * groups + 1024; }
 struct alignas(64) RowMnParams {
   CUtensorMap w;
   RowParams p;
+  int32_t ring;                    // 2 .. kMaxRing
 };
-template <int WF, int AF>
-__global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows_mn(const __grid_constant__ RowMnParams P) {
+template <int WF, int AF, int G>
+__global__ void __launch_bounds__(32 * kRowWarps, 1) k_gated_rows_mn(const __grid_constant__ RowMnParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t landed[kRowWarps][kRing];
+  __shared__ uint64_t landed[kRowWarps][kMaxRing];
   __shared__ int given_up;
   const RowParams& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 64, token0 = blockIdx.y * kRowTokens;
+  constexpr int kOuts = 32 * G, kBytes = 2 * 32 * kOuts;
+  const int n0 = blockIdx.x * kOuts, token0 = blockIdx.y * kRowTokens;
   const int chunks = (p.K + 31) / 32;
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < warps; ++w)
-      for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&landed[w][s]), 1);
-    given_up = 0;
+  if (lane < P.ring) {
+    mbar_init(smem_u32(&landed[warp][lane]), 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) given_up = 0;
   __syncthreads();
   const uint64_t limit = wait_limit_ns();
   const bool expire = expire_mode() == kExpireAll;
   pdl_enter();
-  uint8_t* mine = ring + warp * kRing * kRowChunkBytes;
+  uint8_t* mine = ring + warp * P.ring * kBytes;
   // boxes past K or 2N read zeros there; gate columns past N are the up projection's: what they give is not stored
   auto fetch = [&](int c, int s) {
     if (lane == 0 && c < chunks) {
-      const uint32_t bar = smem_u32(&landed[warp][s]), dst = smem_u32(mine + s * kRowChunkBytes);
-      mbar_arrive_expect_tx(bar, kRowChunkBytes);
+      const uint32_t bar = smem_u32(&landed[warp][s]), dst = smem_u32(mine + s * kBytes);
+      mbar_arrive_expect_tx(bar, kBytes);
       tma_load_2d(dst, &P.w, n0, c * 32, bar);
-      tma_load_2d(dst + kRowChunkBytes / 2, &P.w, p.N + n0, c * 32, bar);
+      tma_load_2d(dst + kBytes / 2, &P.w, p.N + n0, c * 32, bar);
     }
   };
-  for (int s = 0; s < kRing; ++s) fetch(warp + s * warps, s);
+  for (int s = 0; s < P.ring; ++s) fetch(warp + s * warps, s);
   // tokens past M are loaded as the last one; K is a multiple of 16
   const uint8_t* a = p.a + static_cast<int64_t>(min(token0 + g, p.M - 1)) * p.K + 4 * t;
   auto x_of = [&](int c, int h) {
     const int k = c * 32 + 16 * h;
     return k < p.K ? ld_dep(reinterpret_cast<const uint32_t*>(a + k)) : 0u;
   };
-  float acc[8][4];
+  // a lane's k are 4t .. of each 16, read in the order i ^ t, so that the four t of a word lie in different rows of banks
+  int at[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-  uint32_t x0 = x_of(warp, 0), x1 = x_of(warp, 1);
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * t + (i ^ t);
+    at[i] = row * kOuts + (G == 4 ? ((g >> 2) ^ (row & 7)) * 16 + (g & 3) * 4 : 4 * g);
+  }
+  const int order = t == 0 ? 0x3210 : t == 1 ? 0x2301 : t == 2 ? 0x1032 : 0x0123;
+  float acc[4 * G][4];
+#pragma unroll
+  for (int j = 0; j < 4 * G; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+  uint32_t next[kAhead][2];
+  auto load_x = [&](int c) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) next[d][h] = x_of(c + d * warps, h);
+  };
+  load_x(warp);
   int s = 0, parity = 0;
-  for (int c = warp; c < chunks; c += warps) {
-    const uint32_t b0 = x0, b1 = x1;
-    if (c + warps < chunks) x0 = x_of(c + warps, 0), x1 = x_of(c + warps, 1);
-    if (!warp_wait(smem_u32(&landed[warp][s]), parity, limit, expire)) {
-      if (lane == 0) record_error(kErrTimeout);
-      given_up = 1;
-      break;
-    }
-    uint2 v[2][2][4];                                      // [half of the chunk][gate, up][k]
+  bool there = true;
+  for (int c0 = warp; c0 < chunks && there; c0 += kAhead * warps) {
+    uint32_t x[kAhead][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int d = 0; d < kAhead; ++d)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int h = 0; h < 2; ++h) x[d][h] = __byte_perm(next[d][h], 0, order);
+    load_x(c0 + kAhead * warps);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 16 * h + 4 * t + i;
-          v[h][u][i] = *reinterpret_cast<const uint2*>(mine + s * kRowChunkBytes + u * (kRowChunkBytes / 2) + row * 64 +
-                                                       (((g >> 1) ^ ((row >> 1) & 3)) * 16) + (g & 1) * 8);
+    for (int d = 0; d < kAhead; ++d) {
+      const int c = c0 + d * warps;
+      if (c >= chunks || !there) break;
+      there = warp_wait(smem_u32(&landed[warp][s]), parity, limit, expire);
+      if (!there) {
+        if (lane == 0) record_error(kErrTimeout);
+        given_up = 1;
+        break;
+      }
+      const uint8_t* slot = mine + s * kBytes;
+#pragma unroll
+      for (int q = 0; q < G; ++q) {                        // outputs 32q + 4g ..
+        uint32_t v[2][2][4], m[2][2][4];                   // [half of the chunk][gate, up][k]
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[h][u][i] = *reinterpret_cast<const uint32_t*>(slot + (at[i] ^ (G == 4 ? q * 32 : 0)) + h * 16 * kOuts + u * (kBytes / 2) + (G == 4 ? 0 : q * 32));
+        if (q + 1 == G) {
+          __syncwarp();                                    // all have read the slot, and the MMA's lanes come together
+          fetch(c + P.ring * warps, s);
         }
-    __syncwarp();                                          // all have read the slot, and the MMA's lanes come together
-    fetch(c + kRing * warps, s);
-    if (++s == kRing) s = 0, parity ^= 1;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {                          // four outputs at a time
-      uint32_t m[2][2][4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+          for (int u = 0; u < 2; ++u) transpose4(v[h][u], m[h][u]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t in[4] = {q ? v[h][u][0].y : v[h][u][0].x, q ? v[h][u][1].y : v[h][u][1].x,
-                                  q ? v[h][u][2].y : v[h][u][2].x, q ? v[h][u][3].y : v[h][u][3].x};
-          transpose4(in, m[h][u]);
-        }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mma_fp8<WF, AF>(acc[4 * q + j], m[0][0][j], m[0][1][j], m[1][0][j], m[1][1][j], b0, b1);
+        for (int j = 0; j < 4; ++j) mma_fp8<WF, AF>(acc[4 * q + j], m[0][0][j], m[0][1][j], m[1][0][j], m[1][1][j], x[d][0], x[d][1]);
+      }
+      if (++s == P.ring) s = 0, parity ^= 1;
     }
   }
   __syncthreads();
@@ -257,15 +278,15 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) k_gated_rows_mn(const __gri
     if (threadIdx.x == 0 && p.amax_bits) atomicMax(p.amax_bits, 0x7FC00000u);
     return;
   }
-  float* part = reinterpret_cast<float*>(ring);            // [warp][8][4][33]
+  float* part = reinterpret_cast<float*>(ring);            // [warp][4 G][4][33]: 2112 G bytes a warp, of ring 2048 G and more
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 4 * G; ++j)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) part[((warp * 8 + j) * 4 + k) * 33 + lane] = acc[j][k];
+    for (int k = 0; k < 4; ++k) part[((warp * 4 * G + j) * 4 + k) * 33 + lane] = acc[j][k];
   __syncthreads();
-  finish_rows(p, part, warps, 64, n0, token0, [](int o, int& place, int& group) {
-    place = o >> 3;
-    group = o & 7;
+  finish_rows(p, part, warps, kOuts, n0, token0, [](int o, int& place, int& group) {
+    place = (o & 31) >> 2;
+    group = (o >> 5) * 4 + (o & 3);
   });
 }
 

@@ -79,6 +79,29 @@ def test_few_rows(cuda_lib, M, K, N, kinds, b_mn):
     check_forward(*forward(cuda_lib, M, K, N, "silu" if N % 32 else "gelu", b_mn, kinds=kinds))
 
 
+@pytest.mark.parametrize("M", [1, 8])
+@pytest.mark.parametrize("N,K", [(4720, 48), (4752, 48), (9472, 272), (9488, 272), (14208, 48), (14224, 48), (18944, 144), (18960, 48),
+                                 (28672, 80), (40000, 16)])
+@pytest.mark.parametrize("kinds", [(E4, E4), (E5, E4)])
+def test_few_rows_wide_transposed(cuda_lib, M, N, K, kinds):
+    """W as [K][2N] with tiles of 32, 64, 96 and 128 outputs, in one round of the SMs and more; N that ends inside a tile."""
+    o, want = forward(cuda_lib, M, K, N, "silu", True, kinds=kinds, seed=N + M)
+    check_forward(o, want)
+
+
+@pytest.mark.parametrize("M,K,N", [(300, 256, 2768), (1237, 144, 2752), (1000, 272, 5504), (40, 144, 11008), (500, 144, 4160)])
+@pytest.mark.parametrize("kinds", [(E4, E4), (E4, E5)])
+def test_tiles_of_192_columns(cuda_lib, M, K, N, kinds):
+    """Tiles of three quarters of the columns, where they make the clusters' rounds shorter."""
+    o, want = forward(cuda_lib, M, K, N, "gelu", False, kinds=kinds, seed=N)
+    check_forward(o, want)
+
+
+@pytest.mark.parametrize("M,K,N", [(1000, 272, 5504), (300, 144, 11008), (1000, 144, 2768), (40, 400, 16400)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_backward_tiles_of_192_columns(cuda_lib, M, K, N, inplace):
+    check_backward(*backward(cuda_lib, M, K, N, "silu", False, inplace=inplace))
+
 @pytest.mark.parametrize("outs", ["g", "h", "q", "gq", "gh"])
 def test_few_rows_outputs_alone(cuda_lib, outs):
     for b_mn in (False, True):
