@@ -1869,7 +1869,11 @@ fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, int s
   cfg.attrs = early;
   cfg.numAttrs = 1;
   if (!mn) {
-    (void)cudaLaunchKernelEx(&cfg, k_gated_rows<WF, AF>, p);
+    // two CTAs an SM, two chunks ahead, where the SMs' rounds are fewer for it and there are chunks to be ahead (1 x 4096 -> 2 x 9472
+    // 20.0 / 17.4 us, 1 x 11008 -> 2 x 4096 24.9 / 18.4; otherwise 1 x 4096 -> 2 x 11008 20.8 / 21.8)
+    const int64_t ctas = static_cast<int64_t>(cfg.gridDim.x) * cfg.gridDim.y;
+    const bool ahead = p.K >= 2048 && (ctas + 2 * sms - 1) / (2 * sms) * 2 < (ctas + 3 * sms - 1) / (3 * sms) * 3;
+    (void)(ahead ? cudaLaunchKernelEx(&cfg, k_gated_rows<WF, AF, 2>, p) : cudaLaunchKernelEx(&cfg, k_gated_rows<WF, AF, 1>, p));
     return FP8T_OK;
   }
   // Tiles for which the SMs' rounds take the least time, a CTA an SM: its time goes with the width, and something for its start.

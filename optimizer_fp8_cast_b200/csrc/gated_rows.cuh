@@ -87,10 +87,10 @@ __device__ __forceinline__ void finish_rows(const RowParams& p, const float* par
   if (p.scale_inv && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scale_inv = __fdiv_rn(1.0f, scale);
 }
 
-// W [2N][K]: a CTA takes 16 outputs, a warp all of them for its chunks of 64 k; three CTAs on an SM (1 x 4096 -> 2 x 11008 20.7 us;
-// 32 outputs and two CTAs, whose 344 do not all fit at once, 23.2).
-template <int WF, int AF>
-__global__ void __launch_bounds__(32 * kRowWarps, 3) k_gated_rows(const __grid_constant__ RowParams p) {
+// W [2N][K]: a CTA takes 16 outputs, a warp all of them for its chunks of 64 k, whose loads are D chunks ahead. Three CTAs on an SM
+// for D = 1, two for D = 2 (32 outputs and two CTAs, whose 344 do not all fit at once, 23.2 us for 1 x 4096 -> 2 x 11008).
+template <int WF, int AF, int D>
+__global__ void __launch_bounds__(32 * kRowWarps, D == 1 ? 3 : 2) k_gated_rows(const __grid_constant__ RowParams p) {
   constexpr int R = 2;
   __shared__ float part[kRowWarps][R][4][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -110,31 +110,38 @@ __global__ void __launch_bounds__(32 * kRowWarps, 3) k_gated_rows(const __grid_c
 #pragma unroll
   for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
   pdl_enter();
-  uint4 wv[R][2], av;
-  auto load = [&](int c) {
+  uint4 wv[D][R][2], av[D];
+  auto load = [&](int d, int c) {
     const bool in = c * 64 + t * 16 < p.K;                 // K is a multiple of 16
-    av = in ? ld_dep(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
+    av[d] = in ? ld_dep(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        wv[r][h] = in ? ld_dep(reinterpret_cast<const uint4*>(w[r][h])) : make_uint4(0, 0, 0, 0);
+        wv[d][r][h] = in ? ld_dep(reinterpret_cast<const uint4*>(w[r][h])) : make_uint4(0, 0, 0, 0);
         w[r][h] += 64 * warps;
       }
     a += 64 * warps;
   };
-  if (warp < chunks) load(warp);
-  for (int c = warp; c < chunks; c += warps) {
-    uint4 now[R][2];
-    const uint4 x = av;
-#pragma unroll
-    for (int r = 0; r < R; ++r) now[r][0] = wv[r][0], now[r][1] = wv[r][1];
-    if (c + warps < chunks) load(c + warps);
+  auto multiply = [&](const uint4 (&v)[R][2], const uint4& x) {
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      mma_fp8<WF, AF>(acc[r], now[r][0].x, now[r][1].x, now[r][0].y, now[r][1].y, x.x, x.y);
-      mma_fp8<WF, AF>(acc[r], now[r][0].z, now[r][1].z, now[r][0].w, now[r][1].w, x.z, x.w);
+      mma_fp8<WF, AF>(acc[r], v[r][0].x, v[r][1].x, v[r][0].y, v[r][1].y, x.x, x.y);
+      mma_fp8<WF, AF>(acc[r], v[r][0].z, v[r][1].z, v[r][0].w, v[r][1].w, x.z, x.w);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, warp + d * warps);
+  for (int c = warp; c < chunks; c += D * warps) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      uint4 now[R][2];
+      const uint4 x = av[d];
+#pragma unroll
+      for (int r = 0; r < R; ++r) now[r][0] = wv[d][r][0], now[r][1] = wv[d][r][1];
+      if (D > 1 || c + warps < chunks) load(d, c + (D + d) * warps);                   // zeros past K
+      multiply(now, x);
     }
   }
 #pragma unroll
