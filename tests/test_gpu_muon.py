@@ -236,3 +236,71 @@ def test_waits_expire_and_context_survives(cuda_lib, mode, rows, cols):
     cuda_lib.fp8t_check_device_error()
     assert skipped.item() == 0
     check_step(s, old)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-25, 1.0, 1e25, 1e36])
+@pytest.mark.parametrize("rows,cols", [(100, 200), (200, 100), (256, 256), (3, 5)])
+def test_any_magnitude_in_shared_memory(cuda_lib, rows, cols, scale):
+    """Squares past f32 in some rows, in all, and below it, beside rows of zeros."""
+    for spread in (False, True):
+        x = matrix(rows, cols, 7, scale)
+        if spread:
+            x = x * torch.logspace(-20, 0, rows, device="cuda")[:, None]
+            x[rows // 2] = 0
+        out = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+        cuda_lib.muon_orthogonalize([x], [out])
+        cuda_lib.fp8t_check_device_error()
+        check_orth(out, x)
+
+
+def test_small_and_large_in_one_list(cuda_lib):
+    """Matrices of both forms in every batch of a long list, some in place, and the bits that each has alone."""
+    shapes = [(64, 64), (300, 70), (256, 256), (70, 300), (1, 9), (255, 257), (40, 250)] * 8
+    xs = [matrix(r, c, i).to(torch.bfloat16) for i, (r, c) in enumerate(shapes)]
+    alone = []
+    for x in xs:
+        out = torch.empty_like(x)
+        cuda_lib.muon_orthogonalize([x], [out], steps=3)
+        alone.append(out)
+    outs = [x.clone() if i % 3 == 0 else torch.empty_like(x) for i, x in enumerate(xs)]
+    cuda_lib.muon_orthogonalize([o if i % 3 == 0 else x for i, (x, o) in enumerate(zip(xs, outs))], outs, steps=3)
+    cuda_lib.fp8t_check_device_error()
+    for i in range(len(xs)):
+        assert torch.equal(outs[i], alone[i]), shapes[i]
+
+
+def test_small_ones_on_two_streams_and_captured(cuda_lib):
+    """Calls at the same time on two streams, those of one replayed from a graph: each has its own results."""
+    xs = [matrix(200, 256, i).to(torch.bfloat16) for i in range(4)]
+    want = [torch.empty_like(x) for x in xs]
+    for x, w in zip(xs, want):
+        cuda_lib.muon_orthogonalize([x], [w])
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(x) for x in xs]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        for x, o in zip(xs[:2], outs[:2]):
+            cuda_lib.muon_orthogonalize([x], [o])
+    for _ in range(20):
+        graph.replay()
+        with torch.cuda.stream(side):
+            for x, o in zip(xs[2:], outs[2:]):
+                cuda_lib.muon_orthogonalize([x], [o])
+    torch.cuda.synchronize()
+    cuda_lib.fp8t_check_device_error()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("rows,cols", [(600, 700), (200, 130), (130, 200), (255, 33)])
+@pytest.mark.parametrize("mode", [1, 2])
+def test_orthogonalize_waits_expire(cuda_lib, mode, rows, cols):
+    """The result of a product that gave up is NaN throughout; the next call is right."""
+    x = matrix(rows, cols, 1)
+    out, check = guarded(torch.zeros_like(x, dtype=torch.bfloat16))
+    _run_expired(cuda_lib, mode, lambda: cuda_lib.muon_orthogonalize([x], [out]))
+    check()
+    assert bool(out.isnan().all())
+    cuda_lib.muon_orthogonalize([x], [out])
+    cuda_lib.fp8t_check_device_error()
+    check_orth(out, x)
