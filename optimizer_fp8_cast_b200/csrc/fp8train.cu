@@ -1819,7 +1819,10 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int outputs, 
   auto tiles_n = [&](int h) { return (c.N * 128 + outputs * h - 1) / (outputs * h); };
   auto rounds = [&](int h) { return (p.tiles_m * tiles_n(h) + dev->pair_clusters - 1) / dev->pair_clusters; };
   p.half_n = mn ? 128 : rounds(64) == 1 ? 64 : rounds(96) * 96 * 10 <= rounds(128) * 128 * 9 ? 96 : 128;
-  fp8t_status st = encode_kmajor(&p.a, c.A, c.M, c.K, kHalf);
+  // Rows that A does not have are left out of its boxes: what the stage holds there reaches no output. Boxes that begin inside A and
+  // are mostly past it are slow to land (9 x 4096 -> 2 x 11008 33.0 / 24.8 us, 16 rows 31.4 / 24.8).
+  p.a_rows = static_cast<int32_t>(std::min<int64_t>(kHalf, (c.M + 7) / 8 * 8));
+  fp8t_status st = encode_kmajor(&p.a, c.A, c.M, c.K, static_cast<uint32_t>(p.a_rows));
   if (st == FP8T_OK)
     st = mn ? encode_kmajor(&p.b, c.B, c.K, c.b_rows, kBK) : encode_kmajor(&p.b, c.B, c.b_rows, c.K, static_cast<uint32_t>(p.half_n));
   p.tiles_n = static_cast<int32_t>(tiles_n(p.half_n));
@@ -1832,11 +1835,12 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int outputs, 
   p.has_q = c.q != nullptr;
   return st;
 }
-// Few rows: always up to eight, and while the weights, read once for every eight rows, are small. Few-rows kernel / pair tiles,
-// graph replays: 8 x 4096 -> 2 x 11008 19.9 / 28.8 us (W in x out), 21.3 / 29.4 (out x in); 16 rows 36.5 (in 64 outputs a CTA) /
-// 28.2 and 33.7 / 28.4; 16 x 1024 -> 2 x 2752 (11 MB) 7.5 / 7.8 and 3.8 / 7.8; 32 x 256 -> 2 x 688 3.4 / 6.1 and 2.3 / 5.8.
+// Few rows: always up to eight, and up to 32 while the weights, read once for every eight rows, are small. Few-rows kernel / pair
+// tiles, graph replays. W out x in: 8 x 4096 -> 2 x 11008 20.7 / 24.8 us, 16 rows 34.4 / 24.5; 16 x 2048 -> 2 x 5504 (45 MB for two
+// eights) 8.2 / 10.1, 24 rows 15.5 / 10.0; 32 x 1024 -> 2 x 2752 5.7 / 6.5. W in x out: 8 x 4096 -> 2 x 11008 19.9 / 26, 16 rows
+// 35.6 / 25.8; 24 x 2048 -> 2 x 2752 (34 MB) 9.3 / 9.8, 32 rows (45 MB) 10.9 / 9.7; 16 x 256 -> 2 x 688 3.4 / 5.7.
 bool gated_few_rows(const fp8t_gated& d) {
-  const int64_t groups = (d.M + 7) / 8, most = d.b_layout == FP8T_MN_MAJOR ? int64_t(8) << 20 : int64_t(16) << 20;
+  const int64_t groups = (d.M + 7) / 8, most = d.b_layout == FP8T_MN_MAJOR ? int64_t(36) << 20 : int64_t(48) << 20;
   return groups == 1 || (d.M <= 32 && groups * 2 * d.N * d.K <= most);
 }
 // Chunks of a warp's ring for tiles of 32 G outputs: 144 to 192 KB of a CTA.

@@ -37,6 +37,7 @@ struct alignas(64) Params {
   float* scale_inv;
   int32_t M, N;
   int32_t tiles_m, tiles_n, total_tiles, num_kb;
+  int32_t a_rows;                  // rows of A's box: 128, or fewer where M is
   int32_t half_n;                  // rows of B of a CTA: a tile has as many outputs (forward) or twice as many (backward)
   int32_t a_mn, b_mn;
   uint32_t idesc;
@@ -138,6 +139,7 @@ struct Base {
     w.a_row = w.mt * kBM + rank * kHalf;
     w.b_row = w.nt * b_step + rank * b_other;
     w.half_n = g.half_n;
+    w.a_bytes = g.a_rows * kBK;
     w.num_kb = g.num_kb;
     w.a_mn = 0;
     w.b_mn = g.b_mn;

@@ -160,6 +160,7 @@ struct Work {
   int a_row, b_row;                // first row of A and of B that this CTA holds
   int mt, nt;                      // row and column tile
   int half_n;                      // rows of B that each CTA holds: 128; 64 or, of FP8, 96 for narrower tiles (not of MN-major FP8)
+  int a_bytes;                     // of A's boxes of a k-block
   int num_kb;
   int a_mn, b_mn;                  // 1: operand stored MN-major
   uint32_t idesc;
@@ -290,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (one) {
             const uint32_t full_leader = mapa_shared(smem_u32(&S->full[s]), 0);
             const bool second = Op::kF16 && w.half_n > 64;   // B's second box of 64
-            if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), 2 * (kABytes + w.half_n * kBK));
+            if (leader) mbar_arrive_expect_tx(smem_u32(&S->full[s]), 2 * (w.a_bytes + w.half_n * kBK));
             const uint32_t a_dst = smem_u32(smem + s * kStageBytes), b_dst = a_dst + kABytes;
             const int k0 = kb * kElems;
             tma_load_2d_pair(a_dst, w.a, w.a_mn ? w.a_row : k0, w.a_mn ? k0 : w.a_row, full_leader);

@@ -107,6 +107,7 @@ struct Steps {
     w.a_row = w.mt * kBM + rank * kHalf;
     w.half_n = g.tile_n / 2;
     w.b_row = w.nt * g.tile_n + rank * w.half_n;
+    w.a_bytes = kABytes;
     w.num_kb = (inner + 63) / 64;
     w.idesc = make_idesc_f16(w.a_mn, w.b_mn, g.tile_n);
     return w;

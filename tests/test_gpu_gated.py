@@ -89,6 +89,18 @@ def test_few_rows_wide_transposed(cuda_lib, M, N, K, kinds):
     check_forward(o, want)
 
 
+@pytest.mark.parametrize("b_mn", [False, True])
+@pytest.mark.parametrize("M", [9, 17, 31, 33, 100, 127, 128])
+def test_less_than_a_cta_of_rows(cuda_lib, M, b_mn):
+    """Rows that fill part of a box, behind a call whose operands leave NaN codes in shared memory: none reaches an output."""
+    K, N = 528, 48 if M > 32 else 40000
+    a = torch.full((256, K), 0x7F, dtype=torch.uint8, device="cuda")
+    forward(cuda_lib, 256, K, 4736, "silu", b_mn, a=a, w=torch.full((2 * 4736, K), 0x7F, dtype=torch.uint8, device="cuda"))
+    check_forward(*forward(cuda_lib, M, K, N, "silu", b_mn))
+    if N == 48:
+        check_backward(*backward(cuda_lib, M, K, N, "gelu", b_mn))
+
+
 @pytest.mark.parametrize("M,K,N", [(300, 256, 2768), (1237, 144, 2752), (1000, 272, 5504), (40, 144, 11008), (500, 144, 4160)])
 @pytest.mark.parametrize("kinds", [(E4, E4), (E4, E5)])
 def test_tiles_of_192_columns(cuda_lib, M, K, N, kinds):
