@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_consta
 // ------------------------------------------------------------------ small matrices
 // Up to 256 x 256: one CTA pair keeps a matrix in shared memory over all steps. The phases of the grid-wide form have little to do
 // there (6.4 us each, of which the MMAs are one: barrier, first loads, stores); here the epilogue writes the next phase's
-// operand where the tensor cores read it (256 x 256: fifteen launches 142 us a call, grid-wide 97, here 39.5; 1.9 us a phase, of
+// operand where the tensor cores read it (256 x 256: fifteen launches 142 us a call, grid-wide 97, here 40.2; 1.9 us a phase, of
 // which the tensor cores compute 1.1).
 // CTA r holds (FP16, 128-byte swizzle, zeros past the matrix):
 //   xk   rows 128r .. of X, K-major: four blocks of 64 columns
@@ -775,8 +775,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
           *place = q[p];
         }
         if (phase == 0) {                                // where c A^2 is to be added up: b A + a I
+          // A as it was rounded, which is the A of A^2: what its rounding does to b A and to c A^2 then cancels for the most part
+          // where A is near I (b + 2c = -0.7; with the A before its rounding the factor's error was up to twice as large)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * (kB / kC));
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t h = (&q[p].x)[j];
+              const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h));
+              r[8 * p + 2 * j] = __float_as_uint(a.x * (kFactor * kB / kC));
+              r[8 * p + 2 * j + 1] = __float_as_uint(a.y * (kFactor * kB / kC));
+            }
           if (static_cast<int>(rank) * kHalf + quad * 32 == n) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
