@@ -45,6 +45,11 @@ __device__ __forceinline__ void mma_fp8(float (&c)[4], uint32_t a0, uint32_t a1,
 #undef FP8T_MMA
 }
 
+// 1 / scale, by one thread of the grid: also where a wait expired, as the pair tiles do (the scale is not the call's result).
+__device__ __forceinline__ void store_scale_inv(const RowParams& p) {
+  if (p.scale_inv && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scale_inv = __fdiv_rn(1.0f, ld_dep(p.scale));
+}
+
 // The sums of a CTA's warps for output o (of `outs`) and token, and what becomes of them. part: [warp][outs / 8][4][32 + 1] floats, of
 // accumulator j of lane 4g + t: gate (j < 2) or up of the output in place g of group `o / 8`, token 2t + (j & 1); place and group as
 // `at` gives them.
@@ -84,7 +89,7 @@ __device__ __forceinline__ void finish_rows(const RowParams& p, const float* par
     const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7FFFFFFFu);
     if ((threadIdx.x & 31) == 0 && most) atomicMax(p.amax_bits, most > 0x7F800000u ? 0x7FC00000u : most);
   }
-  if (p.scale_inv && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scale_inv = __fdiv_rn(1.0f, scale);
+  store_scale_inv(p);
 }
 
 // W [2N][K]: a CTA takes 16 outputs, a warp all of them for its chunks of 64 k, whose loads are D chunks ahead. Three CTAs on an SM
@@ -283,6 +288,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) k_gated_rows_mn(const __gri
     while (globaltimer_ns() - t0 < kSettleNs) {
     }
     if (threadIdx.x == 0 && p.amax_bits) atomicMax(p.amax_bits, 0x7FC00000u);
+    store_scale_inv(p);
     return;
   }
   float* part = reinterpret_cast<float*>(ring);            // [warp][4 G][4][33]: 2112 G bytes a warp, of ring 2048 G and more
