@@ -618,7 +618,9 @@ fp8t_status muon_orthogonalize(const fp8t_orth_matrix* matrices, int32_t n_matri
  * 0.2 is about AdamW's). If any u has a non-finite norm nothing is changed and *d_skipped_out (int32, or
  * NULL) is 1, else 0. There is no clipping: O does not depend on the gradient's size.
  * Tensors must not overlap, but weight may be the tensor's own grad. Where a wait inside the products expired
- * (FP8T_ERR_TIMEOUT) master and weight of its table stay as they are, momentum is new, and *d_skipped_out is 1.
+ * (FP8T_ERR_TIMEOUT) master and weight of its table (24 tensors) stay as they are, momentum is new, and *d_skipped_out is 1.
+ * The same holds for a call that returns FP8T_ERR_CUDA: with *d_skipped_out at 1 momentum may be new already (repeating
+ * the step would apply the gradient to it twice); arguments are checked, and whatever else can fail is done, before that.
  * Errors and workspace as muon_orthogonalize; hyperparameters finite, loss_scale > 0.
  */
 typedef struct fp8t_muon_tensor {

@@ -542,6 +542,7 @@ def fused_muon_multi_tensor(master, momentum, grads, weights, *, lr, beta=0.95, 
     g = grad / loss_scale; momentum <- beta * momentum + g; u = g + beta * momentum (``nesterov``) or momentum;
     master <- master * (1 - lr * weight_decay) - lr * update_rms * sqrt(max(rows, cols)) * O with O the orthogonal factor
     of u (muon_orthogonalize); weights = BF16 of master. A non-finite u changes nothing and sets ``skipped`` (int32 [1]).
+    ``skipped`` is 0 only behind a whole step; where a wait expired or the call itself raised it is 1, and momentum may be new.
     ``workspace``: a uint8 CUDA tensor of muon_workspace_bytes (allocated per call where it is missing)."""
     n = len(master)
     if not n or not n == len(momentum) == len(grads) == len(weights):

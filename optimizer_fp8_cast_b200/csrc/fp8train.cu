@@ -2106,7 +2106,7 @@ struct MuonPlan {
       copies = std::max(copies, copy);
       partials = std::max(partials, static_cast<size_t>(round_up(chunks * 8, 256)));
     }
-    norms = static_cast<size_t>(round_up(static_cast<int64_t>(n) * sizeof(fp8t::muon::Norm) + 8, 256));   // and two words
+    norms = static_cast<size_t>(round_up(static_cast<int64_t>(n) * sizeof(fp8t::muon::Norm) + 12, 256));   // and three words
   }
   size_t bytes() const { return norms + partials + copies; }
 };
@@ -2137,12 +2137,16 @@ fp8t_status fill_muon_matrix(fp8t::muon::Matrix& m, const MuonSizes& z, char* at
   x_tiles += static_cast<int32_t>(muon_x_tiles(z, tile_n));
   return st;
 }
-// The steps of the table's matrices `which`, grid-wide.
+// The steps of a table's matrices `which`, grid-wide: their launch's parameters, then the launch.
+template <class G>
+G& muon_group() {
+  static thread_local G g;
+  return g;
+}
 template <int NP>
-fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<char*>& at, const std::vector<int32_t>& which, int32_t steps,
-                          const fp8t::pair::Grid& grid, const DeviceInfo* dev, cudaStream_t stream) {
-  using Op = fp8t::muon::Steps<NP>;
-  static thread_local fp8t::muon::Group<NP> g;
+fp8t_status prepare_newton_schulz(const std::vector<MuonSizes>& z, const std::vector<char*>& at, const std::vector<int32_t>& which,
+                                  int32_t steps, const fp8t::pair::Grid& grid, const DeviceInfo* dev) {
+  fp8t::muon::Group<NP>& g = muon_group<fp8t::muon::Group<NP>>();
   g.n = static_cast<int32_t>(which.size());
   g.steps = steps;
   g.sym_tiles = g.x_tiles = 0;
@@ -2160,6 +2164,12 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<cha
     const fp8t_status st = fill_muon_matrix(g.m[k], z[which[k]], at[which[k]], g.tile_n, !g.whole, g.sym_tiles, g.x_tiles);
     if (st != FP8T_OK) return st;
   }
+  return FP8T_OK;
+}
+template <int NP>
+fp8t_status newton_schulz(const DeviceInfo* dev, cudaStream_t stream) {
+  using Op = fp8t::muon::Steps<NP>;
+  const fp8t::muon::Group<NP>& g = muon_group<fp8t::muon::Group<NP>>();
   // its CTAs wait for one another: a cooperative launch has them all resident or fails
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(std::max(g.sym_tiles, g.x_tiles), dev->pair_clusters)), 1, 1);
@@ -2176,10 +2186,10 @@ fp8t_status newton_schulz(const std::vector<MuonSizes>& z, const std::vector<cha
 }
 bool muon_small(const MuonSizes& z) { return std::max(z.rows, z.cols) <= fp8t::muon::kSmallSide; }
 // The same for matrices of at most 256 x 256, a CTA pair each.
-fp8t_status newton_schulz_small(const std::vector<MuonSizes>& z, const std::vector<char*>& at, const std::vector<int32_t>& which,
-                                int32_t steps, int32_t* expired, cudaStream_t stream) {
+fp8t_status prepare_newton_schulz_small(const std::vector<MuonSizes>& z, const std::vector<char*>& at,
+                                        const std::vector<int32_t>& which, int32_t steps, int32_t* expired) {
   using namespace fp8t::muon;
-  static thread_local SmallGroup g;
+  SmallGroup& g = muon_group<SmallGroup>();
   g.steps = steps;
   g.expired = expired;
   for (size_t k = 0; k < which.size(); ++k) {
@@ -2193,13 +2203,12 @@ fp8t_status newton_schulz_small(const std::vector<MuonSizes>& z, const std::vect
     m.cols = static_cast<int32_t>(s.cols);
     m.pitch = static_cast<int32_t>(s.pitch_x);
   }
-  (void)launch_pdl(k_muon_small<kMuon>, 2 * static_cast<int64_t>(which.size()), kSmallThreads, kSmallSmemBytes, stream, 0, g);
-  return after_launch("Newton-Schulz products launch");
+  return FP8T_OK;
 }
 // A table's steps: the longest matrices first, for a cluster takes every n-th tile and the phase of A should end with the
-// shortest (its K is the longer side).
-fp8t_status newton_schulz_table(const std::vector<MuonSizes>& z, char* copies, int32_t steps, const fp8t::pair::Grid& grid,
-                                const DeviceInfo* dev, cudaStream_t stream) {
+// shortest (its K is the longer side). large, small: how many of each form.
+fp8t_status prepare_table(const std::vector<MuonSizes>& z, char* copies, int32_t steps, const fp8t::pair::Grid& grid,
+                          const DeviceInfo* dev, size_t& n_large, size_t& n_small) {
   std::vector<char*> at(z.size());
   std::vector<int32_t> large, small;
   for (size_t k = 0; k < z.size(); copies += z[k].bytes(), ++k) {
@@ -2207,12 +2216,23 @@ fp8t_status newton_schulz_table(const std::vector<MuonSizes>& z, char* copies, i
     (muon_small(z[k]) ? small : large).push_back(static_cast<int32_t>(k));
   }
   std::stable_sort(large.begin(), large.end(), [&](int32_t a, int32_t b) { return std::max(z[a].rows, z[a].cols) > std::max(z[b].rows, z[b].cols); });
+  n_large = large.size();
+  n_small = small.size();
   fp8t_status st = FP8T_OK;
-  if (!large.empty())
-    st = large.size() <= 4 ? newton_schulz<4>(z, at, large, steps, grid, dev, stream)
-                           : newton_schulz<fp8t::muon::kMaxMatrices>(z, at, large, steps, grid, dev, stream);
-  if (st == FP8T_OK && !small.empty()) st = newton_schulz_small(z, at, small, steps, grid.expired, stream);
+  if (n_large > 0)
+    st = n_large <= 4 ? prepare_newton_schulz<4>(z, at, large, steps, grid, dev)
+                      : prepare_newton_schulz<fp8t::muon::kMaxMatrices>(z, at, large, steps, grid, dev);
+  if (st == FP8T_OK && n_small > 0) st = prepare_newton_schulz_small(z, at, small, steps, grid.expired);
   return st;
+}
+fp8t_status launch_table(size_t n_large, size_t n_small, const DeviceInfo* dev, cudaStream_t stream) {
+  using namespace fp8t::muon;
+  fp8t_status st = FP8T_OK;
+  if (n_large > 0) st = n_large <= 4 ? newton_schulz<4>(dev, stream) : newton_schulz<kMaxMatrices>(dev, stream);
+  if (st != FP8T_OK || n_small == 0) return st;
+  (void)launch_pdl(k_muon_small<kMuon>, 2 * static_cast<int64_t>(n_small), kSmallThreads, kSmallSmemBytes, stream, 0,
+                   muon_group<SmallGroup>());
+  return after_launch("Newton-Schulz products launch");
 }
 
 // Of the batch's matrices [b0, b1), those of at most 256 x 256, orthogonalised by one kernel.
@@ -2262,6 +2282,7 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
   t.norms = reinterpret_cast<Norm*>(ws);
   t.grid.counter = reinterpret_cast<unsigned int*>(t.norms + n);
   t.grid.expired = reinterpret_cast<int32_t*>(t.norms + n) + 1;
+  t.gave_up = t.grid.expired + 1;
   t.partials = reinterpret_cast<double*>(ws + plan.norms);
   char* copies = ws + plan.norms + plan.partials;
   t.all = n;
@@ -2303,10 +2324,13 @@ fp8t_status muon_call(const char* name, int32_t n, int32_t steps, fp8t::muon::Ta
       return st;
     if (n > kMaxMatrices) table(b0);
     if (t.n == 0) continue;
+    // what can fail on the host comes before the first kernel that changes a tensor, but for the launches themselves
+    size_t large = 0, small = 0;
+    if ((st = prepare_table(sizes, copies, steps, t.grid, dev, large, small)) != FP8T_OK) return st;
+    t.last = b0 + kMaxMatrices >= n;
     (void)launch_pdl(k_muon_scale<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);
     if ((st = after_launch(name)) != FP8T_OK) return st;
-    st = newton_schulz_table(sizes, copies, steps, t.grid, dev, stream);
-    if (st != FP8T_OK) return st;
+    if ((st = launch_table(large, small, dev, stream)) != FP8T_OK) return st;
     if (steps & 1)                 // the result is in the second copy
       for (int32_t i = 0; i < t.n; ++i) t.t[i].x += sizes[i].x / 2;
     (void)launch_pdl(k_muon_apply<MODE>, t.chunks, kPassThreads, 0, stream, 0, t);

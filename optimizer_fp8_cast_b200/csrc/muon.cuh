@@ -211,7 +211,9 @@ struct Table {
   double* partials;                // one a chunk, of this table
   Norm* norms;                     // one a tensor, of the call
   Grid grid;                       // of the products; expired: one gave up waiting, and X is not to be used
+  int32_t* gave_up;                // kMuon: some table's products have
   int32_t* skipped;
+  int32_t last;                    // 1: the call's last table
 };
 constexpr int kPassThreads = 256, kVec = 8, kChunk = kPassThreads * kVec * 4;   // elements of a CTA's chunk
 
@@ -372,10 +374,12 @@ __global__ void __launch_bounds__(kPassThreads) k_muon_scale(const __grid_consta
   pdl_enter();
   if (blockIdx.x == 0 && threadIdx.x == 0) *t.grid.counter = 0, *t.grid.expired = 0;
   if (MODE == kMuon) {
-    const bool go = all_finite(t);
-    // a later table's 0 would hide that an earlier one's products gave up
-    if (blockIdx.x == 0 && threadIdx.x == 0 && t.skipped && (!go || t.first == 0)) *t.skipped = go ? 0 : 1;
-    if (!go) return;
+    // skipped until the last table's weights are written: a call that fails between the launches has not made the step
+    if (blockIdx.x == 0 && threadIdx.x == 0 && t.first == 0) {
+      *t.gave_up = 0;
+      if (t.skipped) *t.skipped = 1;
+    }
+    if (!all_finite(t)) return;
   }
   const int chunk = blockIdx.x, k = find_tensor(t, chunk);
   const Tensor& T = t.t[k];
@@ -419,10 +423,13 @@ template <int MODE>
 __global__ void __launch_bounds__(kPassThreads) k_muon_apply(const __grid_constant__ Table t) {
   pdl_enter();
   const bool expired = ld_dep(t.grid.expired) != 0;
-  if (MODE == kMuon && !all_finite(t)) return;
-  if (MODE == kMuon && expired) {                          // m is new, p and w stay
-    if (blockIdx.x == 0 && threadIdx.x == 0 && t.skipped) *t.skipped = 1;
-    return;
+  if (MODE == kMuon) {
+    if (!all_finite(t)) return;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      if (expired) *t.gave_up = 1;
+      else if (t.last && t.skipped && ld_dep(t.gave_up) == 0) *t.skipped = 0;
+    }
+    if (expired) return;                                   // m is new, p and w stay
   }
   const int chunk = blockIdx.x, k = find_tensor(t, chunk);
   const Tensor& T = t.t[k];
