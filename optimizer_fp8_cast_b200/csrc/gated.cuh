@@ -4,7 +4,7 @@
 // Forward. W holds the gate's and the up projection's weights side by side (N columns each):
 //   [G | U] = (A . W) * sa * sb,  h = act(G) * U,  act(g) = g * sigmoid(w(g))
 //   w = g (SiLU) or 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU in its tanh form: (1 + tanh(z)) / 2 = sigmoid(2z))
-// One accumulator of a pair tile holds 128 columns of G and the same 128 of U (64 in small products): the even CTA's half of B is
+// One accumulator of a pair tile holds 128 columns of G and the same 128 of U (96 or 64 of each in narrower tiles): the even CTA's half of B is
 // gate rows, the odd CTA's the up rows of the same columns, so every lane has g and u of an element at the same time and h never
 // leaves the registers before it is rounded. h is formed from the f32 accumulators; G and U are rounded to BF16 only
 // where they are kept for the gradient.
@@ -25,7 +25,7 @@ using namespace pair;
 enum : int { kSilu = 1, kGelu = 2 };                       // fp8t_act
 
 struct alignas(64) Params {
-  CUtensorMap a, b;                // A in 128-row boxes (or [K][M]), B
+  CUtensorMap a, b;                // A in boxes of a_rows, B
   CUtensorMap o0, o1;              // 16-bit outputs: G and U (forward), dG and dU (backward)
   CUtensorMap g, u;                // backward: the kept G and U
   CUtensorMap h;                   // forward: h as BF16
@@ -39,7 +39,7 @@ struct alignas(64) Params {
   int32_t tiles_m, tiles_n, total_tiles, num_kb;
   int32_t a_rows;                  // rows of A's box: 128, or fewer where M is
   int32_t half_n;                  // rows of B of a CTA: a tile has as many outputs (forward) or twice as many (backward)
-  int32_t a_mn, b_mn;
+  int32_t b_mn;                    // 1: B is stored MN-major
   uint32_t idesc;
   int32_t act, fmt;                // fmt of the codes
   int32_t keep, has_h, has_q;      // which outputs are written
