@@ -16,9 +16,11 @@
 // pairs (i, i + 4) of a word. The gated form takes the up row of the same output for row g + 8, so a lane has both.
 // A group is 16 rows (8 gated outputs); the warps of a CTA take its chunks of K in turn, and their sums are added in shared
 // memory in warp order.
-// What bounds it: for few weights the launch and one trip to memory (1 x 4096 x 4096 4.6 us, 1.4 of them its bytes); for many the
-// issue of about 4.3 instructions a weight and lane at 24 warps an SM, and the logic pipe, which takes two cycles an operation
-// (4 x 4096 x 2 x 11008 NVFP4 18.2 us, 7.8 its bytes). Measured and not kept: a persistent form with three chunks of a warp in
+// What bounds it: for few weights the launch and one trip to memory (1 x 4096 x 4096 4.6 us, 1.4 of them its bytes). For many
+// (4 x 4096 x 2 x 11008 NVFP4 18.2 us, 7.8 its bytes) no unit is full: by the profiler's counters 3.5 instructions a weight and lane take
+// 58% of the issue slots, the logic pipe 57% and DRAM 30%; 1.3 of a scheduler's 4.9 warps are ready in a cycle, and a third of
+// a warp's time is spent on loads that its chunk has just issued, for nothing is loaded ahead of a chunk's arithmetic here. With
+// one CTA of 16 warps and loads ahead (8 x 11008 x 4096) the slots are at 58% too, 3.9 warps a scheduler, 128 CTAs for 148 SMs. Measured and not kept: a persistent form with three chunks of a warp in
 // flight and x in shared memory in the order of the MMAs (21.9 us, and 8 x 11008 x 4096 17.5: filling 176 KB of x is in
 // nobody's shadow).
 #pragma once

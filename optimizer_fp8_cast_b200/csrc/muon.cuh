@@ -11,8 +11,14 @@
 // of, range, out of the way. |X|_2 <= 1.21 and |B|_2 <= 3.5 bound every entry by 2^10 * 3.5; an entry below 2^-24 of the
 // largest it may have (2^-14 * 2^-10, where FP16 turns subnormal) loses relative precision but its error stays below
 // 2^-35, against a root mean square of X0's entries of 1 / sqrt(rows cols) (2^-12.7 for 4096 x 11008).
-// Each rounding is one of 2^-12 of an entry, not correlated between entries, and the polynomial's slope is at most 3.45.
-// a I stands in B, so X <- B X needs no third operand; its rounding is 2^-12 of a row of X again.
+// What that costs. A rounding is off by at most 2^-11 of an entry (2^-12.2 in root mean square), not correlated between entries. A step
+// moves an error by the polynomial's slope: by 3.4445 in directions that are still small, by less than 1.6 (up to 4.2 at
+// 1.21) in those that have arrived. So where most of them soon arrive the result is off by 1.0e-3 to 1.4e-3 of the factor's norm
+// (matrices of noise, spectra that fall as k^-0.5; BF16 intermediates: about 8 times that), and where few do, the noise
+// of X0's rounding, 2^-12.2 of its norm times 3.4445^5 = 485, decides: about 0.1 in norm beside a factor of norm sqrt(r) with r
+// directions that have arrived. Measured over 256 x 256 to 2600 x 2400, relative to the factor: spectra k^-1 2e-3 to 4e-3, k^-1.5
+// 1.0e-2 to 1.2e-2, k^-2 2.0e-2, k^-3 3.7e-2. (The rounding of a BF16 input does eight times that: k^-2 0.15.)
+// a I stands in B, so X <- B X needs no third operand; its rounding is at most 2^-11.8 of a row of X, alike in every row.
 // A and B are symmetric: only the tiles on and above the diagonal are computed, and a tile off it is stored twice, once
 // transposed. With s = min(rows, cols), l = max: s^2 l + s^3 + 2 s^2 l operations a step.
 // |u|_F is summed in FP64. A call whose any |u|_F is not finite changes no m, p or w (as AdamW skips on a non-finite norm);
@@ -587,8 +593,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) k_
     const int part = warp - 2, n = lane * 8;
     float v[8][8];
     if (warp >= 2) {
-      // A thread's 64 squares in f32 where they are in its range (their sum is off by at most 2^-20, of which the norm has half
-      // and X0's FP16 rounds 2^-11 away); FP64 throughout took 1 us more.
+      // A thread's 64 squares in f32 where they are in its range: sixteen roundings of a partial sum and two of the partials', so
+      // a sum is off by at most 18 * 2^-24, less than 2^-19, of which the norm has half and X0 is rounded to 2^-11; FP64
+      // throughout took 1 us more.
       float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
