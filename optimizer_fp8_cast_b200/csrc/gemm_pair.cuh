@@ -49,6 +49,7 @@ struct PairSmem {
   uint64_t acc_empty[2];          // even CTA: every epilogue warp of both CTAs has read an accumulator
   uint64_t mma_done;              // even CTA: every issued MMA has completed
   uint64_t loaded[kPairEpiWarps]; // an epilogue warp's chunks have landed
+  uint64_t taken[kPairEpiWarps];  // its loads of them have left the queue to shared memory
   uint32_t tmem_base;
   uint32_t amax;                  // largest magnitude pattern that this CTA's epilogue has seen
   uint32_t warps_done;            // phases that its epilogue warps have ended, summed
@@ -83,20 +84,27 @@ struct Out {
   uint32_t count;                 // chunks staged so far
   uint32_t amax;                  // this lane's largest magnitude pattern
   int lane;
-  uint8_t* in;                    // where its chunks are loaded to, and their barrier
+  uint8_t* in;                    // where its chunks are loaded to, and their barriers
   uint32_t loaded, phase;
+  uint32_t taken, taken_phase;
   uint64_t limit;
 };
-// The warp's next chunks: `maps` at column x, row y (whatever lies outside the matrix reads as zeros). The lanes have read
-// what was there.
+// The warp's next chunks: `maps` at column x, row y (whatever lies outside the matrix reads as zeros). The lanes have issued
+// their loads of what was there, but a warp's barrier does not wait for them to be carried out: behind a __syncwarp alone the copy
+// came first for about one chunk in a million, where the tensor cores keep shared memory busy. So each lane orders its loads
+// before the async proxy, and lane 0 sees an arrival that it has queued behind them.
 template <int N>
 __device__ __forceinline__ void fetch(Out& o, const CUtensorMap* const (&maps)[N], const int (&x)[N], int y) {
+  fence_proxy_async_smem();
   __syncwarp();
   if (o.lane == 0) {
+    mbar_arrive(o.taken);
+    mbar_wait(o.taken, o.taken_phase, o.limit);
     mbar_arrive_expect_tx(o.loaded, N * kEpiChunkBytes);
 #pragma unroll
     for (int i = 0; i < N; ++i) tma_load_2d(smem_u32(o.in + i * kEpiChunkBytes), maps[i], x[i], y, o.loaded);
   }
+  o.taken_phase ^= 1;
 }
 // Waits for them; false if the wait expired.
 __device__ __forceinline__ bool fetched(Out& o) {
@@ -246,7 +254,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(smem_u32(&S->acc_empty[a]), 2 * kPairEpiWarps);
     }
     mbar_init(smem_u32(&S->mma_done), 1);
-    for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(smem_u32(&S->loaded[w]), 1);
+    for (int w = 0; w < kPairEpiWarps; ++w) {
+      mbar_init(smem_u32(&S->loaded[w]), 1);
+      mbar_init(smem_u32(&S->taken[w]), 1);
+    }
     *abort_flag = 0;
     S->amax = 0;
     S->warps_done = 0;
@@ -375,7 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ---------------- epilogue warps 2..9 (both CTAs): TMEM lane quarter warp % 4, column half
     const int quad = warp & 3, half = (warp - 2) >> 2;
     Out o{sEpi + (warp - 2) * 2 * kEpiChunkBytes, 0u, 0u, lane,
-          sEpi + (2 * kPairEpiWarps + (warp - 2) * Op::kLoads) * kEpiChunkBytes, smem_u32(&S->loaded[warp - 2]), 0u, limit};
+          sEpi + (2 * kPairEpiWarps + (warp - 2) * Op::kLoads) * kEpiChunkBytes, smem_u32(&S->loaded[warp - 2]), 0u,
+          smem_u32(&S->taken[warp - 2]), 0u, limit};
     const typename Op::Scalars k = Op::scalars(g);
     uint32_t i = 0;
     bool ok = true;
