@@ -185,7 +185,7 @@ template <int WF, int AF, int G>
 __global__ void __launch_bounds__(32 * kRowWarps, 1) k_gated_rows_mn(const __grid_constant__ RowMnParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t landed[kRowWarps][kMaxRing];
+  __shared__ uint64_t landed[kRowWarps][kMaxRing], taken[kRowWarps];
   __shared__ int given_up;
   const RowParams& p = P.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -193,10 +193,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) k_gated_rows_mn(const __gri
   constexpr int kOuts = 32 * G, kBytes = 2 * 32 * kOuts;
   const int n0 = blockIdx.x * kOuts, token0 = blockIdx.y * kRowTokens;
   const int chunks = (p.K + 31) / 32;
-  if (lane < P.ring) {
-    mbar_init(smem_u32(&landed[warp][lane]), 1);
-    fence_mbar_init();
-  }
+  if (lane < P.ring) mbar_init(smem_u32(&landed[warp][lane]), 1);
+  if (lane == 0) mbar_init(smem_u32(&taken[warp]), 1);
+  fence_mbar_init();
   if (threadIdx.x == 0) given_up = 0;
   __syncthreads();
   const uint64_t limit = wait_limit_ns();
@@ -213,6 +212,20 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) k_gated_rows_mn(const __gri
     }
   };
   for (int s = 0; s < P.ring; ++s) fetch(warp + s * warps, s);
+  // A slot that the lanes have issued their loads of: a __syncwarp alone does not keep the copy behind them (pair::fetch), so lane 0
+  // sees an arrival first that it has queued behind them (a round trip: 1 x 11008 -> 2 x 4096 27.7 us, 26.1 without it; seen a
+  // chunk's arithmetic later instead, the slot stays empty for that long, 28.6).
+  uint32_t refills = 0;
+  auto refill = [&](int c, int s) {
+    __syncwarp();
+    if (c >= chunks) return;
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&taken[warp]));
+      mbar_wait(smem_u32(&taken[warp]), refills & 1, limit);
+    }
+    ++refills;
+    fetch(c, s);
+  };
   // tokens past M are loaded as the last one; K is a multiple of 16
   const uint8_t* a = p.a + static_cast<int64_t>(min(token0 + g, p.M - 1)) * p.K + 4 * t;
   auto x_of = [&](int c, int h) {
@@ -268,10 +281,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) k_gated_rows_mn(const __gri
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               v[h][u][i] = *reinterpret_cast<const uint32_t*>(slot + (at[i] ^ (G == 4 ? q * 32 : 0)) + h * 16 * kOuts + u * (kBytes / 2) + (G == 4 ? 0 : q * 32));
-        if (q + 1 == G) {
-          __syncwarp();                                    // all have read the slot, and the MMA's lanes come together
-          fetch(c + P.ring * warps, s);
-        }
+        if (q + 1 == G) refill(c + P.ring * warps, s);
+        __syncwarp();                                      // the MMA's lanes together
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll

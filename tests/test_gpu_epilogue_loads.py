@@ -1,6 +1,6 @@
-"""Products whose epilogue reads tensors that are brought beside the tensor cores' work: the same call gives the same bits every
+"""Products that read tensors through buffers which are filled beside the tensor cores' work: the same call gives the same bits every
 time. A chunk's buffer is filled again as soon as its reads have been issued, so a fill that came before a queued read
-showed as 16-byte pieces of the next chunk, in about one call of a hundred of these sizes."""
+showed as 16-byte pieces of the next chunk, in about one gradient of a hundred of these sizes."""
 import pytest
 import torch
 
@@ -39,5 +39,18 @@ def test_newton_schulz_repeats(cuda_lib, rows, cols, times):
     for _ in range(times):
         cuda_lib.muon_orthogonalize([x], [out], workspace=ws)
         wrong += int(not torch.equal(out.view(torch.int16), want.view(torch.int16)))
+    cuda_lib.fp8t_check_device_error()
+    assert wrong == 0
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 4736), (8, 4096, 9472), (8, 1024, 11008), (24, 2048, 688), (3, 528, 40000)])
+def test_few_rows_repeat(cuda_lib, M, K, N):
+    """W as [K][2N] in tiles of 32 to 128 outputs; the smaller weights stay in L2, so that the next chunk comes soon."""
+    a, w, inv = codes((M, K), E4, 1), codes((K, 2 * N), E4, 2), scalar(0.05)
+    want, h, wrong = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), 0
+    cuda_lib.fp8_gated_gemm(a, 0, w, 0, inv, inv, b_mn=True, h=want)
+    for _ in range(1000):
+        cuda_lib.fp8_gated_gemm(a, 0, w, 0, inv, inv, b_mn=True, h=h)
+        wrong += int(not torch.equal(h.view(torch.int16), want.view(torch.int16)))
     cuda_lib.fp8t_check_device_error()
     assert wrong == 0

@@ -1,5 +1,5 @@
 """A buffer in shared memory that a warp has read and fills again by an asynchronous copy: the reads may still be queued behind
-a __syncwarp, so the source orders them (a proxy fence by every lane) and sees an arrival that it queued behind them."""
+a __syncwarp, so lane 0 sees an arrival that it queued behind them before it starts the copy."""
 import re
 
 import pytest
@@ -8,10 +8,16 @@ from tests.test_early_launch_cpu import body
 from tests.test_feed_forward_abi_cpu import code
 
 
-@pytest.mark.parametrize("name,head", [("gemm_pair.cuh", r"void fetch\(")])
-def test_reads_are_over_before_the_copy(name, head):
+@pytest.mark.parametrize("name,head,copy", [("gemm_pair.cuh", r"void fetch\(", "tma_load_2d("),
+                                            ("gated_rows.cuh", r"auto refill = ", "fetch(")])
+def test_reads_are_over_before_the_copy(name, head, copy):
     f = body(code(name), head)
-    order = [f.index(s) for s in ("fence_proxy_async_smem()", "__syncwarp()", "mbar_arrive(", "mbar_wait(", "mbar_arrive_expect_tx(",
-                                  "tma_load_2d(")]
+    order = [f.index(s) for s in ("__syncwarp()", "mbar_arrive(", "mbar_wait(", copy)]
     assert order == sorted(order)
-    assert len(re.findall(r"tma_load_2d\(", f)) >= 1
+
+
+def test_slots_are_filled_again_in_one_place():
+    text = code("gated_rows.cuh")
+    kernel = text[text.index("k_gated_rows_mn("):]
+    loop = body(kernel, r"for \(int c0 = warp;")
+    assert "refill(" in loop and not re.search(r"\bfetch\(", loop)
