@@ -503,7 +503,7 @@ size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 /* Activation of a gated feed-forward block: act(g) = g * sigmoid(w(g)). */
 typedef enum fp8t_act {
     FP8T_ACT_NONE = 0,             /* fp4_matvec only: no gate                                      */
-    FP8T_ACT_SILU = 1,             /* w = g                                                         */
+    FP8T_ACT_SILU = 1,             /* w = g; a sigmoid below 2^-126 counts as 0 (GELU too)          */
     FP8T_ACT_GELU = 2              /* w = 2 sqrt(2 / pi) (g + 0.044715 g^3): GELU in its tanh form  */
 } fp8t_act;
 

@@ -1836,9 +1836,12 @@ fp8t_status fill_gated(fp8t::gated::Params& p, const GatedCall& c, int outputs, 
   return st;
 }
 // Few rows: always up to eight, and up to 32 while the weights, read once for every eight rows, are small. Few-rows kernel / pair
-// tiles, graph replays. W out x in: 8 x 4096 -> 2 x 11008 20.7 / 24.8 us, 16 rows 34.4 / 24.5; 16 x 2048 -> 2 x 5504 (45 MB for two
-// eights) 8.2 / 10.1, 24 rows 15.5 / 10.0; 32 x 1024 -> 2 x 2752 5.7 / 6.5. W in x out: 8 x 4096 -> 2 x 11008 19.9 / 26, 16 rows
-// 35.6 / 25.8; 24 x 2048 -> 2 x 2752 (34 MB) 9.3 / 9.8, 32 rows (45 MB) 10.9 / 9.7; 16 x 256 -> 2 x 688 3.4 / 5.7.
+// tiles, graph replays, cold weights. W out x in: 8 x 4096 -> 2 x 11008 21.7 / 26.3 us; 16 x 4096 -> 2 x 2048 (34 MB for two eights)
+// 7.8 / 13.4, 16 x 11008 -> 2 x 1024 (45 MB) 14.0 / 27.7, 24 x 2048 -> 2 x 2752 (34 MB) 9.5 / 9.2, 32 x 2048 -> 2 x 2752 (45 MB) 9.9 / 9.2,
+// 32 x 1024 -> 2 x 2752 6.9 / 6.9; past the limit 16 x 4096 -> 2 x 11008 34.4 / 24.5. W in x out: 8 x 4096 -> 2 x 11008 21.0 / 27.3;
+// 16 x 4096 -> 2 x 2048 12.7 / 14.6, 32 x 2048 -> 2 x 1376 (23 MB) 9.8 / 9.9, 24 x 2048 -> 2 x 2752 10.3 / 10.1, 16 x 256 -> 2 x 688 3.3 / 5.6; past
+// the limit 32 x 2048 -> 2 x 2752 11.6 / 10.1. The rule goes by bytes alone: where k is small and n large pair tiles would be faster
+// (32 x 512 -> 2 x 5504 8.1 / 6.9 and 11.4 / 7.2), and in x out long k past the limit would be faster here (16 x 11008 -> 2 x 1024 26.1 / 29.6).
 bool gated_few_rows(const fp8t_gated& d) {
   const int64_t groups = (d.M + 7) / 8, most = d.b_layout == FP8T_MN_MAJOR ? int64_t(36) << 20 : int64_t(48) << 20;
   return groups == 1 || (d.M <= 32 && groups * 2 * d.N * d.K <= most);
@@ -1882,7 +1885,7 @@ fp8t_status launch_gated_rows_as(const fp8t::gated::RowParams& p, bool mn, int s
   }
   // Tiles for which the SMs' rounds take the least time, a CTA an SM: its time goes with the width, and something for its start.
   // The ring keeps a second CTA out: it would be the next call's, and take a place that the scheduler then fills unevenly (1 x 4096
-  // -> 2 x 11008 in 172 tiles of 64, two an SM, 23.0 us; in 115 of 96 18.3).
+  // -> 2 x 11008 in 172 tiles of 64, two an SM, 23.0 us; in 115 of 96 18.3, now 19.4 with slots filled behind their reads).
   const int64_t groups = cfg.gridDim.y;
   int best = 1;
   int64_t least = INT64_MAX;

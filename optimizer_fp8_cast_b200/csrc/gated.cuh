@@ -59,7 +59,7 @@ __device__ __forceinline__ float rcp(float x) {            // 1 / x, to 1 ulp; 0
   return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;
-// Sigmoid of w(g), and w'(g) where the operator needs it (1 for SiLU). g^2 is held to 10^12, far past where the sigmoid is 0 or
+// Sigmoid of w(g), 0 where it is below 2^-126 (g under -87.3 for SiLU, -10.0 for GELU), and w'(g) where the operator needs it (1 for SiLU). g^2 is held to 10^12, far past where the sigmoid is 0 or
 // 1 in f32, so that w' stays finite.
 template <int ACT>
 __device__ __forceinline__ f32x2 gate(f32x2 g, f32x2& dw) {

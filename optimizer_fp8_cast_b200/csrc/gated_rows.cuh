@@ -173,7 +173,8 @@ __device__ __forceinline__ void transpose4(const uint32_t (&v)[4], uint32_t (&o)
 // W [K][2N]: a CTA takes 32 G outputs, a warp all of them for its chunks of 32 k. Each warp keeps `ring` chunks on their way into
 // shared memory (two boxes of 32 k x 32 G outputs, with 128 of them in the 128-byte swizzle, against bank conflicts) and waits for
 // them alone; 144 to 192 KB of an SM are in flight. A's words come kAhead chunks ahead, in registers: one chunk ahead their latency
-// was the chunk's time (8 x 4096 -> 2 x 11008 21.7 -> 19.8 us, 1 x 11008 -> 2 x 4096 28.2 -> 26.2).
+// was the chunk's time (8 x 4096 -> 2 x 11008 21.7 -> 19.8 us, 1 x 11008 -> 2 x 4096 28.2 -> 26.2; since slots are filled behind their
+// reads 21.0 and 27.7).
 constexpr int kMaxRing = 9, kAhead = 4;
 constexpr int row_smem_bytes(int groups, int ring, int warps) { return warps * ring * 2 * 32 * 32 * groups + 1024; }
 struct alignas(64) RowMnParams {
