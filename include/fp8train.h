@@ -591,8 +591,8 @@ fp8t_status fp4_matvec(const fp8t_fp4_matvec* desc, void* stream);
  * muon_orthogonalize — for each matrix X0 (BF16 or f32), out = bf16(X) after `steps` Newton-Schulz steps
  *   X = X0 / |X0|_F;   A = X X^T,  X <- a X + (b A + c A A) X       (a, b, c) = (3.4445, -4.775, 2.0315)
  * which leaves X0's singular vectors and moves its singular values towards 1 (into about 0.68 .. 1.21). FP16
- * products under a factor of 2^10 with FP32 accumulation, |X0|_F in FP64, whatever X0's type: X, A and b A + c A A are rounded to
- * 11 bits. After five steps that leaves about 1.3e-3 of the result (its own rounding to BF16: 1.7e-3) where most singular values
+ * products under a factor of 2^10 with FP32 accumulation, |X0|_F in FP64, whatever X0's type: X, A and a I + b A + c A A are rounded
+ * to 11 bits. After five steps that leaves about 1.3e-3 of the result (its own rounding to BF16: 1.7e-3) where most singular values
  * are within 1/100 of the largest, and an error of about 0.1 in norm where few are (2e-2 of the result for values
  * falling as k^-2, 4e-2 as k^-3). A zero matrix stays zero; one
  * with a non-finite element becomes NaN. Any sizes from 1 x 1 up to 65536 each way.

@@ -518,7 +518,7 @@ def muon_orthogonalize(xs, outs, *, steps=5, workspace=None, stream=None):
     """The nearest-orthogonal factor of each matrix of ``xs`` (all BF16 or all float32) into ``outs`` (BF16 of the same
     shape; may be the BF16 input itself) by ``steps`` Newton-Schulz steps: X = x / |x|_F, then
     X <- aX + (bA + cA^2) X with A = X X^T and (a, b, c) = (3.4445, -4.775, 2.0315); singular values end in about 0.68 to
-    1.21. X, A and bA + cA^2 are held in FP16 (11 bits, FP32 accumulation) whatever the type of ``xs``: about 1.3e-3 of the result
+    1.21. X, A and aI + bA + cA^2 are held in FP16 (11 bits, FP32 accumulation) whatever the type of ``xs``: about 1.3e-3 of the result
     for most matrices, up to 4e-2 where the singular values fall as k^-3. ``workspace``: a uint8 CUDA tensor of muon_workspace_bytes (allocated per call where it is missing)."""
     if not xs or len(xs) != len(outs):
         raise ValueError("xs and outs must be lists of the same length, not empty")
